@@ -235,6 +235,49 @@ rmsnorm_status_t rmsnorm_fwd_grid_noalloc(int32_t dtype, const void* x, const vo
                                           rmsnorm_stream_t stream);
 
 /*
+ * rmsnorm_bwd_f32 -- the backward pass of rmsnorm_fwd_f32 (the page has the
+ * forward pass only).  Given dy = dL/dy, with xh = x * rstd, g = dy * w and
+ * m(.) the mean over a row:
+ *
+ *     dx[r,j] = rstd[r] * (g[r,j] - xh[r,j] * m(g * xh)[r])
+ *     dw[j]   = sum_r dy[r,j] * xh[r,j]
+ *
+ * rstd is computed again from x (same eps).  dy, x, dx: rows*hidden elements,
+ * contiguous; w: hidden elements, NULL for ones; dw: hidden floats (fp32 for
+ * both types), NULL: not computed.  dx == dy or dx == x (in place) is allowed;
+ * any other overlap of an output or the workspace with another argument is
+ * rejected.  fp32 arithmetic; sums have a fixed order (no atomics), so results
+ * are bitwise repeatable.  rows == 0 writes zeros to dw.
+ * workspace: 16-byte aligned device memory of at least the bytes that
+ * rmsnorm_bwd_workspace gives, contents undefined before and after; calls that
+ * can overlap on the GPU (other streams, two captured graphs) need one each.
+ * Allocates nothing; errors as for rmsnorm_fwd_f32.
+ */
+rmsnorm_status_t rmsnorm_bwd_f32(const float* dy, const float* x, const float* w, float* dx,
+                                 float* dw, int64_t rows, int64_t hidden, float eps,
+                                 void* workspace, size_t workspace_bytes,
+                                 rmsnorm_stream_t stream);
+
+/* The same for bfloat16 dy, x, w and dx (raw 16-bit patterns; dx rounded once). */
+rmsnorm_status_t rmsnorm_bwd_bf16(const uint16_t* dy, const uint16_t* x, const uint16_t* w,
+                                  uint16_t* dx, float* dw, int64_t rows, int64_t hidden, float eps,
+                                  void* workspace, size_t workspace_bytes,
+                                  rmsnorm_stream_t stream);
+
+/* Either dtype, with options (`opt` may be NULL): opt->path RMSNORM_PATH_AUTO
+ * or RMSNORM_PATH_TWOPASS (a pair of sums per row, then dx and partial column
+ * sums, each reading x and dy once: any width and alignment).  Every other
+ * field must be zero, else RMSNORM_ERR_INVALID_ARG. */
+rmsnorm_status_t rmsnorm_bwd_ex(int32_t dtype, const void* dy, const void* x, const void* w,
+                                void* dx, float* dw, int64_t rows, int64_t hidden, float eps,
+                                void* workspace, size_t workspace_bytes,
+                                const rmsnorm_options_t* opt, rmsnorm_stream_t stream);
+
+/* Bytes of workspace that a backward pass of this shape takes on the current
+ * device, whatever the pointers' alignment. */
+rmsnorm_status_t rmsnorm_bwd_workspace(int32_t dtype, int64_t rows, int64_t hidden, size_t* bytes);
+
+/*
  * rmsnorm_plan -- no passage of the page: a query of this library's launch
  * heuristics.  Fill *plan with what rmsnorm_fwd_ex(dtype, x, w, y, rows,
  * hidden, ., opt, .) would launch on the current device, without launching.

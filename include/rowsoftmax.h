@@ -102,6 +102,119 @@ rmsnorm_status_t rowsoftmax_plan(int32_t dtype, const void* x, const void* y, in
                                  int64_t cols, const rmsnorm_options_t* opt,
                                  rmsnorm_plan_t* plan);
 
+/*
+ * Row softmax of attention scores with a learned relative position bias, and
+ * its backward pass (the page has no counterpart).
+ *
+ * Scores x[b, h, i, j] (batch, head, query, key), contiguous, rows of k_len.
+ * The query stands at position q = q_offset + q_start[b] + i, a key at j; with
+ * r = j - q and a table t[bucket, head] of learned biases,
+ *
+ *     v[j] = scale * x[j] + t[bucket(r), h]          over the row's valid keys
+ *     y[j] = exp(v[j] - max v) / sum exp(v - max v)  at valid keys, 0 elsewhere
+ *
+ * Valid keys are j < kv_len[b] and, if causal, r <= 0.  Nothing is read at the
+ * others, and a row without a valid key is all zero.  Among valid keys special
+ * values behave as in rowsoftmax_fwd_f32: -inf gives 0; a row of -inf, or any
+ * NaN or +inf, gives NaN at the valid keys.
+ *
+ * Buckets: of the num_buckets, one direction has half (bidirectional: r <= 0
+ * the lower, r > 0 the upper half) or all of them (else: every r > 0 is in
+ * bucket 0).  With n = |r| (n = 0 for those) and near = half / 2, bucket n up
+ * to near, then near + floor(log(n / near) / log(max_distance / near) *
+ * (half - near)), at most half - 1; the logarithm is the real number's, so a
+ * distance exactly on an edge is in the upper bucket.
+ *
+ * Given dy = dL/dy and the outputs y:
+ *
+ *     ds = y * (dy - sum_j y * dy)     dx = scale * ds  (0 at masked keys)
+ *     dt[k, h] = sum of ds over b, i and the valid j with bucket(r) = k
+ *
+ * dt is fp32 for both types; neither y nor dy is read at masked keys.
+ *
+ *  - x, y, dy, dx: batch*heads*q_len*k_len elements; table: num_buckets*heads
+ *    elements of the same type; dtable: num_buckets*heads floats; q_start and
+ *    kv_len: batch int32 values in DEVICE memory, or NULL (q_start 0, kv_len
+ *    k_len); kv_len values are taken into [0, k_len].
+ *  - batch, q_len >= 0 (a product of 0: OK, no launch; the backward pass writes
+ *    zeros to dtable); 1 <= heads <= 65535; 1 <= k_len <= 2^30; batch * q_len <
+ *    2^31; 2 <= num_buckets <= 256 (bidirectional: even, at least 4);
+ *    half / 2 < max_distance <= 4096; scale finite; |q_offset| <= 2^40.
+ *  - y == x, and dx == dy or dx == y, are allowed (in place); any other overlap
+ *    of an output or the workspace with another argument is rejected.
+ *  - Asynchronous on `stream`, allocating nothing, launched and checked as the
+ *    other entry points.  Sums have a fixed order (no atomics): results are
+ *    bitwise repeatable.
+ *  - workspace (needed with dtable): 16-byte aligned device memory of at least
+ *    the bytes that rowsoftmax_relbias_bwd_workspace gives, contents undefined
+ *    before and after; calls that can overlap on the GPU (other streams, two
+ *    captured graphs) need one each.
+ */
+typedef struct {
+    int32_t num_buckets;
+    int32_t max_distance;
+    int32_t bidirectional;   /* 1: positive positions have buckets of their own */
+    int32_t causal;          /* 1: keys after the query are masked */
+    float scale;             /* of the scores, before the bias is added */
+    int32_t reserved;        /* must be 0 */
+    int64_t q_offset;        /* position of query 0, before q_start */
+    const int32_t* q_start;  /* device, [batch], or NULL */
+    const int32_t* kv_len;   /* device, [batch], or NULL */
+} rowsoftmax_relbias_t;
+
+rmsnorm_status_t rowsoftmax_relbias_fwd_f32(const float* x, const float* table, float* y,
+                                            int64_t batch, int64_t heads, int64_t q_len,
+                                            int64_t k_len, const rowsoftmax_relbias_t* bias,
+                                            rmsnorm_stream_t stream);
+
+/* The same for bfloat16 x, table and y (raw 16-bit patterns; fp32 arithmetic). */
+rmsnorm_status_t rowsoftmax_relbias_fwd_bf16(const uint16_t* x, const uint16_t* table, uint16_t* y,
+                                             int64_t batch, int64_t heads, int64_t q_len,
+                                             int64_t k_len, const rowsoftmax_relbias_t* bias,
+                                             rmsnorm_stream_t stream);
+
+/* Either dtype, with options (`opt` may be NULL): opt->path RMSNORM_PATH_AUTO
+ * or RMSNORM_PATH_TWOPASS (rows of any width, read twice).  Every other field
+ * must be zero, else RMSNORM_ERR_INVALID_ARG. */
+rmsnorm_status_t rowsoftmax_relbias_fwd_ex(int32_t dtype, const void* x, const void* table,
+                                           void* y, int64_t batch, int64_t heads, int64_t q_len,
+                                           int64_t k_len, const rowsoftmax_relbias_t* bias,
+                                           const rmsnorm_options_t* opt, rmsnorm_stream_t stream);
+
+/* Bytes of workspace that a backward pass of this shape takes on the current
+ * device, whatever the pointers' alignment. */
+rmsnorm_status_t rowsoftmax_relbias_bwd_workspace(int32_t dtype, int64_t batch, int64_t heads,
+                                                  int64_t q_len, int64_t k_len,
+                                                  const rowsoftmax_relbias_t* bias,
+                                                  size_t* bytes);
+
+/* dx, and dtable unless it is NULL (then the workspace may be NULL too). */
+rmsnorm_status_t rowsoftmax_relbias_bwd_f32(const float* dy, const float* y, float* dx,
+                                            float* dtable, int64_t batch, int64_t heads,
+                                            int64_t q_len, int64_t k_len,
+                                            const rowsoftmax_relbias_t* bias, void* workspace,
+                                            size_t workspace_bytes, rmsnorm_stream_t stream);
+
+/* The same for bfloat16 dy, y and dx. */
+rmsnorm_status_t rowsoftmax_relbias_bwd_bf16(const uint16_t* dy, const uint16_t* y, uint16_t* dx,
+                                             float* dtable, int64_t batch, int64_t heads,
+                                             int64_t q_len, int64_t k_len,
+                                             const rowsoftmax_relbias_t* bias, void* workspace,
+                                             size_t workspace_bytes, rmsnorm_stream_t stream);
+
+/* Either dtype, with options as for rowsoftmax_relbias_fwd_ex. */
+rmsnorm_status_t rowsoftmax_relbias_bwd_ex(int32_t dtype, const void* dy, const void* y, void* dx,
+                                           float* dtable, int64_t batch, int64_t heads,
+                                           int64_t q_len, int64_t k_len,
+                                           const rowsoftmax_relbias_t* bias, void* workspace,
+                                           size_t workspace_bytes, const rmsnorm_options_t* opt,
+                                           rmsnorm_stream_t stream);
+
+/* The bucket of relative position `relative` (host function, no device
+ * needed); -1 if the rule's numbers are out of the ranges above. */
+int32_t rowsoftmax_relbias_bucket(int64_t relative, int32_t num_buckets, int32_t max_distance,
+                                  int32_t bidirectional);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,4 +1,4 @@
-"""ctypes binding of librmsnorm's C ABI (``include/rmsnorm.h``).
+"""ctypes binding of librmsnorm's C ABI (``include/*.h``).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels of ``librmsnorm.so``.  Functions carry the C names.  Tensor-level
@@ -51,6 +51,14 @@ class rmsnorm_plan_t(ctypes.Structure):
                 ("smem_bytes", ctypes.c_int32), ("chunk_bytes", ctypes.c_int32),
                 ("stages", ctypes.c_int32), ("weights_staged", ctypes.c_int32),
                 ("kernel", ctypes.c_char * 48)]
+
+
+class rowsoftmax_relbias_t(ctypes.Structure):
+    _fields_ = [("num_buckets", ctypes.c_int32), ("max_distance", ctypes.c_int32),
+                ("bidirectional", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("q_offset", ctypes.c_int64), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p)]
 
 
 class RmsnormError(RuntimeError):
@@ -112,6 +120,26 @@ def open_library(path: str):
     lib.rowsoftmax_plan.argtypes = [i32, vp, vp, i64, i64, ctypes.POINTER(rmsnorm_options_t),
                                     ctypes.POINTER(rmsnorm_plan_t)]
     lib.rowsoftmax_plan.restype = ctypes.c_int
+    opt, size = ctypes.POINTER(rmsnorm_options_t), ctypes.c_size_t
+    bias = ctypes.POINTER(rowsoftmax_relbias_t)
+    shape = [i64, i64, i64, i64, bias]
+    for family, args in (("layernorm_fwd", [vp] * 6 + [i64, i64, f32]),
+                         ("layernorm_bwd", [vp] * 8 + [i64, i64, vp, size]),
+                         ("rmsnorm_bwd", [vp] * 5 + [i64, i64, f32, vp, size]),
+                         ("rowsoftmax_relbias_fwd", [vp] * 3 + shape),
+                         ("rowsoftmax_relbias_bwd", [vp] * 4 + shape + [vp, size])):
+        for suffix, before, after in (("_f32", [], []), ("_bf16", [], []), ("_ex", [i32], [opt])):
+            fn = getattr(lib, family + suffix)
+            fn.argtypes = before + args + after + [vp]
+            fn.restype = ctypes.c_int
+    for name in ("layernorm_bwd_workspace", "rmsnorm_bwd_workspace"):
+        fn = getattr(lib, name)
+        fn.argtypes = [i32, i64, i64, ctypes.POINTER(size)]
+        fn.restype = ctypes.c_int
+    lib.rowsoftmax_relbias_bwd_workspace.argtypes = [i32] + shape + [ctypes.POINTER(size)]
+    lib.rowsoftmax_relbias_bwd_workspace.restype = ctypes.c_int
+    lib.rowsoftmax_relbias_bucket.argtypes = [i64, i32, i32, i32]
+    lib.rowsoftmax_relbias_bucket.restype = ctypes.c_int32
     return lib
 
 
@@ -134,7 +162,7 @@ def declared_functions() -> list[str]:
         text = open(os.path.join(inc, fname)).read()
         text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
         text = re.sub(r"//[^\n]*", "", text)
-        for m in re.finditer(r"\b((?:rmsnorm|rowsoftmax)_[a-z0-9_]+)\s*\(", text):
+        for m in re.finditer(r"\b((?:rmsnorm|rowsoftmax|layernorm)_[a-z0-9_]+)\s*\(", text):
             if m.group(1) not in names:
                 names.append(m.group(1))
     return names
@@ -384,6 +412,417 @@ def rowsoftmax_plan(x, y=None, options=None) -> dict:
     d["kernel"] = plan.kernel.decode()
     d["path_name"] = PATH_NAMES.get(plan.path, "?")
     return d
+
+
+# ---------------------------------- layer norm and the norm backward passes --
+#
+# These functions work on the device of their tensors and on that device's
+# current stream (or `stream`).  What they allocate -- outputs that are not
+# given, workspaces -- is allocated on the stream the kernels run on, so the
+# caching allocator hands none of it out again before they are done.
+
+def _dtype_code(x):
+    torch = _torch()
+    if x.dtype == torch.float32:
+        return RMSNORM_DTYPE_F32
+    if x.dtype == torch.bfloat16:
+        return RMSNORM_DTYPE_BF16
+    raise TypeError(f"expected float32 or bfloat16, got {x.dtype}")
+
+
+def _require(name, t, dtype, shape, device):
+    """Refuse a tensor of another type, shape, layout or device."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _on_stream(device, stream, body):
+    """body(stream handle) with `device` current and its allocations on the stream."""
+    torch = _torch()
+    if stream is None and device.index == torch.cuda.current_device():
+        return body(torch.cuda.current_stream().cuda_stream)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device) if stream
+                  else torch.cuda.default_stream(device))
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check(st, what):
+    if st != RMSNORM_OK:
+        raise RmsnormError(st, what)
+
+
+def _opt(options):
+    if options is None:
+        return None
+    return ctypes.byref(make_options(**options) if isinstance(options, dict) else options)
+
+
+def _rows_of(x):
+    """(rows, hidden) of a contiguous CUDA tensor with a last dim."""
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise ValueError("x must have a non-empty last dim")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    hidden = x.shape[-1]
+    return x.numel() // hidden, hidden
+
+
+def _workspace(workspace, size, device):
+    """The caller's workspace checked, or a new one: (tensor, bytes)."""
+    if workspace is None:
+        return _torch().empty(size, dtype=_torch().uint8, device=device), size
+    if not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace must be contiguous, on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _layernorm_fwd(name, x, w, b, y, mean, rstd, eps, stats, options, stream):
+    torch = _torch()
+    dt = _dtype_code(x)
+    rows, hidden = _rows_of(x)
+    device, lead = x.device, x.shape[:-1]
+    for n, t, d, shape in (("w", w, x.dtype, (hidden,)), ("b", b, x.dtype, (hidden,)),
+                           ("y", y, x.dtype, x.shape), ("mean", mean, torch.float32, lead),
+                           ("rstd", rstd, torch.float32, lead)):
+        if t is not None:
+            _require(n, t, d, shape, device)
+
+    def body(handle):
+        out = torch.empty_like(x) if y is None else y
+        m, r = mean, rstd
+        if stats:
+            m = torch.empty(lead, dtype=torch.float32, device=device) if m is None else m
+            r = torch.empty(lead, dtype=torch.float32, device=device) if r is None else r
+        if rows:
+            _check(load().layernorm_fwd_ex(dt, x.data_ptr(), _ptr(w), _ptr(b), out.data_ptr(),
+                                           _ptr(m), _ptr(r), rows, hidden, eps, _opt(options),
+                                           handle or None), name)
+        return (out, m, r) if stats else out
+    return _on_stream(device, stream, body)
+
+
+def layernorm_fwd_f32(x, w=None, b=None, y=None, mean=None, rstd=None, eps: float = 1e-5,
+                      stats: bool = False, stream=None):
+    """y = LayerNorm(x) * w + b for float32 CUDA tensors (last dim = hidden).
+    w and b may be None (ones, zeros); mean and rstd (float32, x.shape[:-1])
+    are written if given.  stats=True returns (y, mean, rstd)."""
+    _want(x, RMSNORM_DTYPE_F32)
+    return _layernorm_fwd("layernorm_fwd_f32", x, w, b, y, mean, rstd, eps, stats, None, stream)
+
+
+def layernorm_fwd_bf16(x, w=None, b=None, y=None, mean=None, rstd=None, eps: float = 1e-5,
+                       stats: bool = False, stream=None):
+    """The same for bfloat16 CUDA tensors (fp32 arithmetic)."""
+    _want(x, RMSNORM_DTYPE_BF16)
+    return _layernorm_fwd("layernorm_fwd_bf16", x, w, b, y, mean, rstd, eps, stats, None, stream)
+
+
+def layernorm_fwd_ex(x, w=None, b=None, y=None, mean=None, rstd=None, eps: float = 1e-5,
+                     stats: bool = False, options=None, stream=None):
+    """Either dtype, with options (path auto or twopass)."""
+    return _layernorm_fwd("layernorm_fwd_ex", x, w, b, y, mean, rstd, eps, stats, options, stream)
+
+
+def _want(x, dtype):
+    if _dtype_code(x) != dtype:
+        raise TypeError(f"this entry point takes {'float32' if dtype == 0 else 'bfloat16'}, "
+                        f"got {x.dtype}")
+
+
+def _norm_bwd(name, layer, dy, x, w, mean, rstd, dx, dw, db, eps, weight_grads, workspace,
+              options, stream):
+    torch = _torch()
+    lib = load()
+    dt = _dtype_code(x)
+    rows, hidden = _rows_of(x)
+    device, lead = x.device, x.shape[:-1]
+    _require("dy", dy, x.dtype, x.shape, device)
+    if layer:
+        _require("mean", mean, torch.float32, lead, device)
+        _require("rstd", rstd, torch.float32, lead, device)
+    for n, t, d, shape in (("w", w, x.dtype, (hidden,)), ("dx", dx, x.dtype, x.shape),
+                           ("dw", dw, torch.float32, (hidden,)),
+                           ("db", db, torch.float32, (hidden,))):
+        if t is not None:
+            _require(n, t, d, shape, device)
+
+    def body(handle):
+        out = torch.empty_like(x) if dx is None else dx
+        gw, gb = dw, db
+        if weight_grads:
+            gw = torch.empty(hidden, dtype=torch.float32, device=device) if gw is None else gw
+            if layer and gb is None:
+                gb = torch.empty(hidden, dtype=torch.float32, device=device)
+        if rows == 0:
+            for t in (gw, gb):
+                if t is not None:
+                    t.zero_()
+            return (out, gw, gb) if layer else (out, gw)
+        size = ctypes.c_size_t()
+        query = lib.layernorm_bwd_workspace if layer else lib.rmsnorm_bwd_workspace
+        _check(query(dt, rows, hidden, ctypes.byref(size)), name)
+        ws, n = _workspace(workspace, size.value, device)
+        if layer:
+            st = lib.layernorm_bwd_ex(dt, dy.data_ptr(), x.data_ptr(), _ptr(w), mean.data_ptr(),
+                                      rstd.data_ptr(), out.data_ptr(), _ptr(gw), _ptr(gb), rows,
+                                      hidden, ws.data_ptr(), n, _opt(options), handle or None)
+        else:
+            st = lib.rmsnorm_bwd_ex(dt, dy.data_ptr(), x.data_ptr(), _ptr(w), out.data_ptr(),
+                                    _ptr(gw), rows, hidden, eps, ws.data_ptr(), n, _opt(options),
+                                    handle or None)
+        _check(st, name)
+        return (out, gw, gb) if layer else (out, gw)
+    return _on_stream(device, stream, body)
+
+
+def layernorm_bwd_f32(dy, x, w, mean, rstd, dx=None, dw=None, db=None, weight_grads: bool = True,
+                      workspace=None, stream=None):
+    """(dx, dw, db) of layer norm for float32 CUDA tensors; mean and rstd from
+    the forward pass, w may be None (ones).  dw and db are float32;
+    weight_grads=False computes only those given.  workspace: at least
+    layernorm_bwd_workspace(x) bytes, else one is allocated."""
+    _want(x, RMSNORM_DTYPE_F32)
+    return _norm_bwd("layernorm_bwd_f32", True, dy, x, w, mean, rstd, dx, dw, db, 0.0,
+                     weight_grads, workspace, None, stream)
+
+
+def layernorm_bwd_bf16(dy, x, w, mean, rstd, dx=None, dw=None, db=None, weight_grads: bool = True,
+                       workspace=None, stream=None):
+    """The same for bfloat16 dy, x, w and dx (dw and db are float32)."""
+    _want(x, RMSNORM_DTYPE_BF16)
+    return _norm_bwd("layernorm_bwd_bf16", True, dy, x, w, mean, rstd, dx, dw, db, 0.0,
+                     weight_grads, workspace, None, stream)
+
+
+def layernorm_bwd_ex(dy, x, w, mean, rstd, dx=None, dw=None, db=None, weight_grads: bool = True,
+                     workspace=None, options=None, stream=None):
+    """Either dtype, with options (path auto or twopass)."""
+    return _norm_bwd("layernorm_bwd_ex", True, dy, x, w, mean, rstd, dx, dw, db, 0.0,
+                     weight_grads, workspace, options, stream)
+
+
+def rmsnorm_bwd_f32(dy, x, w, dx=None, dw=None, eps: float = 1e-6, weight_grads: bool = True,
+                    workspace=None, stream=None):
+    """(dx, dw) of RMSNorm for float32 CUDA tensors; w may be None (ones).
+    dw is float32; weight_grads=False computes it only if given.  workspace:
+    at least rmsnorm_bwd_workspace(x) bytes, else one is allocated."""
+    _want(x, RMSNORM_DTYPE_F32)
+    return _norm_bwd("rmsnorm_bwd_f32", False, dy, x, w, None, None, dx, dw, None, eps,
+                     weight_grads, workspace, None, stream)
+
+
+def rmsnorm_bwd_bf16(dy, x, w, dx=None, dw=None, eps: float = 1e-6, weight_grads: bool = True,
+                     workspace=None, stream=None):
+    """The same for bfloat16 dy, x, w and dx (dw is float32)."""
+    _want(x, RMSNORM_DTYPE_BF16)
+    return _norm_bwd("rmsnorm_bwd_bf16", False, dy, x, w, None, None, dx, dw, None, eps,
+                     weight_grads, workspace, None, stream)
+
+
+def rmsnorm_bwd_ex(dy, x, w, dx=None, dw=None, eps: float = 1e-6, weight_grads: bool = True,
+                   workspace=None, options=None, stream=None):
+    """Either dtype, with options (path auto or twopass)."""
+    return _norm_bwd("rmsnorm_bwd_ex", False, dy, x, w, None, None, dx, dw, None, eps,
+                     weight_grads, workspace, options, stream)
+
+
+def _bwd_workspace(name, x):
+    rows, hidden = _rows_of(x)
+    size = ctypes.c_size_t()
+    with _torch().cuda.device(x.device):
+        _check(getattr(load(), name)(_dtype_code(x), rows, hidden, ctypes.byref(size)), name)
+    return size.value
+
+
+def layernorm_bwd_workspace(x) -> int:
+    """Bytes of workspace of layernorm_bwd_* for a tensor of x's shape and type."""
+    return _bwd_workspace("layernorm_bwd_workspace", x)
+
+
+def rmsnorm_bwd_workspace(x) -> int:
+    """Bytes of workspace of rmsnorm_bwd_* for a tensor of x's shape and type."""
+    return _bwd_workspace("rmsnorm_bwd_workspace", x)
+
+
+# ------------------------------ row softmax with a relative position bias --
+
+def _relbias(x, num_buckets, max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len):
+    if x.dim() != 4 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("scores must be a contiguous CUDA tensor [batch, heads, queries, keys]")
+    for n, t in (("q_start", q_start), ("kv_len", kv_len)):
+        if t is not None:
+            _require(n, t, _torch().int32, x.shape[:1], x.device)
+    return rowsoftmax_relbias_t(num_buckets, max_distance, bool(bidirectional), bool(causal),
+                                scale, 0, q_offset, _ptr(q_start), _ptr(kv_len))
+
+
+def _relbias_fwd(name, x, table, y, rule, options, stream):
+    torch = _torch()
+    dt = _dtype_code(x)
+    if table.dim() != 2:
+        raise ValueError("table must have shape (num_buckets, heads)")
+    a = _relbias(x, table.shape[0], **rule)
+    _require("table", table, x.dtype, (table.shape[0], x.shape[1]), x.device)
+    if y is not None:
+        _require("y", y, x.dtype, x.shape, x.device)
+
+    def body(handle):
+        out = torch.empty_like(x) if y is None else y
+        if x.numel():
+            _check(load().rowsoftmax_relbias_fwd_ex(dt, x.data_ptr(), table.data_ptr(),
+                                                    out.data_ptr(), *x.shape, ctypes.byref(a),
+                                                    _opt(options), handle or None), name)
+        return out
+    return _on_stream(x.device, stream, body)
+
+
+def _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len):
+    return dict(max_distance=max_distance, bidirectional=bidirectional, causal=causal,
+                scale=scale, q_offset=q_offset, q_start=q_start, kv_len=kv_len)
+
+
+def rowsoftmax_relbias_fwd_f32(x, table, y=None, *, max_distance: int = 128,
+                               bidirectional: bool = True, causal: bool = False,
+                               scale: float = 1.0, q_offset: int = 0, q_start=None, kv_len=None,
+                               stream=None):
+    """y = softmax(scale * x + table[bucket(key - query), head]) over the valid
+    keys of float32 scores [batch, heads, queries, keys]; table is
+    [num_buckets, heads].  Query i of sequence b stands at q_offset +
+    q_start[b] + i; keys from kv_len[b] on, and with `causal` keys after the
+    query, are masked (0).  q_start and kv_len: int32 [batch]."""
+    _want(x, RMSNORM_DTYPE_F32)
+    rule = _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len)
+    return _relbias_fwd("rowsoftmax_relbias_fwd_f32", x, table, y, rule, None, stream)
+
+
+def rowsoftmax_relbias_fwd_bf16(x, table, y=None, *, max_distance: int = 128,
+                                bidirectional: bool = True, causal: bool = False,
+                                scale: float = 1.0, q_offset: int = 0, q_start=None, kv_len=None,
+                                stream=None):
+    """The same for bfloat16 scores and table (fp32 arithmetic)."""
+    _want(x, RMSNORM_DTYPE_BF16)
+    rule = _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len)
+    return _relbias_fwd("rowsoftmax_relbias_fwd_bf16", x, table, y, rule, None, stream)
+
+
+def rowsoftmax_relbias_fwd_ex(x, table, y=None, *, max_distance: int = 128,
+                              bidirectional: bool = True, causal: bool = False,
+                              scale: float = 1.0, q_offset: int = 0, q_start=None, kv_len=None,
+                              options=None, stream=None):
+    """Either dtype, with options (path auto or twopass)."""
+    rule = _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len)
+    return _relbias_fwd("rowsoftmax_relbias_fwd_ex", x, table, y, rule, options, stream)
+
+
+def _relbias_bwd(name, dy, y, num_buckets, dx, dtable, table_grad, workspace, rule, options,
+                 stream):
+    torch = _torch()
+    lib = load()
+    dt = _dtype_code(y)
+    a = _relbias(y, num_buckets, **rule)
+    shape = (num_buckets, y.shape[1])
+    _require("dy", dy, y.dtype, y.shape, y.device)
+    if dx is not None:
+        _require("dx", dx, y.dtype, y.shape, y.device)
+    if dtable is not None:
+        _require("dtable", dtable, torch.float32, shape, y.device)
+
+    def body(handle):
+        out = torch.empty_like(y) if dx is None else dx
+        gt = dtable
+        if gt is None and table_grad:
+            gt = torch.empty(shape, dtype=torch.float32, device=y.device)
+        if y.numel() == 0:
+            return out, gt if gt is None else gt.zero_()
+        ws, n = None, 0
+        if gt is not None:
+            size = ctypes.c_size_t()
+            _check(lib.rowsoftmax_relbias_bwd_workspace(dt, *y.shape, ctypes.byref(a),
+                                                        ctypes.byref(size)), name)
+            ws, n = _workspace(workspace, size.value, y.device)
+        _check(lib.rowsoftmax_relbias_bwd_ex(dt, dy.data_ptr(), y.data_ptr(), out.data_ptr(),
+                                             _ptr(gt), *y.shape, ctypes.byref(a), _ptr(ws), n,
+                                             _opt(options), handle or None), name)
+        return out, gt
+    return _on_stream(y.device, stream, body)
+
+
+def rowsoftmax_relbias_bwd_f32(dy, y, num_buckets, dx=None, dtable=None, *,
+                               max_distance: int = 128, bidirectional: bool = True,
+                               causal: bool = False, scale: float = 1.0, q_offset: int = 0,
+                               q_start=None, kv_len=None, table_grad: bool = True, workspace=None,
+                               stream=None):
+    """(dx, dtable) from dy and the forward pass's outputs y, float32 [batch,
+    heads, queries, keys]; the rule as for the forward pass.  dtable is float32
+    [num_buckets, heads]; table_grad=False computes it only if given.
+    workspace: at least rowsoftmax_relbias_bwd_workspace(...) bytes, else one
+    is allocated."""
+    _want(y, RMSNORM_DTYPE_F32)
+    rule = _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len)
+    return _relbias_bwd("rowsoftmax_relbias_bwd_f32", dy, y, num_buckets, dx, dtable, table_grad,
+                        workspace, rule, None, stream)
+
+
+def rowsoftmax_relbias_bwd_bf16(dy, y, num_buckets, dx=None, dtable=None, *,
+                                max_distance: int = 128, bidirectional: bool = True,
+                                causal: bool = False, scale: float = 1.0, q_offset: int = 0,
+                                q_start=None, kv_len=None, table_grad: bool = True, workspace=None,
+                                stream=None):
+    """The same for bfloat16 dy, y and dx (dtable is float32)."""
+    _want(y, RMSNORM_DTYPE_BF16)
+    rule = _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len)
+    return _relbias_bwd("rowsoftmax_relbias_bwd_bf16", dy, y, num_buckets, dx, dtable, table_grad,
+                        workspace, rule, None, stream)
+
+
+def rowsoftmax_relbias_bwd_ex(dy, y, num_buckets, dx=None, dtable=None, *,
+                              max_distance: int = 128, bidirectional: bool = True,
+                              causal: bool = False, scale: float = 1.0, q_offset: int = 0,
+                              q_start=None, kv_len=None, table_grad: bool = True, workspace=None,
+                              options=None, stream=None):
+    """Either dtype, with options (path auto or twopass)."""
+    rule = _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len)
+    return _relbias_bwd("rowsoftmax_relbias_bwd_ex", dy, y, num_buckets, dx, dtable, table_grad,
+                        workspace, rule, options, stream)
+
+
+def rowsoftmax_relbias_bwd_workspace(y, num_buckets, max_distance: int = 128,
+                                     bidirectional: bool = True) -> int:
+    """Bytes of workspace of rowsoftmax_relbias_bwd_* for scores of y's shape and type."""
+    a = _relbias(y, num_buckets, max_distance, bidirectional, False, 1.0, 0, None, None)
+    size = ctypes.c_size_t()
+    with _torch().cuda.device(y.device):
+        _check(load().rowsoftmax_relbias_bwd_workspace(_dtype_code(y), *y.shape, ctypes.byref(a),
+                                                       ctypes.byref(size)),
+               "rowsoftmax_relbias_bwd_workspace")
+    return size.value
+
+
+def rowsoftmax_relbias_bucket(relative: int, num_buckets: int, max_distance: int = 128,
+                              bidirectional: bool = True) -> int:
+    """The bucket of a relative position (key - query); -1 for an invalid rule."""
+    return load().rowsoftmax_relbias_bucket(relative, num_buckets, max_distance,
+                                            int(bool(bidirectional)))
 
 
 def rmsnorm_last_device_status(stream=None) -> int:

@@ -14,6 +14,7 @@ struct LaunchShape {
     int cluster;    // CTAs per cluster (1 = plain launch)
     int smem;       // dynamic shared memory bytes
     bool cooperative = false;   // all CTAs resident at once (grid-split kernels)
+    int grid_y = 1;
 };
 
 // Kernel instances; nullptr when the combination is not compiled.
@@ -101,11 +102,13 @@ constexpr int kStagedHeaderHost = 1024;
 // weights come through L1/L2) + nslots chunk slots (-1 if nslots is out of range).
 int64_t staged_smem_bytes(int64_t chunk_bytes, int nslots, int64_t w_bytes);
 
-// cudaLaunchKernelEx with an optional cluster shape.
-inline cudaError_t launch_ex(KernelFn kernel, const LaunchShape& s, cudaStream_t stream,
-                             const Params& p) {
+// cudaLaunchKernelEx with an optional cluster shape; P is the kernel's
+// parameter block.
+template <class P>
+inline cudaError_t launch_ex(void (*kernel)(P), const LaunchShape& s, cudaStream_t stream,
+                             const P& p) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(s.grid), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(s.grid), static_cast<unsigned>(s.grid_y), 1);
     cfg.blockDim = dim3(static_cast<unsigned>(s.block), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(s.smem);
     cfg.stream = stream;

@@ -1,0 +1,302 @@
+// relbias_api.cu -- C ABI of the row softmax with a learned relative position
+// bias (include/rowsoftmax.h): validation, the bucket rule, kernel choice and
+// launch.
+#include "rowsoftmax.h"
+#include "checks.h"
+#include "device.h"
+#include "relbias_launch.h"
+
+#include <cmath>
+#include <cstring>
+
+namespace rmsnorm {
+namespace {
+
+constexpr int64_t kMaxOffset = 1ll << 40;
+
+// Smallest distance of each bucket of one direction (half of them): one by one
+// up to half / 2 =: near, then where
+//     near + log(n / near) / log(max_distance / near) * (half - near)
+// reaches the bucket's number, for real logarithms: an edge that is a whole
+// number (near * (max_distance / near)^(k / (half - near)) often is) belongs to
+// the upper bucket.  powl is off by a few units of its last place (2^-63 or
+// finer); no edge below 4096 that is not whole lies within 1e-16 of one.
+void bucket_edges(int half, int max_distance, int32_t* edges) {
+    const int near = half / 2;
+    for (int k = 0; k < near; ++k) edges[k] = k;
+    const long double ratio = static_cast<long double>(max_distance) / near;
+    for (int k = near; k < half; ++k) {
+        const long double e =
+            near * powl(ratio, static_cast<long double>(k - near) / (half - near));
+        const long double whole = roundl(e);
+        edges[k] = static_cast<int32_t>(fabsl(e - whole) <= 1e-16L * e ? whole : ceill(e));
+    }
+}
+
+rmsnorm_status_t check_rule(int num_buckets, int max_distance, int both, int* half) {
+    if (both != 0 && both != 1) return RMSNORM_ERR_INVALID_ARG;
+    if (num_buckets < 2 || num_buckets > kBiasMaxBuckets) return RMSNORM_ERR_INVALID_ARG;
+    if (both && (num_buckets < 4 || num_buckets % 2 != 0)) return RMSNORM_ERR_INVALID_ARG;
+    *half = both ? num_buckets / 2 : num_buckets;
+    if (max_distance <= *half / 2 || max_distance > kBiasMaxDistance) return RMSNORM_ERR_INVALID_ARG;
+    return RMSNORM_OK;
+}
+
+// The edges cost some powl calls; a thread keeps those of its last rule.
+void fill_edges(BiasParams* p, int max_distance) {
+    struct Last {
+        int half = 0, max_distance = 0;
+        int32_t edges[kBiasMaxBuckets];
+    };
+    static thread_local Last last;
+    if (last.half != p->half || last.max_distance != max_distance) {
+        bucket_edges(p->half, max_distance, last.edges);
+        last.half = p->half;
+        last.max_distance = max_distance;
+    }
+    std::memcpy(p->edges, last.edges, sizeof(int32_t) * p->half);
+}
+
+struct BiasCall {
+    int sz = 0;
+    int vb = 0;
+    int64_t elems = 0;
+    int64_t window = 0;         // the last edge
+    BiasParams p;
+    DeviceView dv;
+};
+
+rmsnorm_status_t check_call(int32_t dtype, int64_t batch, int64_t heads, int64_t q_len,
+                            int64_t k_len, const rowsoftmax_relbias_t* a,
+                            const rmsnorm_options_t* opt, BiasCall* c) {
+    if (dtype != RMSNORM_DTYPE_F32 && dtype != RMSNORM_DTYPE_BF16) return RMSNORM_ERR_INVALID_ARG;
+    if (!a || a->reserved != 0 || (a->causal != 0 && a->causal != 1)) return RMSNORM_ERR_INVALID_ARG;
+    if (!std::isfinite(a->scale)) return RMSNORM_ERR_INVALID_ARG;
+    if (batch < 0 || q_len < 0 || heads <= 0 || k_len <= 0) return RMSNORM_ERR_INVALID_ARG;
+    if (heads > 65535 || k_len > kBiasMaxKeys) return RMSNORM_ERR_INVALID_ARG;
+    if (q_len > 0x7FFFFFFFll || (q_len > 0 && batch > 0x7FFFFFFFll / q_len) || batch > 0x7FFFFFFFll)
+        return RMSNORM_ERR_INVALID_ARG;
+    if (a->q_offset > kMaxOffset || a->q_offset < -kMaxOffset) return RMSNORM_ERR_INVALID_ARG;
+    if (!aligned(a->q_start, 4) || !aligned(a->kv_len, 4)) return RMSNORM_ERR_INVALID_ARG;
+    std::memset(&c->p, 0, sizeof(c->p));
+    BiasParams& p = c->p;
+    const rmsnorm_status_t st = check_rule(a->num_buckets, a->max_distance, a->bidirectional, &p.half);
+    if (st != RMSNORM_OK) return st;
+    c->sz = dtype == RMSNORM_DTYPE_F32 ? 4 : 2;
+    // batch * q_len < 2^31 and heads * k_len < 2^46: the product may pass 63 bits
+    if (batch * q_len > 0 && heads * k_len > (INT64_MAX / 8) / (batch * q_len))
+        return RMSNORM_ERR_INVALID_ARG;
+    c->elems = batch * q_len * heads * k_len;
+    if (opt) {
+        const rmsnorm_options_t& o = *opt;
+        if (o.cluster || o.threads || o.grid || o.vec_bytes || o.chunk_bytes || o.stages ||
+            o.weights || o.reserved || o.epilogue || o.fault_inject)
+            return RMSNORM_ERR_INVALID_ARG;
+        if (o.path != RMSNORM_PATH_AUTO && o.path != RMSNORM_PATH_TWOPASS)
+            return RMSNORM_ERR_INVALID_ARG;
+    }
+    p.q_start = a->q_start;
+    p.kv_len = a->kv_len;
+    p.q_offset = a->q_offset;
+    p.scale = a->scale;
+    p.head_rows = static_cast<int32_t>(batch * q_len);
+    p.q_len = static_cast<int32_t>(q_len);
+    p.k_len = static_cast<int32_t>(k_len);
+    p.heads = static_cast<int32_t>(heads);
+    p.causal = a->causal;
+    p.both = a->bidirectional;
+    p.num_buckets = a->num_buckets;
+    fill_edges(&p, a->max_distance);
+    c->window = p.edges[p.half - 1];
+    return RMSNORM_OK;
+}
+
+// CTAs per head: whole rows, about `per_sm` CTAs per SM over all heads.
+int parts_per_head(const BiasCall& c, int64_t row_blocks, int64_t per_sm) {
+    int64_t n = div_up(per_sm * c.dv.sms, c.p.heads);
+    if (n > row_blocks) n = row_blocks;
+    return static_cast<int>(n < 1 ? 1 : n);
+}
+
+constexpr int64_t kWideCtasPerSm = 8;
+
+int wide_parts(const BiasCall& c) { return parts_per_head(c, c.p.head_rows, kWideCtasPerSm); }
+
+rmsnorm_status_t launch(const BiasCall& c, BiasFn fn, const LaunchShape& s, cudaStream_t stream) {
+    if (ensure_prepared(c.dv.dev, reinterpret_cast<KernelFn>(fn), c.dv.smem_optin) != cudaSuccess)
+        return RMSNORM_ERR_CUDA;
+    return note(launch_ex(fn, s, stream, c.p)) == cudaSuccess ? RMSNORM_OK : RMSNORM_ERR_CUDA;
+}
+
+void count_vectors(BiasCall* c, uintptr_t bits) {
+    c->vb = widest_vector(bits, static_cast<int64_t>(c->p.k_len) * c->sz, c->sz);
+    c->p.nvec = c->p.k_len / (c->vb / c->sz);
+}
+
+int window_bytes(const BiasCall& c) {
+    const int lo = static_cast<int>(c.window);
+    return 4 * bias_window_slots(lo, c.p.both ? lo : 0, c.vb / c.sz);
+}
+
+rmsnorm_status_t fwd_run(int32_t dtype, const void* x, const void* table, void* y, int64_t batch,
+                         int64_t heads, int64_t q_len, int64_t k_len,
+                         const rowsoftmax_relbias_t* a, const rmsnorm_options_t* opt,
+                         cudaStream_t stream) {
+    BiasCall c;
+    const rmsnorm_status_t st = check_call(dtype, batch, heads, q_len, k_len, a, opt, &c);
+    if (st != RMSNORM_OK) return st;
+    if (!x || !table || !y) return RMSNORM_ERR_INVALID_ARG;
+    const uintptr_t sz = static_cast<uintptr_t>(c.sz);
+    if (!aligned(x, sz) || !aligned(table, sz) || !aligned(y, sz)) return RMSNORM_ERR_INVALID_ARG;
+    const uint64_t n = static_cast<uint64_t>(c.elems) * sz;
+    const uint64_t nb = static_cast<uint64_t>(batch) * 4;
+    const Span in[] = {span(x, n), span(table, static_cast<uint64_t>(a->num_buckets) * heads * sz),
+                       span(a->q_start, nb), span(a->kv_len, nb)};
+    if (clashes(span(y, n), in, 4, 1)) return RMSNORM_ERR_INVALID_ARG;
+    if (c.elems == 0) return RMSNORM_OK;
+    if (current_device(&c.dv) != cudaSuccess) return RMSNORM_ERR_CUDA;
+    c.p.x = x;
+    c.p.table = table;
+    c.p.out = y;
+    count_vectors(&c, reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y));
+    c.p.parts = wide_parts(c);
+    const LaunchShape s{c.p.parts * c.p.heads, relbias_wide_block(), 1, window_bytes(c)};
+    return launch(c, relbias_fwd_wide_ptr(dtype, c.vb), s, stream);
+}
+
+// The parts never exceed wide_parts for any vector width or alignment.
+uint64_t space_needed(const BiasCall& c) {
+    return static_cast<uint64_t>(wide_parts(c)) * c.p.heads * c.p.num_buckets * 8;
+}
+
+rmsnorm_status_t bwd_run(int32_t dtype, const void* dy, const void* y, void* dx, float* dtable,
+                         int64_t batch, int64_t heads, int64_t q_len, int64_t k_len,
+                         const rowsoftmax_relbias_t* a, void* workspace, size_t workspace_bytes,
+                         const rmsnorm_options_t* opt, cudaStream_t stream) {
+    BiasCall c;
+    rmsnorm_status_t st = check_call(dtype, batch, heads, q_len, k_len, a, opt, &c);
+    if (st != RMSNORM_OK) return st;
+    if (!dy || !y || !dx) return RMSNORM_ERR_INVALID_ARG;
+    const uintptr_t sz = static_cast<uintptr_t>(c.sz);
+    if (!aligned(dy, sz) || !aligned(y, sz) || !aligned(dx, sz) || !aligned(dtable, 4) ||
+        !aligned(workspace, 16))
+        return RMSNORM_ERR_INVALID_ARG;
+    const uint64_t n = static_cast<uint64_t>(c.elems) * sz;
+    const uint64_t nb = static_cast<uint64_t>(batch) * 4;
+    const uint64_t nt = static_cast<uint64_t>(a->num_buckets) * heads * 4;
+    const Span s[] = {span(dy, n), span(y, n), span(a->q_start, nb), span(a->kv_len, nb),
+                      span(dx, n), span(dtable, nt)};
+    if (clashes(s[4], s, 4, 2) || clashes(s[5], s, 5, 0) ||
+        clashes(span(workspace, workspace_bytes), s, 6, 0))
+        return RMSNORM_ERR_INVALID_ARG;
+    if (c.elems == 0) {          // sums over no rows
+        if (dtable && note(cudaMemsetAsync(dtable, 0, nt, stream)) != cudaSuccess)
+            return RMSNORM_ERR_CUDA;
+        return RMSNORM_OK;
+    }
+    if (dtable && !workspace) return RMSNORM_ERR_INVALID_ARG;
+    if (current_device(&c.dv) != cudaSuccess) return RMSNORM_ERR_CUDA;
+    if (dtable && workspace_bytes < space_needed(c)) return RMSNORM_ERR_INVALID_ARG;
+    c.p.x = dy;
+    c.p.y = y;
+    c.p.out = dx;
+    c.p.part = dtable ? static_cast<double*>(workspace) : nullptr;
+    c.p.dtable = dtable;
+    count_vectors(&c, s[0].p | s[1].p | s[4].p);
+    c.p.parts = wide_parts(c);
+    const LaunchShape ls{c.p.parts * c.p.heads, relbias_wide_block(), 1, window_bytes(c)};
+    st = launch(c, relbias_bwd_wide_ptr(dtype, c.vb), ls, stream);
+    if (st != RMSNORM_OK || !dtable) return st;
+    const LaunchShape rs{c.p.heads, relbias_reduce_block(), 1, 0};
+    return launch(c, relbias_reduce_ptr(), rs, stream);
+}
+
+}  // namespace
+}  // namespace rmsnorm
+
+using namespace rmsnorm;
+
+extern "C" {
+
+rmsnorm_status_t rowsoftmax_relbias_fwd_f32(const float* x, const float* table, float* y,
+                                            int64_t batch, int64_t heads, int64_t q_len,
+                                            int64_t k_len, const rowsoftmax_relbias_t* bias,
+                                            rmsnorm_stream_t stream) {
+    return fwd_run(RMSNORM_DTYPE_F32, x, table, y, batch, heads, q_len, k_len, bias, nullptr,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+rmsnorm_status_t rowsoftmax_relbias_fwd_bf16(const uint16_t* x, const uint16_t* table, uint16_t* y,
+                                             int64_t batch, int64_t heads, int64_t q_len,
+                                             int64_t k_len, const rowsoftmax_relbias_t* bias,
+                                             rmsnorm_stream_t stream) {
+    return fwd_run(RMSNORM_DTYPE_BF16, x, table, y, batch, heads, q_len, k_len, bias, nullptr,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+rmsnorm_status_t rowsoftmax_relbias_fwd_ex(int32_t dtype, const void* x, const void* table,
+                                           void* y, int64_t batch, int64_t heads, int64_t q_len,
+                                           int64_t k_len, const rowsoftmax_relbias_t* bias,
+                                           const rmsnorm_options_t* opt,
+                                           rmsnorm_stream_t stream) {
+    return fwd_run(dtype, x, table, y, batch, heads, q_len, k_len, bias, opt,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+rmsnorm_status_t rowsoftmax_relbias_bwd_workspace(int32_t dtype, int64_t batch, int64_t heads,
+                                                  int64_t q_len, int64_t k_len,
+                                                  const rowsoftmax_relbias_t* bias,
+                                                  size_t* bytes) {
+    BiasCall c;
+    if (!bytes) return RMSNORM_ERR_INVALID_ARG;
+    const rmsnorm_status_t st = check_call(dtype, batch, heads, q_len, k_len, bias, nullptr, &c);
+    if (st != RMSNORM_OK) return st;
+    *bytes = 0;
+    if (c.elems == 0) return RMSNORM_OK;
+    if (current_device(&c.dv) != cudaSuccess) return RMSNORM_ERR_CUDA;
+    *bytes = space_needed(c);
+    return RMSNORM_OK;
+}
+
+rmsnorm_status_t rowsoftmax_relbias_bwd_f32(const float* dy, const float* y, float* dx,
+                                            float* dtable, int64_t batch, int64_t heads,
+                                            int64_t q_len, int64_t k_len,
+                                            const rowsoftmax_relbias_t* bias, void* workspace,
+                                            size_t workspace_bytes, rmsnorm_stream_t stream) {
+    return bwd_run(RMSNORM_DTYPE_F32, dy, y, dx, dtable, batch, heads, q_len, k_len, bias,
+                   workspace, workspace_bytes, nullptr, reinterpret_cast<cudaStream_t>(stream));
+}
+
+rmsnorm_status_t rowsoftmax_relbias_bwd_bf16(const uint16_t* dy, const uint16_t* y, uint16_t* dx,
+                                             float* dtable, int64_t batch, int64_t heads,
+                                             int64_t q_len, int64_t k_len,
+                                             const rowsoftmax_relbias_t* bias, void* workspace,
+                                             size_t workspace_bytes, rmsnorm_stream_t stream) {
+    return bwd_run(RMSNORM_DTYPE_BF16, dy, y, dx, dtable, batch, heads, q_len, k_len, bias,
+                   workspace, workspace_bytes, nullptr, reinterpret_cast<cudaStream_t>(stream));
+}
+
+rmsnorm_status_t rowsoftmax_relbias_bwd_ex(int32_t dtype, const void* dy, const void* y, void* dx,
+                                           float* dtable, int64_t batch, int64_t heads,
+                                           int64_t q_len, int64_t k_len,
+                                           const rowsoftmax_relbias_t* bias, void* workspace,
+                                           size_t workspace_bytes, const rmsnorm_options_t* opt,
+                                           rmsnorm_stream_t stream) {
+    return bwd_run(dtype, dy, y, dx, dtable, batch, heads, q_len, k_len, bias, workspace,
+                   workspace_bytes, opt, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int32_t rowsoftmax_relbias_bucket(int64_t relative, int32_t num_buckets, int32_t max_distance,
+                                  int32_t bidirectional) {
+    int half;
+    if (check_rule(num_buckets, max_distance, bidirectional, &half) != RMSNORM_OK) return -1;
+    int32_t edges[kBiasMaxBuckets];
+    bucket_edges(half, max_distance, edges);
+    int64_t n = relative < 0 ? (relative == INT64_MIN ? INT64_MAX : -relative)
+                             : (bidirectional ? relative : 0);
+    int32_t k = half - 1;
+    while (edges[k] > n) --k;
+    return k + (bidirectional && relative > 0 ? half : 0);
+}
+
+}  // extern "C"
