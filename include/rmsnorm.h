@@ -264,10 +264,15 @@ rmsnorm_status_t rmsnorm_bwd_bf16(const uint16_t* dy, const uint16_t* x, const u
                                   void* workspace, size_t workspace_bytes,
                                   rmsnorm_stream_t stream);
 
-/* Either dtype, with options (`opt` may be NULL): opt->path RMSNORM_PATH_AUTO
- * or RMSNORM_PATH_TWOPASS (a pair of sums per row, then dx and partial column
- * sums, each reading x and dy once: any width and alignment).  Every other
- * field must be zero, else RMSNORM_ERR_INVALID_ARG. */
+/* Either dtype, with options (`opt` may be NULL): opt->path RMSNORM_PATH_AUTO,
+ * RMSNORM_PATH_STAGED (rows staged in shared memory by bulk copies, x and dy
+ * read from HBM once: both on a 16-byte boundary, rows of up to 512 threads of
+ * 16 elements, else RMSNORM_ERR_UNSUPPORTED) or RMSNORM_PATH_TWOPASS (a pair of
+ * sums per row, then dx and partial column sums, each reading x and dy once:
+ * any width and alignment); opt->wait_timeout_ns; and in the test build of the
+ * library opt->fault_inject = 1 with RMSNORM_PATH_STAGED (each CTA's first copy
+ * is withheld; elsewhere RMSNORM_ERR_UNSUPPORTED).  Every other field must be
+ * zero, else RMSNORM_ERR_INVALID_ARG. */
 rmsnorm_status_t rmsnorm_bwd_ex(int32_t dtype, const void* dy, const void* x, const void* w,
                                 void* dx, float* dw, int64_t rows, int64_t hidden, float eps,
                                 void* workspace, size_t workspace_bytes,

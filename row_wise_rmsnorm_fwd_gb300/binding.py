@@ -539,7 +539,7 @@ def layernorm_fwd_bf16(x, w=None, b=None, y=None, mean=None, rstd=None, eps: flo
 
 def layernorm_fwd_ex(x, w=None, b=None, y=None, mean=None, rstd=None, eps: float = 1e-5,
                      stats: bool = False, options=None, stream=None):
-    """Either dtype, with options (path auto or twopass)."""
+    """Either dtype, with options (path auto, staged or twopass)."""
     return _layernorm_fwd("layernorm_fwd_ex", x, w, b, y, mean, rstd, eps, stats, options, stream)
 
 
@@ -616,7 +616,7 @@ def layernorm_bwd_bf16(dy, x, w, mean, rstd, dx=None, dw=None, db=None, weight_g
 
 def layernorm_bwd_ex(dy, x, w, mean, rstd, dx=None, dw=None, db=None, weight_grads: bool = True,
                      workspace=None, options=None, stream=None):
-    """Either dtype, with options (path auto or twopass)."""
+    """Either dtype, with options (path auto, staged or twopass)."""
     return _norm_bwd("layernorm_bwd_ex", True, dy, x, w, mean, rstd, dx, dw, db, 0.0,
                      weight_grads, workspace, options, stream)
 
@@ -641,7 +641,7 @@ def rmsnorm_bwd_bf16(dy, x, w, dx=None, dw=None, eps: float = 1e-6, weight_grads
 
 def rmsnorm_bwd_ex(dy, x, w, dx=None, dw=None, eps: float = 1e-6, weight_grads: bool = True,
                    workspace=None, options=None, stream=None):
-    """Either dtype, with options (path auto or twopass)."""
+    """Either dtype, with options (path auto, staged or twopass)."""
     return _norm_bwd("rmsnorm_bwd_ex", False, dy, x, w, None, None, dx, dw, None, eps,
                      weight_grads, workspace, options, stream)
 

@@ -12,7 +12,9 @@
 // bitwise repeatable.
 #pragma once
 #include "common.cuh"
+#include "k_blockring.cuh"
 #include "norm_launch.h"
+#include "pairs.cuh"
 
 namespace rmsnorm {
 
@@ -135,8 +137,239 @@ __global__ void __launch_bounds__(kBwdColsThreads) norm_bwd_cols_kernel(const No
     }
 }
 
-// dw and db from the parts: a CTA takes 32 columns, its 16 rows of threads
-// every 16th part each, then their sums in order.  grid.y: 0 = dw, 1 = db.
+// ------------------------------------------------- rows staged: one pass --
+// x and dy are read from HBM once: blocks of R * p.rows_per_cta rows come into
+// shared memory by bulk copies (k_blockring.cuh); G threads work on R rows at a
+// time, NV vectors per thread and row.  Each iteration forms the rows' two
+// sums, has one block barrier, and then reads the slot again for dx.  The
+// column sums stay in registers (a thread has the same columns of every row it
+// sees) until the CTA's rows are done; its row groups are then added through
+// shared memory and written as one part.
+//
+// At 6 bytes an element (bf16) the issue slots are as scarce as the bandwidth,
+// so the arithmetic is on packed pairs and arranged for few operations: with
+// u = x - mean (RMSNorm: x), the first pass needs d * u once for both
+// m(g * xh) and dw, and dx = (d * w) * rstd + k1 + u * k2 with two constants
+// of the row.  R = 2 gives each thread two independent rows between barriers.
+// FULL: every thread has NV whole vectors and there are weights; else vectors
+// past the row's end are read as zeros (they add nothing anywhere) and not
+// stored.
+template <typename T, int VB, int NV, bool LAYER, int R, bool FULL>
+__global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_staged_kernel(const NormParams p) {
+    constexpr int EPV = VecTraits<T, VB>::kElems;
+    constexpr int PN = PairTraits<T, VB>::N;
+    constexpr int W = PairTraits<T, VB>::W;
+    using L = Lanes<W>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ alignas(8) uint64_t bars[kBlockRingMaxSlots];
+    __shared__ float2 red[2][R][32];
+    pdl_trigger();
+    const int G = p.group;
+    const int width = G < 32 ? G : 32;
+    const int tid = threadIdx.x;
+    const int g = tid / G;
+    const int t = tid - g * G;
+    const int warp = tid >> 5, lane = tid & 31;
+    const int wpg = G >> 5;
+    const int gw0 = g * wpg;
+    const int rpc = p.rows_per_cta;          // row groups of the CTA
+    const int row_bytes = p.hidden * static_cast<int>(sizeof(T));
+
+    BlockRing ring;
+    ring.nslots = p.nslots;
+    ring.slot_bytes = p.slot_bytes;
+    ring.block_bytes = static_cast<int64_t>(R * rpc) * row_bytes;
+    ring.total_bytes = p.rows * row_bytes;
+    ring.init(p.x, p.dy, smem, bars, (p.rows + R * rpc - 1) / (R * rpc));
+    int merge_width = 1;
+    while (merge_width < wpg) merge_width <<= 1;
+    bool valid[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) valid[i] = FULL || i * G + t < p.nvec;
+    __syncthreads();
+    pdl_wait();
+    if (tid == 0) ring.prologue(p.fault);
+
+    const char* wb = static_cast<const char*>(p.w) + t * VB;
+    L aw[NV * PN], ab[LAYER ? NV * PN : 1];
+#pragma unroll
+    for (int k = 0; k < NV * PN; ++k) aw[k] = L::all(0.f);
+#pragma unroll
+    for (int k = 0; k < (LAYER ? NV * PN : 1); ++k) ab[k] = L::all(0.f);
+    // row r of the group's R rows of this block: row + r * rpc
+    int64_t row = static_cast<int64_t>(blockIdx.x) * (R * rpc) + g;
+    const int64_t row_step = static_cast<int64_t>(gridDim.x) * (R * rpc);
+    float mean[R], rstd[R];
+    auto stats = [&](int64_t from, float (&m)[R], float (&q)[R]) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = q[r] = 0.f;
+            if (LAYER && from + r * rpc < p.rows) {
+                m[r] = p.mean[from + r * rpc];
+                q[r] = p.rstd[from + r * rpc];
+            }
+        }
+    };
+    stats(row, mean, rstd);
+    auto weights = [&](int i) {
+        if constexpr (FULL) {
+            return ld_ro<VB>(wb + i * G * VB);
+        } else {
+            return p.w && valid[i] ? ld_ro<VB>(wb + i * G * VB) : ones_vec<T, VB>();
+        }
+    };
+    RingStep step;
+    int n = 0;
+    for (; n < ring.count; ++n, row += row_step) {
+        // the next rows' statistics, under way while this block is awaited
+        float next_mean[R], next_rstd[R];
+        stats(row + row_step, next_mean, next_rstd);
+        const bool ok = ring.wait(step, p.timeout_ns);
+        if (n >= ring.tail_from) ring.finish<T>(step.slot, n);
+        const uint32_t in_slot = static_cast<uint32_t>(ring.start(n) & 15) +
+                                 static_cast<uint32_t>(g * row_bytes + t * VB);
+        const uint32_t xs = ring.base(step.slot, 0) + in_slot;
+        const uint32_t ds = ring.base(step.slot, 1) + in_slot;
+        const uint32_t next_row = static_cast<uint32_t>(rpc * row_bytes);
+
+        float a[R], b[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool here = row + r * rpc < p.rows;
+            const L minus = L::all(-mean[r]), q = L::all(rstd[r]);
+            L sa = L::all(0.f), sb = L::all(0.f);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const bool on = here && valid[i];
+                const Vec<VB> x = ld_slot_if<VB>(xs + r * next_row + i * G * VB, on);
+                const Vec<VB> d = ld_slot_if<VB>(ds + r * next_row + i * G * VB, on);
+                const Vec<VB> w = weights(i);
+#pragma unroll
+                for (int k = 0; k < PN; ++k) {
+                    const L dk = lanes<T, VB>(d, k), wk = lanes<T, VB>(w, k);
+                    L u;
+                    if constexpr (LAYER) u = lanes_plus<T, VB>(x, k, minus);
+                    else u = lanes<T, VB>(x, k);
+                    const L du = dk * u;
+                    if constexpr (LAYER) {
+                        sa = fma(dk, wk, sa);
+                        aw[i * PN + k] = fma(du, q, aw[i * PN + k]);
+                        ab[i * PN + k] = ab[i * PN + k] + dk;
+                    } else {
+                        sa = fma(u, u, sa);
+                    }
+                    sb = fma(du, wk, sb);
+                }
+            }
+            a[r] = sa.total();
+            b[r] = sb.total();
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            a[r] = share_sum(a[r], width);
+            b[r] = share_sum(b[r], width);
+        }
+        if (wpg > 1 && lane == 0) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) red[n & 1][r][warp] = make_float2(a[r], b[r]);
+        }
+        if (__syncthreads_or(!ok)) break;            // uniform; also frees the previous slot
+        if (tid == 0) ring.refill(step, n, p.fault);
+        if (wpg > 1) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float2 e = make_float2(0.f, 0.f);
+                if (lane < wpg) e = red[n & 1][r][gw0 + lane];
+                a[r] = group_allreduce_sum(e.x, merge_width);
+                b[r] = group_allreduce_sum(e.y, merge_width);
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                a[r] = __shfl_sync(0xffffffffu, a[r], 0);
+                b[r] = __shfl_sync(0xffffffffu, b[r], 0);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool here = row + r * rpc < p.rows;
+            float k1 = 0.f;
+            if constexpr (LAYER) {
+                k1 = -a[r] * p.inv_hidden * rstd[r];
+            } else {
+                rstd[r] = rsqrtf(fmaf(a[r], p.inv_hidden, p.eps));
+            }
+            // u * k2 = -rstd * xh * m(g * xh), m(g * xh) = rstd * b / H
+            const float k2 = -(b[r] * p.inv_hidden * rstd[r]) * rstd[r] * rstd[r];
+            const L minus = L::all(-mean[r]), q = L::all(rstd[r]);
+            const L c1 = L::all(k1), c2 = L::all(k2);
+            char* dst = static_cast<char*>(p.out) + (row + r * rpc) * row_bytes + t * VB;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const bool on = here && valid[i];
+                const Vec<VB> x = ld_slot_if<VB>(xs + r * next_row + i * G * VB, on);
+                const Vec<VB> d = ld_slot_if<VB>(ds + r * next_row + i * G * VB, on);
+                const Vec<VB> w = weights(i);
+                float o[EPV];
+#pragma unroll
+                for (int k = 0; k < PN; ++k) {
+                    const L dk = lanes<T, VB>(d, k), wk = lanes<T, VB>(w, k);
+                    L u, in;
+                    if constexpr (LAYER) {
+                        u = lanes_plus<T, VB>(x, k, minus);
+                        in = fma(dk * wk, q, c1);
+                    } else {
+                        u = lanes<T, VB>(x, k);
+                        in = dk * wk * q;
+                        aw[i * PN + k] = fma(dk * u, q, aw[i * PN + k]);
+                    }
+                    fma(u, c2, in).put(o + k * W);
+                }
+                if (on) st_stream<VB>(dst + i * G * VB, pack<T, VB>(o));
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mean[r] = next_mean[r];
+            rstd[r] = next_rstd[r];
+        }
+        step.next(ring.nslots);
+    }
+    if (n < ring.count) {
+        // a wait ran out: report it, and let the copies that are under way land
+        if (tid == 0) {
+            report_timeout(p.status, kSiteStagedFull);
+            ring.drain(step, n, p.timeout_ns);
+        }
+        __syncthreads();
+        return;
+    }
+    // the CTA's part: its row groups' sums, in order
+    auto write_part = [&](const L* acc, float* part) {
+        float* sums = reinterpret_cast<float*>(smem);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (valid[i]) {
+#pragma unroll
+                for (int k = 0; k < PN; ++k)
+                    acc[i * PN + k].put(sums + g * p.hidden + (i * G + t) * EPV + k * W);
+            }
+        }
+        __syncthreads();
+        float* out = part + static_cast<int64_t>(blockIdx.x) * p.hidden;
+        for (int c = tid; c < p.hidden; c += blockDim.x) {
+            float v = 0.f;
+            for (int k = 0; k < rpc; ++k) v += sums[k * p.hidden + c];
+            out[c] = v;
+        }
+    };
+    if (p.part_w) write_part(aw, p.part_w);
+    if (LAYER && p.part_b) write_part(ab, p.part_b);
+}
+
+// dw and db from the parts: a CTA takes 8 columns (a
+// sector of a part), its 32 rows of threads every 32nd part each, ten loads in
+// flight, then their sums in order.  grid.y: 0 = dw, 1 = db.
 static __global__ void __launch_bounds__(kNormReduceCols * kNormReduceLanes)
 norm_bwd_reduce_kernel(const NormParams p) {
     __shared__ float red[kNormReduceLanes][kNormReduceCols + 1];
@@ -147,11 +380,17 @@ norm_bwd_reduce_kernel(const NormParams p) {
     const float* part = blockIdx.y ? p.part_b : p.part_w;
     float* out = blockIdx.y ? p.db : p.dw;
     if (!part) return;
+    // loads past the last part repeat it and are not added
+    constexpr int U = 10;
+    const float* from = part + (col < p.hidden ? col : 0);
     float s = 0.f;
-    if (col < p.hidden) {
-#pragma unroll 4
-        for (int k = l; k < p.parts; k += kNormReduceLanes)
-            s += part[static_cast<int64_t>(k) * p.hidden + col];
+    for (int k = l; k < p.parts; k += U * kNormReduceLanes) {
+        float v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            v[u] = from[static_cast<int64_t>(min(k + u * kNormReduceLanes, p.parts - 1)) * p.hidden];
+#pragma unroll
+        for (int u = 0; u < U; ++u) s += k + u * kNormReduceLanes < p.parts ? v[u] : 0.f;
     }
     red[l][c] = s;
     __syncthreads();

@@ -39,18 +39,28 @@ rmsnorm_status_t check_shape(int32_t dtype, int64_t rows, int64_t hidden, NormCa
     return RMSNORM_OK;
 }
 
-// Options these operators take: a path, and nothing else.
+// Options these operators take: a path, the limit of its waits and, in the
+// test build of the library, the staged path's fault.
 rmsnorm_status_t check_options(const rmsnorm_options_t* opt, NormCall* c) {
     if (!opt) return RMSNORM_OK;
     const rmsnorm_options_t& o = *opt;
     if (o.cluster || o.threads || o.grid || o.vec_bytes || o.chunk_bytes || o.stages || o.weights ||
-        o.reserved || o.epilogue)
+        o.reserved || o.epilogue || o.fault_inject < 0 || o.fault_inject > 2)
         return RMSNORM_ERR_INVALID_ARG;
-    if (o.fault_inject) return o.fault_inject < 0 || o.fault_inject > 2 ? RMSNORM_ERR_INVALID_ARG
-                                                                        : RMSNORM_ERR_UNSUPPORTED;
-    if (o.path != RMSNORM_PATH_AUTO && o.path != RMSNORM_PATH_TWOPASS) return RMSNORM_ERR_INVALID_ARG;
+    if (o.path != RMSNORM_PATH_AUTO && o.path != RMSNORM_PATH_STAGED &&
+        o.path != RMSNORM_PATH_TWOPASS)
+        return RMSNORM_ERR_INVALID_ARG;
+    if (o.fault_inject &&
+        (!RMSNORM_FAULT_INJECT || o.fault_inject != 1 || o.path != RMSNORM_PATH_STAGED))
+        return RMSNORM_ERR_UNSUPPORTED;
     c->opt = o;
     return RMSNORM_OK;
+}
+
+void set_waits(NormCall* c) {
+    c->p.status = c->dv.status;
+    c->p.fault = c->opt.fault_inject;
+    c->p.timeout_ns = c->opt.wait_timeout_ns ? c->opt.wait_timeout_ns : kDefaultTimeoutNs;
 }
 
 void count_vectors(NormCall* c, uintptr_t bits) {
@@ -62,9 +72,62 @@ rmsnorm_status_t launch(const NormCall& c, NormFn fn, const LaunchShape& s, cuda
     return note(launch_ex(fn, s, stream, c.p)) == cudaSuccess ? RMSNORM_OK : RMSNORM_ERR_CUDA;
 }
 
+int pow2_ceil(int64_t v) {
+    int p = 1;
+    while (p < v) p <<= 1;
+    return p;
+}
+
 int clamp_grid(int64_t want, int64_t most) { return static_cast<int>(want < most ? want : most); }
 
 // ------------------------------------------------------ layer norm forward --
+
+// Rows staged in shared memory: 64 bytes of a row per thread (16 vectors of 2
+// bytes: 32), CTAs of 256 threads or one row, a ring of two blocks, one wave of
+// resident CTAs.  Measured (% of the HBM copy peak), 65536 rows of 4096 fp32 /
+// 4096 bf16 / 1024 bf16: 32 bytes a thread 73 / 52 / 50, 64 bytes 98 / 92 / 86,
+// 128 bytes 94 / 77 / 71 (fewer, longer threads); rings of three blocks 94 /
+// 87 / 81 (fewer CTAs); CTAs of about four blocks each instead of one wave 92 /
+// 85 / 81 (each CTA starts with an empty ring).  Leaves *fn null, status OK,
+// where rows do not fit two slots or x is not on a 16-byte boundary.
+constexpr int64_t kStagedRowBytesPerThread = 64;
+constexpr int64_t kStagedMaxVecsPerThread = 16;
+constexpr int64_t kStagedBlock = 256;
+constexpr int64_t kStagedSlots = 2;
+
+int group_of(int64_t nvec, int64_t vecs_per_thread) {
+    const int64_t g = div_up(nvec, vecs_per_thread);
+    if (g > 1024) return 1024;
+    return g <= 32 ? pow2_ceil(g) : static_cast<int>(div_up(g, 32) * 32);
+}
+
+rmsnorm_status_t plan_staged(int32_t dtype, NormCall* c, LaunchShape* s, NormFn* fn) {
+    const int64_t row_bytes = static_cast<int64_t>(c->p.hidden) * c->sz;
+    if (!aligned(c->p.x, 16)) return RMSNORM_OK;
+    int64_t vecs = kStagedRowBytesPerThread / c->vb;
+    if (vecs > kStagedMaxVecsPerThread) vecs = kStagedMaxVecsPerThread;
+    const int group = group_of(c->p.nvec, vecs);
+    const int64_t rpc = group < kStagedBlock ? kStagedBlock / group : 1;
+    const int block = static_cast<int>(rpc * group);
+    const int64_t slot = div_up(rpc * row_bytes + 32, 128) * 128;     // 16-byte rounding at both ends
+    if (kStagedSlots * slot > c->dv.smem_optin - 2048) return RMSNORM_OK;
+    const int smem = static_cast<int>(kStagedSlots * slot);
+    const NormFn f = layernorm_staged_ptr(dtype, c->vb);
+    int occ = 0;
+    if (cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(f), block, smem, 1,
+                         &occ) != cudaSuccess)
+        return RMSNORM_ERR_CUDA;
+    if (occ < 1) return RMSNORM_OK;
+    *s = LaunchShape{clamp_grid(div_up(c->p.rows, rpc), static_cast<int64_t>(c->dv.sms) * occ), block,
+                     1, smem};
+    *fn = f;
+    c->p.group = group;
+    c->p.rows_per_cta = static_cast<int32_t>(rpc);
+    c->p.nslots = static_cast<int32_t>(kStagedSlots);
+    c->p.slot_bytes = static_cast<int32_t>(slot);
+    set_waits(c);
+    return RMSNORM_OK;
+}
 
 rmsnorm_status_t layernorm_run(int32_t dtype, const void* x, const void* w, const void* b, void* y,
                                float* mean, float* rstd, int64_t rows, int64_t hidden, float eps,
@@ -94,8 +157,18 @@ rmsnorm_status_t layernorm_run(int32_t dtype, const void* x, const void* w, cons
     c.p.rstd = rstd;
     c.p.eps = eps;
     count_vectors(&c, in[0].p | in[1].p | in[2].p | in[3].p);
-    const LaunchShape s{clamp_grid(rows, 8ll * c.dv.sms), layernorm_twopass_block(), 1, 0};
-    return launch(c, layernorm_twopass_ptr(dtype, c.vb), s, stream);
+    LaunchShape s{0, 0, 1, 0};
+    NormFn fn = nullptr;
+    if (c.opt.path != RMSNORM_PATH_TWOPASS) {
+        st = plan_staged(dtype, &c, &s, &fn);
+        if (st == RMSNORM_ERR_CUDA) return st;
+    }
+    if (!fn) {
+        if (c.opt.path == RMSNORM_PATH_STAGED) return RMSNORM_ERR_UNSUPPORTED;
+        s = LaunchShape{clamp_grid(rows, 8ll * c.dv.sms), layernorm_twopass_block(), 1, 0};
+        fn = layernorm_twopass_ptr(dtype, c.vb);
+    }
+    return launch(c, fn, s, stream);
 }
 
 // --------------------------------------------------------- backward passes --
@@ -114,6 +187,70 @@ int64_t bwd_parts(const DeviceView& dv, int64_t rows, int64_t hidden, int sz) {
     return parts < 1 ? 1 : parts;
 }
 
+// Rows staged in shared memory, read once: 16 elements of a row per thread,
+// CTAs of 256 threads or one row, a ring of three blocks, one wave of resident
+// CTAs.  Two rows between barriers where the rows are enough to give every CTA
+// several such blocks, except for RMSNorm in bf16, whose kernel needs few
+// registers with one row (62: four CTAs per SM) and many with two (74: three).
+// Measured (% of the HBM copy peak, one row / two rows between barriers):
+// layer norm bf16 rows of 8192 88 / 90, of 4096 87 / 87, fp32 rows of 4096 94 /
+// 97; RMSNorm bf16 rows of 4096 96 / 85.  Rings of two blocks 62-66 (layer
+// norm bf16), of four 88 or, where they cost a CTA per SM, 65.  8 elements per
+// thread instead of 16: bf16 rows of 4096 68, fp32 99.
+constexpr int64_t kBwdBlock = 256;
+constexpr int64_t kBwdSlots = 3;
+constexpr int64_t kBwdTwoRowBlocks = 2;     // blocks per CTA from which two rows pay
+
+// Most CTAs of the one-pass kernel, and so its most parts: four per SM, fewer
+// for rows that take a large share of an SM's threads.
+int64_t bwd_staged_ctas(const DeviceView& dv, int64_t hidden) {
+    const int64_t per_sm = 16384 / hidden;
+    return dv.sms * (per_sm < 1 ? 1 : (per_sm > 4 ? 4 : per_sm));
+}
+
+rmsnorm_status_t plan_bwd_staged(int32_t dtype, NormCall* c, LaunchShape* s, NormFn* fn) {
+    const int64_t row_bytes = static_cast<int64_t>(c->p.hidden) * c->sz;
+    if (!aligned(c->p.x, 16) || !aligned(c->p.dy, 16)) return RMSNORM_OK;
+    const int64_t vecs = kNormBwdElems / (c->vb / c->sz);
+    const int group = group_of(c->p.nvec, vecs);
+    if (c->p.nvec > kNormBwdMaxThreads * vecs) return RMSNORM_OK;
+    const int64_t rpc = group < kBwdBlock ? kBwdBlock / group : 1;
+    const int block = static_cast<int>(rpc * group);
+    const bool full = c->p.w && c->p.nvec == group * vecs;
+    const bool bf16 = dtype == RMSNORM_DTYPE_BF16;
+    const int64_t budget = c->dv.smem_optin - 2048;
+    const int64_t ctas_most = bwd_staged_ctas(c->dv, c->p.hidden);
+    // one array's share of a slot: its rows, rounded to 16 bytes at both ends
+    auto slot_of = [&](int rows) { return div_up(rows * rpc * row_bytes + 32, 128) * 128; };
+    int rows = 1;
+    if (full && (c->layer || !bf16) && 4 * slot_of(2) <= budget &&
+        c->p.rows >= 2 * rpc * kBwdTwoRowBlocks * ctas_most)
+        rows = 2;
+    const int64_t slot = slot_of(rows);
+    int64_t slots = kBwdSlots;
+    while (slots > 2 && 2 * slots * slot > budget) --slots;
+    if (2 * slots * slot > budget) return RMSNORM_OK;
+    const int smem = static_cast<int>(2 * slots * slot);
+    const NormFn f = bf16 ? norm_bwd_staged_ptr_bf16(c->vb, c->layer, rows, full)
+                          : norm_bwd_staged_ptr_f32(c->vb, c->layer, rows, full);
+    int occ = 0;
+    if (cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(f), block, smem, 1,
+                         &occ) != cudaSuccess)
+        return RMSNORM_ERR_CUDA;
+    if (occ < 1) return RMSNORM_OK;
+    int64_t ctas = static_cast<int64_t>(c->dv.sms) * occ;
+    if (ctas > ctas_most) ctas = ctas_most;
+    *s = LaunchShape{clamp_grid(div_up(c->p.rows, rows * rpc), ctas), block, 1, smem};
+    *fn = f;
+    c->p.group = group;
+    c->p.rows_per_cta = static_cast<int32_t>(rpc);
+    c->p.nslots = static_cast<int32_t>(slots);
+    c->p.slot_bytes = static_cast<int32_t>(slot);
+    c->p.parts = s->grid;
+    set_waits(c);
+    return RMSNORM_OK;
+}
+
 struct BwdSpace {
     int64_t parts;
     uint64_t row_stats, part_w, part_b, bytes;    // offsets, and the size
@@ -123,11 +260,21 @@ BwdSpace bwd_space(const DeviceView& dv, int64_t rows, int64_t hidden, int sz, b
     BwdSpace s;
     auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
     s.parts = bwd_parts(dv, rows, hidden, sz);
+    int64_t staged = bwd_staged_ctas(dv, hidden);
+    if (staged > rows) staged = rows;
+    if (s.parts < staged) s.parts = staged;
     s.row_stats = 0;
     s.part_w = up(static_cast<uint64_t>(rows) * 8);
     s.part_b = s.part_w + up(static_cast<uint64_t>(s.parts) * hidden * 4);
     s.bytes = layer ? s.part_b + up(static_cast<uint64_t>(s.parts) * hidden * 4) : s.part_b;
     return s;
+}
+
+rmsnorm_status_t launch_reduce(const NormCall& c, cudaStream_t stream) {
+    LaunchShape s{static_cast<int>(div_up(c.p.hidden, kNormReduceCols)),
+                  kNormReduceCols * kNormReduceLanes, 1, 0};
+    s.grid_y = c.p.db ? 2 : 1;
+    return launch(c, norm_bwd_reduce_ptr(), s, stream);
 }
 
 rmsnorm_status_t bwd_workspace(int32_t dtype, int64_t rows, int64_t hidden, bool layer,
@@ -190,7 +337,20 @@ rmsnorm_status_t bwd_run(int32_t dtype, bool layer, const void* dy, const void* 
     c.p.dw = dw;
     c.p.db = db;
     count_vectors(&c, a[0].p | a[1].p | a[2].p | a[5].p);
-    c.p.rows_per_part = div_up(rows, ws.parts);
+    c.layer = layer;
+    if (c.opt.path != RMSNORM_PATH_TWOPASS) {
+        LaunchShape s{0, 0, 1, 0};
+        NormFn fn = nullptr;
+        st = plan_bwd_staged(dtype, &c, &s, &fn);
+        if (st == RMSNORM_ERR_CUDA) return st;
+        if (fn) {
+            st = launch(c, fn, s, stream);
+            if (st != RMSNORM_OK || (!dw && !db)) return st;
+            return launch_reduce(c, stream);
+        }
+        if (c.opt.path == RMSNORM_PATH_STAGED) return RMSNORM_ERR_UNSUPPORTED;
+    }
+    c.p.rows_per_part = div_up(rows, bwd_parts(c.dv, rows, hidden, c.sz));
     c.p.parts = static_cast<int32_t>(div_up(rows, c.p.rows_per_part));
     const LaunchShape rs{clamp_grid(rows, 8ll * c.dv.sms), norm_bwd_rows_block(), 1, 0};
     st = launch(c, norm_bwd_rows_ptr(dtype, c.vb, layer), rs, stream);
@@ -199,10 +359,7 @@ rmsnorm_status_t bwd_run(int32_t dtype, bool layer, const void* dy, const void* 
     cs.grid_y = c.p.parts;
     st = launch(c, norm_bwd_cols_ptr(dtype, c.vb, layer), cs, stream);
     if (st != RMSNORM_OK || (!dw && !db)) return st;
-    LaunchShape ds{static_cast<int>(div_up(hidden, kNormReduceCols)),
-                   kNormReduceCols * kNormReduceLanes, 1, 0};
-    ds.grid_y = db ? 2 : 1;
-    return launch(c, norm_bwd_reduce_ptr(), ds, stream);
+    return launch_reduce(c, stream);
 }
 
 }  // namespace

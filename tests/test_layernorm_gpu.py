@@ -1,5 +1,7 @@
 """Layer norm forward and backward, and RMSNorm backward, against 64-bit
 references (GPU)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -329,3 +331,69 @@ def test_more_than_two_to_the_31_elements():
     dx, _ = binding.rmsnorm_bwd_bf16(y, x, w.cuda())
     want, tol = ref.rmsnorm_bwd(y[-3:].cpu(), last, w, 1e-6)
     close(dx[-3:], want[0], tol[0])
+
+
+@pytest.fixture(scope="module")
+def flib():
+    lib = binding.open_library(build.FAULT_LIB_PATH)
+    assert lib.rmsnorm_fault_injection_enabled() == 1
+    return lib
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("hidden", [500, 2048, 8192])
+@pytest.mark.parametrize("op", ["layernorm_fwd", "layernorm_bwd", "rmsnorm_bwd"])
+def test_withheld_copy_ends_in_a_status(flib, op, hidden, t):
+    """A staged kernel whose first copy never lands leaves after its wait's
+    limit with RMSNORM_ERR_TIMEOUT in the status word; the next call is right."""
+    rows = 1000
+    x, w, b, dy = inputs(t, rows, hidden, 130)
+    dt = binding.RMSNORM_DTYPE_F32 if t == "f32" else binding.RMSNORM_DTYPE_BF16
+    xs, ws, bs, ds = (v.cuda() for v in (x, w, b, dy))
+    out = torch.empty_like(xs)
+    mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    dw, db = torch.empty(hidden, device="cuda"), torch.empty(hidden, device="cuda")
+    room = torch.empty(binding.layernorm_bwd_workspace(xs), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def call(**kw):
+        o = ctypes.byref(binding.make_options(path="staged", **kw))
+        p = [v.data_ptr() for v in (xs, ws, bs, ds, out, mean, rstd, dw, db, room)]
+        x_, w_, b_, d_, o_, m_, r_, dw_, db_, room_ = p
+        if op == "layernorm_fwd":
+            return flib.layernorm_fwd_ex(dt, x_, w_, b_, o_, m_, r_, rows, hidden, 1e-5, o, stream)
+        if op == "layernorm_bwd":
+            return flib.layernorm_bwd_ex(dt, d_, x_, w_, m_, r_, o_, dw_, db_, rows, hidden, room_,
+                                         room.numel(), o, stream)
+        return flib.rmsnorm_bwd_ex(dt, d_, x_, w_, o_, dw_, rows, hidden, 1e-5, room_, room.numel(),
+                                   o, stream)
+
+    assert call(fault_inject=1, wait_timeout_ns=20_000_000) == binding.RMSNORM_OK
+    assert flib.rmsnorm_last_device_status(stream) == binding.RMSNORM_ERR_TIMEOUT
+    assert call() == binding.RMSNORM_OK
+    assert flib.rmsnorm_last_device_status(stream) == binding.RMSNORM_OK
+    if op == "layernorm_fwd":
+        check_fwd((out, mean, rstd), x, w, b)
+    elif op == "layernorm_bwd":
+        want, tol = ref.layernorm_bwd(dy, x, w, mean.cpu(), rstd.cpu())
+        for g, r, e in zip((out, dw, db), want, tol):
+            close(g, r, e)
+    else:
+        want, tol = ref.rmsnorm_bwd(dy, x, w, 1e-5)
+        for g, r, e in zip((out, dw), want, tol):
+            close(g, r, e)
+
+
+def test_forced_staged_path_refuses_what_it_cannot_serve():
+    x, w, _, dy = inputs("f32", 3, 40000, 140)
+    xs, ws, ds = x.cuda(), w.cuda(), dy.cuda()
+    staged = {"path": "staged"}
+    for call in (lambda: binding.layernorm_fwd_ex(xs, ws, options=staged),
+                 lambda: binding.rmsnorm_bwd_ex(ds, xs, ws, options=staged)):
+        with pytest.raises(binding.RmsnormError) as e:
+            call()
+        assert e.value.status == binding.RMSNORM_ERR_UNSUPPORTED
+    off = torch.zeros(65, device="cuda")[1:].view(1, 64)
+    with pytest.raises(binding.RmsnormError) as e:
+        binding.layernorm_fwd_ex(off, options=staged)
+    assert e.value.status == binding.RMSNORM_ERR_UNSUPPORTED
