@@ -113,8 +113,8 @@ rmsnorm_status_t rowsoftmax_plan(int32_t dtype, const void* x, const void* y, in
  *     v[j] = scale * x[j] + t[bucket(r), h]          over the row's valid keys
  *     y[j] = exp(v[j] - max v) / sum exp(v - max v)  at valid keys, 0 elsewhere
  *
- * Valid keys are j < kv_len[b] and, if causal, r <= 0.  Nothing is read at the
- * others, and a row without a valid key is all zero.  Among valid keys special
+ * Valid keys are j < kv_len[b] and, if causal, r <= 0.  What the others hold
+ * does not matter, NaN included, and a row without a valid key is all zero.  Among valid keys special
  * values behave as in rowsoftmax_fwd_f32: -inf gives 0; a row of -inf, or any
  * NaN or +inf, gives NaN at the valid keys.
  *
@@ -130,15 +130,15 @@ rmsnorm_status_t rowsoftmax_plan(int32_t dtype, const void* x, const void* y, in
  *     ds = y * (dy - sum_j y * dy)     dx = scale * ds  (0 at masked keys)
  *     dt[k, h] = sum of ds over b, i and the valid j with bucket(r) = k
  *
- * dt is fp32 for both types; neither y nor dy is read at masked keys.
+ * dt is fp32 for both types; what y and dy hold at masked keys does not matter.
  *
  *  - x, y, dy, dx: batch*heads*q_len*k_len elements; table: num_buckets*heads
  *    elements of the same type; dtable: num_buckets*heads floats; q_start and
  *    kv_len: batch int32 values in DEVICE memory, or NULL (q_start 0, kv_len
  *    k_len); kv_len values are taken into [0, k_len].
  *  - batch, q_len >= 0 (a product of 0: OK, no launch; the backward pass writes
- *    zeros to dtable); 1 <= heads <= 65535; 1 <= k_len <= 2^30; batch * q_len <
- *    2^31; 2 <= num_buckets <= 256 (bidirectional: even, at least 4);
+ *    zeros to dtable); 1 <= heads <= 65535; 1 <= k_len <= 2^30; batch * q_len <=
+ *    2^30; 2 <= num_buckets <= 256 (bidirectional: even, at least 4);
  *    half / 2 < max_distance <= 4096; scale finite; |q_offset| <= 2^40.
  *  - y == x, and dx == dy or dx == y, are allowed (in place); any other overlap
  *    of an output or the workspace with another argument is rejected.
@@ -173,9 +173,10 @@ rmsnorm_status_t rowsoftmax_relbias_fwd_bf16(const uint16_t* x, const uint16_t* 
                                              int64_t k_len, const rowsoftmax_relbias_t* bias,
                                              rmsnorm_stream_t stream);
 
-/* Either dtype, with options (`opt` may be NULL): opt->path RMSNORM_PATH_AUTO
- * or RMSNORM_PATH_TWOPASS (rows of any width, read twice).  Every other field
- * must be zero, else RMSNORM_ERR_INVALID_ARG. */
+/* Either dtype, with options (`opt` may be NULL): opt->path RMSNORM_PATH_AUTO,
+ * RMSNORM_PATH_ROWREG (rows of up to 32 KB less a few keys, held in registers; x,
+ * y, dy and dx on 16-byte boundaries; else RMSNORM_ERR_UNSUPPORTED) or RMSNORM_PATH_TWOPASS (rows of any width, read
+ * twice).  Every other field must be zero, else RMSNORM_ERR_INVALID_ARG. */
 rmsnorm_status_t rowsoftmax_relbias_fwd_ex(int32_t dtype, const void* x, const void* table,
                                            void* y, int64_t batch, int64_t heads, int64_t q_len,
                                            int64_t k_len, const rowsoftmax_relbias_t* bias,

@@ -729,7 +729,7 @@ def rowsoftmax_relbias_fwd_ex(x, table, y=None, *, max_distance: int = 128,
                               bidirectional: bool = True, causal: bool = False,
                               scale: float = 1.0, q_offset: int = 0, q_start=None, kv_len=None,
                               options=None, stream=None):
-    """Either dtype, with options (path auto or twopass)."""
+    """Either dtype, with options (path auto, rowreg or twopass)."""
     rule = _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len)
     return _relbias_fwd("rowsoftmax_relbias_fwd_ex", x, table, y, rule, options, stream)
 
@@ -800,7 +800,7 @@ def rowsoftmax_relbias_bwd_ex(dy, y, num_buckets, dx=None, dtable=None, *,
                               causal: bool = False, scale: float = 1.0, q_offset: int = 0,
                               q_start=None, kv_len=None, table_grad: bool = True, workspace=None,
                               options=None, stream=None):
-    """Either dtype, with options (path auto or twopass)."""
+    """Either dtype, with options (path auto, rowreg or twopass)."""
     rule = _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len)
     return _relbias_bwd("rowsoftmax_relbias_bwd_ex", dy, y, num_buckets, dx, dtable, table_grad,
                         workspace, rule, options, stream)

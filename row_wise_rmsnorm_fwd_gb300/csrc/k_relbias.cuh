@@ -6,7 +6,7 @@
 //     v = scale * x + t[bucket(r), h]      over the valid keys of the row,
 //     y = exp(v - max v) / sum exp(v - max v),  0 at the other keys.
 // Both masks, j < kv_len[b] and (causal) r <= 0, leave a prefix [0, n) of the
-// row valid; nothing outside it is read, and a row with n = 0 is all zero.
+// row valid; what is outside it does not matter, and a row with n = 0 is all zero.
 //     backward: ds = y * (dy - sum_j y * dy), dx = scale * ds,
 //               dt[k, h] = sum of ds over b, i and the j with bucket(r) = k.
 //
@@ -25,7 +25,7 @@
 // per bucket in a fixed order (which also keeps the fp32 chains short).
 #pragma once
 #include "k_normbwd.cuh"
-#include "k_softmax.cuh"
+#include "pairs.cuh"
 #include "relbias_launch.h"
 
 namespace rmsnorm {
@@ -38,18 +38,20 @@ __device__ __forceinline__ int bias_slot(int idx) {
 }
 
 // Buckets of one direction: the last one whose edge is at most n.
-__device__ __forceinline__ int bias_bucket_of(const BiasParams& p, int n) {
+__device__ __forceinline__ int bias_bucket_of(const BiasParams& p, const int* edges, int n) {
     int lo = 0, hi = p.half;                     // edges[lo] <= n < edges[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.edges[mid] <= n) lo = mid; else hi = mid;
+        if (edges[mid] <= n) lo = mid; else hi = mid;
     }
     return lo;
 }
 
-__device__ __forceinline__ int bias_bucket(const BiasParams& p, int r) {
-    if (p.both) return bias_bucket_of(p, r < 0 ? -r : r) + (r > 0 ? p.half : 0);
-    return bias_bucket_of(p, r < 0 ? -r : 0);
+// `edges`: p.edges, or a copy in shared memory, which threads of different
+// positions read faster than the parameters.
+__device__ __forceinline__ int bias_bucket(const BiasParams& p, const int* edges, int r) {
+    if (p.both) return bias_bucket_of(p, edges, r < 0 ? -r : r) + (r > 0 ? p.half : 0);
+    return bias_bucket_of(p, edges, r < 0 ? -r : 0);
 }
 
 struct BiasWindow {
@@ -65,9 +67,7 @@ struct BiasRow {
     int r0;
 };
 
-__device__ __forceinline__ BiasRow bias_row(const BiasParams& p, int head, int row) {
-    const int b = row / p.q_len;
-    const int i = row - b * p.q_len;
+__device__ __forceinline__ BiasRow bias_row_of(const BiasParams& p, int head, int b, int i) {
     BiasRow o;
     o.at = ((static_cast<int64_t>(b) * p.heads + head) * p.q_len + i) * p.k_len;
     int64_t q = p.q_offset + i;
@@ -84,6 +84,27 @@ __device__ __forceinline__ BiasRow bias_row(const BiasParams& p, int head, int r
     return o;
 }
 
+__device__ __forceinline__ BiasRow bias_row(const BiasParams& p, int head, int row) {
+    const int b = row / p.q_len;
+    return bias_row_of(p, head, b, row - b * p.q_len);
+}
+
+// The relative positions [ra, rb] of a bucket, the sides' buckets as far as
+// -low and high.
+__device__ __forceinline__ void bias_bucket_range(const BiasParams& p, int k, int low, int high,
+                                                  int* ra, int* rb) {
+    const int e = k < p.half ? k : k - p.half;
+    const int first = p.edges[e];                            // distances of the bucket
+    const bool outer = e + 1 == p.half;
+    if (k < p.half) {
+        *ra = outer ? -low : 1 - p.edges[e + 1];
+        *rb = e == 0 && !p.both ? high : -first;             // one direction: r > 0 is bucket 0
+    } else {
+        *ra = first > 1 ? first : 1;
+        *rb = outer ? high : p.edges[e + 1] - 1;
+    }
+}
+
 // The head's biases over the window, and the constants on its two sides.
 template <typename T, int EPV>
 __device__ __forceinline__ void bias_load_window(const BiasParams& p, const BiasWindow& w, int head,
@@ -95,7 +116,7 @@ __device__ __forceinline__ void bias_load_window(const BiasParams& p, const Bias
     };
     const int size = w.lo + w.hi + 2 * EPV;
     for (int i = threadIdx.x; i < size; i += blockDim.x)
-        win[bias_slot<EPV>(i)] = at(bias_bucket(p, i - w.lo - EPV));
+        win[bias_slot<EPV>(i)] = at(bias_bucket(p, p.edges, i - w.lo - EPV));
     *low = at(p.half - 1);
     *high = at(p.both ? 2 * p.half - 1 : 0);
 }
@@ -141,17 +162,8 @@ __device__ __forceinline__ void bias_fold(const BiasParams& p, const BiasWindow&
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarp = blockDim.x >> 5;
     for (int k = warp; k < p.num_buckets; k += nwarp) {
-        const int e = k < p.half ? k : k - p.half;
-        const int first = p.edges[e];                        // distances of the bucket
-        const int last = e + 1 < p.half ? p.edges[e + 1] - 1 : w.lo + EPV;
         int ra, rb;                                          // relative positions [ra, rb]
-        if (k < p.half) {
-            ra = -last;
-            rb = e == 0 && !p.both ? EPV - 1 : -first;       // one direction: r > 0 is bucket 0
-        } else {
-            ra = first > 1 ? first : 1;
-            rb = e + 1 < p.half ? last : w.hi + EPV - 1;
-        }
+        bias_bucket_range(p, k, w.lo + EPV, w.hi + EPV - 1, &ra, &rb);
         float s = 0.f;
         for (int r = ra + lane; r <= rb; r += 32) {
             const int slot = bias_slot<EPV>(r + w.lo + EPV);
@@ -317,7 +329,597 @@ __global__ void __launch_bounds__(kBiasWideThreads) relbias_bwd_wide_kernel(cons
     }
 }
 
-// dt[k, h] from the CTAs' sums: one CTA per head, a warp per bucket.
+// ------------------------------------------------------ rows in registers --
+// G threads per row (p.group: a multiple of 32, or a power of two below 32 for
+// several rows per warp), NV vectors per thread, read once.  One exchange per
+// row: a warp (lane group) forms its exponentials relative to its own maximum,
+// and the (maximum, sum) pairs of a row's warps meet behind one barrier.
+//
+// exp(v - m) is 2^((v - m) * log2(e)) with the subtraction first: v - m is
+// never positive and exact for every key that counts, so scores of any
+// magnitude, the type's lowest value included, come out right (an all-lowest
+// row is uniform), which folding log2(e) into the scale would overflow.
+//
+// The window is laid out for whole vectors: vector v of a row starts at window
+// position base + EPV * v, so all its vectors have the row's phase base % 4,
+// and four copies of the window, each shifted by one position, let every one
+// be read (backward: updated) by 16-byte accesses, two for 8 keys, whose even
+// and odd chunks lie in separate halves so that neighbouring lanes hit
+// neighbouring chunks.  It is padded by two vectors of each side's constant:
+// a vector beyond is moved to the padding, so lookups need no bounds.
+
+//
+// Accesses are 16-byte vectors whatever the rows' length: with SHIFT (rows that
+// are not a multiple of 16 bytes) a row's vector 0 is the one that holds its
+// first key, `shift` elements into it, so keys have indices from `shift` on;
+// the vectors at its two ends are stored element by element.
+constexpr int kBiasVecs = 4;             // vectors per thread
+
+// Registers per thread: what the widest instances take without spilling and,
+// above that, no more, for resident warps (the row's loads are the only ones in
+// flight).  Measured (% of the HBM copy peak): bf16 forward 96 / 112 / 128
+// registers 89 / 90 / 90 on rows of 2048 and 41 / 38 / 38 on a decoding step;
+// backward 64 / 72 / 80 registers, bf16 rows of 2048 90 / 94 / 96, causal 73 /
+// 75 / 71, of 512 68 / 80 / 69, fp32 rows of 1024 89 / 91 / 91.
+template <typename T>
+constexpr int bias_fwd_regs() { return sizeof(T) == 2 ? 96 : 80; }
+constexpr int kBiasBwdRegs = 72;
+
+__device__ __forceinline__ float bias_max(float v, int width) {
+    for (int m = width >> 1; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
+    return v;
+}
+
+// Where the pair (m, .) stands relative to the maximum M >= m; 1 if both are -inf.
+__device__ __forceinline__ float bias_factor(float m, float M) {
+    return m == M ? 1.f : exp2f((m - M) * kLog2e);
+}
+
+template <int EPV>
+struct VecWindow {
+    BiasVecWindow s;
+    int lo, hi;
+    __device__ __forceinline__ explicit VecWindow(const BiasWindow& w)
+        : s(bias_vec_window(w.lo, w.hi, EPV)), lo(w.lo), hi(w.hi) {}
+    __device__ __forceinline__ int floats() const { return s.copies * s.copy; }
+    // position of relative position r, and the r of position 0
+    __device__ __forceinline__ int first() const { return -lo - 2 * EPV; }
+    static constexpr int C = EPV < 4 ? EPV : 4;       // copies, and floats of a chunk
+    // where copy c keeps position idx >= c
+    __device__ __forceinline__ int slot(int c, int idx) const {
+        const int d = idx - c, q = d / C, h = d % C;      // C is a power of two, d >= 0
+        const int chunk = EPV == 8 ? (q & 1) * s.half + (q >> 1) : q;
+        return c * s.copy + chunk * C + h;
+    }
+};
+
+// A row's view of a window: vector v's chunks are at p0 + v (and p1 + v), v
+// moved into [vmin, vmax]; vectors up to vmin are all low, from vmax on all high.
+template <int EPV>
+struct WindowRow {
+    static constexpr int C = EPV < 4 ? EPV : 4;       // floats of a chunk
+    int p0, p1;                                       // float offsets
+    int vmin, vmax;
+    __device__ __forceinline__ WindowRow(const VecWindow<EPV>& w, int r0) {
+        const int base = r0 - w.first();              // position of the row's vector 0
+        constexpr int SH = EPV == 8 ? 3 : EPV == 4 ? 2 : EPV == 2 ? 1 : 0;
+        const int phase = base & (EPV - 1);           // 0 .. EPV - 1
+        const int v0 = base >> SH;                    // whole vectors before it
+        vmin = -v0;
+        vmax = ((w.lo + w.hi + 3 * EPV - 1 - phase) >> SH) - v0;
+        const int c = phase & (C - 1);
+        if constexpr (EPV == 8) {
+            const int odd = phase >> 2;
+            const int a = c * w.s.copy + v0 * C;
+            p0 = odd ? a + w.s.half * C : a;
+            p1 = odd ? a + C : a + w.s.half * C;
+        } else {
+            p0 = c * w.s.copy + v0 * C;
+            p1 = 0;
+        }
+    }
+    __device__ __forceinline__ int moved(int v) const { return min(max(v, vmin), vmax); }
+    __device__ __forceinline__ void read(const float* win, int v, float (&b)[EPV]) const {
+        if constexpr (EPV == 8) {
+            const float4 x = *reinterpret_cast<const float4*>(win + p0 + v * C);
+            const float4 y = *reinterpret_cast<const float4*>(win + p1 + v * C);
+            b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w;
+            b[4] = y.x; b[5] = y.y; b[6] = y.z; b[7] = y.w;
+        } else if constexpr (EPV == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(win + p0 + v * C);
+            b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w;
+        } else if constexpr (EPV == 2) {
+            const float2 x = *reinterpret_cast<const float2*>(win + p0 + v * C);
+            b[0] = x.x; b[1] = x.y;
+        } else {
+            b[0] = win[p0 + v];
+        }
+    }
+    __device__ __forceinline__ void write(float* win, int v, const float (&b)[EPV]) const {
+        if constexpr (EPV == 8) {
+            *reinterpret_cast<float4*>(win + p0 + v * C) = make_float4(b[0], b[1], b[2], b[3]);
+            *reinterpret_cast<float4*>(win + p1 + v * C) = make_float4(b[4], b[5], b[6], b[7]);
+        } else if constexpr (EPV == 4) {
+            *reinterpret_cast<float4*>(win + p0 + v * C) = make_float4(b[0], b[1], b[2], b[3]);
+        } else if constexpr (EPV == 2) {
+            *reinterpret_cast<float2*>(win + p0 + v * C) = make_float2(b[0], b[1]);
+        } else {
+            win[p0 + v] = b[0];
+        }
+    }
+};
+
+// The rows of one group of a CTA, first + k * step of its head, without a
+// division per row.  Rows behind the head's last one have no valid keys and
+// are not written (at < 0).
+struct BiasRows {
+    int row, b, i;
+    int step, step_b, step_i;
+    __device__ __forceinline__ BiasRows(const BiasParams& p, int first, int step_)
+        : row(first), b(first / p.q_len), i(first - b * p.q_len), step(step_),
+          step_b(step_ / p.q_len), step_i(step_ - step_b * p.q_len) {}
+    __device__ __forceinline__ BiasRow get(const BiasParams& p, int head) const {
+        BiasRow o;
+        o.at = -1;
+        o.n = o.r0 = 0;
+        if (row < p.head_rows) o = bias_row_of(p, head, b, i);
+        return o;
+    }
+    __device__ __forceinline__ void next(const BiasParams& p) {
+        row += step;
+        b += step_b;
+        i += step_i;
+        if (i >= p.q_len) {
+            i -= p.q_len;
+            ++b;
+        }
+    }
+};
+
+// What the warp has of vector number i of its threads, one bit each: valid keys
+// only (full), none at all, or (neither) some; valid keys are [from, to).  A
+// masked row then pays the per-element masks only where its valid keys end.
+template <int EPV, int NV>
+struct VecClasses {
+    uint32_t f = 0, s = 0;
+    __device__ __forceinline__ VecClasses(int from, int to, int t, int G) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = (i * G + t) * EPV;
+            f |= __all_sync(0xffffffffu, j >= from && j + EPV <= to) ? 1u << i : 0u;
+            s |= __any_sync(0xffffffffu, j < to) ? 1u << i : 0u;
+        }
+    }
+    __device__ __forceinline__ bool all() const { return f == (1u << NV) - 1; }
+    __device__ __forceinline__ bool full(int i) const { return f >> i & 1u; }
+    __device__ __forceinline__ bool none(int i) const { return !(s >> i & 1u); }
+};
+
+// A row in vectors: element `at` (a multiple of EPV) is its vector 0's first,
+// its keys have indices [shift, shift + k_len), the valid ones [shift, to).
+template <bool SHIFT, int EPV>
+struct VecRow {
+    int64_t at;
+    int shift, to, end;
+    bool here;
+    __device__ __forceinline__ VecRow(const BiasRow& r, int k_len) {
+        shift = SHIFT ? static_cast<int>(r.at & (EPV - 1)) : 0;
+        at = r.at - shift;
+        to = r.n > 0 ? r.n + shift : 0;
+        end = k_len + shift;
+        here = r.at >= 0;
+    }
+};
+
+// Vector at element e of an array of `total` elements: whole, or what of it
+// lies inside the array.
+template <typename T, bool SHIFT>
+__device__ __forceinline__ Vec<16> ld_vec(const void* base, int64_t e, int64_t total) {
+    constexpr int EPV = VecTraits<T, 16>::kElems;
+    const char* p = static_cast<const char*>(base) + e * static_cast<int>(sizeof(T));
+    if (!SHIFT || e + EPV <= total) return ld_stream<16>(p);
+    Vec<16> v = zero_vec<16>();
+#pragma unroll
+    for (int k = 0; k < EPV; ++k) {
+        if (e + k < total) {
+            if constexpr (sizeof(T) == 4) {
+                v.u[k] = ld_stream<4>(p + 4 * k).u[0];
+            } else {
+                v.u[k / 2] |= static_cast<uint32_t>(ld_stream<2>(p + 2 * k).h) << (16 * (k & 1));
+            }
+        }
+    }
+    return v;
+}
+
+// Store a row's vector j / EPV: whole, or the elements inside the row.
+template <typename T, bool SHIFT, class Row>
+__device__ __forceinline__ void st_vec(void* base, const Row& r, int j, const Vec<16>& v) {
+    constexpr int EPV = VecTraits<T, 16>::kElems;
+    char* p = static_cast<char*>(base) + (r.at + j) * static_cast<int>(sizeof(T));
+    if (!SHIFT || (j >= r.shift && j + EPV <= r.end)) {
+        st_stream<16>(p, v);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < EPV; ++k) {
+        if (j + k >= r.shift && j + k < r.end) {
+            if constexpr (sizeof(T) == 4) {
+                Vec<4> o;
+                o.u[0] = v.u[k];
+                st_stream<4>(p + 4 * k, o);
+            } else {
+                Vec<2> o;
+                o.h = static_cast<uint16_t>(v.u[k / 2] >> (16 * (k & 1)));
+                st_stream<2>(p + 2 * k, o);
+            }
+        }
+    }
+}
+
+template <typename T, bool SHIFT>
+__global__ void __maxnreg__(bias_fwd_regs<T>()) relbias_fwd_rowreg_kernel(const BiasParams p) {
+    constexpr int EPV = VecTraits<T, 16>::kElems;
+    constexpr int NV = kBiasVecs;
+    constexpr int PN = PairTraits<T, 16>::N;
+    using L = Lanes<2>;
+    extern __shared__ __align__(16) float win[];
+    __shared__ float2 red[2][32];
+    __shared__ float biases[kBiasMaxBuckets];
+    __shared__ int edges[kBiasMaxBuckets];
+    pdl_trigger();
+    const BiasWindow bw(p);
+    const VecWindow<EPV> w(bw);
+    const int G = p.group;
+    const int width = G < 32 ? G : 32;
+    const int tid = threadIdx.x;
+    const int g = tid / G;
+    const int t = tid - g * G;
+    const int warp = tid >> 5, lane = tid & 31;
+    const int wpg = G >> 5;
+    const int gw0 = g * wpg;
+    const int rpc = p.rows_per_cta;
+    const int head = blockIdx.x / p.parts;
+    int merge_width = 1;
+    while (merge_width < wpg) merge_width <<= 1;
+    int block = blockIdx.x - head * p.parts;
+    const int nblocks = (p.head_rows + rpc - 1) / rpc;
+    BiasRows rows(p, block * rpc + g, p.parts * rpc);
+    pdl_wait();
+
+    using Row = VecRow<SHIFT, EPV>;
+    Vec<16> cur[NV], nxt[NV];
+    auto load = [&](Vec<16> (&dst)[NV], const Row& r) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = (i * G + t) * EPV;
+            if (j < r.to) dst[i] = ld_vec<T, SHIFT>(p.x, r.at + j, p.elems);
+        }
+    };
+    BiasRow info = rows.get(p, head);
+    Row ri(info, p.k_len);
+    int r0 = info.r0 - ri.shift;                 // relative position of index 0
+    load(cur, ri);
+    for (int k = tid; k < p.num_buckets; k += blockDim.x) {
+        const char* table = static_cast<const char*>(p.table);
+        const int64_t e = static_cast<int64_t>(k) * p.heads + head;
+        biases[k] = get<T, sizeof(T)>(ld_ro<sizeof(T)>(table + e * static_cast<int>(sizeof(T))), 0);
+        edges[k] = p.edges[k];
+    }
+    __syncthreads();
+    for (int idx = tid; idx < w.s.size; idx += blockDim.x) {
+        const float v = biases[bias_bucket(p, edges, w.first() + idx)];
+        for (int c = 0; c < w.C && c <= idx; ++c) win[w.slot(c, idx)] = v;
+    }
+    __syncthreads();
+    const float low = win[w.slot(0, 0)], high = win[w.slot(0, w.s.size - 1)];
+    const L scale = L::all(p.scale), log2e = L::all(kLog2e);
+    for (int it = 0; block < nblocks; block += p.parts, ++it) {
+        rows.next(p);
+        info = rows.get(p, head);
+        const Row rn(info, p.k_len);
+        load(nxt, rn);
+        L e[NV * PN];
+        float m = -INFINITY, s = 0.f;
+        const WindowRow<EPV> wr(w, r0);
+        const VecClasses<EPV, NV> is(ri.shift, ri.to, t, G);
+        // each pass twice: `all` vectors of the warp valid in full, or by class
+        auto scores = [&](auto all) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (!all && is.none(i)) continue;
+                const int v = i * G + t, j = v * EPV;
+                const bool off = !all && j >= ri.to;
+                const bool below = __all_sync(0xffffffffu, v <= wr.vmin || off);
+                if (below || __all_sync(0xffffffffu, v >= wr.vmax || off)) {
+                    const L c = L::all(below ? low : high);
+#pragma unroll
+                    for (int k = 0; k < PN; ++k) e[i * PN + k] = fma(lanes<T, 16>(cur[i], k), scale, c);
+                } else {
+                    float b[EPV];
+                    wr.read(win, wr.moved(v), b);
+#pragma unroll
+                    for (int k = 0; k < PN; ++k)
+                        e[i * PN + k] = fma(lanes<T, 16>(cur[i], k), scale, L::of(b + 2 * k));
+                }
+                if (!all && !is.full(i)) {           // masked keys
+#pragma unroll
+                    for (int k = 0; k < PN; ++k) {
+                        float a[2];
+                        e[i * PN + k].put(a);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = j + 2 * k + h;
+                            if (at >= ri.to || (SHIFT && at < ri.shift)) a[h] = -INFINITY;
+                        }
+                        e[i * PN + k] = L::of(a);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < PN; ++k) m = e[i * PN + k].largest(m);
+            }
+        };
+        const bool all = is.all();
+        if (all) scores(std::true_type()); else scores(std::false_type());
+        m = width == 32 ? warp_allreduce_max(m) : bias_max(m, width);
+        const L minus = L::all(m == -INFINITY ? 0.f : -m);
+        L s0 = L::all(0.f), s1 = L::all(0.f);
+        auto exponentials = [&](auto all) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (!all && is.none(i)) continue;
+#pragma unroll
+                for (int k = 0; k < PN; ++k) {
+                    float a[2];
+                    ((e[i * PN + k] + minus) * log2e).put(a);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) a[h] = row_exp_arg<T>(a[h]);
+                    e[i * PN + k] = L::of(a);
+                    if (k & 1) s1 = s1 + e[i * PN + k]; else s0 = s0 + e[i * PN + k];
+                }
+            }
+        };
+        if (all) exponentials(std::true_type()); else exponentials(std::false_type());
+        s = share_sum((s0 + s1).total(), width);
+        float f = 1.f;
+        if (wpg > 1) {
+            float2* slot = red[it & 1];
+            if (lane == 0) slot[warp] = make_float2(m, s);
+            __syncthreads();
+            float2 o = make_float2(-INFINITY, 0.f);
+            if (lane < wpg) o = slot[gw0 + lane];
+            const float M = __shfl_sync(0xffffffffu, bias_max(o.x, merge_width), 0);
+            s = group_allreduce_sum(o.y * bias_factor(o.x, M), merge_width);
+            s = __shfl_sync(0xffffffffu, s, 0);
+            f = bias_factor(m, M);
+        }
+        // a row of -inf: s = 0, 0 * (1 / 0) = NaN at its valid keys
+        const L inv = L::all(f / s);
+        auto outputs = [&](auto all) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int j = (i * G + t) * EPV;
+                if (!all && is.none(i)) {
+                    if (ri.here && j < ri.end) st_vec<T, SHIFT>(p.out, ri, j, zero_vec<16>());
+                    continue;
+                }
+                float o[EPV];
+#pragma unroll
+                for (int k = 0; k < PN; ++k) (e[i * PN + k] * inv).put(o + 2 * k);
+                if (all || is.full(i)) {
+                    st_vec<T, false>(p.out, ri, j, pack<T, 16>(o));
+                } else if (ri.here && j < ri.end) {
+#pragma unroll
+                    for (int k = 0; k < EPV; ++k)
+                        if (j + k >= ri.to) o[k] = 0.f;
+                    st_vec<T, SHIFT>(p.out, ri, j, pack<T, 16>(o));
+                }
+            }
+        };
+        if (all) outputs(std::true_type()); else outputs(std::false_type());
+        ri = rn;
+        r0 = info.r0 - rn.shift;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) cur[i] = nxt[i];
+    }
+}
+
+// Fold the windows of `groups` row groups and the threads' side sums into
+// sums[bucket], and clear them: first a thread per position over all groups and
+// copies (into `total`, w.s.size floats), then a warp per bucket.  All threads
+// of the block.
+template <int EPV>
+__device__ __forceinline__ void bias_fold_vec(const BiasParams& p, const VecWindow<EPV>& w,
+                                              float* wins, float* total, int groups, float& low,
+                                              float& high, double* sums, float2* red) {
+    constexpr int C = VecWindow<EPV>::C;
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarp = blockDim.x >> 5;
+    for (int idx = threadIdx.x; idx < w.s.size; idx += blockDim.x) {
+        float s[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) s[c] = 0.f;
+        for (int g = 0; g < groups; ++g) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if (c <= idx) {
+                    float* at = wins + g * w.floats() + w.slot(c, idx);
+                    s[c] += *at;
+                    *at = 0.f;
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 1; c < C; ++c) s[0] += s[c];
+        total[idx] = s[0];
+    }
+    const float2 side = block_sum2(low, high, red);          // a barrier: total[] is written
+    for (int k = warp; k < p.num_buckets; k += nwarp) {
+        int ra, rb;                                          // relative positions [ra, rb]
+        bias_bucket_range(p, k, w.lo + 2 * EPV, w.hi + 2 * EPV - 1, &ra, &rb);
+        float s = 0.f;
+        for (int r = ra + lane; r <= rb; r += 32) s += total[r - w.first()];
+        s = warp_allreduce_sum(s);
+        if (lane == 0) {
+            double d = static_cast<double>(s);
+            if (k == p.half - 1) d += static_cast<double>(side.x);
+            if (k == (p.both ? 2 * p.half - 1 : 0)) d += static_cast<double>(side.y);
+            sums[k] += d;
+        }
+    }
+    low = high = 0.f;
+    __syncthreads();
+}
+
+// Backward: y and dy of a row in registers, the row's dot product exchanged
+// behind one barrier, which also orders the rows' updates of the group's
+// window (rows_per_cta windows per CTA).
+template <typename T, bool SHIFT>
+__global__ void __maxnreg__(kBiasBwdRegs) relbias_bwd_rowreg_kernel(const BiasParams p) {
+    constexpr int EPV = VecTraits<T, 16>::kElems;
+    constexpr int NV = kBiasVecs;
+    constexpr int PN = PairTraits<T, 16>::N;
+    using L = Lanes<2>;
+    extern __shared__ __align__(16) float wins[];
+    __shared__ double sums[kBiasMaxBuckets];
+    __shared__ float red[2][32];
+    __shared__ float2 fold_red[32];
+    pdl_trigger();
+    const BiasWindow bw(p);
+    const VecWindow<EPV> w(bw);
+    const int G = p.group;
+    const int width = G < 32 ? G : 32;
+    const int tid = threadIdx.x;
+    const int g = tid / G;
+    const int t = tid - g * G;
+    const int warp = tid >> 5, lane = tid & 31;
+    const int wpg = G >> 5;
+    const int gw0 = g * wpg;
+    const int rpc = p.rows_per_cta;
+    const int head = blockIdx.x / p.parts;
+    int merge_width = 1;
+    while (merge_width < wpg) merge_width <<= 1;
+    float* win = wins + g * w.floats();
+    float* total = wins + rpc * w.floats();
+    if (p.part) {
+        for (int i = tid; i < rpc * w.floats(); i += blockDim.x) wins[i] = 0.f;
+        for (int k = tid; k < p.num_buckets; k += blockDim.x) sums[k] = 0.0;
+    }
+    int block = blockIdx.x - head * p.parts;
+    const int nblocks = (p.head_rows + rpc - 1) / rpc;
+    BiasRows rows(p, block * rpc + g, p.parts * rpc);
+    __syncthreads();
+    pdl_wait();
+
+    const L scale = L::all(p.scale);
+    float low = 0.f, high = 0.f;
+    for (int it = 0; block < nblocks; block += p.parts, ++it, rows.next(p)) {
+        const BiasRow info = rows.get(p, head);
+        const VecRow<SHIFT, EPV> ri(info, p.k_len);
+        const WindowRow<EPV> wr(w, info.r0 - ri.shift);
+        const VecClasses<EPV, NV> is(ri.shift, ri.to, t, G);
+        const bool all = is.all();
+        Vec<16> y[NV], d[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = (i * G + t) * EPV;
+            if (j < ri.to) {
+                y[i] = ld_vec<T, SHIFT>(p.y, ri.at + j, p.elems);
+                d[i] = ld_vec<T, SHIFT>(p.x, ri.at + j, p.elems);
+            }
+        }
+        L s0 = L::all(0.f), s1 = L::all(0.f);
+        // each pass twice: `all` vectors of the warp valid in full, or by class
+        auto products = [&](auto all) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (!all && is.none(i)) continue;
+                if (!all && !is.full(i)) {           // clear what is not a valid key
+                    const int j = (i * G + t) * EPV;
+                    clear_from<T, 16>(y[i], max(ri.to - j, 0));
+                    clear_from<T, 16>(d[i], max(ri.to - j, 0));
+                    if (SHIFT) {
+                        clear_below<T, 16>(y[i], ri.shift - j);
+                        clear_below<T, 16>(d[i], ri.shift - j);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < PN; ++k) {
+                    if (k & 1) s1 = fma(lanes<T, 16>(y[i], k), lanes<T, 16>(d[i], k), s1);
+                    else s0 = fma(lanes<T, 16>(y[i], k), lanes<T, 16>(d[i], k), s0);
+                }
+            }
+        };
+        if (all) products(std::true_type()); else products(std::false_type());
+        float dot = share_sum((s0 + s1).total(), width);
+        if (wpg > 1) {
+            float* slot = red[it & 1];
+            if (lane == 0) slot[warp] = dot;
+            __syncthreads();
+            dot = group_allreduce_sum(lane < wpg ? slot[gw0 + lane] : 0.f, merge_width);
+            dot = __shfl_sync(0xffffffffu, dot, 0);
+        } else {
+            __syncwarp();
+        }
+        const L minus = L::all(-dot);
+        auto outputs = [&](auto all) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int v = i * G + t, j = v * EPV;
+                if (!all && is.none(i)) {
+                    if (ri.here && j < ri.end) st_vec<T, SHIFT>(p.out, ri, j, zero_vec<16>());
+                    continue;
+                }
+                L gk[PN];
+#pragma unroll
+                for (int k = 0; k < PN; ++k)
+                    gk[k] = lanes<T, 16>(y[i], k) * (lanes<T, 16>(d[i], k) + minus);
+                if (!all && !is.full(i)) {           // 0 there, whatever the row's sum is
+#pragma unroll
+                    for (int k = 0; k < PN; ++k) {
+                        float a[2];
+                        gk[k].put(a);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = j + 2 * k + h;
+                            if (at >= ri.to || (SHIFT && at < ri.shift)) a[h] = 0.f;
+                        }
+                        gk[k] = L::of(a);
+                    }
+                }
+                float o[EPV];
+#pragma unroll
+                for (int k = 0; k < PN; ++k) (gk[k] * scale).put(o + 2 * k);
+                if (all || is.full(i)) st_vec<T, false>(p.out, ri, j, pack<T, 16>(o));
+                else if (ri.here && j < ri.end) st_vec<T, SHIFT>(p.out, ri, j, pack<T, 16>(o));
+                if (p.part && (all || j < ri.to)) {
+                    if (v > wr.vmin && v < wr.vmax) {
+                        float a[EPV];
+                        wr.read(win, v, a);
+#pragma unroll
+                        for (int k = 0; k < PN; ++k) (L::of(a + 2 * k) + gk[k]).put(a + 2 * k);
+                        wr.write(win, v, a);
+                    } else {
+                        L sum = gk[0];
+#pragma unroll
+                        for (int k = 1; k < PN; ++k) sum = sum + gk[k];
+                        if (v >= wr.vmax) high += sum.total(); else low += sum.total();
+                    }
+                }
+            }
+        };
+        if (all) outputs(std::true_type()); else outputs(std::false_type());
+        if (p.part && it % kBiasFoldRows == kBiasFoldRows - 1)
+            bias_fold_vec<EPV>(p, w, wins, total, rpc, low, high, sums, fold_red);
+    }
+    if (p.part) {
+        bias_fold_vec<EPV>(p, w, wins, total, rpc, low, high, sums, fold_red);
+        double* to = p.part + static_cast<int64_t>(blockIdx.x) * p.num_buckets;
+        for (int k = tid; k < p.num_buckets; k += blockDim.x) to[k] = sums[k];
+    }
+}
+
+// dt[k, h] from the CTAs' sums: blockIdx.x is the head, a warp per bucket.
 constexpr int kBiasReduceThreads = 256;
 
 static __global__ void __launch_bounds__(kBiasReduceThreads)
@@ -325,14 +927,15 @@ relbias_reduce_kernel(const BiasParams p) {
     pdl_trigger();
     pdl_wait();
     const int head = blockIdx.x, lane = threadIdx.x & 31;
-    for (int k = threadIdx.x >> 5; k < p.num_buckets; k += kBiasReduceThreads / 32) {
-        const double* src = p.part + static_cast<int64_t>(head) * p.parts * p.num_buckets + k;
-        double s = 0.0;
-        for (int c = lane; c < p.parts; c += 32) s += src[static_cast<int64_t>(c) * p.num_buckets];
+    const int k = (blockIdx.y * kBiasReduceThreads + threadIdx.x) >> 5;
+    if (k >= p.num_buckets) return;
+    const double* src = p.part + static_cast<int64_t>(head) * p.parts * p.num_buckets + k;
+    double s = 0.0;
+#pragma unroll 4
+    for (int c = lane; c < p.parts; c += 32) s += src[static_cast<int64_t>(c) * p.num_buckets];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        if (lane == 0) p.dtable[static_cast<int64_t>(k) * p.heads + head] = static_cast<float>(s);
-    }
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (lane == 0) p.dtable[static_cast<int64_t>(k) * p.heads + head] = static_cast<float>(s);
 }
 
 }  // namespace rmsnorm

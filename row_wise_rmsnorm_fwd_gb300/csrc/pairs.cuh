@@ -11,6 +11,12 @@ template <int W> struct Lanes;
 template <> struct Lanes<2> {
     uint64_t v;
     static __device__ __forceinline__ Lanes all(float a) { return {pack_x2(a, a)}; }
+    static __device__ __forceinline__ Lanes of(const float* f) { return {pack_x2(f[0], f[1])}; }
+    __device__ __forceinline__ float largest(float m) const {
+        float a, b;
+        unpack_x2(v, a, b);
+        return fmaxf(fmaxf(a, b), m);
+    }
     __device__ __forceinline__ Lanes operator+(Lanes o) const { return {add_x2(v, o.v)}; }
     __device__ __forceinline__ Lanes operator*(Lanes o) const { return {mul_x2(v, o.v)}; }
     __device__ __forceinline__ float total() const {
@@ -23,6 +29,8 @@ template <> struct Lanes<2> {
 template <> struct Lanes<1> {
     float v;
     static __device__ __forceinline__ Lanes all(float a) { return {a}; }
+    static __device__ __forceinline__ Lanes of(const float* f) { return {f[0]}; }
+    __device__ __forceinline__ float largest(float m) const { return fmaxf(v, m); }
     __device__ __forceinline__ Lanes operator+(Lanes o) const { return {v + o.v}; }
     __device__ __forceinline__ Lanes operator*(Lanes o) const { return {v * o.v}; }
     __device__ __forceinline__ float total() const { return v; }
@@ -52,6 +60,44 @@ __device__ __forceinline__ Lanes<PairTraits<T, VB>::W> lanes(const Vec<VB>& v, i
     } else {
         return {get<T, VB>(v, 0)};
     }
+}
+
+// Zero the elements from number n (0 <= n) of a vector on.
+template <typename T, int VB>
+__device__ __forceinline__ void clear_from(Vec<VB>& v, int n) {
+    if constexpr (VB == 2) {
+        if (n < 1) v.h = 0;
+    } else {
+        constexpr int PER = 4 / static_cast<int>(sizeof(T));     // elements of a word
+#pragma unroll
+        for (int k = 0; k < VB / 4; ++k) {
+            if (n <= k * PER) v.u[k] = 0u;
+            else if (PER == 2 && n == k * PER + 1) v.u[k] &= 0xFFFFu;
+        }
+    }
+}
+
+// Zero the elements below number n (n <= 0: none).
+template <typename T, int VB>
+__device__ __forceinline__ void clear_below(Vec<VB>& v, int n) {
+    constexpr int PER = 4 / static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int k = 0; k < VB / 4; ++k) {
+        if (n >= (k + 1) * PER) v.u[k] = 0u;
+        else if (PER == 2 && n == k * PER + 1) v.u[k] &= 0xFFFF0000u;
+    }
+}
+
+template <int VB>
+__device__ __forceinline__ Vec<VB> zero_vec() {
+    Vec<VB> v;
+    if constexpr (VB == 2) {
+        v.h = 0;
+    } else {
+#pragma unroll
+        for (int k = 0; k < VB / 4; ++k) v.u[k] = 0u;
+    }
+    return v;
 }
 
 // A vector of ones.

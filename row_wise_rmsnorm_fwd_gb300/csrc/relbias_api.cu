@@ -13,6 +13,8 @@ namespace rmsnorm {
 namespace {
 
 constexpr int64_t kMaxOffset = 1ll << 40;
+constexpr int64_t kMaxHeadRows = 1ll << 30;    // a row's number plus a grid's stride is a 32-bit int
+constexpr int64_t kWindowBudget = 64 << 10;    // shared memory of a CTA's windows, about
 
 // Smallest distance of each bucket of one direction (half of them): one by one
 // up to half / 2 =: near, then where
@@ -74,7 +76,7 @@ rmsnorm_status_t check_call(int32_t dtype, int64_t batch, int64_t heads, int64_t
     if (!std::isfinite(a->scale)) return RMSNORM_ERR_INVALID_ARG;
     if (batch < 0 || q_len < 0 || heads <= 0 || k_len <= 0) return RMSNORM_ERR_INVALID_ARG;
     if (heads > 65535 || k_len > kBiasMaxKeys) return RMSNORM_ERR_INVALID_ARG;
-    if (q_len > 0x7FFFFFFFll || (q_len > 0 && batch > 0x7FFFFFFFll / q_len) || batch > 0x7FFFFFFFll)
+    if (q_len > kMaxHeadRows || batch > kMaxHeadRows || (q_len > 0 && batch > kMaxHeadRows / q_len))
         return RMSNORM_ERR_INVALID_ARG;
     if (a->q_offset > kMaxOffset || a->q_offset < -kMaxOffset) return RMSNORM_ERR_INVALID_ARG;
     if (!aligned(a->q_start, 4) || !aligned(a->kv_len, 4)) return RMSNORM_ERR_INVALID_ARG;
@@ -83,7 +85,7 @@ rmsnorm_status_t check_call(int32_t dtype, int64_t batch, int64_t heads, int64_t
     const rmsnorm_status_t st = check_rule(a->num_buckets, a->max_distance, a->bidirectional, &p.half);
     if (st != RMSNORM_OK) return st;
     c->sz = dtype == RMSNORM_DTYPE_F32 ? 4 : 2;
-    // batch * q_len < 2^31 and heads * k_len < 2^46: the product may pass 63 bits
+    // batch * q_len <= 2^30 and heads * k_len < 2^46: the product may pass 63 bits
     if (batch * q_len > 0 && heads * k_len > (INT64_MAX / 8) / (batch * q_len))
         return RMSNORM_ERR_INVALID_ARG;
     c->elems = batch * q_len * heads * k_len;
@@ -92,9 +94,11 @@ rmsnorm_status_t check_call(int32_t dtype, int64_t batch, int64_t heads, int64_t
         if (o.cluster || o.threads || o.grid || o.vec_bytes || o.chunk_bytes || o.stages ||
             o.weights || o.reserved || o.epilogue || o.fault_inject)
             return RMSNORM_ERR_INVALID_ARG;
-        if (o.path != RMSNORM_PATH_AUTO && o.path != RMSNORM_PATH_TWOPASS)
+        if (o.path != RMSNORM_PATH_AUTO && o.path != RMSNORM_PATH_ROWREG &&
+            o.path != RMSNORM_PATH_TWOPASS)
             return RMSNORM_ERR_INVALID_ARG;
     }
+    p.elems = c->elems;
     p.q_start = a->q_start;
     p.kv_len = a->kv_len;
     p.q_offset = a->q_offset;
@@ -111,16 +115,19 @@ rmsnorm_status_t check_call(int32_t dtype, int64_t batch, int64_t heads, int64_t
     return RMSNORM_OK;
 }
 
-// CTAs per head: whole rows, about `per_sm` CTAs per SM over all heads.
+int path(const rmsnorm_options_t* opt) { return opt ? opt->path : RMSNORM_PATH_AUTO; }
+
+// CTAs per head: at most `per_sm` CTAs per SM over all heads (one wave), at
+// most one per row block, at least one.
 int parts_per_head(const BiasCall& c, int64_t row_blocks, int64_t per_sm) {
-    int64_t n = div_up(per_sm * c.dv.sms, c.p.heads);
+    int64_t n = per_sm * c.dv.sms / c.p.heads;
     if (n > row_blocks) n = row_blocks;
     return static_cast<int>(n < 1 ? 1 : n);
 }
 
-constexpr int64_t kWideCtasPerSm = 8;
+constexpr int64_t kCtasPerSm = 8;           // at most, over all heads
 
-int wide_parts(const BiasCall& c) { return parts_per_head(c, c.p.head_rows, kWideCtasPerSm); }
+int most_parts(const BiasCall& c) { return parts_per_head(c, c.p.head_rows, kCtasPerSm); }
 
 rmsnorm_status_t launch(const BiasCall& c, BiasFn fn, const LaunchShape& s, cudaStream_t stream) {
     if (ensure_prepared(c.dv.dev, reinterpret_cast<KernelFn>(fn), c.dv.smem_optin) != cudaSuccess)
@@ -136,6 +143,55 @@ void count_vectors(BiasCall* c, uintptr_t bits) {
 int window_bytes(const BiasCall& c) {
     const int lo = static_cast<int>(c.window);
     return 4 * bias_window_slots(lo, c.p.both ? lo : 0, c.vb / c.sz);
+}
+
+// Rows in registers, if they fit and the arrays start on 16-byte boundaries:
+// the launch shape and the kernel; else leaves *fn null, status OK.
+rmsnorm_status_t plan_rowreg(int32_t dtype, BiasCall* c, uintptr_t bases, bool bwd, LaunchShape* s,
+                             BiasFn* fn) {
+    if (bases % 16 != 0) return RMSNORM_OK;
+    const int64_t epv = 16 / c->sz;
+    const bool shift = c->p.k_len % epv != 0;
+    // vectors a row touches, wherever it starts
+    const int64_t nvec = shift ? (c->p.k_len + 2 * (epv - 1)) / epv : c->p.k_len / epv;
+    int64_t group = div_up(nvec, kBiasRowBytesPerThread / 16);
+    if (group > kBiasMaxThreads) return RMSNORM_OK;
+    if (group > 32) {
+        group = div_up(group, 32) * 32;
+    } else {
+        int64_t g = 1;
+        while (g < group) g <<= 1;
+        group = g;
+    }
+    const int lo = static_cast<int>(c->window);
+    const BiasVecWindow vw = bias_vec_window(lo, c->p.both ? lo : 0, static_cast<int>(epv));
+    const int window = 4 * vw.copies * vw.copy;
+    const bool sums = bwd && c->p.part;
+    // CTAs of 256 threads; forward bf16 and backward rows of two warps and more
+    // 128.  Measured (us, 128 / 256 threads): forward bf16 rows of 2048 344 /
+    // 399, fp32 rows of 1024 89 / 83; backward bf16 rows of 2048 503 / 508,
+    // causal 422 / 444, rows of 512 (16 lanes) 106 / 75.
+    const int64_t threads = bwd ? (group >= 64 ? 128 : 256) : (c->sz == 2 ? 128 : 256);
+    int64_t rpc = group < threads ? threads / group : 1;
+    if (sums && rpc > kWindowBudget / window) rpc = kWindowBudget / window;   // a window per row group
+    if (rpc < 1) rpc = 1;
+    if (group < 32) rpc = div_up(rpc, 32 / group) * (32 / group);              // whole warps
+    const int64_t smem = bwd ? (sums ? rpc * window + 4 * vw.size : 0) : window;
+    if (smem > c->dv.smem_optin - 8192) return RMSNORM_OK;
+    const int block = static_cast<int>(rpc * group);
+    const BiasFn f = bwd ? relbias_bwd_rowreg_ptr(dtype, shift) : relbias_fwd_rowreg_ptr(dtype, shift);
+    int occ = 0;
+    if (cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(f), block,
+                         static_cast<int>(smem), 1, &occ) != cudaSuccess)
+        return RMSNORM_ERR_CUDA;
+    if (occ < 1) return RMSNORM_OK;
+    c->p.nvec = static_cast<int32_t>(nvec);
+    c->p.group = static_cast<int32_t>(group);
+    c->p.rows_per_cta = static_cast<int32_t>(rpc);
+    c->p.parts = parts_per_head(*c, div_up(c->p.head_rows, rpc), occ > kCtasPerSm ? kCtasPerSm : occ);
+    *s = LaunchShape{c->p.parts * c->p.heads, block, 1, static_cast<int>(smem)};
+    *fn = f;
+    return RMSNORM_OK;
 }
 
 rmsnorm_status_t fwd_run(int32_t dtype, const void* x, const void* table, void* y, int64_t batch,
@@ -158,15 +214,25 @@ rmsnorm_status_t fwd_run(int32_t dtype, const void* x, const void* table, void* 
     c.p.x = x;
     c.p.table = table;
     c.p.out = y;
-    count_vectors(&c, reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y));
-    c.p.parts = wide_parts(c);
-    const LaunchShape s{c.p.parts * c.p.heads, relbias_wide_block(), 1, window_bytes(c)};
-    return launch(c, relbias_fwd_wide_ptr(dtype, c.vb), s, stream);
+    const uintptr_t bases = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y);
+    LaunchShape s{0, 0, 1, 0};
+    BiasFn fn = nullptr;
+    if (path(opt) != RMSNORM_PATH_TWOPASS &&
+        plan_rowreg(dtype, &c, bases, false, &s, &fn) != RMSNORM_OK)
+        return RMSNORM_ERR_CUDA;
+    if (!fn) {
+        if (path(opt) == RMSNORM_PATH_ROWREG) return RMSNORM_ERR_UNSUPPORTED;
+        count_vectors(&c, bases);
+        c.p.parts = most_parts(c);
+        s = LaunchShape{c.p.parts * c.p.heads, relbias_wide_block(), 1, window_bytes(c)};
+        fn = relbias_fwd_wide_ptr(dtype, c.vb);
+    }
+    return launch(c, fn, s, stream);
 }
 
-// The parts never exceed wide_parts for any vector width or alignment.
+// The parts never exceed most_parts for any vector width or alignment.
 uint64_t space_needed(const BiasCall& c) {
-    return static_cast<uint64_t>(wide_parts(c)) * c.p.heads * c.p.num_buckets * 8;
+    return static_cast<uint64_t>(most_parts(c)) * c.p.heads * c.p.num_buckets * 8;
 }
 
 rmsnorm_status_t bwd_run(int32_t dtype, const void* dy, const void* y, void* dx, float* dtable,
@@ -202,12 +268,23 @@ rmsnorm_status_t bwd_run(int32_t dtype, const void* dy, const void* y, void* dx,
     c.p.out = dx;
     c.p.part = dtable ? static_cast<double*>(workspace) : nullptr;
     c.p.dtable = dtable;
-    count_vectors(&c, s[0].p | s[1].p | s[4].p);
-    c.p.parts = wide_parts(c);
-    const LaunchShape ls{c.p.parts * c.p.heads, relbias_wide_block(), 1, window_bytes(c)};
-    st = launch(c, relbias_bwd_wide_ptr(dtype, c.vb), ls, stream);
+    const uintptr_t bases = s[0].p | s[1].p | s[4].p;
+    LaunchShape ls{0, 0, 1, 0};
+    BiasFn fn = nullptr;
+    if (path(opt) != RMSNORM_PATH_TWOPASS &&
+        plan_rowreg(dtype, &c, bases, true, &ls, &fn) != RMSNORM_OK)
+        return RMSNORM_ERR_CUDA;
+    if (!fn) {
+        if (path(opt) == RMSNORM_PATH_ROWREG) return RMSNORM_ERR_UNSUPPORTED;
+        count_vectors(&c, bases);
+        c.p.parts = most_parts(c);
+        ls = LaunchShape{c.p.parts * c.p.heads, relbias_wide_block(), 1, window_bytes(c)};
+        fn = relbias_bwd_wide_ptr(dtype, c.vb);
+    }
+    st = launch(c, fn, ls, stream);
     if (st != RMSNORM_OK || !dtable) return st;
-    const LaunchShape rs{c.p.heads, relbias_reduce_block(), 1, 0};
+    LaunchShape rs{c.p.heads, relbias_reduce_block(), 1, 0};
+    rs.grid_y = static_cast<int>(div_up(32ll * c.p.num_buckets, relbias_reduce_block()));
     return launch(c, relbias_reduce_ptr(), rs, stream);
 }
 

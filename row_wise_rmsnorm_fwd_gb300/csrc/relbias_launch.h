@@ -19,6 +19,7 @@ struct BiasParams {
     const int32_t* q_start; // [batch] or null
     const int32_t* kv_len;  // [batch] or null
     int64_t q_offset;
+    int64_t elems;          // of x, y and out
     float scale;
     int32_t head_rows;      // rows of one head: batch * q_len
     int32_t q_len;
@@ -44,9 +45,30 @@ constexpr int bias_window_slots(int lo, int hi, int epv) {
     return n + (epv > 1 ? n / epv : 0) + 1;
 }
 
+// The same for the register kernels' window: `copies` shifted copies of it in
+// chunks that a vector load takes (see k_relbias.cuh).
+struct BiasVecWindow {
+    int size, copies, half, copy;      // positions, copies, chunks of a half, floats of a copy
+};
+constexpr BiasVecWindow bias_vec_window(int lo, int hi, int epv) {
+    BiasVecWindow w{};
+    w.size = lo + hi + 4 * epv;
+    w.copies = epv < 4 ? epv : 4;
+    const int chunks = w.size / w.copies + 1;
+    w.half = (chunks + 1) / 2;
+    w.copy = (epv == 8 ? 2 * w.half : chunks) * w.copies;
+    return w;
+}
+
 BiasFn relbias_fwd_wide_ptr(int dtype, int vb);
 BiasFn relbias_bwd_wide_ptr(int dtype, int vb);
 int relbias_wide_block();
+// Rows in registers: 64 bytes per thread, blocks of up to kBiasMaxThreads
+// threads; shift: rows that are not a multiple of 16 bytes.
+BiasFn relbias_fwd_rowreg_ptr(int dtype, bool shift);
+BiasFn relbias_bwd_rowreg_ptr(int dtype, bool shift);
+constexpr int kBiasMaxThreads = 512;
+constexpr int kBiasRowBytesPerThread = 64;
 BiasFn relbias_reduce_ptr();
 int relbias_reduce_block();
 

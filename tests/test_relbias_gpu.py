@@ -148,6 +148,28 @@ def test_a_nan_stays_in_its_row(options):
     assert not dt[:, [0, 1, 3]].isnan().any()
 
 
+@pytest.mark.parametrize("options", PATHS, ids=["auto", "twopass"])
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ["padded", "causal", "decode"])
+def test_masked_keys_are_zero_in_a_nan_row(name, t, options):
+    """A NaN at a row's first valid key leaves the masked keys' outputs zero,
+    and the buckets that only masked keys would have reached clean."""
+    x, table, dy, rule = tensors(name, t, 35)
+    shape, _ = CASES[name]
+    which, valid = rule.places(shape[0], shape[2], shape[3])
+    y = probabilities(x, table, rule)
+    x[..., 0] = dy[..., 0] = float("nan")
+    kw = rule.kwargs()
+    out = binding.rowsoftmax_relbias_fwd_ex(x.cuda(), table.cuda(), options=options, **kw).cpu()
+    dx, dt = binding.rowsoftmax_relbias_bwd_ex(dy.cuda(), y.cuda(), 32, options=options, **kw)
+    masked = ~valid[:, None].expand(shape)
+    assert (out[masked] == 0).all() and (dx.cpu()[masked] == 0).all()
+    assert out[~masked].isnan().all()
+    reached = {int(b) for b in which[valid]}
+    for k in range(32):
+        assert dt[k].isnan().any().item() == (k in reached)
+
+
 @pytest.mark.parametrize("t", ["f32", "bf16"])
 @pytest.mark.parametrize("name", ["odd", "square", "longer", "padded"])
 @pytest.mark.parametrize("shift", [1, 4])
