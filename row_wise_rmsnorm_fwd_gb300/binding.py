@@ -12,6 +12,7 @@ no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -146,6 +147,8 @@ def open_library(path: str):
 def load():
     """Load librmsnorm.so (built in-tree by ``build.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             _lib = open_library(library_path())
@@ -419,19 +422,49 @@ def rowsoftmax_plan(x, y=None, options=None) -> dict:
 # These functions work on the device of their tensors and on that device's
 # current stream (or `stream`).  What they allocate -- outputs that are not
 # given, workspaces -- is allocated on the stream the kernels run on, so the
-# caching allocator hands none of it out again before they are done.
+# caching allocator hands none of it out again before they are done.  Small
+# calls are bound by the host, so the checks are a few comparisons each and the
+# common case (this device, its current stream) enters no context.
 
-def _dtype_code(x):
+_T = None             # torch, once it is imported
+_CODES = {}           # torch dtype -> dtype code
+_raw_stream = None    # device index -> handle of its current stream
+_current_device = None
+
+
+def _warm():
+    """Import torch once, and what every call looks up."""
+    global _T, _raw_stream, _current_device
     torch = _torch()
-    if x.dtype == torch.float32:
-        return RMSNORM_DTYPE_F32
-    if x.dtype == torch.bfloat16:
-        return RMSNORM_DTYPE_BF16
-    raise TypeError(f"expected float32 or bfloat16, got {x.dtype}")
+    _CODES.update({torch.float32: RMSNORM_DTYPE_F32, torch.bfloat16: RMSNORM_DTYPE_BF16})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = torch.cuda.current_device
+    _T = torch
+    return torch
 
 
-def _require(name, t, dtype, shape, device):
-    """Refuse a tensor of another type, shape, layout or device."""
+def _code(x, want):
+    """The dtype code of x, which must be `want` (None: either)."""
+    code = _CODES.get(x.dtype)
+    if code is None or (want is not None and code != want):
+        names = {None: "float32 or bfloat16", 0: "float32", 1: "bfloat16"}
+        raise TypeError(f"expected {names[want]}, got {x.dtype}")
+    return code
+
+
+def _input(x):
+    """Refuse an x without a last dim, off the GPU or not contiguous."""
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise ValueError("x must have a non-empty last dim")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+
+
+def _require(name, t, dtype, shape, index):
+    """Refuse `t` unless it is a contiguous tensor of this type, shape and device."""
     if t is None:
         raise ValueError(f"{name} is missing")
     if t.dtype != dtype:
@@ -440,33 +473,27 @@ def _require(name, t, dtype, shape, device):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on device cuda:{index}, got {t.device}")
 
 
-def _on_stream(device, stream, body):
-    """body(stream handle) with `device` current and its allocations on the stream."""
-    torch = _torch()
-    if stream is None and device.index == torch.cuda.current_device():
-        return body(torch.cuda.current_stream().cuda_stream)
+def _elsewhere(index, stream, body, *args):
+    """body(handle, *args) of a call on another device or stream than the
+    current ones: with those current, so that its allocations are theirs."""
+    torch = _T
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        stream = torch.cuda.current_stream(index)
     elif isinstance(stream, int):
-        stream = (torch.cuda.ExternalStream(stream, device) if stream
-                  else torch.cuda.default_stream(device))
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        stream = (torch.cuda.ExternalStream(stream, index) if stream
+                  else torch.cuda.default_stream(index))
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
     with torch.cuda.stream(stream):
-        return body(stream.cuda_stream)
+        return body(stream.cuda_stream, *args)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
-
-
-def _check(st, what):
-    if st != RMSNORM_OK:
-        raise RmsnormError(st, what)
 
 
 def _opt(options):
@@ -475,50 +502,68 @@ def _opt(options):
     return ctypes.byref(make_options(**options) if isinstance(options, dict) else options)
 
 
-def _rows_of(x):
-    """(rows, hidden) of a contiguous CUDA tensor with a last dim."""
-    if x.dim() == 0 or x.shape[-1] == 0:
-        raise ValueError("x must have a non-empty last dim")
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    if not x.is_contiguous():
-        raise ValueError("x must be contiguous")
-    hidden = x.shape[-1]
-    return x.numel() // hidden, hidden
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace(name, code, rows, hidden, index):
+    """Bytes of workspace (with device `index` current)."""
+    size = ctypes.c_size_t()
+    st = getattr(load(), name)(code, rows, hidden, ctypes.byref(size))
+    if st != RMSNORM_OK:
+        raise RmsnormError(st, name)
+    return size.value
 
 
-def _workspace(workspace, size, device):
+def _room(workspace, size, x):
     """The caller's workspace checked, or a new one: (tensor, bytes)."""
     if workspace is None:
-        return _torch().empty(size, dtype=_torch().uint8, device=device), size
-    if not workspace.is_contiguous() or workspace.device != device:
-        raise ValueError(f"workspace must be contiguous, on {device}")
+        return _T.empty(size, dtype=_T.uint8, device=x.device), size
+    if not workspace.is_contiguous() or workspace.get_device() != x.get_device():
+        raise ValueError(f"workspace must be contiguous, on {x.device}")
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _layernorm_fwd(name, x, w, b, y, mean, rstd, eps, stats, options, stream):
-    torch = _torch()
-    dt = _dtype_code(x)
-    rows, hidden = _rows_of(x)
-    device, lead = x.device, x.shape[:-1]
-    for n, t, d, shape in (("w", w, x.dtype, (hidden,)), ("b", b, x.dtype, (hidden,)),
-                           ("y", y, x.dtype, x.shape), ("mean", mean, torch.float32, lead),
-                           ("rstd", rstd, torch.float32, lead)):
-        if t is not None:
-            _require(n, t, d, shape, device)
+def _layernorm_fwd(name, want, x, w, b, y, mean, rstd, eps, stats, options, stream):
+    torch = _T or _warm()
+    code = _code(x, want)
+    dt, shape, index = x.dtype, x.shape, x.get_device()
+    if index < 0 or not shape or not shape[-1] or not x.is_contiguous():
+        _input(x)
+    hidden = shape[-1]
+    if w is not None:
+        _require("w", w, dt, (hidden,), index)
+    if b is not None:
+        _require("b", b, dt, (hidden,), index)
+    if y is not None:
+        _require("y", y, dt, shape, index)
+    if mean is not None:
+        _require("mean", mean, torch.float32, shape[:-1], index)
+    if rstd is not None:
+        _require("rstd", rstd, torch.float32, shape[:-1], index)
+    if stream is None and index == _current_device():
+        return _layernorm_fwd_on(_raw_stream(index), name, code, x, w, b, y, mean, rstd, eps,
+                                 stats, options, hidden)
+    return _elsewhere(index, stream, _layernorm_fwd_on, name, code, x, w, b, y, mean, rstd, eps,
+                      stats, options, hidden)
 
-    def body(handle):
-        out = torch.empty_like(x) if y is None else y
-        m, r = mean, rstd
-        if stats:
-            m = torch.empty(lead, dtype=torch.float32, device=device) if m is None else m
-            r = torch.empty(lead, dtype=torch.float32, device=device) if r is None else r
-        if rows:
-            _check(load().layernorm_fwd_ex(dt, x.data_ptr(), _ptr(w), _ptr(b), out.data_ptr(),
-                                           _ptr(m), _ptr(r), rows, hidden, eps, _opt(options),
-                                           handle or None), name)
-        return (out, m, r) if stats else out
-    return _on_stream(device, stream, body)
+
+def _layernorm_fwd_on(handle, name, code, x, w, b, y, mean, rstd, eps, stats, options, hidden):
+    if y is None:
+        y = _T.empty_like(x)
+    if stats:
+        if mean is None:
+            mean = _T.empty(x.shape[:-1], dtype=_T.float32, device=x.device)
+        if rstd is None:
+            rstd = _T.empty_like(mean)
+    rows = x.numel() // hidden
+    if rows:
+        st = (_lib or load()).layernorm_fwd_ex(
+            code, x.data_ptr(), w.data_ptr() if w is not None else None,
+            b.data_ptr() if b is not None else None, y.data_ptr(),
+            mean.data_ptr() if mean is not None else None,
+            rstd.data_ptr() if rstd is not None else None, rows, hidden, eps,
+            _opt(options) if options is not None else None, handle)
+        if st:
+            raise RmsnormError(st, name)
+    return (y, mean, rstd) if stats else y
 
 
 def layernorm_fwd_f32(x, w=None, b=None, y=None, mean=None, rstd=None, eps: float = 1e-5,
@@ -526,73 +571,82 @@ def layernorm_fwd_f32(x, w=None, b=None, y=None, mean=None, rstd=None, eps: floa
     """y = LayerNorm(x) * w + b for float32 CUDA tensors (last dim = hidden).
     w and b may be None (ones, zeros); mean and rstd (float32, x.shape[:-1])
     are written if given.  stats=True returns (y, mean, rstd)."""
-    _want(x, RMSNORM_DTYPE_F32)
-    return _layernorm_fwd("layernorm_fwd_f32", x, w, b, y, mean, rstd, eps, stats, None, stream)
+    return _layernorm_fwd("layernorm_fwd_f32", RMSNORM_DTYPE_F32, x, w, b, y, mean, rstd, eps,
+                          stats, None, stream)
 
 
 def layernorm_fwd_bf16(x, w=None, b=None, y=None, mean=None, rstd=None, eps: float = 1e-5,
                        stats: bool = False, stream=None):
     """The same for bfloat16 CUDA tensors (fp32 arithmetic)."""
-    _want(x, RMSNORM_DTYPE_BF16)
-    return _layernorm_fwd("layernorm_fwd_bf16", x, w, b, y, mean, rstd, eps, stats, None, stream)
+    return _layernorm_fwd("layernorm_fwd_bf16", RMSNORM_DTYPE_BF16, x, w, b, y, mean, rstd, eps,
+                          stats, None, stream)
 
 
 def layernorm_fwd_ex(x, w=None, b=None, y=None, mean=None, rstd=None, eps: float = 1e-5,
                      stats: bool = False, options=None, stream=None):
     """Either dtype, with options (path auto, staged or twopass)."""
-    return _layernorm_fwd("layernorm_fwd_ex", x, w, b, y, mean, rstd, eps, stats, options, stream)
+    return _layernorm_fwd("layernorm_fwd_ex", None, x, w, b, y, mean, rstd, eps, stats, options,
+                          stream)
 
 
-def _want(x, dtype):
-    if _dtype_code(x) != dtype:
-        raise TypeError(f"this entry point takes {'float32' if dtype == 0 else 'bfloat16'}, "
-                        f"got {x.dtype}")
-
-
-def _norm_bwd(name, layer, dy, x, w, mean, rstd, dx, dw, db, eps, weight_grads, workspace,
+def _norm_bwd(name, want, layer, dy, x, w, mean, rstd, dx, dw, db, eps, weight_grads, workspace,
               options, stream):
-    torch = _torch()
-    lib = load()
-    dt = _dtype_code(x)
-    rows, hidden = _rows_of(x)
-    device, lead = x.device, x.shape[:-1]
-    _require("dy", dy, x.dtype, x.shape, device)
+    torch = _T or _warm()
+    code = _code(x, want)
+    dt, shape, index = x.dtype, x.shape, x.get_device()
+    if index < 0 or not shape or not shape[-1] or not x.is_contiguous():
+        _input(x)
+    hidden, f32 = shape[-1], torch.float32
+    _require("dy", dy, dt, shape, index)
     if layer:
-        _require("mean", mean, torch.float32, lead, device)
-        _require("rstd", rstd, torch.float32, lead, device)
-    for n, t, d, shape in (("w", w, x.dtype, (hidden,)), ("dx", dx, x.dtype, x.shape),
-                           ("dw", dw, torch.float32, (hidden,)),
-                           ("db", db, torch.float32, (hidden,))):
-        if t is not None:
-            _require(n, t, d, shape, device)
+        _require("mean", mean, f32, shape[:-1], index)
+        _require("rstd", rstd, f32, shape[:-1], index)
+    if w is not None:
+        _require("w", w, dt, (hidden,), index)
+    if dx is not None:
+        _require("dx", dx, dt, shape, index)
+    if dw is not None:
+        _require("dw", dw, f32, (hidden,), index)
+    if db is not None:
+        _require("db", db, f32, (hidden,), index)
+    args = (name, code, layer, dy, x, w, mean, rstd, dx, dw, db, eps, weight_grads, workspace,
+            options, hidden, index)
+    if stream is None and index == _current_device():
+        return _norm_bwd_on(_raw_stream(index), *args)
+    return _elsewhere(index, stream, _norm_bwd_on, *args)
 
-    def body(handle):
-        out = torch.empty_like(x) if dx is None else dx
-        gw, gb = dw, db
-        if weight_grads:
-            gw = torch.empty(hidden, dtype=torch.float32, device=device) if gw is None else gw
-            if layer and gb is None:
-                gb = torch.empty(hidden, dtype=torch.float32, device=device)
-        if rows == 0:
-            for t in (gw, gb):
-                if t is not None:
-                    t.zero_()
-            return (out, gw, gb) if layer else (out, gw)
-        size = ctypes.c_size_t()
-        query = lib.layernorm_bwd_workspace if layer else lib.rmsnorm_bwd_workspace
-        _check(query(dt, rows, hidden, ctypes.byref(size)), name)
-        ws, n = _workspace(workspace, size.value, device)
-        if layer:
-            st = lib.layernorm_bwd_ex(dt, dy.data_ptr(), x.data_ptr(), _ptr(w), mean.data_ptr(),
-                                      rstd.data_ptr(), out.data_ptr(), _ptr(gw), _ptr(gb), rows,
-                                      hidden, ws.data_ptr(), n, _opt(options), handle or None)
-        else:
-            st = lib.rmsnorm_bwd_ex(dt, dy.data_ptr(), x.data_ptr(), _ptr(w), out.data_ptr(),
-                                    _ptr(gw), rows, hidden, eps, ws.data_ptr(), n, _opt(options),
-                                    handle or None)
-        _check(st, name)
-        return (out, gw, gb) if layer else (out, gw)
-    return _on_stream(device, stream, body)
+
+def _norm_bwd_on(handle, name, code, layer, dy, x, w, mean, rstd, dx, dw, db, eps, weight_grads,
+                 workspace, options, hidden, index):
+    if dx is None:
+        dx = _T.empty_like(x)
+    if weight_grads:
+        if dw is None:
+            dw = _T.empty(hidden, dtype=_T.float32, device=x.device)
+        if layer and db is None:
+            db = _T.empty_like(dw)
+    rows = x.numel() // hidden
+    if rows == 0:
+        for t in (dw, db):
+            if t is not None:
+                t.zero_()
+        return (dx, dw, db) if layer else (dx, dw)
+    lib = _lib or load()
+    opt = _opt(options) if options is not None else None
+    if layer:
+        ws, n = _room(workspace, _norm_workspace("layernorm_bwd_workspace", code, rows, hidden,
+                                                 index), x)
+        st = lib.layernorm_bwd_ex(code, dy.data_ptr(), x.data_ptr(), _ptr(w), mean.data_ptr(),
+                                  rstd.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db), rows,
+                                  hidden, ws.data_ptr(), n, opt, handle)
+    else:
+        ws, n = _room(workspace, _norm_workspace("rmsnorm_bwd_workspace", code, rows, hidden,
+                                                 index), x)
+        st = lib.rmsnorm_bwd_ex(code, dy.data_ptr(), x.data_ptr(), _ptr(w), dx.data_ptr(),
+                                _ptr(dw), rows, hidden, eps, ws.data_ptr(), n, opt, handle)
+    if st:
+        raise RmsnormError(st, name)
+    return (dx, dw, db) if layer else (dx, dw)
 
 
 def layernorm_bwd_f32(dy, x, w, mean, rstd, dx=None, dw=None, db=None, weight_grads: bool = True,
@@ -601,23 +655,21 @@ def layernorm_bwd_f32(dy, x, w, mean, rstd, dx=None, dw=None, db=None, weight_gr
     the forward pass, w may be None (ones).  dw and db are float32;
     weight_grads=False computes only those given.  workspace: at least
     layernorm_bwd_workspace(x) bytes, else one is allocated."""
-    _want(x, RMSNORM_DTYPE_F32)
-    return _norm_bwd("layernorm_bwd_f32", True, dy, x, w, mean, rstd, dx, dw, db, 0.0,
-                     weight_grads, workspace, None, stream)
+    return _norm_bwd("layernorm_bwd_f32", RMSNORM_DTYPE_F32, True, dy, x, w, mean, rstd, dx, dw,
+                     db, 0.0, weight_grads, workspace, None, stream)
 
 
 def layernorm_bwd_bf16(dy, x, w, mean, rstd, dx=None, dw=None, db=None, weight_grads: bool = True,
                        workspace=None, stream=None):
     """The same for bfloat16 dy, x, w and dx (dw and db are float32)."""
-    _want(x, RMSNORM_DTYPE_BF16)
-    return _norm_bwd("layernorm_bwd_bf16", True, dy, x, w, mean, rstd, dx, dw, db, 0.0,
-                     weight_grads, workspace, None, stream)
+    return _norm_bwd("layernorm_bwd_bf16", RMSNORM_DTYPE_BF16, True, dy, x, w, mean, rstd, dx, dw,
+                     db, 0.0, weight_grads, workspace, None, stream)
 
 
 def layernorm_bwd_ex(dy, x, w, mean, rstd, dx=None, dw=None, db=None, weight_grads: bool = True,
                      workspace=None, options=None, stream=None):
     """Either dtype, with options (path auto, staged or twopass)."""
-    return _norm_bwd("layernorm_bwd_ex", True, dy, x, w, mean, rstd, dx, dw, db, 0.0,
+    return _norm_bwd("layernorm_bwd_ex", None, True, dy, x, w, mean, rstd, dx, dw, db, 0.0,
                      weight_grads, workspace, options, stream)
 
 
@@ -626,32 +678,30 @@ def rmsnorm_bwd_f32(dy, x, w, dx=None, dw=None, eps: float = 1e-6, weight_grads:
     """(dx, dw) of RMSNorm for float32 CUDA tensors; w may be None (ones).
     dw is float32; weight_grads=False computes it only if given.  workspace:
     at least rmsnorm_bwd_workspace(x) bytes, else one is allocated."""
-    _want(x, RMSNORM_DTYPE_F32)
-    return _norm_bwd("rmsnorm_bwd_f32", False, dy, x, w, None, None, dx, dw, None, eps,
-                     weight_grads, workspace, None, stream)
+    return _norm_bwd("rmsnorm_bwd_f32", RMSNORM_DTYPE_F32, False, dy, x, w, None, None, dx, dw,
+                     None, eps, weight_grads, workspace, None, stream)
 
 
 def rmsnorm_bwd_bf16(dy, x, w, dx=None, dw=None, eps: float = 1e-6, weight_grads: bool = True,
                      workspace=None, stream=None):
     """The same for bfloat16 dy, x, w and dx (dw is float32)."""
-    _want(x, RMSNORM_DTYPE_BF16)
-    return _norm_bwd("rmsnorm_bwd_bf16", False, dy, x, w, None, None, dx, dw, None, eps,
-                     weight_grads, workspace, None, stream)
+    return _norm_bwd("rmsnorm_bwd_bf16", RMSNORM_DTYPE_BF16, False, dy, x, w, None, None, dx, dw,
+                     None, eps, weight_grads, workspace, None, stream)
 
 
 def rmsnorm_bwd_ex(dy, x, w, dx=None, dw=None, eps: float = 1e-6, weight_grads: bool = True,
                    workspace=None, options=None, stream=None):
     """Either dtype, with options (path auto, staged or twopass)."""
-    return _norm_bwd("rmsnorm_bwd_ex", False, dy, x, w, None, None, dx, dw, None, eps,
+    return _norm_bwd("rmsnorm_bwd_ex", None, False, dy, x, w, None, None, dx, dw, None, eps,
                      weight_grads, workspace, options, stream)
 
 
 def _bwd_workspace(name, x):
-    rows, hidden = _rows_of(x)
-    size = ctypes.c_size_t()
-    with _torch().cuda.device(x.device):
-        _check(getattr(load(), name)(_dtype_code(x), rows, hidden, ctypes.byref(size)), name)
-    return size.value
+    torch = _T or _warm()
+    _input(x)
+    hidden, index = x.shape[-1], x.get_device()
+    with torch.cuda.device(index):
+        return _norm_workspace(name, _code(x, None), x.numel() // hidden, hidden, index)
 
 
 def layernorm_bwd_workspace(x) -> int:
@@ -666,39 +716,46 @@ def rmsnorm_bwd_workspace(x) -> int:
 
 # ------------------------------ row softmax with a relative position bias --
 
-def _relbias(x, num_buckets, max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len):
-    if x.dim() != 4 or not x.is_cuda or not x.is_contiguous():
+def _relbias(x, index, num_buckets, max_distance, bidirectional, causal, scale, q_offset, q_start,
+             kv_len):
+    if index < 0 or x.dim() != 4 or not x.is_contiguous():
         raise ValueError("scores must be a contiguous CUDA tensor [batch, heads, queries, keys]")
-    for n, t in (("q_start", q_start), ("kv_len", kv_len)):
-        if t is not None:
-            _require(n, t, _torch().int32, x.shape[:1], x.device)
+    if q_start is not None:
+        _require("q_start", q_start, _T.int32, x.shape[:1], index)
+    if kv_len is not None:
+        _require("kv_len", kv_len, _T.int32, x.shape[:1], index)
     return rowsoftmax_relbias_t(num_buckets, max_distance, bool(bidirectional), bool(causal),
                                 scale, 0, q_offset, _ptr(q_start), _ptr(kv_len))
 
 
-def _relbias_fwd(name, x, table, y, rule, options, stream):
-    torch = _torch()
-    dt = _dtype_code(x)
+def _relbias_fwd(name, want, x, table, y, max_distance, bidirectional, causal, scale, q_offset,
+                 q_start, kv_len, options, stream):
+    if _T is None:
+        _warm()
+    code = _code(x, want)
     if table.dim() != 2:
         raise ValueError("table must have shape (num_buckets, heads)")
-    a = _relbias(x, table.shape[0], **rule)
-    _require("table", table, x.dtype, (table.shape[0], x.shape[1]), x.device)
+    num_buckets, index = table.shape[0], x.get_device()
+    a = _relbias(x, index, num_buckets, max_distance, bidirectional, causal, scale, q_offset,
+                 q_start, kv_len)
+    _require("table", table, x.dtype, (num_buckets, x.shape[1]), index)
     if y is not None:
-        _require("y", y, x.dtype, x.shape, x.device)
-
-    def body(handle):
-        out = torch.empty_like(x) if y is None else y
-        if x.numel():
-            _check(load().rowsoftmax_relbias_fwd_ex(dt, x.data_ptr(), table.data_ptr(),
-                                                    out.data_ptr(), *x.shape, ctypes.byref(a),
-                                                    _opt(options), handle or None), name)
-        return out
-    return _on_stream(x.device, stream, body)
+        _require("y", y, x.dtype, x.shape, index)
+    if stream is None and index == _current_device():
+        return _relbias_fwd_on(_raw_stream(index), name, code, x, table, y, a, options)
+    return _elsewhere(index, stream, _relbias_fwd_on, name, code, x, table, y, a, options)
 
 
-def _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len):
-    return dict(max_distance=max_distance, bidirectional=bidirectional, causal=causal,
-                scale=scale, q_offset=q_offset, q_start=q_start, kv_len=kv_len)
+def _relbias_fwd_on(handle, name, code, x, table, y, a, options):
+    if y is None:
+        y = _T.empty_like(x)
+    if x.numel():
+        st = (_lib or load()).rowsoftmax_relbias_fwd_ex(
+            code, x.data_ptr(), table.data_ptr(), y.data_ptr(), *x.shape, ctypes.byref(a),
+            _opt(options) if options is not None else None, handle)
+        if st:
+            raise RmsnormError(st, name)
+    return y
 
 
 def rowsoftmax_relbias_fwd_f32(x, table, y=None, *, max_distance: int = 128,
@@ -710,9 +767,9 @@ def rowsoftmax_relbias_fwd_f32(x, table, y=None, *, max_distance: int = 128,
     [num_buckets, heads].  Query i of sequence b stands at q_offset +
     q_start[b] + i; keys from kv_len[b] on, and with `causal` keys after the
     query, are masked (0).  q_start and kv_len: int32 [batch]."""
-    _want(x, RMSNORM_DTYPE_F32)
-    rule = _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len)
-    return _relbias_fwd("rowsoftmax_relbias_fwd_f32", x, table, y, rule, None, stream)
+    return _relbias_fwd("rowsoftmax_relbias_fwd_f32", RMSNORM_DTYPE_F32, x, table, y,
+                        max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len,
+                        None, stream)
 
 
 def rowsoftmax_relbias_fwd_bf16(x, table, y=None, *, max_distance: int = 128,
@@ -720,9 +777,9 @@ def rowsoftmax_relbias_fwd_bf16(x, table, y=None, *, max_distance: int = 128,
                                 scale: float = 1.0, q_offset: int = 0, q_start=None, kv_len=None,
                                 stream=None):
     """The same for bfloat16 scores and table (fp32 arithmetic)."""
-    _want(x, RMSNORM_DTYPE_BF16)
-    rule = _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len)
-    return _relbias_fwd("rowsoftmax_relbias_fwd_bf16", x, table, y, rule, None, stream)
+    return _relbias_fwd("rowsoftmax_relbias_fwd_bf16", RMSNORM_DTYPE_BF16, x, table, y,
+                        max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len,
+                        None, stream)
 
 
 def rowsoftmax_relbias_fwd_ex(x, table, y=None, *, max_distance: int = 128,
@@ -730,41 +787,51 @@ def rowsoftmax_relbias_fwd_ex(x, table, y=None, *, max_distance: int = 128,
                               scale: float = 1.0, q_offset: int = 0, q_start=None, kv_len=None,
                               options=None, stream=None):
     """Either dtype, with options (path auto, rowreg or twopass)."""
-    rule = _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len)
-    return _relbias_fwd("rowsoftmax_relbias_fwd_ex", x, table, y, rule, options, stream)
+    return _relbias_fwd("rowsoftmax_relbias_fwd_ex", None, x, table, y, max_distance,
+                        bidirectional, causal, scale, q_offset, q_start, kv_len, options, stream)
 
 
-def _relbias_bwd(name, dy, y, num_buckets, dx, dtable, table_grad, workspace, rule, options,
-                 stream):
-    torch = _torch()
-    lib = load()
-    dt = _dtype_code(y)
-    a = _relbias(y, num_buckets, **rule)
-    shape = (num_buckets, y.shape[1])
-    _require("dy", dy, y.dtype, y.shape, y.device)
+def _relbias_bwd(name, want, dy, y, num_buckets, dx, dtable, table_grad, workspace, max_distance,
+                 bidirectional, causal, scale, q_offset, q_start, kv_len, options, stream):
+    if _T is None:
+        _warm()
+    code, index = _code(y, want), y.get_device()
+    a = _relbias(y, index, num_buckets, max_distance, bidirectional, causal, scale, q_offset,
+                 q_start, kv_len)
+    _require("dy", dy, y.dtype, y.shape, index)
     if dx is not None:
-        _require("dx", dx, y.dtype, y.shape, y.device)
+        _require("dx", dx, y.dtype, y.shape, index)
     if dtable is not None:
-        _require("dtable", dtable, torch.float32, shape, y.device)
+        _require("dtable", dtable, _T.float32, (num_buckets, y.shape[1]), index)
+    args = (name, code, dy, y, num_buckets, dx, dtable, table_grad, workspace, a, options)
+    if stream is None and index == _current_device():
+        return _relbias_bwd_on(_raw_stream(index), *args)
+    return _elsewhere(index, stream, _relbias_bwd_on, *args)
 
-    def body(handle):
-        out = torch.empty_like(y) if dx is None else dx
-        gt = dtable
-        if gt is None and table_grad:
-            gt = torch.empty(shape, dtype=torch.float32, device=y.device)
-        if y.numel() == 0:
-            return out, gt if gt is None else gt.zero_()
-        ws, n = None, 0
-        if gt is not None:
-            size = ctypes.c_size_t()
-            _check(lib.rowsoftmax_relbias_bwd_workspace(dt, *y.shape, ctypes.byref(a),
-                                                        ctypes.byref(size)), name)
-            ws, n = _workspace(workspace, size.value, y.device)
-        _check(lib.rowsoftmax_relbias_bwd_ex(dt, dy.data_ptr(), y.data_ptr(), out.data_ptr(),
-                                             _ptr(gt), *y.shape, ctypes.byref(a), _ptr(ws), n,
-                                             _opt(options), handle or None), name)
-        return out, gt
-    return _on_stream(y.device, stream, body)
+
+def _relbias_bwd_on(handle, name, code, dy, y, num_buckets, dx, dtable, table_grad, workspace, a,
+                    options):
+    if dx is None:
+        dx = _T.empty_like(y)
+    shape = y.shape
+    if dtable is None and table_grad:
+        dtable = _T.empty((num_buckets, shape[1]), dtype=_T.float32, device=y.device)
+    if y.numel() == 0:
+        return dx, dtable if dtable is None else dtable.zero_()
+    lib = _lib or load()
+    ws, n, rule = None, 0, ctypes.byref(a)
+    if dtable is not None:
+        size = ctypes.c_size_t()
+        st = lib.rowsoftmax_relbias_bwd_workspace(code, *shape, rule, ctypes.byref(size))
+        if st:
+            raise RmsnormError(st, name)
+        ws, n = _room(workspace, size.value, y)
+    st = lib.rowsoftmax_relbias_bwd_ex(code, dy.data_ptr(), y.data_ptr(), dx.data_ptr(),
+                                       _ptr(dtable), *shape, rule, _ptr(ws), n,
+                                       _opt(options) if options is not None else None, handle)
+    if st:
+        raise RmsnormError(st, name)
+    return dx, dtable
 
 
 def rowsoftmax_relbias_bwd_f32(dy, y, num_buckets, dx=None, dtable=None, *,
@@ -777,10 +844,9 @@ def rowsoftmax_relbias_bwd_f32(dy, y, num_buckets, dx=None, dtable=None, *,
     [num_buckets, heads]; table_grad=False computes it only if given.
     workspace: at least rowsoftmax_relbias_bwd_workspace(...) bytes, else one
     is allocated."""
-    _want(y, RMSNORM_DTYPE_F32)
-    rule = _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len)
-    return _relbias_bwd("rowsoftmax_relbias_bwd_f32", dy, y, num_buckets, dx, dtable, table_grad,
-                        workspace, rule, None, stream)
+    return _relbias_bwd("rowsoftmax_relbias_bwd_f32", RMSNORM_DTYPE_F32, dy, y, num_buckets, dx,
+                        dtable, table_grad, workspace, max_distance, bidirectional, causal,
+                        scale, q_offset, q_start, kv_len, None, stream)
 
 
 def rowsoftmax_relbias_bwd_bf16(dy, y, num_buckets, dx=None, dtable=None, *,
@@ -789,10 +855,9 @@ def rowsoftmax_relbias_bwd_bf16(dy, y, num_buckets, dx=None, dtable=None, *,
                                 q_start=None, kv_len=None, table_grad: bool = True, workspace=None,
                                 stream=None):
     """The same for bfloat16 dy, y and dx (dtable is float32)."""
-    _want(y, RMSNORM_DTYPE_BF16)
-    rule = _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len)
-    return _relbias_bwd("rowsoftmax_relbias_bwd_bf16", dy, y, num_buckets, dx, dtable, table_grad,
-                        workspace, rule, None, stream)
+    return _relbias_bwd("rowsoftmax_relbias_bwd_bf16", RMSNORM_DTYPE_BF16, dy, y, num_buckets, dx,
+                        dtable, table_grad, workspace, max_distance, bidirectional, causal,
+                        scale, q_offset, q_start, kv_len, None, stream)
 
 
 def rowsoftmax_relbias_bwd_ex(dy, y, num_buckets, dx=None, dtable=None, *,
@@ -801,20 +866,22 @@ def rowsoftmax_relbias_bwd_ex(dy, y, num_buckets, dx=None, dtable=None, *,
                               q_start=None, kv_len=None, table_grad: bool = True, workspace=None,
                               options=None, stream=None):
     """Either dtype, with options (path auto, rowreg or twopass)."""
-    rule = _rule(max_distance, bidirectional, causal, scale, q_offset, q_start, kv_len)
-    return _relbias_bwd("rowsoftmax_relbias_bwd_ex", dy, y, num_buckets, dx, dtable, table_grad,
-                        workspace, rule, options, stream)
+    return _relbias_bwd("rowsoftmax_relbias_bwd_ex", None, dy, y, num_buckets, dx, dtable,
+                        table_grad, workspace, max_distance, bidirectional, causal, scale,
+                        q_offset, q_start, kv_len, options, stream)
 
 
 def rowsoftmax_relbias_bwd_workspace(y, num_buckets, max_distance: int = 128,
                                      bidirectional: bool = True) -> int:
     """Bytes of workspace of rowsoftmax_relbias_bwd_* for scores of y's shape and type."""
-    a = _relbias(y, num_buckets, max_distance, bidirectional, False, 1.0, 0, None, None)
+    torch, index = _T or _warm(), y.get_device()
+    a = _relbias(y, index, num_buckets, max_distance, bidirectional, False, 1.0, 0, None, None)
     size = ctypes.c_size_t()
-    with _torch().cuda.device(y.device):
-        _check(load().rowsoftmax_relbias_bwd_workspace(_dtype_code(y), *y.shape, ctypes.byref(a),
-                                                       ctypes.byref(size)),
-               "rowsoftmax_relbias_bwd_workspace")
+    with torch.cuda.device(index):
+        st = load().rowsoftmax_relbias_bwd_workspace(_code(y, None), *y.shape, ctypes.byref(a),
+                                                     ctypes.byref(size))
+    if st != RMSNORM_OK:
+        raise RmsnormError(st, "rowsoftmax_relbias_bwd_workspace")
     return size.value
 
 
