@@ -1,24 +1,32 @@
 // k_blockring.cuh -- row blocks brought into shared memory by 1-D bulk copies,
 // a ring of them in flight.
 //
-// A CTA works on row blocks first, first + stride, ...; a block is
-// `block_bytes` of consecutive rows of one or two arrays of the same layout.
-// Rows may have any length: a bulk copy wants 16-byte boundaries, so a block is
-// copied from the boundary at or before its start to the one at or after its
-// end, and its rows begin `shift` bytes into the slot.  The bytes around it
-// belong to the neighbouring rows (the arrays start on a boundary); only
-// behind the arrays' last boundary nothing may be read, so what a block has
-// there, less than 16 bytes, is copied by threads (finish_block).
+// A CTA works on blocks of `block_rows` rows of one or two arrays of the same
+// layout.  Bulk copies and vector accesses want 16-byte boundaries:
+//
+// Aligned rows (a multiple of 16 bytes): a block is consecutive rows, one copy
+// per array.
+//
+// SHIFT, rows of any length (from 32 bytes): row r begins r * H mod EPV elements
+// behind a boundary, which has a period of `period` (1, 2, 4 or 8) rows.  A CTA
+// takes rows r = its number mod period only, so all its rows have the same
+// shift, and every column the same place in a vector: row by row its vectors,
+// weights and column sums line up as for aligned rows, `shift` elements later.
+// Each row is copied by itself, from the boundary at or before its start to the
+// one at or after its end; the bytes around it belong to the neighbouring
+// rows (the arrays start on a boundary).  Only behind the arrays' last boundary
+// nothing may be read: what the arrays' last row has there, less than 16 bytes,
+// is copied by threads (finish).
 //
 // Slots are handed back without "empty" barriers: a kernel has one block-wide
 // barrier in each iteration, and behind the one of iteration n every thread is
-// done with iteration n - 1, whose slot one thread then refills.  Proxy rule
-// as in k_ring.cuh: a slot that the async proxy writes is read by generic loads
-// only behind the mbarrier wait, and refilled behind the block barrier;
-// finish_block's generic writes go to a CTA's last block, which nothing
-// overwrites.
+// done with iteration n - 1, whose slot one warp then refills.  Proxy rule as in
+// k_ring.cuh: a slot that the async proxy writes is read by generic loads only
+// behind the mbarrier wait, and refilled behind the block barrier; finish's
+// generic writes go to a CTA's last block, which nothing overwrites.
 #pragma once
 #include "common.cuh"
+#include "norm_launch.h"
 
 namespace rmsnorm {
 
@@ -36,160 +44,227 @@ struct RingStep {
     }
 };
 
-struct BlockRing {
-    const char* src[2];          // src[1] null: one array
-    uint32_t slots;              // shared-memory address of nslots * narrays * slot_bytes
-    uint32_t bars;               // of nslots mbarriers
-    int nslots;
-    int slot_bytes;              // one array's share of a slot
-    int narrays;
-    int64_t block_bytes;
-    int64_t total_bytes;         // of one array
+// The kernel's parameters are read where they are needed (they are in constant
+// memory) rather than kept in registers; NARR arrays (x, and dy).
+template <typename T, bool SHIFT, int NARR>
+struct RowRing {
+    static constexpr int EPV = 16 / static_cast<int>(sizeof(T));
+    const NormParams& p;
+    const int block_rows;
+    uint32_t slots;              // shared-memory address of p.nslots * NARR * block_rows * row slots
+    uint32_t bars;               // of p.nslots mbarriers
+    int shift;                   // elements of a row's first vector before the row
+    int64_t first, step;         // the CTA's first row, and rows from block to block
     int count;                   // blocks of this CTA
-    int tail_from;               // of those, the first that reaches behind the arrays' last boundary
 
-    static __device__ __forceinline__ int64_t down(int64_t v) { return v - (v & 15); }
-    __device__ __forceinline__ int64_t start(int n) const {
-        return (blockIdx.x + static_cast<int64_t>(n) * gridDim.x) * block_bytes;
+    __device__ __forceinline__ int period() const { return SHIFT ? p.period : 1; }
+    __device__ __forceinline__ int row_bytes() const { return p.hidden * static_cast<int>(sizeof(T)); }
+    __device__ __forceinline__ int row_slot() const { return SHIFT ? p.row_slot : row_bytes(); }
+    // Bytes of an array before its last boundary.
+    __device__ __forceinline__ int64_t inside() const { return p.rows * row_bytes() / 16 * 16; }
+    // Shared-memory address of array a's part of a slot.
+    __device__ __forceinline__ uint32_t base(int slot, int a) const {
+        return slots + static_cast<uint32_t>((slot * NARR + a) * block_rows * row_slot());
     }
 
-    // `units` blocks in all; all threads, then a barrier before the first issue.
-    __device__ __forceinline__ void init(const void* a0, const void* a1, unsigned char* smem,
-                                         uint64_t* barriers, int64_t units) {
-        src[0] = static_cast<const char*>(a0);
-        src[1] = static_cast<const char*>(a1);
-        narrays = a1 ? 2 : 1;
-        slots = smem_addr(smem);
-        bars = smem_addr(barriers);
-        const int64_t grid = gridDim.x, mine = blockIdx.x;
-        count = mine < units ? static_cast<int>((units - mine + grid - 1) / grid) : 0;
-        tail_from = count;
-        while (tail_from > 0 && start(tail_from - 1) + block_bytes > down(total_bytes)) --tail_from;
+    // All threads; then a barrier before the first issue.
+    __device__ __forceinline__ RowRing(const NormParams& p_, int block_rows_, unsigned char* smem,
+                                       uint64_t* barriers)
+        : p(p_), block_rows(block_rows_), slots(smem_addr(smem)), bars(smem_addr(barriers)) {
+        const int cls = static_cast<int>(blockIdx.x) % period();
+        const int mine = static_cast<int>(blockIdx.x) / period();
+        // CTAs of the class, and its blocks
+        const int64_t ctas = (static_cast<int>(gridDim.x) - cls + period() - 1) / period();
+        const int64_t class_rows = p.rows > cls ? (p.rows - cls + period() - 1) / period() : 0;
+        const int64_t blocks = (class_rows + block_rows - 1) / block_rows;
+        count = mine < blocks ? static_cast<int>((blocks - mine + ctas - 1) / ctas) : 0;
+        first = cls + static_cast<int64_t>(mine) * block_rows * period();
+        step = ctas * block_rows * period();
+        shift = SHIFT ? static_cast<int>(static_cast<int64_t>(cls) * p.hidden % EPV) : 0;
         if (threadIdx.x == 0) {
-            for (int k = 0; k < nslots; ++k) mbar_init(bars + 8 * k, 1);
+            for (int k = 0; k < p.nslots; ++k) mbar_init(bars + 8 * k, 1);
             fence_mbarrier_init_cluster();
         }
     }
 
-    // Shared-memory address of array a's part of a slot; the n-th block's rows
-    // begin start(n) & 15 bytes into it.
-    __device__ __forceinline__ uint32_t base(int slot, int a) const {
-        return slots + static_cast<uint32_t>((slot * narrays + a) * slot_bytes);
-    }
-
-    // One thread: start the copies of the CTA's n-th block into `slot`.
-    __device__ __forceinline__ void issue(int slot, int n, int fault) const {
-        const int64_t from = down(start(n));
-        const int64_t to = min(down(start(n) + block_bytes + 15), down(total_bytes));
-        const uint32_t bytes = to > from ? static_cast<uint32_t>(to - from) : 0u;
+    // One warp: start the copies of the CTA's n-th block into `slot`.
+    __device__ __forceinline__ void issue(int slot, int n) const {
+        const int lane = threadIdx.x & 31;
         const uint32_t bar = bars + 8 * slot;
+        const char* x = static_cast<const char*>(p.x);
+        const char* dy = static_cast<const char*>(p.dy);
+        const int64_t row0 = first + n * step;
+        const int64_t left = (p.rows - row0 + period() - 1) / period();  // rows of the class from there
+        const int nrows = static_cast<int>(left < block_rows ? left : block_rows);
 #if RMSNORM_FAULT_INJECT
-        if (fault == kFaultStagedWithholdCopy && n == 0) {   // armed for bytes that never come
-            mbar_arrive_expect_tx(bar, 16);
+        if (p.fault == kFaultStagedWithholdCopy && n == 0) {   // armed for bytes that never come
+            if (lane == 0) mbar_arrive_expect_tx(bar, 16);
             return;
         }
-#else
-        (void)fault;
 #endif
-        mbar_arrive_expect_tx(bar, bytes * narrays);
-        if (bytes == 0) return;
-        for (int a = 0; a < narrays; ++a) bulk_g2s_plain(base(slot, a), src[a] + from, bytes, bar);
-    }
-
-    // One thread: the CTA's first blocks.
-    __device__ __forceinline__ void prologue(int fault) const {
-        for (int k = 0; k < nslots && k < count; ++k) issue(k, k, fault);
-    }
-
-    // One thread, behind the barrier of iteration n: refill the slot of n - 1.
-    __device__ __forceinline__ void refill(const RingStep& step, int n, int fault) const {
-        if (n > 0 && n - 1 + nslots < count)
-            issue(step.slot ? step.slot - 1 : nslots - 1, n - 1 + nslots, fault);
-    }
-
-    // All threads, after block n >= tail_from has landed: its bytes behind the
-    // arrays' last boundary.  Ends with a barrier.
-    template <typename T>
-    __device__ __forceinline__ void finish(int slot, int n) const {
-        const int64_t at = start(n);
-        const int64_t end = min(at + block_bytes, total_bytes);
-        const int64_t from = max(down(total_bytes), at);
-        const int tail = static_cast<int>((end - from) / static_cast<int>(sizeof(T)));
-        if (static_cast<int>(threadIdx.x) < tail) {
-            for (int a = 0; a < narrays; ++a) {
-                const T v = reinterpret_cast<const T*>(src[a] + from)[threadIdx.x];
-                const uint32_t to = base(slot, a) + static_cast<uint32_t>(from - down(at)) +
-                                    threadIdx.x * static_cast<uint32_t>(sizeof(T));
-                if constexpr (sizeof(T) == 4) {
-                    asm volatile("st.shared.u32 [%0], %1;" :: "r"(to), "r"(__float_as_uint(v))
-                                 : "memory");
-                } else {
-                    asm volatile("st.shared.u16 [%0], %1;" :: "r"(to), "h"(__bfloat16_as_ushort(v))
-                                 : "memory");
-                }
+        if constexpr (!SHIFT) {
+            if (lane == 0) {
+                const uint32_t bytes = static_cast<uint32_t>(nrows * row_bytes());
+                const int64_t at = row0 * row_bytes();
+                mbar_arrive_expect_tx(bar, bytes * NARR);
+                bulk_g2s_plain(base(slot, 0), x + at, bytes, bar);
+                if (NARR == 2) bulk_g2s_plain(base(slot, 1), dy + at, bytes, bar);
             }
+        } else {
+            // a row's window is the same size for all rows of the class but the arrays' last
+            const uint32_t whole = static_cast<uint32_t>((shift * static_cast<int>(sizeof(T)) +
+                                                          row_bytes() + 15) / 16 * 16);
+            const int64_t from = row0 * row_bytes() / 16 * 16;
+            const int64_t stride = static_cast<int64_t>(period()) * row_bytes();
+            const int64_t end = from + (nrows - 1) * stride + whole;     // of the last row's window
+            const uint32_t over = end > inside() ? static_cast<uint32_t>(end - inside()) : 0u;
+            if (lane == 0) mbar_arrive_expect_tx(bar, (whole * nrows - over) * NARR);
+            __syncwarp();
+            for (int r = lane; r < nrows; r += 32) {
+                const uint32_t bytes = r == nrows - 1 ? whole - over : whole;
+                const uint32_t to = static_cast<uint32_t>(r * row_slot());
+                bulk_g2s_plain(base(slot, 0) + to, x + from + r * stride, bytes, bar);
+                if (NARR == 2) bulk_g2s_plain(base(slot, 1) + to, dy + from + r * stride, bytes, bar);
+            }
+        }
+    }
+
+    // One warp: the CTA's first blocks.
+    __device__ __forceinline__ void prologue() const {
+        for (int k = 0; k < p.nslots && k < count; ++k) issue(k, k);
+    }
+
+    // One warp, behind the barrier of iteration n: refill the slot of n - 1.
+    __device__ __forceinline__ void refill(const RingStep& s, int n) const {
+        if (n > 0 && n - 1 + p.nslots < count)
+            issue(s.slot ? s.slot - 1 : p.nslots - 1, n - 1 + p.nslots);
+    }
+
+    // All threads, after the CTA's last block has landed: what the arrays' last
+    // row, if it is among its rows, has behind their last boundary.  Ends with a
+    // barrier if there is any.
+    __device__ __forceinline__ void finish(int slot, int n) const {
+        if (!SHIFT || n != count - 1) return;
+        const int64_t total = p.rows * row_bytes();
+        const int64_t row0 = first + n * step;
+        const int64_t last = p.rows - 1;
+        const int tail = static_cast<int>((total - inside()) / static_cast<int>(sizeof(T)));
+        if (tail == 0 || last < row0 || (last - row0) % period() != 0 ||
+            (last - row0) / period() >= block_rows)
+            return;                                          // uniform
+        if (static_cast<int>(threadIdx.x) < tail) {
+            const int r = static_cast<int>((last - row0) / period());
+            const int64_t at = last * row_bytes() / 16 * 16;   // the row's window starts there
+            const uint32_t to = static_cast<uint32_t>(r * row_slot()) +
+                                static_cast<uint32_t>(inside() - at) +
+                                threadIdx.x * static_cast<uint32_t>(sizeof(T));
+            copy_elem(base(slot, 0) + to, static_cast<const char*>(p.x) + inside());
+            if (NARR == 2) copy_elem(base(slot, 1) + to, static_cast<const char*>(p.dy) + inside());
         }
         __syncthreads();
     }
-
-    // Wait (bounded) for the block in `slot` on the slot's `use`-th use.
-    __device__ __forceinline__ bool wait(const RingStep& step, uint64_t timeout_ns) const {
-        return mbar_wait_bounded<false>(bars + 8 * step.slot, step.use & 1u, timeout_ns);
+    __device__ __forceinline__ void copy_elem(uint32_t to, const char* from) const {
+        const T v = reinterpret_cast<const T*>(from)[threadIdx.x];
+        if constexpr (sizeof(T) == 4) {
+            asm volatile("st.shared.u32 [%0], %1;" :: "r"(to), "r"(__float_as_uint(v)) : "memory");
+        } else {
+            asm volatile("st.shared.u16 [%0], %1;" :: "r"(to), "h"(__bfloat16_as_ushort(v))
+                         : "memory");
+        }
     }
 
-    // One thread, after the wait for block n, at `step`, has run out and every
+    // Wait (bounded) for the block at `s`.
+    __device__ __forceinline__ bool wait(const RingStep& s) const {
+        return mbar_wait_bounded<false>(bars + 8 * s.slot, s.use & 1u, p.timeout_ns);
+    }
+
+    // One thread, after the wait for block n, at `s`, has run out and every
     // thread has left the loop before its refill: wait (bounded) for what is
     // under way.
-    __device__ __forceinline__ void drain(RingStep step, int n, uint64_t timeout_ns) const {
-        const int issued = n == 0 ? nslots : nslots - 1;     // blocks n, n + 1, ...
+    __device__ __forceinline__ void drain(RingStep s, int n) const {
+        const int issued = n == 0 ? p.nslots : p.nslots - 1;   // blocks n, n + 1, ...
         for (int k = 0; k < issued && n + k < count; ++k) {
-            wait(step, timeout_ns);
-            step.next(nslots);
+            wait(s);
+            s.next(p.nslots);
         }
     }
 };
 
-// A vector of shared memory.  Volatile: a kernel that passes over its rows
+// 16 bytes of shared memory.  Volatile: a kernel that passes over its rows
 // several times reads them again instead of keeping them, widened, in registers.
-template <int VB>
-__device__ __forceinline__ Vec<VB> ld_slot(uint32_t a) {
-    Vec<VB> v;
-    if constexpr (VB == 16) {
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3]) : "r"(a));
-    } else if constexpr (VB == 8) {
-        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.u[0]), "=r"(v.u[1]) : "r"(a));
-    } else if constexpr (VB == 4) {
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v.u[0]) : "r"(a));
-    } else {
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v.h) : "r"(a));
-    }
+__device__ __forceinline__ Vec<16> ld_slot(uint32_t a) {
+    Vec<16> v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3]) : "r"(a));
     return v;
 }
 
 // The same where `on`, else zeros: one predicated load, no branch.
-template <int VB>
-__device__ __forceinline__ Vec<VB> ld_slot_if(uint32_t a, bool on) {
-    Vec<VB> v;
+__device__ __forceinline__ Vec<16> ld_slot_if(uint32_t a, bool on) {
+    Vec<16> v;
     const uint32_t q = on;
-    if constexpr (VB == 16) {
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-                     "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-                     "@p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
-                     : "=&r"(v.u[0]), "=&r"(v.u[1]), "=&r"(v.u[2]), "=&r"(v.u[3]) : "r"(a), "r"(q));
-    } else if constexpr (VB == 8) {
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-                     "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
-                     "@p ld.shared.v2.u32 {%0,%1}, [%2];\n\t}"
-                     : "=&r"(v.u[0]), "=&r"(v.u[1]) : "r"(a), "r"(q));
-    } else if constexpr (VB == 4) {
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t"
-                     "@p ld.shared.u32 %0, [%1];\n\t}" : "=&r"(v.u[0]) : "r"(a), "r"(q));
-    } else {
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t"
-                     "@p ld.shared.u16 %0, [%1];\n\t}" : "=&h"(v.h) : "r"(a), "r"(q));
-    }
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+                 "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+                 "@p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+                 : "=&r"(v.u[0]), "=&r"(v.u[1]), "=&r"(v.u[2]), "=&r"(v.u[3]) : "r"(a), "r"(q));
     return v;
+}
+
+// A row in its slot: whole vectors, and with SHIFT up to EPV - 1 elements before
+// the first and behind the last of them (its edges), which threads take one
+// by one, so that the loops over vectors stay those of aligned rows.
+template <typename T, bool SHIFT>
+struct RowVecs {
+    static constexpr int EPV = 16 / static_cast<int>(sizeof(T));
+    int nvec, hidden;
+    int head, edges;         // elements before the vectors, and on both sides
+    int skip;                // of the slot's first vector, elements before the row
+    __device__ __forceinline__ RowVecs(int shift, int hidden_) : hidden(hidden_) {
+        skip = SHIFT ? shift : 0;
+        head = SHIFT ? min((EPV - skip) % EPV, hidden) : 0;
+        nvec = (hidden - head) / EPV;
+        edges = SHIFT ? hidden - nvec * EPV : 0;
+    }
+    // column of vector v's first element, and its bytes from the slot's row on
+    __device__ __forceinline__ int col(int v) const { return head + v * EPV; }
+    __device__ __forceinline__ int vec_at() const { return SHIFT && skip > 0 ? 16 : 0; }
+    // the same for edge element e
+    __device__ __forceinline__ int edge_col(int e) const { return e < head ? e : e + nvec * EPV; }
+    __device__ __forceinline__ int edge_at(int e) const {
+        return (skip + edge_col(e)) * static_cast<int>(sizeof(T));
+    }
+};
+
+// One element of shared memory, widened; stored to global memory.
+template <typename T>
+__device__ __forceinline__ float ld_elem(uint32_t a) {
+    if constexpr (sizeof(T) == 4) {
+        float v;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+        return v;
+    } else {
+        Vec<2> v;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v.h) : "r"(a));
+        return get<T, 2>(v, 0);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void st_elem(void* base, int64_t at, float v) {
+    constexpr int sz = static_cast<int>(sizeof(T));
+    const float f[1] = {v};
+    st_stream<sz>(static_cast<char*>(base) + at * sz, pack<T, sz>(f));
+}
+
+// Weights laid out like a row in its slot, in shared memory; size = elements of
+// a row's slot.
+template <typename T>
+__device__ __forceinline__ void copy_shifted(T* to, const void* from, int skip, int hidden, int size,
+                                             float fill) {
+    const T* w = static_cast<const T*>(from);
+    for (int j = threadIdx.x; j < size; j += blockDim.x) {
+        const bool in = j >= skip && j < skip + hidden;
+        to[j] = w && in ? w[j - skip] : static_cast<T>(fill);
+    }
 }
 
 // The vectors t, t + G, ... of a row of nvec: `full` of them (nvec / G) every

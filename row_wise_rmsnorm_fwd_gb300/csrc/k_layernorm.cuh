@@ -134,7 +134,8 @@ layernorm_twopass_kernel(const NormParams p) {
     }
 }
 
-// Rows staged in shared memory by bulk copies (k_blockring.cuh): blocks of
+// Rows staged in shared memory by bulk copies (k_blockring.cuh; SHIFT: rows of
+// any length, the weights copied to shared memory in their layout): blocks of
 // p.rows_per_cta rows, G threads per row (p.group: a multiple of 32, or a power
 // of two below 32 for several rows per warp); x is read from HBM once and from
 // shared memory three times (sum, squares, output), which costs no registers,
@@ -144,14 +145,15 @@ layernorm_twopass_kernel(const NormParams p) {
 // exchange through shared memory, behind one barrier, merges the warps' pairs:
 // the merge update above, for shares of fixed counts, with the row's mean
 // known first.
-template <typename T, int VB>
+template <typename T, bool SHIFT>
 __global__ void __launch_bounds__(1024) layernorm_staged_kernel(const NormParams p) {
-    constexpr int EPV = VecTraits<T, VB>::kElems;
-    constexpr int PN = PairTraits<T, VB>::N;
-    using L = Lanes<PairTraits<T, VB>::W>;
+    constexpr int EPV = VecTraits<T, 16>::kElems;
+    constexpr int PN = PairTraits<T, 16>::N;
+    using L = Lanes<2>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ alignas(8) uint64_t bars[kBlockRingMaxSlots];
     __shared__ float2 red[2][32];
+    __shared__ float2 count[32];             // elements of a warp's share, and 1 / that
     pdl_trigger();
     const int G = p.group;
     const int width = G < 32 ? G : 32;       // lanes of a share
@@ -161,79 +163,93 @@ __global__ void __launch_bounds__(1024) layernorm_staged_kernel(const NormParams
     const int warp = tid >> 5, lane = tid & 31;
     const int wpg = G >> 5;
     const int gw0 = g * wpg;
-    const int rpc = p.rows_per_cta;
-    const int row_bytes = p.hidden * static_cast<int>(sizeof(T));
 
-    BlockRing ring;
-    ring.nslots = p.nslots;
-    ring.slot_bytes = p.slot_bytes;
-    ring.block_bytes = static_cast<int64_t>(rpc) * row_bytes;
-    ring.total_bytes = p.rows * row_bytes;
-    ring.init(p.x, nullptr, smem, bars, (p.rows + rpc - 1) / rpc);
+    const RowRing<T, SHIFT, 1> ring(p, p.rows_per_cta, smem, bars);
+    const RowVecs<T, SHIFT> rv(ring.shift, p.hidden);
+    const int full = rv.nvec / G;
+    const bool more = t < rv.nvec - full * G;
     // elements of this share of a row, and of the share that lane k < wpg merges
-    auto share_of = [&](int w) {
-        int n = 0;
-        for (int v = w * 32; v < p.nvec; v += G) n += min(32, p.nvec - v);
-        return static_cast<float>(n * EPV);
-    };
-    const float cnt = wpg > 1 ? share_of(warp - gw0) : static_cast<float>(p.hidden);
+    int mine = 0;
+    for_vectors(t, G, full, more, [&](int) { mine += EPV; });
+    for (int e = t; e < rv.edges; e += G) ++mine;
+    const float cnt = share_sum(static_cast<float>(mine), width);
     const float inv_cnt = cnt > 0.f ? 1.f / cnt : 0.f;
-    const float cnt_k = wpg > 1 && lane < wpg ? share_of(lane) : 0.f;
-    const float inv_k = cnt_k > 0.f ? 1.f / cnt_k : 0.f;
+    if (wpg > 1 && lane == 0) count[warp] = make_float2(cnt, inv_cnt);
     int merge_width = 1;
     while (merge_width < wpg) merge_width <<= 1;
-    const int full = p.nvec / G;
-    const bool more = t < p.nvec - full * G;
     __syncthreads();
+    float2 share = make_float2(0.f, 0.f);
+    if (wpg > 1 && lane < wpg) share = count[gw0 + lane];
     pdl_wait();
-    if (tid == 0) ring.prologue(p.fault);
+    if (warp == 0) ring.prologue();
 
-    const char* wb = static_cast<const char*>(p.w);
-    const char* bb = static_cast<const char*>(p.b);
-    int64_t row = static_cast<int64_t>(blockIdx.x) * rpc + g;
-    const int64_t row_step = static_cast<int64_t>(gridDim.x) * rpc;
+    // the weights: in global memory, or laid out like the rows behind the ring
+    const char* wg = static_cast<const char*>(p.w);
+    const char* bg = static_cast<const char*>(p.b);
+    uint32_t ws = 0, bs = 0;
+    if constexpr (SHIFT) {
+        T* wc = reinterpret_cast<T*>(smem + (ring.base(p.nslots, 0) - ring.base(0, 0)));
+        const int size = ring.row_slot() / static_cast<int>(sizeof(T));
+        T* bc = wc + size;
+        copy_shifted<T>(wc, p.w, rv.skip, p.hidden, size, 1.f);
+        copy_shifted<T>(bc, p.b, rv.skip, p.hidden, size, 0.f);
+        ws = smem_addr(wc);
+        bs = smem_addr(bc);
+        // read behind the first iteration's barrier
+    }
+    int64_t row = ring.first + static_cast<int64_t>(g) * ring.period();
     RingStep step;
     int n = 0;
-    for (; n < ring.count; ++n, row += row_step) {
-        const bool ok = ring.wait(step, p.timeout_ns);
-        if (n >= ring.tail_from) ring.finish<T>(step.slot, n);
-        const uint32_t src = ring.base(step.slot, 0) + static_cast<uint32_t>(ring.start(n) & 15) +
-                             static_cast<uint32_t>(g * row_bytes);
+    for (; n < ring.count; ++n, row += ring.step) {
+        const bool ok = ring.wait(step);
+        ring.finish(step.slot, n);
+        const uint32_t in_slot = ring.base(step.slot, 0) + static_cast<uint32_t>(g * ring.row_slot());
+        const uint32_t src = in_slot + static_cast<uint32_t>(rv.vec_at());
 
         L s0 = L::all(0.f), s1 = L::all(0.f);
         for_vectors(t, G, full, more, [&](int v) {
-            const Vec<VB> x = ld_slot<VB>(src + v * VB);
+            const Vec<16> x = ld_slot(src + v * 16);
 #pragma unroll
             for (int k = 0; k < PN; ++k) {
-                if (k & 1) s1 = lanes_plus<T, VB>(x, k, s1); else s0 = lanes_plus<T, VB>(x, k, s0);
+                if (k & 1) s1 = lanes_plus<T, 16>(x, k, s1); else s0 = lanes_plus<T, 16>(x, k, s0);
             }
         });
-        const float sum = share_sum((s0 + s1).total(), width);
+        float sum = (s0 + s1).total();
+        if constexpr (SHIFT)
+            for (int e = t; e < rv.edges; e += G) sum += ld_elem<T>(in_slot + rv.edge_at(e));
+        sum = share_sum(sum, width);
         const float part = sum * inv_cnt;            // mean of the share
         const L about = L::all(-part);
         s0 = s1 = L::all(0.f);
         for_vectors(t, G, full, more, [&](int v) {
-            const Vec<VB> x = ld_slot<VB>(src + v * VB);
+            const Vec<16> x = ld_slot(src + v * 16);
 #pragma unroll
             for (int k = 0; k < PN; ++k) {
-                const L d = lanes_plus<T, VB>(x, k, about);
+                const L d = lanes_plus<T, 16>(x, k, about);
                 if (k & 1) s1 = fma(d, d, s1); else s0 = fma(d, d, s0);
             }
         });
-        float m2 = share_sum((s0 + s1).total(), width);
+        float m2 = (s0 + s1).total();
+        if constexpr (SHIFT) {
+            for (int e = t; e < rv.edges; e += G) {
+                const float d = ld_elem<T>(in_slot + rv.edge_at(e)) - part;
+                m2 = fmaf(d, d, m2);
+            }
+        }
+        m2 = share_sum(m2, width);
         float mean = part;
         float2* slot = red[n & 1];
         if (wpg > 1 && lane == 0) slot[warp] = make_float2(sum, m2);
         if (__syncthreads_or(!ok)) break;            // uniform; also frees the previous slot
-        if (tid == 0) ring.refill(step, n, p.fault);
+        if (warp == 0) ring.refill(step, n);
         if (wpg > 1) {
             float2 e = make_float2(0.f, 0.f);
             if (lane < wpg) e = slot[gw0 + lane];
             mean = group_allreduce_sum(e.x, merge_width);
             mean = __shfl_sync(0xffffffffu, mean, 0) * p.inv_hidden;
             // n_k * (mean_k - mean)^2, from the share's sum and count
-            const float d = fmaf(-cnt_k, mean, e.x);
-            m2 = group_allreduce_sum(fmaf(d * inv_k, d, e.y), merge_width);
+            const float d = fmaf(-share.x, mean, e.x);
+            m2 = group_allreduce_sum(fmaf(d * share.y, d, e.y), merge_width);
             m2 = __shfl_sync(0xffffffffu, m2, 0);
         }
         const float rstd = rsqrtf(fmaf(m2, p.inv_hidden, p.eps));
@@ -242,45 +258,56 @@ __global__ void __launch_bounds__(1024) layernorm_staged_kernel(const NormParams
                 if (p.mean) p.mean[row] = mean;
                 if (p.rstd) p.rstd[row] = rstd;
             }
-            char* dst = static_cast<char*>(p.out) + row * row_bytes;
+            const int64_t at = row * p.hidden;
+            char* dst = static_cast<char*>(p.out) + (at + rv.head) * static_cast<int>(sizeof(T));
             const L minus = L::all(-mean), r = L::all(rstd);
             auto write = [&](auto with_w, auto with_b) {
                 for_vectors(t, G, full, more, [&](int v) {
-                    const Vec<VB> x = ld_slot<VB>(src + v * VB);
-                    Vec<VB> wi, bi;
-                    if constexpr (with_w) wi = ld_ro<VB>(wb + v * VB);
-                    if constexpr (with_b) bi = ld_ro<VB>(bb + v * VB);
+                    const Vec<16> x = ld_slot(src + v * 16);
+                    Vec<16> wi, bi;
+                    if constexpr (with_w)
+                        wi = SHIFT ? ld_slot(ws + rv.vec_at() + v * 16) : ld_ro<16>(wg + v * 16);
+                    if constexpr (with_b)
+                        bi = SHIFT ? ld_slot(bs + rv.vec_at() + v * 16) : ld_ro<16>(bg + v * 16);
                     float o[EPV];
 #pragma unroll
                     for (int k = 0; k < PN; ++k) {
-                        L y = lanes_plus<T, VB>(x, k, minus) * r;
+                        L y = lanes_plus<T, 16>(x, k, minus) * r;
                         if constexpr (with_w && with_b) {
-                            y = fma(y, lanes<T, VB>(wi, k), lanes<T, VB>(bi, k));
+                            y = fma(y, lanes<T, 16>(wi, k), lanes<T, 16>(bi, k));
                         } else if constexpr (with_w) {
-                            y = y * lanes<T, VB>(wi, k);
+                            y = y * lanes<T, 16>(wi, k);
                         } else if constexpr (with_b) {
-                            y = y + lanes<T, VB>(bi, k);
+                            y = y + lanes<T, 16>(bi, k);
                         }
-                        y.put(o + k * (EPV / PN));
+                        y.put(o + 2 * k);
                     }
-                    st_stream<VB>(dst + v * VB, pack<T, VB>(o));
+                    st_stream<16>(dst + v * 16, pack<T, 16>(o));
                 });
             };
             using Yes = std::true_type;
             using No = std::false_type;
-            if (wb) {
-                if (bb) write(Yes(), Yes()); else write(Yes(), No());
+            if (SHIFT) {
+                write(Yes(), Yes());                 // ones and zeros where there are none
+                for (int e = t; e < rv.edges; e += G) {
+                    const int j = rv.edge_at(e);
+                    const float xh = (ld_elem<T>(in_slot + j) - mean) * rstd;
+                    st_elem<T>(p.out, at + rv.edge_col(e),
+                               fmaf(xh, ld_elem<T>(ws + j), ld_elem<T>(bs + j)));
+                }
+            } else if (p.w) {
+                if (p.b) write(Yes(), Yes()); else write(Yes(), No());
             } else {
-                if (bb) write(No(), Yes()); else write(No(), No());
+                if (p.b) write(No(), Yes()); else write(No(), No());
             }
         }
-        step.next(ring.nslots);
+        step.next(p.nslots);
     }
     if (n < ring.count) {
         // a wait ran out: report it, and let the copies that are under way land
         if (tid == 0) {
             report_timeout(p.status, kSiteStagedFull);
-            ring.drain(step, n, p.timeout_ns);
+            ring.drain(step, n);
         }
         __syncthreads();
     }

@@ -151,15 +151,33 @@ __global__ void __launch_bounds__(kBwdColsThreads) norm_bwd_cols_kernel(const No
 // u = x - mean (RMSNorm: x), the first pass needs d * u once for both
 // m(g * xh) and dw, and dx = (d * w) * rstd + k1 + u * k2 with two constants
 // of the row.  R = 2 gives each thread two independent rows between barriers.
-// FULL: every thread has NV whole vectors and there are weights; else vectors
-// past the row's end are read as zeros (they add nothing anywhere) and not
-// stored.
-template <typename T, int VB, int NV, bool LAYER, int R, bool FULL>
-__global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_staged_kernel(const NormParams p) {
-    constexpr int EPV = VecTraits<T, VB>::kElems;
-    constexpr int PN = PairTraits<T, VB>::N;
-    constexpr int W = PairTraits<T, VB>::W;
-    using L = Lanes<W>;
+// Modes: kWhole: every thread has NV whole vectors and there are weights;
+// kPartial: aligned rows of any length, with or without weights; kShift: rows
+// of any length, the weights copied to shared memory in their layout, a
+// shifted row's edges taken by one thread per element.  Vectors past the row's
+// end are read as zeros: they add nothing anywhere and are not stored.
+//
+// Rows of more than 512 threads of 16 elements take 32 per thread (all of a
+// thread's 128 registers) rather than the kernels above, which read them twice.
+enum : int { kWhole, kPartial, kShift };
+
+// Registers per thread, at most: with one row of 16 elements between barriers
+// resident warps count for more than registers.  Measured (us, at most 64 / 80 /
+// 96 / 128): RMSNorm bf16 65536 x 4096 478 (spills) / 249 / - / -, shifted
+// 16384 x 4097 106 / 99 / 104 / -; layer norm bf16 shifted 16384 x 4097 - / 178 /
+// 123 / 114, 8191 x 2050 - / 60 / 40 / 38.
+constexpr int norm_bwd_regs(int elems, bool layer, int rows) {
+    return elems == 32 || rows == 2 || layer ? 128 : 80;
+}
+
+template <typename T, int NV, bool LAYER, int R, int MODE>
+__global__ void
+__maxnreg__((norm_bwd_regs(NV * VecTraits<T, 16>::kElems, LAYER, R)))
+norm_bwd_staged_kernel(const NormParams p) {
+    constexpr int EPV = VecTraits<T, 16>::kElems;
+    constexpr int PN = PairTraits<T, 16>::N;
+    constexpr bool SHIFT = MODE == kShift;
+    using L = Lanes<2>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ alignas(8) uint64_t bars[kBlockRingMaxSlots];
     __shared__ float2 red[2][R][32];
@@ -173,83 +191,90 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_staged_kernel(con
     const int wpg = G >> 5;
     const int gw0 = g * wpg;
     const int rpc = p.rows_per_cta;          // row groups of the CTA
-    const int row_bytes = p.hidden * static_cast<int>(sizeof(T));
 
-    BlockRing ring;
-    ring.nslots = p.nslots;
-    ring.slot_bytes = p.slot_bytes;
-    ring.block_bytes = static_cast<int64_t>(R * rpc) * row_bytes;
-    ring.total_bytes = p.rows * row_bytes;
-    ring.init(p.x, p.dy, smem, bars, (p.rows + R * rpc - 1) / (R * rpc));
+    const RowRing<T, SHIFT, 2> ring(p, R * rpc, smem, bars);
+    const RowVecs<T, SHIFT> rv(ring.shift, p.hidden);
     int merge_width = 1;
     while (merge_width < wpg) merge_width <<= 1;
     bool valid[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) valid[i] = FULL || i * G + t < p.nvec;
+    for (int i = 0; i < NV; ++i) valid[i] = MODE == kWhole || i * G + t < rv.nvec;
     __syncthreads();
     pdl_wait();
-    if (tid == 0) ring.prologue(p.fault);
+    if (warp == 0) ring.prologue();
 
-    const char* wb = static_cast<const char*>(p.w) + t * VB;
+    const char* wg = static_cast<const char*>(p.w) + t * 16;
+    uint32_t ws = 0;
+    if constexpr (SHIFT) {
+        T* wc = reinterpret_cast<T*>(smem + (ring.base(p.nslots, 0) - ring.base(0, 0)));
+        copy_shifted<T>(wc, p.w, rv.skip, p.hidden, ring.row_slot() / static_cast<int>(sizeof(T)), 1.f);
+        ws = smem_addr(wc);
+        __syncthreads();
+    }
+    // this thread's edge element (there are at most 14 and G >= 16), its weight and sums
+    const bool edge = SHIFT && t < rv.edges;
+    const int edge_at = edge ? rv.edge_at(t) : 0;
+    const float edge_w = edge ? ld_elem<T>(ws + edge_at) : 0.f;
+    float edge_aw = 0.f, edge_ab = 0.f;
+    ws += rv.vec_at() + t * 16;
     L aw[NV * PN], ab[LAYER ? NV * PN : 1];
 #pragma unroll
     for (int k = 0; k < NV * PN; ++k) aw[k] = L::all(0.f);
 #pragma unroll
     for (int k = 0; k < (LAYER ? NV * PN : 1); ++k) ab[k] = L::all(0.f);
-    // row r of the group's R rows of this block: row + r * rpc
-    int64_t row = static_cast<int64_t>(blockIdx.x) * (R * rpc) + g;
-    const int64_t row_step = static_cast<int64_t>(gridDim.x) * (R * rpc);
+    // row r of the group's R rows of this block: row + r * apart
+    const int apart = rpc * ring.period();
+    int64_t row = ring.first + static_cast<int64_t>(g) * ring.period();
     float mean[R], rstd[R];
     auto stats = [&](int64_t from, float (&m)[R], float (&q)[R]) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             m[r] = q[r] = 0.f;
-            if (LAYER && from + r * rpc < p.rows) {
-                m[r] = p.mean[from + r * rpc];
-                q[r] = p.rstd[from + r * rpc];
+            if (LAYER && from + r * apart < p.rows) {
+                m[r] = p.mean[from + r * apart];
+                q[r] = p.rstd[from + r * apart];
             }
         }
     };
     stats(row, mean, rstd);
     auto weights = [&](int i) {
-        if constexpr (FULL) {
-            return ld_ro<VB>(wb + i * G * VB);
-        } else {
-            return p.w && valid[i] ? ld_ro<VB>(wb + i * G * VB) : ones_vec<T, VB>();
-        }
+        if constexpr (SHIFT) return ld_slot_if(ws + i * G * 16, valid[i]);
+        else if constexpr (MODE == kWhole) return ld_ro<16>(wg + i * G * 16);
+        else return p.w && valid[i] ? ld_ro<16>(wg + i * G * 16) : ones_vec<T, 16>();
     };
     RingStep step;
     int n = 0;
-    for (; n < ring.count; ++n, row += row_step) {
+    for (; n < ring.count; ++n, row += ring.step) {
         // the next rows' statistics, under way while this block is awaited
         float next_mean[R], next_rstd[R];
-        stats(row + row_step, next_mean, next_rstd);
-        const bool ok = ring.wait(step, p.timeout_ns);
-        if (n >= ring.tail_from) ring.finish<T>(step.slot, n);
-        const uint32_t in_slot = static_cast<uint32_t>(ring.start(n) & 15) +
-                                 static_cast<uint32_t>(g * row_bytes + t * VB);
+        stats(row + ring.step, next_mean, next_rstd);
+        const bool ok = ring.wait(step);
+        ring.finish(step.slot, n);
+        const uint32_t in_slot = static_cast<uint32_t>(g * ring.row_slot() + rv.vec_at() + t * 16);
         const uint32_t xs = ring.base(step.slot, 0) + in_slot;
         const uint32_t ds = ring.base(step.slot, 1) + in_slot;
-        const uint32_t next_row = static_cast<uint32_t>(rpc * row_bytes);
+        const uint32_t edge_x = ring.base(step.slot, 0) + static_cast<uint32_t>(g * ring.row_slot() + edge_at);
+        const uint32_t edge_d = ring.base(step.slot, 1) + static_cast<uint32_t>(g * ring.row_slot() + edge_at);
+        const uint32_t next_row = static_cast<uint32_t>(rpc * ring.row_slot());
 
         float a[R], b[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const bool here = row + r * rpc < p.rows;
+            const bool here = row + r * apart < p.rows;
             const L minus = L::all(-mean[r]), q = L::all(rstd[r]);
             L sa = L::all(0.f), sb = L::all(0.f);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const bool on = here && valid[i];
-                const Vec<VB> x = ld_slot_if<VB>(xs + r * next_row + i * G * VB, on);
-                const Vec<VB> d = ld_slot_if<VB>(ds + r * next_row + i * G * VB, on);
-                const Vec<VB> w = weights(i);
+                const Vec<16> x = ld_slot_if(xs + r * next_row + i * G * 16, on);
+                const Vec<16> d = ld_slot_if(ds + r * next_row + i * G * 16, on);
+                const Vec<16> w = weights(i);
 #pragma unroll
                 for (int k = 0; k < PN; ++k) {
-                    const L dk = lanes<T, VB>(d, k), wk = lanes<T, VB>(w, k);
+                    const L dk = lanes<T, 16>(d, k), wk = lanes<T, 16>(w, k);
                     L u;
-                    if constexpr (LAYER) u = lanes_plus<T, VB>(x, k, minus);
-                    else u = lanes<T, VB>(x, k);
+                    if constexpr (LAYER) u = lanes_plus<T, 16>(x, k, minus);
+                    else u = lanes<T, 16>(x, k);
                     const L du = dk * u;
                     if constexpr (LAYER) {
                         sa = fma(dk, wk, sa);
@@ -263,6 +288,15 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_staged_kernel(con
             }
             a[r] = sa.total();
             b[r] = sb.total();
+            if (SHIFT && edge && here) {
+                const float d = ld_elem<T>(edge_d), u = ld_elem<T>(edge_x) - mean[r];
+                a[r] = LAYER ? fmaf(d, edge_w, a[r]) : fmaf(u, u, a[r]);
+                b[r] = fmaf(d * u, edge_w, b[r]);
+                if (LAYER) {
+                    edge_aw = fmaf(d * u, rstd[r], edge_aw);
+                    edge_ab += d;
+                }
+            }
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -274,7 +308,7 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_staged_kernel(con
             for (int r = 0; r < R; ++r) red[n & 1][r][warp] = make_float2(a[r], b[r]);
         }
         if (__syncthreads_or(!ok)) break;            // uniform; also frees the previous slot
-        if (tid == 0) ring.refill(step, n, p.fault);
+        if (warp == 0) ring.refill(step, n);
         if (wpg > 1) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -291,7 +325,7 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_staged_kernel(con
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const bool here = row + r * rpc < p.rows;
+            const bool here = row + r * apart < p.rows;
             float k1 = 0.f;
             if constexpr (LAYER) {
                 k1 = -a[r] * p.inv_hidden * rstd[r];
@@ -302,29 +336,35 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_staged_kernel(con
             const float k2 = -(b[r] * p.inv_hidden * rstd[r]) * rstd[r] * rstd[r];
             const L minus = L::all(-mean[r]), q = L::all(rstd[r]);
             const L c1 = L::all(k1), c2 = L::all(k2);
-            char* dst = static_cast<char*>(p.out) + (row + r * rpc) * row_bytes + t * VB;
+            const int64_t at = (row + r * apart) * p.hidden;
+            char* dst = static_cast<char*>(p.out) + (at + rv.head) * static_cast<int>(sizeof(T)) + t * 16;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const bool on = here && valid[i];
-                const Vec<VB> x = ld_slot_if<VB>(xs + r * next_row + i * G * VB, on);
-                const Vec<VB> d = ld_slot_if<VB>(ds + r * next_row + i * G * VB, on);
-                const Vec<VB> w = weights(i);
+                const Vec<16> x = ld_slot_if(xs + r * next_row + i * G * 16, on);
+                const Vec<16> d = ld_slot_if(ds + r * next_row + i * G * 16, on);
+                const Vec<16> w = weights(i);
                 float o[EPV];
 #pragma unroll
                 for (int k = 0; k < PN; ++k) {
-                    const L dk = lanes<T, VB>(d, k), wk = lanes<T, VB>(w, k);
+                    const L dk = lanes<T, 16>(d, k), wk = lanes<T, 16>(w, k);
                     L u, in;
                     if constexpr (LAYER) {
-                        u = lanes_plus<T, VB>(x, k, minus);
+                        u = lanes_plus<T, 16>(x, k, minus);
                         in = fma(dk * wk, q, c1);
                     } else {
-                        u = lanes<T, VB>(x, k);
+                        u = lanes<T, 16>(x, k);
                         in = dk * wk * q;
                         aw[i * PN + k] = fma(dk * u, q, aw[i * PN + k]);
                     }
-                    fma(u, c2, in).put(o + k * W);
+                    fma(u, c2, in).put(o + 2 * k);
                 }
-                if (on) st_stream<VB>(dst + i * G * VB, pack<T, VB>(o));
+                if (on) st_stream<16>(dst + i * G * 16, pack<T, 16>(o));
+            }
+            if (SHIFT && edge && here) {
+                const float d = ld_elem<T>(edge_d), u = ld_elem<T>(edge_x) - mean[r];
+                if (!LAYER) edge_aw = fmaf(d * u, rstd[r], edge_aw);
+                st_elem<T>(p.out, at + rv.edge_col(t), fmaf(u, k2, fmaf(d * edge_w, rstd[r], k1)));
             }
         }
 #pragma unroll
@@ -332,19 +372,19 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_staged_kernel(con
             mean[r] = next_mean[r];
             rstd[r] = next_rstd[r];
         }
-        step.next(ring.nslots);
+        step.next(p.nslots);
     }
     if (n < ring.count) {
         // a wait ran out: report it, and let the copies that are under way land
         if (tid == 0) {
             report_timeout(p.status, kSiteStagedFull);
-            ring.drain(step, n, p.timeout_ns);
+            ring.drain(step, n);
         }
         __syncthreads();
         return;
     }
     // the CTA's part: its row groups' sums, in order
-    auto write_part = [&](const L* acc, float* part) {
+    auto write_part = [&](const L* acc, float edge_acc, float* part) {
         float* sums = reinterpret_cast<float*>(smem);
         __syncthreads();
 #pragma unroll
@@ -352,9 +392,10 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_staged_kernel(con
             if (valid[i]) {
 #pragma unroll
                 for (int k = 0; k < PN; ++k)
-                    acc[i * PN + k].put(sums + g * p.hidden + (i * G + t) * EPV + k * W);
+                    acc[i * PN + k].put(sums + g * p.hidden + rv.col(i * G + t) + 2 * k);
             }
         }
+        if (edge) sums[g * p.hidden + rv.edge_col(t)] = edge_acc;
         __syncthreads();
         float* out = part + static_cast<int64_t>(blockIdx.x) * p.hidden;
         for (int c = tid; c < p.hidden; c += blockDim.x) {
@@ -363,20 +404,21 @@ __global__ void __launch_bounds__(kNormBwdMaxThreads) norm_bwd_staged_kernel(con
             out[c] = v;
         }
     };
-    if (p.part_w) write_part(aw, p.part_w);
-    if (LAYER && p.part_b) write_part(ab, p.part_b);
+    if (p.part_w) write_part(aw, edge_aw, p.part_w);
+    if (LAYER && p.part_b) write_part(ab, edge_ab, p.part_b);
 }
 
-// dw and db from the parts: a CTA takes 8 columns (a
-// sector of a part), its 32 rows of threads every 32nd part each, ten loads in
-// flight, then their sums in order.  grid.y: 0 = dw, 1 = db.
-static __global__ void __launch_bounds__(kNormReduceCols * kNormReduceLanes)
+// dw and db from the parts: a CTA takes 256 / p.lanes columns, a column's
+// threads every p.lanes-th part each, ten loads in flight, then their sums in
+// order.  grid.y: 0 = dw, 1 = db.
+static __global__ void __launch_bounds__(kNormReduceThreads)
 norm_bwd_reduce_kernel(const NormParams p) {
-    __shared__ float red[kNormReduceLanes][kNormReduceCols + 1];
+    __shared__ float red[kNormReduceThreads];
     pdl_trigger();
     pdl_wait();
-    const int c = threadIdx.x % kNormReduceCols, l = threadIdx.x / kNormReduceCols;
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * kNormReduceCols + c;
+    const int lanes = p.lanes, cols = kNormReduceThreads / lanes;
+    const int c = threadIdx.x % cols, l = threadIdx.x / cols;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * cols + c;
     const float* part = blockIdx.y ? p.part_b : p.part_w;
     float* out = blockIdx.y ? p.db : p.dw;
     if (!part) return;
@@ -384,19 +426,19 @@ norm_bwd_reduce_kernel(const NormParams p) {
     constexpr int U = 10;
     const float* from = part + (col < p.hidden ? col : 0);
     float s = 0.f;
-    for (int k = l; k < p.parts; k += U * kNormReduceLanes) {
+    for (int k = l; k < p.parts; k += U * lanes) {
         float v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            v[u] = from[static_cast<int64_t>(min(k + u * kNormReduceLanes, p.parts - 1)) * p.hidden];
+            v[u] = from[static_cast<int64_t>(min(k + u * lanes, p.parts - 1)) * p.hidden];
 #pragma unroll
-        for (int u = 0; u < U; ++u) s += k + u * kNormReduceLanes < p.parts ? v[u] : 0.f;
+        for (int u = 0; u < U; ++u) s += k + u * lanes < p.parts ? v[u] : 0.f;
     }
-    red[l][c] = s;
+    red[threadIdx.x] = s;
     __syncthreads();
     if (l == 0 && col < p.hidden) {
         s = 0.f;
-        for (int k = 0; k < kNormReduceLanes; ++k) s += red[k][c];
+        for (int k = 0; k < lanes; ++k) s += red[k * cols + c];
         out[col] = s;
     }
 }

@@ -82,49 +82,80 @@ int clamp_grid(int64_t want, int64_t most) { return static_cast<int>(want < most
 
 // ------------------------------------------------------ layer norm forward --
 
-// Rows staged in shared memory: 64 bytes of a row per thread (16 vectors of 2
-// bytes: 32), CTAs of 256 threads or one row, a ring of two blocks, one wave of
+// How rows are staged (k_blockring.cuh): as they are where they, the arrays and
+// the weights are on 16-byte boundaries, else shifted, which wants the arrays on
+// one and rows of 32 bytes at least.
+struct StagedRows {
+    bool shift;
+    int period;             // rows after which their alignment repeats
+    int64_t nvec;           // whole vectors of a row, at most
+    int64_t row_slot;       // bytes of a row in shared memory: the vectors it touches
+};
+
+bool staged_rows(const NormCall& c, uintptr_t more_weights, StagedRows* r) {
+    const NormParams& p = c.p;
+    const int64_t row_bytes = static_cast<int64_t>(p.hidden) * c.sz;
+    if (!aligned(p.x, 16) || !aligned(p.dy, 16) || !aligned(p.out, 16)) return false;
+    const int epv = 16 / c.sz;
+    r->shift = row_bytes % 16 != 0 || !aligned(p.w, 16) || more_weights % 16 != 0;
+    r->period = 1;
+    r->nvec = row_bytes / 16;
+    r->row_slot = row_bytes;
+    if (!r->shift) return true;
+    if (row_bytes < 32 || row_bytes > (1 << 20)) return false;
+    while (r->period * p.hidden % epv != 0) r->period *= 2;
+    r->nvec = p.hidden / epv;
+    r->row_slot = (static_cast<int64_t>(p.hidden) + 2 * (epv - 1)) / epv * 16;
+    return true;
+}
+
+// CTAs for blocks of `block_rows` rows: one wave, at least one per alignment.
+int staged_grid(const NormCall& c, const StagedRows& r, int64_t block_rows, int64_t resident) {
+    const int64_t blocks = r.period * div_up(div_up(c.p.rows, r.period), block_rows);
+    const int64_t n = blocks < resident ? blocks : resident;
+    return static_cast<int>(n < r.period ? r.period : n);
+}
+
+// Rows staged in shared memory: 64 bytes of a row per thread, CTAs of 256 threads or one row, a ring of two blocks, one wave of
 // resident CTAs.  Measured (% of the HBM copy peak), 65536 rows of 4096 fp32 /
 // 4096 bf16 / 1024 bf16: 32 bytes a thread 73 / 52 / 50, 64 bytes 98 / 92 / 86,
 // 128 bytes 94 / 77 / 71 (fewer, longer threads); rings of three blocks 94 /
 // 87 / 81 (fewer CTAs); CTAs of about four blocks each instead of one wave 92 /
 // 85 / 81 (each CTA starts with an empty ring).  Leaves *fn null, status OK,
-// where rows do not fit two slots or x is not on a 16-byte boundary.
+// where rows cannot be staged or two do not fit shared memory.
 constexpr int64_t kStagedRowBytesPerThread = 64;
-constexpr int64_t kStagedMaxVecsPerThread = 16;
 constexpr int64_t kStagedBlock = 256;
 constexpr int64_t kStagedSlots = 2;
 
-int group_of(int64_t nvec, int64_t vecs_per_thread) {
-    const int64_t g = div_up(nvec, vecs_per_thread);
+int group_of(int64_t nvec, int64_t vecs_per_thread, int least) {
+    int64_t g = div_up(nvec, vecs_per_thread);
     if (g > 1024) return 1024;
+    if (g < least) g = least;
     return g <= 32 ? pow2_ceil(g) : static_cast<int>(div_up(g, 32) * 32);
 }
 
 rmsnorm_status_t plan_staged(int32_t dtype, NormCall* c, LaunchShape* s, NormFn* fn) {
-    const int64_t row_bytes = static_cast<int64_t>(c->p.hidden) * c->sz;
-    if (!aligned(c->p.x, 16)) return RMSNORM_OK;
-    int64_t vecs = kStagedRowBytesPerThread / c->vb;
-    if (vecs > kStagedMaxVecsPerThread) vecs = kStagedMaxVecsPerThread;
-    const int group = group_of(c->p.nvec, vecs);
+    StagedRows r;
+    if (!staged_rows(*c, reinterpret_cast<uintptr_t>(c->p.b), &r)) return RMSNORM_OK;
+    const int group = group_of(r.nvec, kStagedRowBytesPerThread / 16, 1);
     const int64_t rpc = group < kStagedBlock ? kStagedBlock / group : 1;
     const int block = static_cast<int>(rpc * group);
-    const int64_t slot = div_up(rpc * row_bytes + 32, 128) * 128;     // 16-byte rounding at both ends
-    if (kStagedSlots * slot > c->dv.smem_optin - 2048) return RMSNORM_OK;
-    const int smem = static_cast<int>(kStagedSlots * slot);
-    const NormFn f = layernorm_staged_ptr(dtype, c->vb);
+    const int64_t bytes = kStagedSlots * rpc * r.row_slot + (r.shift ? 2 * r.row_slot : 0);
+    if (bytes > c->dv.smem_optin - 2048) return RMSNORM_OK;
+    const int smem = static_cast<int>(bytes);
+    const NormFn f = layernorm_staged_ptr(dtype, r.shift);
     int occ = 0;
     if (cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(f), block, smem, 1,
                          &occ) != cudaSuccess)
         return RMSNORM_ERR_CUDA;
     if (occ < 1) return RMSNORM_OK;
-    *s = LaunchShape{clamp_grid(div_up(c->p.rows, rpc), static_cast<int64_t>(c->dv.sms) * occ), block,
-                     1, smem};
+    *s = LaunchShape{staged_grid(*c, r, rpc, static_cast<int64_t>(c->dv.sms) * occ), block, 1, smem};
     *fn = f;
     c->p.group = group;
     c->p.rows_per_cta = static_cast<int32_t>(rpc);
     c->p.nslots = static_cast<int32_t>(kStagedSlots);
-    c->p.slot_bytes = static_cast<int32_t>(slot);
+    c->p.row_slot = static_cast<int32_t>(r.row_slot);
+    c->p.period = r.period;
     set_waits(c);
     return RMSNORM_OK;
 }
@@ -209,30 +240,33 @@ int64_t bwd_staged_ctas(const DeviceView& dv, int64_t hidden) {
 }
 
 rmsnorm_status_t plan_bwd_staged(int32_t dtype, NormCall* c, LaunchShape* s, NormFn* fn) {
-    const int64_t row_bytes = static_cast<int64_t>(c->p.hidden) * c->sz;
-    if (!aligned(c->p.x, 16) || !aligned(c->p.dy, 16)) return RMSNORM_OK;
-    const int64_t vecs = kNormBwdElems / (c->vb / c->sz);
-    const int group = group_of(c->p.nvec, vecs);
-    if (c->p.nvec > kNormBwdMaxThreads * vecs) return RMSNORM_OK;
+    StagedRows r;
+    if (!staged_rows(*c, 0, &r)) return RMSNORM_OK;
+    const int epv = 16 / c->sz;
+    const int elems = r.nvec * epv > 16 * kNormBwdMaxThreads ? 32 : 16;
+    const int64_t vecs = elems / epv;
+    if (r.nvec > kNormBwdMaxThreads * vecs) return RMSNORM_OK;
+    const int group = group_of(r.nvec, vecs, r.shift ? 16 : 1);     // shifted: a thread per edge element
     const int64_t rpc = group < kBwdBlock ? kBwdBlock / group : 1;
     const int block = static_cast<int>(rpc * group);
-    const bool full = c->p.w && c->p.nvec == group * vecs;
     const bool bf16 = dtype == RMSNORM_DTYPE_BF16;
-    const int64_t budget = c->dv.smem_optin - 2048;
+    const int mode = r.shift ? 2 : (c->p.w && r.nvec == group * vecs ? 0 : 1);
+    const int64_t weights = r.shift ? r.row_slot : 0;
+    const int64_t budget = c->dv.smem_optin - 2048 - weights;
     const int64_t ctas_most = bwd_staged_ctas(c->dv, c->p.hidden);
-    // one array's share of a slot: its rows, rounded to 16 bytes at both ends
-    auto slot_of = [&](int rows) { return div_up(rows * rpc * row_bytes + 32, 128) * 128; };
+    // one array's share of a slot
+    auto slot_of = [&](int rows) { return rows * rpc * r.row_slot; };
     int rows = 1;
-    if (full && (c->layer || !bf16) && 4 * slot_of(2) <= budget &&
+    if (mode == 0 && elems == 16 && (c->layer || !bf16) && 4 * slot_of(2) <= budget &&
         c->p.rows >= 2 * rpc * kBwdTwoRowBlocks * ctas_most)
         rows = 2;
     const int64_t slot = slot_of(rows);
     int64_t slots = kBwdSlots;
     while (slots > 2 && 2 * slots * slot > budget) --slots;
     if (2 * slots * slot > budget) return RMSNORM_OK;
-    const int smem = static_cast<int>(2 * slots * slot);
-    const NormFn f = bf16 ? norm_bwd_staged_ptr_bf16(c->vb, c->layer, rows, full)
-                          : norm_bwd_staged_ptr_f32(c->vb, c->layer, rows, full);
+    const int smem = static_cast<int>(2 * slots * slot + weights);
+    const NormFn f = bf16 ? norm_bwd_staged_ptr_bf16(elems, c->layer, rows, mode)
+                          : norm_bwd_staged_ptr_f32(elems, c->layer, rows, mode);
     int occ = 0;
     if (cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(f), block, smem, 1,
                          &occ) != cudaSuccess)
@@ -240,12 +274,13 @@ rmsnorm_status_t plan_bwd_staged(int32_t dtype, NormCall* c, LaunchShape* s, Nor
     if (occ < 1) return RMSNORM_OK;
     int64_t ctas = static_cast<int64_t>(c->dv.sms) * occ;
     if (ctas > ctas_most) ctas = ctas_most;
-    *s = LaunchShape{clamp_grid(div_up(c->p.rows, rows * rpc), ctas), block, 1, smem};
+    *s = LaunchShape{staged_grid(*c, r, rows * rpc, ctas), block, 1, smem};
     *fn = f;
     c->p.group = group;
     c->p.rows_per_cta = static_cast<int32_t>(rpc);
     c->p.nslots = static_cast<int32_t>(slots);
-    c->p.slot_bytes = static_cast<int32_t>(slot);
+    c->p.row_slot = static_cast<int32_t>(r.row_slot);
+    c->p.period = r.period;
     c->p.parts = s->grid;
     set_waits(c);
     return RMSNORM_OK;
@@ -261,7 +296,7 @@ BwdSpace bwd_space(const DeviceView& dv, int64_t rows, int64_t hidden, int sz, b
     auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
     s.parts = bwd_parts(dv, rows, hidden, sz);
     int64_t staged = bwd_staged_ctas(dv, hidden);
-    if (staged > rows) staged = rows;
+    if (staged > rows + 8) staged = rows + 8;     // a block more per alignment at most
     if (s.parts < staged) s.parts = staged;
     s.row_stats = 0;
     s.part_w = up(static_cast<uint64_t>(rows) * 8);
@@ -270,11 +305,16 @@ BwdSpace bwd_space(const DeviceView& dv, int64_t rows, int64_t hidden, int sz, b
     return s;
 }
 
-rmsnorm_status_t launch_reduce(const NormCall& c, cudaStream_t stream) {
-    LaunchShape s{static_cast<int>(div_up(c.p.hidden, kNormReduceCols)),
-                  kNormReduceCols * kNormReduceLanes, 1, 0};
-    s.grid_y = c.p.db ? 2 : 1;
-    return launch(c, norm_bwd_reduce_ptr(), s, stream);
+// Few parts: eight threads per column, whose ten loads in flight take 80 parts
+// at once; more: 32 threads, 8 columns (one sector of a part) to a CTA.
+constexpr int kReduceFewParts = 80;
+
+rmsnorm_status_t launch_reduce(NormCall* c, cudaStream_t stream) {
+    c->p.lanes = c->p.parts <= kReduceFewParts ? 8 : 32;
+    LaunchShape s{static_cast<int>(div_up(c->p.hidden, kNormReduceThreads / c->p.lanes)),
+                  kNormReduceThreads, 1, 0};
+    s.grid_y = c->p.db ? 2 : 1;
+    return launch(*c, norm_bwd_reduce_ptr(), s, stream);
 }
 
 rmsnorm_status_t bwd_workspace(int32_t dtype, int64_t rows, int64_t hidden, bool layer,
@@ -346,7 +386,7 @@ rmsnorm_status_t bwd_run(int32_t dtype, bool layer, const void* dy, const void* 
         if (fn) {
             st = launch(c, fn, s, stream);
             if (st != RMSNORM_OK || (!dw && !db)) return st;
-            return launch_reduce(c, stream);
+            return launch_reduce(&c, stream);
         }
         if (c.opt.path == RMSNORM_PATH_STAGED) return RMSNORM_ERR_UNSUPPORTED;
     }
@@ -359,7 +399,7 @@ rmsnorm_status_t bwd_run(int32_t dtype, bool layer, const void* dy, const void* 
     cs.grid_y = c.p.parts;
     st = launch(c, norm_bwd_cols_ptr(dtype, c.vb, layer), cs, stream);
     if (st != RMSNORM_OK || (!dw && !db)) return st;
-    return launch_reduce(c, stream);
+    return launch_reduce(&c, stream);
 }
 
 }  // namespace

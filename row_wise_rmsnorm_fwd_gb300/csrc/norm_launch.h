@@ -26,8 +26,10 @@ struct NormParams {
     int32_t parts;
     int32_t group;         // staged kernels: threads per row
     int32_t rows_per_cta;  // rows of a block
-    int32_t nslots;        // ring slots, and one array's bytes of each
-    int32_t slot_bytes;
+    int32_t lanes;         // backward, sums over the parts: threads per column
+    int32_t nslots;        // ring slots
+    int32_t row_slot;      // bytes of a row in them
+    int32_t period;        // rows after which the rows' alignment repeats
     int32_t fault;         // failure-detection test builds only (else always 0)
     unsigned* status;
     uint64_t timeout_ns;
@@ -40,7 +42,8 @@ using NormFn = void (*)(NormParams);
 // dtype: 0 = fp32, 1 = bf16; vb = bytes per vector.
 NormFn layernorm_twopass_ptr(int dtype, int vb);
 int layernorm_twopass_block();
-NormFn layernorm_staged_ptr(int dtype, int vb);
+// Rows staged in shared memory; shift: rows of any length (see k_blockring.cuh).
+NormFn layernorm_staged_ptr(int dtype, bool shift);
 // Backward in three kernels: a pair of sums for each row, then dx and the
 // partial column sums, then the sums over the parts.  layer: layer norm, else
 // RMSNorm.
@@ -48,15 +51,14 @@ NormFn norm_bwd_rows_ptr(int dtype, int vb, bool layer);
 int norm_bwd_rows_block();
 NormFn norm_bwd_cols_ptr(int dtype, int vb, bool layer);
 int norm_bwd_cols_block();
-// One pass over staged rows, kNormBwdElems elements per thread and row: rows =
-// rows of a thread between barriers (2: only if full), full: whole vectors only
-// and weights given.
-NormFn norm_bwd_staged_ptr_f32(int vb, bool layer, int rows, bool full);
-NormFn norm_bwd_staged_ptr_bf16(int vb, bool layer, int rows, bool full);
-constexpr int kNormBwdElems = 16;
+// One pass over staged rows, elems (16 or 32) elements per thread and row; mode:
+// 0 whole vectors only and weights given, 1 aligned rows, 2 rows of any length;
+// rows = rows of a thread between barriers (2: 16 elements and mode 0 only).
+NormFn norm_bwd_staged_ptr_f32(int elems, bool layer, int rows, int mode);
+NormFn norm_bwd_staged_ptr_bf16(int elems, bool layer, int rows, int mode);
 constexpr int kNormBwdMaxThreads = 512;
 NormFn norm_bwd_reduce_ptr();
-constexpr int kNormReduceCols = 8;       // columns of one CTA of the last kernel
-constexpr int kNormReduceLanes = 32;     // parts it adds side by side
+// The last kernel's CTA of 256 threads: `lanes` threads to a column.
+constexpr int kNormReduceThreads = 256;
 
 }  // namespace rmsnorm

@@ -3,28 +3,26 @@
 
 namespace rmsnorm {
 
-template <int VB, bool LAYER>
-static NormFn pick(int rows, bool full) {
+template <int ELEMS, bool LAYER>
+static NormFn pick(int rows, int mode) {
     using T = __nv_bfloat16;
-    constexpr int NV = kNormBwdElems / VecTraits<T, VB>::kElems;
-    if (!full) return rows == 1 ? norm_bwd_staged_kernel<T, VB, NV, LAYER, 1, false> : nullptr;
-    return rows == 1 ? norm_bwd_staged_kernel<T, VB, NV, LAYER, 1, true>
-                     : norm_bwd_staged_kernel<T, VB, NV, LAYER, 2, true>;
-}
-
-template <int VB>
-static NormFn staged(bool layer, int rows, bool full) {
-    return layer ? pick<VB, true>(rows, full) : pick<VB, false>(rows, full);
-}
-
-NormFn norm_bwd_staged_ptr_bf16(int vb, bool layer, int rows, bool full) {
-    switch (vb) {
-        case 16: return staged<16>(layer, rows, full);
-        case 8: return staged<8>(layer, rows, full);
-        case 4: return staged<4>(layer, rows, full);
-        case 2: return staged<2>(layer, rows, full);
+    constexpr int NV = ELEMS / VecTraits<T, 16>::kElems;
+    if (rows == 2) {
+        if constexpr (ELEMS == 16)
+            if (mode == kWhole) return norm_bwd_staged_kernel<T, NV, LAYER, 2, kWhole>;
+        return nullptr;
+    }
+    switch (mode) {
+        case kWhole: return norm_bwd_staged_kernel<T, NV, LAYER, 1, kWhole>;
+        case kPartial: return norm_bwd_staged_kernel<T, NV, LAYER, 1, kPartial>;
+        case kShift: return norm_bwd_staged_kernel<T, NV, LAYER, 1, kShift>;
         default: return nullptr;
     }
+}
+
+NormFn norm_bwd_staged_ptr_bf16(int elems, bool layer, int rows, int mode) {
+    if (elems == 32) return layer ? pick<32, true>(rows, mode) : pick<32, false>(rows, mode);
+    return layer ? pick<16, true>(rows, mode) : pick<16, false>(rows, mode);
 }
 
 }  // namespace rmsnorm

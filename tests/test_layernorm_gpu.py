@@ -24,7 +24,11 @@ def lib():
 # several rows per warp, one per CTA, rows too wide for one CTA's registers
 SHAPES = [(1, 1), (5, 3), (3, 8), (7, 33), (33, 64), (300, 100), (9, 257), (200, 512),
           (31, 1000), (128, 2048), (17, 2050), (40, 3584), (19, 4097), (3, 8191), (160, 8192),
-          (5, 8200), (3, 16384), (2, 16390), (2, 40000), (1, 70001)]
+          (5, 8200), (3, 16384), (2, 16390), (2, 40000), (1, 70001),
+          # rows that touch a boundary differently one after the other: every odd residue, few
+          # rows per alignment, the last row's end on and off a boundary
+          (1, 16), (2, 17), (9, 19), (16, 21), (23, 23), (8, 1025), (9, 1026), (41, 1028),
+          (7, 12001), (10, 12002), (3, 16383)]
 PATHS = [None, {"path": "twopass"}]
 
 
@@ -88,7 +92,8 @@ def test_rmsnorm_backward(rows, hidden, t, options):
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,hidden", [(2000, 64), (700, 1024), (1300, 2048), (611, 130)])
+@pytest.mark.parametrize("rows,hidden", [(2000, 64), (700, 1024), (1300, 2048), (611, 130),
+                                         (3001, 33), (2500, 255), (1999, 1001), (1500, 2050)])
 def test_many_rows_per_cta(rows, hidden, t):
     x, w, b, dy = inputs(t, rows, hidden, 9)
     check_fwd(fwd(x, w, b), x, w, b)
@@ -108,7 +113,7 @@ def test_without_weight_or_bias(hidden, t, with_w, with_b):
 
 
 @pytest.mark.parametrize("options", PATHS, ids=["auto", "twopass"])
-@pytest.mark.parametrize("hidden", [48, 2048, 8192, 40000])
+@pytest.mark.parametrize("hidden", [48, 333, 2048, 4099, 8192, 40000])
 def test_rows_far_from_zero(hidden, options):
     """A mean a thousand times the spread: a variance formed as E[x^2] - E[x]^2
     in fp32 would be off by 10%."""
@@ -121,7 +126,7 @@ def test_rows_far_from_zero(hidden, options):
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
-@pytest.mark.parametrize("hidden", [64, 100, 4096, 40000])
+@pytest.mark.parametrize("hidden", [64, 100, 259, 4096, 4098, 40000])
 def test_constant_rows_and_bad_rows(hidden, t):
     """A constant row gives b exactly (rstd = eps^-1/2); a NaN or an infinity
     makes its own row NaN and no other."""
@@ -140,8 +145,8 @@ def test_constant_rows_and_bad_rows(hidden, t):
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
-@pytest.mark.parametrize("hidden", [64, 1024, 4096, 8192, 40000])
-@pytest.mark.parametrize("shift", [1, 2, 4])
+@pytest.mark.parametrize("hidden", [64, 77, 1024, 2050, 4096, 8192, 40000])
+@pytest.mark.parametrize("shift", [1, 2, 4, 8])
 def test_pointers_off_a_vector_boundary(hidden, t, shift):
     """Views that start `shift` elements into a buffer; guards on both sides
     of every output stay as they were."""
@@ -177,7 +182,7 @@ def test_pointers_off_a_vector_boundary(hidden, t, shift):
 
 @pytest.mark.parametrize("options", PATHS, ids=["auto", "twopass"])
 @pytest.mark.parametrize("t", ["f32", "bf16"])
-@pytest.mark.parametrize("hidden", [64, 130, 2048, 8192, 16384, 40000])
+@pytest.mark.parametrize("hidden", [64, 130, 1025, 2048, 8192, 16384, 40000])
 def test_in_place(hidden, t, options):
     x, w, b, dy = inputs(t, 37, hidden, 60)
     xs, ws, bs, ds = (v.cuda() for v in (x, w, b, dy))
@@ -229,6 +234,21 @@ def test_optional_outputs_and_exact_workspace(t):
     assert torch.equal(dx, full[0]) and dw is None
     with pytest.raises(binding.RmsnormError):
         binding.rmsnorm_bwd_ex(ds, xs, ws, workspace=room[:size - 16])
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,hidden", [(1, 333), (9, 333), (40, 2049), (700, 1026), (5000, 97)])
+def test_workspace_of_rows_of_any_length(rows, hidden, t):
+    """The stated workspace suffices whatever the rows' alignment does."""
+    x, w, _, dy = inputs(t, rows, hidden, 75)
+    xs, ws, ds = x.cuda(), w.cuda(), dy.cuda()
+    size = binding.rmsnorm_bwd_workspace(xs)
+    room = torch.full((size + 65536,), 0xA5, dtype=torch.uint8, device="cuda")
+    got = binding.rmsnorm_bwd_ex(ds, xs, ws, workspace=room[:size])
+    want, tol = ref.rmsnorm_bwd(dy, x, w, 1e-6)
+    for g, r, e in zip(got, want, tol):
+        close(g, r, e)
+    assert (room[size:] == 0xA5).all()
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
@@ -341,7 +361,7 @@ def flib():
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
-@pytest.mark.parametrize("hidden", [500, 2048, 8192])
+@pytest.mark.parametrize("hidden", [500, 501, 2048, 8192])
 @pytest.mark.parametrize("op", ["layernorm_fwd", "layernorm_bwd", "rmsnorm_bwd"])
 def test_withheld_copy_ends_in_a_status(flib, op, hidden, t):
     """A staged kernel whose first copy never lands leaves after its wait's
