@@ -353,17 +353,19 @@ __global__ void __launch_bounds__(kBiasWideThreads) relbias_bwd_wide_kernel(cons
 // are not a multiple of 16 bytes) a row's vector 0 is the one that holds its
 // first key, `shift` elements into it, so keys have indices from `shift` on;
 // the vectors at its two ends are stored element by element.
-constexpr int kBiasVecs = 4;             // vectors per thread
 
 // Registers per thread: what the widest instances take without spilling and,
 // above that, no more, for resident warps (the row's loads are the only ones in
-// flight).  Measured (% of the HBM copy peak): bf16 forward 96 / 112 / 128
+// flight).  Measured (% of the HBM copy peak, 4 vectors): bf16 forward 96 / 112 / 128
 // registers 89 / 90 / 90 on rows of 2048 and 41 / 38 / 38 on a decoding step;
 // backward 64 / 72 / 80 registers, bf16 rows of 2048 90 / 94 / 96, causal 73 /
 // 75 / 71, of 512 68 / 80 / 69, fp32 rows of 1024 89 / 91 / 91.
-template <typename T>
-constexpr int bias_fwd_regs() { return sizeof(T) == 2 ? 96 : 80; }
-constexpr int kBiasBwdRegs = 72;
+template <typename T, int NV>
+constexpr int bias_fwd_regs() {
+    return NV == 4 ? (sizeof(T) == 2 ? 96 : 80) : (sizeof(T) == 2 ? 128 : 104);
+}
+template <int NV>
+constexpr int bias_bwd_regs() { return NV == 4 ? 72 : 96; }
 
 __device__ __forceinline__ float bias_max(float v, int width) {
     for (int m = width >> 1; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
@@ -501,23 +503,24 @@ template <bool SHIFT, int EPV>
 struct VecRow {
     int64_t at;
     int shift, to, end;
-    bool here;
-    __device__ __forceinline__ VecRow(const BiasRow& r, int k_len) {
+    bool here, cut;               // cut: its last valid keys' vector passes the array's end
+    __device__ __forceinline__ VecRow(const BiasRow& r, int k_len, int64_t total) {
         shift = SHIFT ? static_cast<int>(r.at & (EPV - 1)) : 0;
         at = r.at - shift;
         to = r.n > 0 ? r.n + shift : 0;
         end = k_len + shift;
         here = r.at >= 0;
+        cut = SHIFT && at + (to + EPV - 1) / EPV * EPV > total;
     }
 };
 
-// Vector at element e of an array of `total` elements: whole, or what of it
-// lies inside the array.
-template <typename T, bool SHIFT>
-__device__ __forceinline__ Vec<16> ld_vec(const void* base, int64_t e, int64_t total) {
+// Vector at element e of an array; `cut`: only what of it lies inside the
+// array of `total` elements.
+template <typename T>
+__device__ __forceinline__ Vec<16> ld_vec(const void* base, int64_t e, bool cut, int64_t total) {
     constexpr int EPV = VecTraits<T, 16>::kElems;
     const char* p = static_cast<const char*>(base) + e * static_cast<int>(sizeof(T));
-    if (!SHIFT || e + EPV <= total) return ld_stream<16>(p);
+    if (!cut) return ld_stream<16>(p);
     Vec<16> v = zero_vec<16>();
 #pragma unroll
     for (int k = 0; k < EPV; ++k) {
@@ -533,17 +536,19 @@ __device__ __forceinline__ Vec<16> ld_vec(const void* base, int64_t e, int64_t t
 }
 
 // Store a row's vector j / EPV: whole, or the elements inside the row.
+// `first`: it may be the row's first one.
 template <typename T, bool SHIFT, class Row>
-__device__ __forceinline__ void st_vec(void* base, const Row& r, int j, const Vec<16>& v) {
+__device__ __forceinline__ void st_vec(void* base, const Row& r, bool first, int j,
+                                       const Vec<16>& v) {
     constexpr int EPV = VecTraits<T, 16>::kElems;
     char* p = static_cast<char*>(base) + (r.at + j) * static_cast<int>(sizeof(T));
-    if (!SHIFT || (j >= r.shift && j + EPV <= r.end)) {
+    if (!SHIFT || ((!first || j >= r.shift) && j + EPV <= r.end)) {
         st_stream<16>(p, v);
         return;
     }
 #pragma unroll
     for (int k = 0; k < EPV; ++k) {
-        if (j + k >= r.shift && j + k < r.end) {
+        if ((!first || j + k >= r.shift) && j + k < r.end) {
             if constexpr (sizeof(T) == 4) {
                 Vec<4> o;
                 o.u[0] = v.u[k];
@@ -557,10 +562,9 @@ __device__ __forceinline__ void st_vec(void* base, const Row& r, int j, const Ve
     }
 }
 
-template <typename T, bool SHIFT>
-__global__ void __maxnreg__(bias_fwd_regs<T>()) relbias_fwd_rowreg_kernel(const BiasParams p) {
+template <typename T, int NV, bool SHIFT>
+__global__ void __maxnreg__((bias_fwd_regs<T, NV>())) relbias_fwd_rowreg_kernel(const BiasParams p) {
     constexpr int EPV = VecTraits<T, 16>::kElems;
-    constexpr int NV = kBiasVecs;
     constexpr int PN = PairTraits<T, 16>::N;
     using L = Lanes<2>;
     extern __shared__ __align__(16) float win[];
@@ -590,14 +594,17 @@ __global__ void __maxnreg__(bias_fwd_regs<T>()) relbias_fwd_rowreg_kernel(const 
     using Row = VecRow<SHIFT, EPV>;
     Vec<16> cur[NV], nxt[NV];
     auto load = [&](Vec<16> (&dst)[NV], const Row& r) {
+        auto vectors = [&](auto cut) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = (i * G + t) * EPV;
-            if (j < r.to) dst[i] = ld_vec<T, SHIFT>(p.x, r.at + j, p.elems);
-        }
+            for (int i = 0; i < NV; ++i) {
+                const int j = (i * G + t) * EPV;
+                if (j < r.to) dst[i] = ld_vec<T>(p.x, r.at + j, cut && j + EPV > r.to, p.elems);
+            }
+        };
+        if (r.cut) vectors(std::true_type()); else vectors(std::false_type());
     };
     BiasRow info = rows.get(p, head);
-    Row ri(info, p.k_len);
+    Row ri(info, p.k_len, p.elems);
     int r0 = info.r0 - ri.shift;                 // relative position of index 0
     load(cur, ri);
     for (int k = tid; k < p.num_buckets; k += blockDim.x) {
@@ -617,7 +624,7 @@ __global__ void __maxnreg__(bias_fwd_regs<T>()) relbias_fwd_rowreg_kernel(const 
     for (int it = 0; block < nblocks; block += p.parts, ++it) {
         rows.next(p);
         info = rows.get(p, head);
-        const Row rn(info, p.k_len);
+        const Row rn(info, p.k_len, p.elems);
         load(nxt, rn);
         L e[NV * PN];
         float m = -INFINITY, s = 0.f;
@@ -650,7 +657,7 @@ __global__ void __maxnreg__(bias_fwd_regs<T>()) relbias_fwd_rowreg_kernel(const 
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int at = j + 2 * k + h;
-                            if (at >= ri.to || (SHIFT && at < ri.shift)) a[h] = -INFINITY;
+                            if (at >= ri.to || (SHIFT && i == 0 && at < ri.shift)) a[h] = -INFINITY;
                         }
                         e[i * PN + k] = L::of(a);
                     }
@@ -700,19 +707,19 @@ __global__ void __maxnreg__(bias_fwd_regs<T>()) relbias_fwd_rowreg_kernel(const 
             for (int i = 0; i < NV; ++i) {
                 const int j = (i * G + t) * EPV;
                 if (!all && is.none(i)) {
-                    if (ri.here && j < ri.end) st_vec<T, SHIFT>(p.out, ri, j, zero_vec<16>());
+                    if (ri.here && j < ri.end) st_vec<T, SHIFT>(p.out, ri, i == 0, j, zero_vec<16>());
                     continue;
                 }
                 float o[EPV];
 #pragma unroll
                 for (int k = 0; k < PN; ++k) (e[i * PN + k] * inv).put(o + 2 * k);
                 if (all || is.full(i)) {
-                    st_vec<T, false>(p.out, ri, j, pack<T, 16>(o));
+                    st_vec<T, false>(p.out, ri, false, j, pack<T, 16>(o));
                 } else if (ri.here && j < ri.end) {
 #pragma unroll
                     for (int k = 0; k < EPV; ++k)
                         if (j + k >= ri.to) o[k] = 0.f;
-                    st_vec<T, SHIFT>(p.out, ri, j, pack<T, 16>(o));
+                    st_vec<T, SHIFT>(p.out, ri, i == 0, j, pack<T, 16>(o));
                 }
             }
         };
@@ -774,10 +781,9 @@ __device__ __forceinline__ void bias_fold_vec(const BiasParams& p, const VecWind
 // Backward: y and dy of a row in registers, the row's dot product exchanged
 // behind one barrier, which also orders the rows' updates of the group's
 // window (rows_per_cta windows per CTA).
-template <typename T, bool SHIFT>
-__global__ void __maxnreg__(kBiasBwdRegs) relbias_bwd_rowreg_kernel(const BiasParams p) {
+template <typename T, int NV, bool SHIFT>
+__global__ void __maxnreg__(bias_bwd_regs<NV>()) relbias_bwd_rowreg_kernel(const BiasParams p) {
     constexpr int EPV = VecTraits<T, 16>::kElems;
-    constexpr int NV = kBiasVecs;
     constexpr int PN = PairTraits<T, 16>::N;
     using L = Lanes<2>;
     extern __shared__ __align__(16) float wins[];
@@ -815,19 +821,22 @@ __global__ void __maxnreg__(kBiasBwdRegs) relbias_bwd_rowreg_kernel(const BiasPa
     float low = 0.f, high = 0.f;
     for (int it = 0; block < nblocks; block += p.parts, ++it, rows.next(p)) {
         const BiasRow info = rows.get(p, head);
-        const VecRow<SHIFT, EPV> ri(info, p.k_len);
+        const VecRow<SHIFT, EPV> ri(info, p.k_len, p.elems);
         const WindowRow<EPV> wr(w, info.r0 - ri.shift);
         const VecClasses<EPV, NV> is(ri.shift, ri.to, t, G);
         const bool all = is.all();
         Vec<16> y[NV], d[NV];
+        auto load = [&](auto cut) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = (i * G + t) * EPV;
-            if (j < ri.to) {
-                y[i] = ld_vec<T, SHIFT>(p.y, ri.at + j, p.elems);
-                d[i] = ld_vec<T, SHIFT>(p.x, ri.at + j, p.elems);
+            for (int i = 0; i < NV; ++i) {
+                const int j = (i * G + t) * EPV;
+                if (j < ri.to) {
+                    y[i] = ld_vec<T>(p.y, ri.at + j, cut && j + EPV > ri.to, p.elems);
+                    d[i] = ld_vec<T>(p.x, ri.at + j, cut && j + EPV > ri.to, p.elems);
+                }
             }
-        }
+        };
+        if (ri.cut) load(std::true_type()); else load(std::false_type());
         L s0 = L::all(0.f), s1 = L::all(0.f);
         // each pass twice: `all` vectors of the warp valid in full, or by class
         auto products = [&](auto all) {
@@ -838,7 +847,7 @@ __global__ void __maxnreg__(kBiasBwdRegs) relbias_bwd_rowreg_kernel(const BiasPa
                     const int j = (i * G + t) * EPV;
                     clear_from<T, 16>(y[i], max(ri.to - j, 0));
                     clear_from<T, 16>(d[i], max(ri.to - j, 0));
-                    if (SHIFT) {
+                    if (SHIFT && i == 0) {
                         clear_below<T, 16>(y[i], ri.shift - j);
                         clear_below<T, 16>(d[i], ri.shift - j);
                     }
@@ -861,20 +870,23 @@ __global__ void __maxnreg__(kBiasBwdRegs) relbias_bwd_rowreg_kernel(const BiasPa
         } else {
             __syncwarp();
         }
-        const L minus = L::all(-dot);
+        const L minus = L::all(-dot), zero = L::all(0.f);
+        // what was cleared stays 0 in y * (dy - dot) unless the dot product is
+        // infinite or NaN
+        const bool sound = fabsf(dot) < INFINITY;
         auto outputs = [&](auto all) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int v = i * G + t, j = v * EPV;
                 if (!all && is.none(i)) {
-                    if (ri.here && j < ri.end) st_vec<T, SHIFT>(p.out, ri, j, zero_vec<16>());
+                    if (ri.here && j < ri.end) st_vec<T, SHIFT>(p.out, ri, i == 0, j, zero_vec<16>());
                     continue;
                 }
                 L gk[PN];
 #pragma unroll
                 for (int k = 0; k < PN; ++k)
                     gk[k] = lanes<T, 16>(y[i], k) * (lanes<T, 16>(d[i], k) + minus);
-                if (!all && !is.full(i)) {           // 0 there, whatever the row's sum is
+                if (!all && !sound && !is.full(i)) {
 #pragma unroll
                     for (int k = 0; k < PN; ++k) {
                         float a[2];
@@ -882,16 +894,16 @@ __global__ void __maxnreg__(kBiasBwdRegs) relbias_bwd_rowreg_kernel(const BiasPa
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int at = j + 2 * k + h;
-                            if (at >= ri.to || (SHIFT && at < ri.shift)) a[h] = 0.f;
+                            if (at >= ri.to || (SHIFT && i == 0 && at < ri.shift)) a[h] = 0.f;
                         }
                         gk[k] = L::of(a);
                     }
                 }
                 float o[EPV];
 #pragma unroll
-                for (int k = 0; k < PN; ++k) (gk[k] * scale).put(o + 2 * k);
-                if (all || is.full(i)) st_vec<T, false>(p.out, ri, j, pack<T, 16>(o));
-                else if (ri.here && j < ri.end) st_vec<T, SHIFT>(p.out, ri, j, pack<T, 16>(o));
+                for (int k = 0; k < PN; ++k) fma(gk[k], scale, zero).put(o + 2 * k);   // -0: 0
+                if (all || is.full(i)) st_vec<T, false>(p.out, ri, false, j, pack<T, 16>(o));
+                else if (ri.here && j < ri.end) st_vec<T, SHIFT>(p.out, ri, i == 0, j, pack<T, 16>(o));
                 if (p.part && (all || j < ri.to)) {
                     if (v > wr.vmin && v < wr.vmax) {
                         float a[EPV];

@@ -154,15 +154,28 @@ rmsnorm_status_t plan_rowreg(int32_t dtype, BiasCall* c, uintptr_t bases, bool b
     const bool shift = c->p.k_len % epv != 0;
     // vectors a row touches, wherever it starts
     const int64_t nvec = shift ? (c->p.k_len + 2 * (epv - 1)) / epv : c->p.k_len / epv;
-    int64_t group = div_up(nvec, kBiasRowBytesPerThread / 16);
-    if (group > kBiasMaxThreads) return RMSNORM_OK;
-    if (group > 32) {
-        group = div_up(group, 32) * 32;
-    } else {
+    // Threads per row, of nv vectors each: whole warps, or a power of two.
+    auto threads_of = [&](int64_t nv) {
+        const int64_t n = div_up(nvec, nv);
+        if (n > 32) return div_up(n, 32) * 32;
         int64_t g = 1;
-        while (g < group) g <<= 1;
-        group = g;
+        while (g < n) g <<= 1;
+        return g;
+    };
+    // A row's time hardly depends on how many of its threads' vectors are in use,
+    // so 6 vectors per thread where they spare half of the threads, up to a warp
+    // per row.  Measured (us, 4 / 6): forward fp32 rows of 640 156 / 107, of 260
+    // 72 / 58, bf16 rows of 1536 180 / 147, of 768 80 / 76; backward bf16 rows of
+    // 1536 227 / 182, fp32 rows of 516 169 / 144.  Not below half a warp (fp32
+    // rows of 160, backward: 59 / 62) nor above a warp (forward fp32 rows of 2048
+    // 163 / 221, bf16 rows of 2056 155 / 164; backward 187 / 167 and 247 / 300).
+    int nv = 4;
+    int64_t group = threads_of(nv);
+    if (threads_of(6) < group && threads_of(6) >= 16 && threads_of(6) <= 32) {
+        nv = 6;
+        group = threads_of(nv);
     }
+    if (group > kBiasMaxThreads) return RMSNORM_OK;
     const int lo = static_cast<int>(c->window);
     const BiasVecWindow vw = bias_vec_window(lo, c->p.both ? lo : 0, static_cast<int>(epv));
     const int window = 4 * vw.copies * vw.copy;
@@ -179,7 +192,7 @@ rmsnorm_status_t plan_rowreg(int32_t dtype, BiasCall* c, uintptr_t bases, bool b
     const int64_t smem = bwd ? (sums ? rpc * window + 4 * vw.size : 0) : window;
     if (smem > c->dv.smem_optin - 8192) return RMSNORM_OK;
     const int block = static_cast<int>(rpc * group);
-    const BiasFn f = bwd ? relbias_bwd_rowreg_ptr(dtype, shift) : relbias_fwd_rowreg_ptr(dtype, shift);
+    const BiasFn f = relbias_rowreg_ptr(dtype, nv, shift, bwd);
     int occ = 0;
     if (cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(f), block,
                          static_cast<int>(smem), 1, &occ) != cudaSuccess)

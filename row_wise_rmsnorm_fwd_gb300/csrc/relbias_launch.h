@@ -63,12 +63,10 @@ constexpr BiasVecWindow bias_vec_window(int lo, int hi, int epv) {
 BiasFn relbias_fwd_wide_ptr(int dtype, int vb);
 BiasFn relbias_bwd_wide_ptr(int dtype, int vb);
 int relbias_wide_block();
-// Rows in registers: 64 bytes per thread, blocks of up to kBiasMaxThreads
+// Rows in registers: nv (4 or 6) 16-byte vectors per thread, blocks of up to kBiasMaxThreads
 // threads; shift: rows that are not a multiple of 16 bytes.
-BiasFn relbias_fwd_rowreg_ptr(int dtype, bool shift);
-BiasFn relbias_bwd_rowreg_ptr(int dtype, bool shift);
+BiasFn relbias_rowreg_ptr(int dtype, int nv, bool shift, bool bwd);
 constexpr int kBiasMaxThreads = 512;
-constexpr int kBiasRowBytesPerThread = 64;
 BiasFn relbias_reduce_ptr();
 int relbias_reduce_block();
 

@@ -46,6 +46,12 @@ CASES = {
     "far_queries": ((1, 2, 3, 100), Rule(q_offset=1 << 40)),
     "far_keys": ((1, 2, 3, 100), Rule(q_offset=-(1 << 40))),
     "many_rows": ((7, 2, 200, 48), Rule()),
+    # six vectors per thread: half a warp and a warp per row, either type
+    "half_warp": ((2, 3, 20, 264), Rule(q_offset=100, kv_len=[131, 264])),
+    "warp_odd": ((3, 2, 40, 601), Rule(both=False, causal=True, q_start=[561, 0, -20],
+                                       kv_len=[601, 40, 597])),
+    "warp_bf16": ((2, 2, 70, 1400), Rule(both=False, causal=True, q_offset=700)),
+    "warp_bf16_odd": ((2, 2, 33, 1283), Rule(q_offset=600, kv_len=[1283, 1025])),
 }
 
 
