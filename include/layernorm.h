@@ -57,8 +57,9 @@ rmsnorm_status_t layernorm_fwd_bf16(const uint16_t* x, const uint16_t* w, const 
 
 /* Either dtype, with options (`opt` may be NULL): opt->path RMSNORM_PATH_AUTO,
  * RMSNORM_PATH_STAGED (rows staged in shared memory by bulk copies, read from
- * HBM once: x on a 16-byte boundary, two blocks of rows within shared memory,
- * else RMSNORM_ERR_UNSUPPORTED) or RMSNORM_PATH_TWOPASS (a CTA per row that
+ * HBM once: x and y on 16-byte boundaries, rows of any length from 32 bytes (16,
+ * if they, w and b are multiples of 16 bytes, on such boundaries) to what two of
+ * fit shared memory, else RMSNORM_ERR_UNSUPPORTED) or RMSNORM_PATH_TWOPASS (a CTA per row that
  * reads it twice: any width and alignment); opt->wait_timeout_ns; and in the
  * test build of the library opt->fault_inject = 1 with RMSNORM_PATH_STAGED
  * (each CTA's first copy is withheld; elsewhere RMSNORM_ERR_UNSUPPORTED).
@@ -87,8 +88,8 @@ rmsnorm_status_t layernorm_bwd_bf16(const uint16_t* dy, const uint16_t* x, const
                                     size_t workspace_bytes, rmsnorm_stream_t stream);
 
 /* Either dtype, with options as for layernorm_fwd_ex.  RMSNORM_PATH_STAGED: x
- * and dy read from HBM once (both on a 16-byte boundary, rows of up to 512
- * threads of 16 elements); RMSNORM_PATH_TWOPASS: a pair of sums per row, then
+ * and dy read from HBM once (x, dy and dx on 16-byte boundaries, rows as there
+ * and of at most 16384 elements); RMSNORM_PATH_TWOPASS: a pair of sums per row, then
  * dx and partial column sums, each reading x and dy once. */
 rmsnorm_status_t layernorm_bwd_ex(int32_t dtype, const void* dy, const void* x, const void* w,
                                   const float* mean, const float* rstd, void* dx, float* dw,

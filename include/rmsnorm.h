@@ -266,8 +266,9 @@ rmsnorm_status_t rmsnorm_bwd_bf16(const uint16_t* dy, const uint16_t* x, const u
 
 /* Either dtype, with options (`opt` may be NULL): opt->path RMSNORM_PATH_AUTO,
  * RMSNORM_PATH_STAGED (rows staged in shared memory by bulk copies, x and dy
- * read from HBM once: both on a 16-byte boundary, rows of up to 512 threads of
- * 16 elements, else RMSNORM_ERR_UNSUPPORTED) or RMSNORM_PATH_TWOPASS (a pair of
+ * read from HBM once: they and dx on 16-byte boundaries, rows of any length from
+ * 32 bytes (16, if they and w are multiples of 16 bytes, on such boundaries) to
+ * 16384 elements and what fits shared memory, else RMSNORM_ERR_UNSUPPORTED) or RMSNORM_PATH_TWOPASS (a pair of
  * sums per row, then dx and partial column sums, each reading x and dy once:
  * any width and alignment); opt->wait_timeout_ns; and in the test build of the
  * library opt->fault_inject = 1 with RMSNORM_PATH_STAGED (each CTA's first copy

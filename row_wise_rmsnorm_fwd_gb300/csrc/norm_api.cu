@@ -116,13 +116,14 @@ int staged_grid(const NormCall& c, const StagedRows& r, int64_t block_rows, int6
     return static_cast<int>(n < r.period ? r.period : n);
 }
 
-// Rows staged in shared memory: 64 bytes of a row per thread, CTAs of 256 threads or one row, a ring of two blocks, one wave of
-// resident CTAs.  Measured (% of the HBM copy peak), 65536 rows of 4096 fp32 /
-// 4096 bf16 / 1024 bf16: 32 bytes a thread 73 / 52 / 50, 64 bytes 98 / 92 / 86,
-// 128 bytes 94 / 77 / 71 (fewer, longer threads); rings of three blocks 94 /
-// 87 / 81 (fewer CTAs); CTAs of about four blocks each instead of one wave 92 /
-// 85 / 81 (each CTA starts with an empty ring).  Leaves *fn null, status OK,
-// where rows cannot be staged or two do not fit shared memory.
+// Rows staged in shared memory: 64 bytes of a row per thread, CTAs of 256 threads
+// or one row, a ring of two blocks, one wave of resident CTAs.  Measured (% of
+// the HBM copy peak), 65536 rows of 4096 fp32 / 4096 bf16 / 8192 bf16: 32 bytes a
+// thread 75 / 70 / 68, 64 bytes 99 / 91 / 92, 128 bytes (fewer, longer threads)
+// 89 / 87 / 88; rings of three blocks (fewer CTAs) 92 / 87 / 88; CTAs of about
+// four blocks each instead of one wave 92 / 85 / 81 (each CTA starts with an
+// empty ring).  Leaves *fn null, status OK, where rows cannot be staged or two
+// blocks do not fit shared memory.
 constexpr int64_t kStagedRowBytesPerThread = 64;
 constexpr int64_t kStagedBlock = 256;
 constexpr int64_t kStagedSlots = 2;
@@ -218,16 +219,17 @@ int64_t bwd_parts(const DeviceView& dv, int64_t rows, int64_t hidden, int sz) {
     return parts < 1 ? 1 : parts;
 }
 
-// Rows staged in shared memory, read once: 16 elements of a row per thread,
-// CTAs of 256 threads or one row, a ring of three blocks, one wave of resident
-// CTAs.  Two rows between barriers where the rows are enough to give every CTA
-// several such blocks, except for RMSNorm in bf16, whose kernel needs few
-// registers with one row (62: four CTAs per SM) and many with two (74: three).
-// Measured (% of the HBM copy peak, one row / two rows between barriers):
-// layer norm bf16 rows of 8192 88 / 90, of 4096 87 / 87, fp32 rows of 4096 94 /
-// 97; RMSNorm bf16 rows of 4096 96 / 85.  Rings of two blocks 62-66 (layer
-// norm bf16), of four 88 or, where they cost a CTA per SM, 65.  8 elements per
-// thread instead of 16: bf16 rows of 4096 68, fp32 99.
+// Rows staged in shared memory, read once: 16 elements of a row per thread, 32
+// where a row needs more than 512 threads otherwise; CTAs of 256 threads or one
+// row, a ring of three blocks, one wave of resident CTAs.  Two rows between
+// barriers (whole rows, 16 elements) where that leaves every CTA two such blocks
+// at least.  Measured (% of the HBM copy peak) one row / two: layer norm bf16
+// rows of 8192 88 / 89, fp32 of 4096 91 / 97; RMSNorm bf16 of 4096 95 / 98, of
+// 8192 82 / 96, fp32 of 4096 92 / 97.  Rings of two blocks 80 (layer norm bf16,
+// 8192), 84 (fp32), 61 (RMSNorm bf16, 4096); of four the same as three or, where
+// they cost a CTA per SM, 65 (layer norm bf16, 4096).  8 elements per thread:
+// bf16 rows of 4096 68, fp32 99.  32 elements against two reads of the row:
+// layer norm bf16 rows of 16384 80 / 49, RMSNorm 97.
 constexpr int64_t kBwdBlock = 256;
 constexpr int64_t kBwdSlots = 3;
 constexpr int64_t kBwdTwoRowBlocks = 2;     // blocks per CTA from which two rows pay
@@ -257,7 +259,7 @@ rmsnorm_status_t plan_bwd_staged(int32_t dtype, NormCall* c, LaunchShape* s, Nor
     // one array's share of a slot
     auto slot_of = [&](int rows) { return rows * rpc * r.row_slot; };
     int rows = 1;
-    if (mode == 0 && elems == 16 && (c->layer || !bf16) && 4 * slot_of(2) <= budget &&
+    if (mode == 0 && elems == 16 && 4 * slot_of(2) <= budget &&
         c->p.rows >= 2 * rpc * kBwdTwoRowBlocks * ctas_most)
         rows = 2;
     const int64_t slot = slot_of(rows);
