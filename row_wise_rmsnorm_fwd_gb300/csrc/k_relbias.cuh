@@ -619,7 +619,6 @@ __global__ void __maxnreg__((bias_fwd_regs<T, NV>())) relbias_fwd_rowreg_kernel(
         for (int c = 0; c < w.C && c <= idx; ++c) win[w.slot(c, idx)] = v;
     }
     __syncthreads();
-    const float low = win[w.slot(0, 0)], high = win[w.slot(0, w.s.size - 1)];
     const L scale = L::all(p.scale), log2e = L::all(kLog2e);
     for (int it = 0; block < nblocks; block += p.parts, ++it) {
         rows.next(p);
@@ -636,19 +635,14 @@ __global__ void __maxnreg__((bias_fwd_regs<T, NV>())) relbias_fwd_rowreg_kernel(
             for (int i = 0; i < NV; ++i) {
                 if (!all && is.none(i)) continue;
                 const int v = i * G + t, j = v * EPV;
-                const bool off = !all && j >= ri.to;
-                const bool below = __all_sync(0xffffffffu, v <= wr.vmin || off);
-                if (below || __all_sync(0xffffffffu, v >= wr.vmax || off)) {
-                    const L c = L::all(below ? low : high);
+                // a lookup for every vector: asking first whether the whole warp's are
+                // outside the window costs more (fp32 rows of 517 217 / 203 us, bf16 of
+                // 520 87 / 64)
+                float b[EPV];
+                wr.read(win, wr.moved(v), b);
 #pragma unroll
-                    for (int k = 0; k < PN; ++k) e[i * PN + k] = fma(lanes<T, 16>(cur[i], k), scale, c);
-                } else {
-                    float b[EPV];
-                    wr.read(win, wr.moved(v), b);
-#pragma unroll
-                    for (int k = 0; k < PN; ++k)
-                        e[i * PN + k] = fma(lanes<T, 16>(cur[i], k), scale, L::of(b + 2 * k));
-                }
+                for (int k = 0; k < PN; ++k)
+                    e[i * PN + k] = fma(lanes<T, 16>(cur[i], k), scale, L::of(b + 2 * k));
                 if (!all && !is.full(i)) {           // masked keys
 #pragma unroll
                     for (int k = 0; k < PN; ++k) {
