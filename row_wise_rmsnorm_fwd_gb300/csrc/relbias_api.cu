@@ -163,17 +163,24 @@ rmsnorm_status_t plan_rowreg(int32_t dtype, BiasCall* c, uintptr_t bases, bool b
         return g;
     };
     // A row's time hardly depends on how many of its threads' vectors are in use,
-    // so 6 vectors per thread where they spare half of the threads, up to a warp
-    // per row.  Measured (us, 4 / 6): forward fp32 rows of 640 156 / 107, of 260
-    // 72 / 58, bf16 rows of 1536 180 / 147, of 768 80 / 76; backward bf16 rows of
-    // 1536 227 / 182, fp32 rows of 516 169 / 144.  Not below half a warp (fp32
-    // rows of 160, backward: 59 / 62) nor above a warp (forward fp32 rows of 2048
-    // 163 / 221, bf16 rows of 2056 155 / 164; backward 187 / 167 and 247 / 300).
+    // so 6 vectors per thread where that takes fewer threads without room for more
+    // vectors: up to two warps per row, forward bf16 at any width.  Measured (us,
+    // 4 / 6): forward fp32 rows of 640 150 / 102, of 260 69 / 55, bf16 rows of 1536
+    // 179 / 140, of 2056 156 / 131, of 6000 336 / 282, of 12000 101 / 74; backward
+    // bf16 rows of 1536 226 / 182, of 2056 187 / 167, fp32 rows of 516 168 / 143.
+    // Not below half a warp (backward, fp32 rows of 160: 60 / 62), nor with room for
+    // more (forward, fp32 rows of 2048: 168 / 219; backward, bf16 rows of 3100: 246 /
+    // 301), nor with more than two warps otherwise (forward, fp32 rows of 3000: 246 /
+    // 260; backward, bf16 rows of 12000: 100 / 107).  And where 4 would need more
+    // than the largest block, against the kernels that read rows twice (bf16 rows
+    // of 24000, causal: forward 293 / 153, backward 294 / 214).
     int nv = 4;
     int64_t group = threads_of(nv);
-    if (threads_of(6) < group && threads_of(6) >= 16 && threads_of(6) <= 32) {
+    const int64_t six = threads_of(6);
+    const bool fewer = 6 * six <= 4 * group && six >= 16 && (six <= 64 || (c->sz == 2 && !bwd));
+    if (fewer || group > kBiasMaxThreads) {
         nv = 6;
-        group = threads_of(nv);
+        group = six;
     }
     if (group > kBiasMaxThreads) return RMSNORM_OK;
     const int lo = static_cast<int>(c->window);
@@ -181,9 +188,9 @@ rmsnorm_status_t plan_rowreg(int32_t dtype, BiasCall* c, uintptr_t bases, bool b
     const int window = 4 * vw.copies * vw.copy;
     const bool sums = bwd && c->p.part;
     // CTAs of 256 threads; forward bf16 and backward rows of two warps and more
-    // 128.  Measured (us, 128 / 256 threads): forward bf16 rows of 2048 344 /
-    // 399, fp32 rows of 1024 89 / 83; backward bf16 rows of 2048 503 / 508,
-    // causal 422 / 444, rows of 512 (16 lanes) 106 / 75.
+    // 128.  Measured (us, 128 / 256 threads): forward bf16 rows of 2048 360 /
+    // 411, fp32 rows of 1024 181 / 170; backward bf16 rows of 2048 509 / 532,
+    // causal 427 / 460, rows of 512 (16 lanes) 99 / 75.
     const int64_t threads = bwd ? (group >= 64 ? 128 : 256) : (c->sz == 2 ? 128 : 256);
     int64_t rpc = group < threads ? threads / group : 1;
     if (sums && rpc > kWindowBudget / window) rpc = kWindowBudget / window;   // a window per row group

@@ -51,6 +51,13 @@ CASES = {
     "warp_odd": ((3, 2, 40, 601), Rule(both=False, causal=True, q_start=[561, 0, -20],
                                        kv_len=[601, 40, 597])),
     "warp_bf16": ((2, 2, 70, 1400), Rule(both=False, causal=True, q_offset=700)),
+    # two warps of six vectors, many, and the widest rows that they hold
+    "two_warps": ((2, 2, 21, 1400), Rule(kv_len=[1400, 900], q_offset=3)),
+    "two_warps_odd": ((1, 3, 40, 2571), Rule(both=False, causal=True, q_offset=2531)),
+    "many_warps": ((1, 2, 9, 6005), Rule(both=False, causal=True, q_offset=5996)),
+    "widest": ((1, 2, 5, 12280), Rule(q_offset=6000)),
+    "widest_bf16": ((2, 1, 3, 24560), Rule(both=False, causal=True, q_start=[24557, 9000])),
+    "widest_bf16_odd": ((1, 2, 3, 20011), Rule(q_offset=19000, kv_len=[20010])),
     "warp_bf16_odd": ((2, 2, 33, 1283), Rule(q_offset=600, kv_len=[1283, 1025])),
 }
 
