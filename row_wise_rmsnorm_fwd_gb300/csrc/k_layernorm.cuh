@@ -52,7 +52,9 @@ __device__ __forceinline__ Moments warp_merge(Moments a) {
 }
 
 // Any width and alignment: one CTA per row, which reads the row twice (the
-// second read normally from L2).
+// second read normally from L2).  Two dependent reads with a block barrier
+// between them bound it: a third of the HBM copy peak for fp32 rows of 4096, a
+// sixth for bf16; it takes what the staged kernel below cannot.
 constexpr int kLayerTwopassThreads = 512;
 constexpr int kLayerTwopassGroup = 4;      // vectors merged at a time
 
@@ -145,6 +147,12 @@ layernorm_twopass_kernel(const NormParams p) {
 // exchange through shared memory, behind one barrier, merges the warps' pairs:
 // the merge update above, for shares of fixed counts, with the row's mean
 // known first.
+//
+// Measured (% of the HBM copy peak): fp32 65536 x 4096 320 us, 99, bound by HBM;
+// bf16 65536 x 8192 345 us, 92, 131072 x 1024 86 us, 92: half as many bytes for
+// the same instructions.  Rows of any length, whose edges are stored element by
+// element: bf16 16384 x 4097 70 us, 56, 8191 x 2050 23.5 us, 42.  Reading the row
+// twice instead (above): 954 and, bf16 65536 x 4096, 938 us against 175.
 template <typename T, bool SHIFT>
 __global__ void __launch_bounds__(1024) layernorm_staged_kernel(const NormParams p) {
     constexpr int EPV = VecTraits<T, 16>::kElems;
