@@ -232,22 +232,24 @@ int64_t bwd_parts(const DeviceView& dv, int64_t rows, int64_t hidden, int sz) {
 // layer norm bf16 rows of 16384 80 / 49, RMSNorm 97.
 constexpr int64_t kBwdBlock = 256;
 constexpr int64_t kBwdSlots = 3;
+constexpr int64_t kBwdMaxHidden = 32ll * kNormBwdMaxThreads;
 constexpr int64_t kBwdTwoRowBlocks = 2;     // blocks per CTA from which two rows pay
 
 // Most CTAs of the one-pass kernel, and so its most parts: four per SM, fewer
-// for rows that take a large share of an SM's threads.
+// for rows that take a large share of an SM's threads, none for rows that it
+// cannot hold.
 int64_t bwd_staged_ctas(const DeviceView& dv, int64_t hidden) {
+    if (hidden > kBwdMaxHidden) return 0;
     const int64_t per_sm = 16384 / hidden;
     return dv.sms * (per_sm < 1 ? 1 : (per_sm > 4 ? 4 : per_sm));
 }
 
 rmsnorm_status_t plan_bwd_staged(int32_t dtype, NormCall* c, LaunchShape* s, NormFn* fn) {
     StagedRows r;
-    if (!staged_rows(*c, 0, &r)) return RMSNORM_OK;
+    if (c->p.hidden > kBwdMaxHidden || !staged_rows(*c, 0, &r)) return RMSNORM_OK;
     const int epv = 16 / c->sz;
     const int elems = r.nvec * epv > 16 * kNormBwdMaxThreads ? 32 : 16;
     const int64_t vecs = elems / epv;
-    if (r.nvec > kNormBwdMaxThreads * vecs) return RMSNORM_OK;
     const int group = group_of(r.nvec, vecs, r.shift ? 16 : 1);     // shifted: a thread per edge element
     const int64_t rpc = group < kBwdBlock ? kBwdBlock / group : 1;
     const int block = static_cast<int>(rpc * group);

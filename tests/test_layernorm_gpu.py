@@ -237,7 +237,8 @@ def test_optional_outputs_and_exact_workspace(t):
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,hidden", [(1, 333), (9, 333), (40, 2049), (700, 1026), (5000, 97)])
+@pytest.mark.parametrize("rows,hidden", [(1, 333), (9, 333), (40, 2049), (700, 1026), (5000, 97),
+                                         (9, 16383), (9, 16384), (9, 16385), (9, 16391)])
 def test_workspace_of_rows_of_any_length(rows, hidden, t):
     """The stated workspace suffices whatever the rows' alignment does."""
     x, w, _, dy = inputs(t, rows, hidden, 75)
@@ -249,6 +250,16 @@ def test_workspace_of_rows_of_any_length(rows, hidden, t):
     for g, r, e in zip(got, want, tol):
         close(g, r, e)
     assert (room[size:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("hidden", [16385, 70001, 5000000])
+def test_workspace_of_wide_rows_is_a_few_rows(hidden):
+    """Few rows too wide for one CTA: a pair per row, and per column sum a row of
+    fp32 for every four rows."""
+    x = torch.empty((8, hidden), dtype=torch.bfloat16, device="cuda")
+    parts = 2 * (hidden * 4 + 256)
+    assert binding.rmsnorm_bwd_workspace(x) <= 8 * 8 + 256 + parts
+    assert binding.layernorm_bwd_workspace(x) <= 8 * 8 + 256 + 2 * parts
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
