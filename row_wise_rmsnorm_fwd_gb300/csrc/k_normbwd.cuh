@@ -169,11 +169,10 @@ __global__ void __launch_bounds__(kBwdColsThreads) norm_bwd_cols_kernel(const No
 // 910 us for bf16 65536 x 8192, 469 us for fp32 32768 x 4096.
 enum : int { kWhole, kPartial, kShift };
 
-// Registers per thread, at most: with one row of 16 elements between barriers
-// resident warps count for more than registers.  Measured (us, at most 64 / 80 /
-// 96 / 128): RMSNorm bf16 65536 x 4096 478 (spills) / 249 / - / -, shifted
-// 16384 x 4097 106 / 99 / 104 / -; layer norm bf16 shifted 16384 x 4097 - / 178 /
-// 123 / 114, 8191 x 2050 - / 60 / 40 / 38.
+// Registers per thread, at most: RMSNorm with one row of 16 elements between
+// barriers wants resident warps more than registers.  Measured (us, at most 64 /
+// 80 / 96 / 128): RMSNorm bf16 shifted 16384 x 4097 106 / 99 / 104 / -; layer norm
+// bf16 shifted 16384 x 4097 - / 178 / 123 / 114, 8191 x 2050 - / 60 / 40 / 38.
 constexpr int norm_bwd_regs(int elems, bool layer, int rows) {
     return elems == 32 || rows == 2 || layer ? 128 : 80;
 }

@@ -222,18 +222,22 @@ int64_t bwd_parts(const DeviceView& dv, int64_t rows, int64_t hidden, int sz) {
 // Rows staged in shared memory, read once: 16 elements of a row per thread, 32
 // where a row needs more than 512 threads otherwise; CTAs of 256 threads or one
 // row, a ring of three blocks, one wave of resident CTAs.  Two rows between
-// barriers (whole rows, 16 elements) where that leaves every CTA two such blocks
-// at least.  Measured (% of the HBM copy peak) one row / two: layer norm bf16
-// rows of 8192 88 / 89, fp32 of 4096 91 / 97; RMSNorm bf16 of 4096 95 / 98, of
-// 8192 82 / 96, fp32 of 4096 92 / 97.  Rings of two blocks 80 (layer norm bf16,
-// 8192), 84 (fp32), 61 (RMSNorm bf16, 4096); of four the same as three or, where
-// they cost a CTA per SM, 65 (layer norm bf16, 4096).  8 elements per thread:
-// bf16 rows of 4096 68, fp32 99.  32 elements against two reads of the row:
-// layer norm bf16 rows of 16384 80 / 49, RMSNorm 97.
+// barriers (whole rows, 16 elements) for RMSNorm, and for layer norm, whose
+// kernel then starts more slowly, where that leaves every CTA a dozen such blocks.
+// Measured (us, one row / two): layer norm fp32 65536 x 1024 132 / 125, 16384 x
+// 4096 131 / 131, 8192 x 4096 72 / 73, 4096 x 4096 42 / 45, bf16 65536 x 8192 539 /
+// 531, 4096 x 4096 30 / 34; RMSNorm bf16 65536 x 8192 581 / 496, 131072 x 512 80 /
+// 67, 4096 x 512 9.9 / 7.1, 128 x 2048 6.5 / 5.6, fp32 32768 x 4096 258 / 246, 1024 x
+// 4096 18.3 / 18.1.  Rings of two blocks, % of the HBM copy peak: 80 against 89
+// (layer norm bf16, 8192), 84 against 97 (fp32), 61 against 95 (RMSNorm bf16,
+// 4096); of four the same as three or, where they cost a CTA per SM, 65 (layer norm
+// bf16, 4096).  8 elements per thread: bf16 rows of 4096 68, fp32 99.  32 elements
+// against two reads of the row: bf16 rows of 16384, layer norm 75 / 50, RMSNorm
+// 96 / 52.
 constexpr int64_t kBwdBlock = 256;
 constexpr int64_t kBwdSlots = 3;
 constexpr int64_t kBwdMaxHidden = 32ll * kNormBwdMaxThreads;
-constexpr int64_t kBwdTwoRowBlocks = 2;     // blocks per CTA from which two rows pay
+constexpr int64_t kBwdTwoRowBlocks = 12;    // layer norm: blocks per CTA from which two rows pay
 
 // Most CTAs of the one-pass kernel, and so its most parts: four per SM, fewer
 // for rows that take a large share of an SM's threads, none for rows that it
@@ -262,7 +266,7 @@ rmsnorm_status_t plan_bwd_staged(int32_t dtype, NormCall* c, LaunchShape* s, Nor
     auto slot_of = [&](int rows) { return rows * rpc * r.row_slot; };
     int rows = 1;
     if (mode == 0 && elems == 16 && 4 * slot_of(2) <= budget &&
-        c->p.rows >= 2 * rpc * kBwdTwoRowBlocks * ctas_most)
+        (!c->layer || c->p.rows >= 2 * rpc * kBwdTwoRowBlocks * ctas_most))
         rows = 2;
     const int64_t slot = slot_of(rows);
     int64_t slots = kBwdSlots;

@@ -13,7 +13,9 @@ static NormFn pick(int rows, int mode) {
         return nullptr;
     }
     switch (mode) {
-        case kWhole: return norm_bwd_staged_kernel<T, NV, LAYER, 1, kWhole>;
+        case kWhole:             // RMSNorm, 16 elements: two rows always fit (32 KB an array)
+            if constexpr (LAYER || ELEMS == 32) return norm_bwd_staged_kernel<T, NV, LAYER, 1, kWhole>;
+            return nullptr;
         case kPartial: return norm_bwd_staged_kernel<T, NV, LAYER, 1, kPartial>;
         case kShift: return norm_bwd_staged_kernel<T, NV, LAYER, 1, kShift>;
         default: return nullptr;

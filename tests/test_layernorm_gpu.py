@@ -102,6 +102,21 @@ def test_many_rows_per_cta(rows, hidden, t):
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,hidden", [(59999, 1024), (14777, 4096)])
+def test_rows_enough_for_two_between_barriers(rows, hidden, t):
+    """Layer norm's backward pass with a dozen blocks of two rows for every CTA;
+    the 64-bit reference runs on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    rand = lambda *shape: torch.randn(shape, generator=g, device="cuda").to(TYPES[t])  # noqa: E731
+    x, dy, w = rand(rows, hidden) * 2 + 1, rand(rows, hidden), rand(hidden)
+    _, mean, rstd = binding.layernorm_fwd_ex(x, w, stats=True)
+    got = binding.layernorm_bwd_ex(dy, x, w, mean, rstd)
+    want, tol = ref.layernorm_bwd(dy, x, w, mean, rstd)
+    for a, b, e, n in zip(got, want, tol, ("dx", "dw", "db")):
+        assert ((a.double() - b).abs() <= e).all(), n
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
 @pytest.mark.parametrize("with_w,with_b", [(False, False), (True, False), (False, True)])
 @pytest.mark.parametrize("hidden", [64, 257, 4096, 40000])
 def test_without_weight_or_bias(hidden, t, with_w, with_b):
