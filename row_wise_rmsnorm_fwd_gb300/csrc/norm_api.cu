@@ -313,16 +313,12 @@ BwdSpace bwd_space(const DeviceView& dv, int64_t rows, int64_t hidden, int sz, b
     return s;
 }
 
-// Few parts: eight threads per column, whose ten loads in flight take 80 parts
-// at once; more: 32 threads, 8 columns (one sector of a part) to a CTA.
-constexpr int kReduceFewParts = 80;
-
-rmsnorm_status_t launch_reduce(NormCall* c, cudaStream_t stream) {
-    c->p.lanes = c->p.parts <= kReduceFewParts ? 8 : 32;
-    LaunchShape s{static_cast<int>(div_up(c->p.hidden, kNormReduceThreads / c->p.lanes)),
-                  kNormReduceThreads, 1, 0};
-    s.grid_y = c->p.db ? 2 : 1;
-    return launch(*c, norm_bwd_reduce_ptr(), s, stream);
+rmsnorm_status_t launch_reduce(const NormCall& c, cudaStream_t stream) {
+    const int width = c.p.hidden % 4 == 0 ? 4 : 1;
+    LaunchShape s{static_cast<int>(div_up(c.p.hidden, kNormReduceCols * width)), kNormReduceThreads,
+                  1, 0};
+    s.grid_y = c.p.db ? 2 : 1;
+    return launch(c, norm_bwd_reduce_ptr(width), s, stream);
 }
 
 rmsnorm_status_t bwd_workspace(int32_t dtype, int64_t rows, int64_t hidden, bool layer,
@@ -394,7 +390,7 @@ rmsnorm_status_t bwd_run(int32_t dtype, bool layer, const void* dy, const void* 
         if (fn) {
             st = launch(c, fn, s, stream);
             if (st != RMSNORM_OK || (!dw && !db)) return st;
-            return launch_reduce(&c, stream);
+            return launch_reduce(c, stream);
         }
         if (c.opt.path == RMSNORM_PATH_STAGED) return RMSNORM_ERR_UNSUPPORTED;
     }
@@ -407,7 +403,7 @@ rmsnorm_status_t bwd_run(int32_t dtype, bool layer, const void* dy, const void* 
     cs.grid_y = c.p.parts;
     st = launch(c, norm_bwd_cols_ptr(dtype, c.vb, layer), cs, stream);
     if (st != RMSNORM_OK || (!dw && !db)) return st;
-    return launch_reduce(&c, stream);
+    return launch_reduce(c, stream);
 }
 
 }  // namespace

@@ -26,7 +26,6 @@ struct NormParams {
     int32_t parts;
     int32_t group;         // staged kernels: threads per row
     int32_t rows_per_cta;  // rows of a block
-    int32_t lanes;         // backward, sums over the parts: threads per column
     int32_t nslots;        // ring slots
     int32_t row_slot;      // bytes of a row in them
     int32_t period;        // rows after which the rows' alignment repeats
@@ -57,8 +56,10 @@ int norm_bwd_cols_block();
 NormFn norm_bwd_staged_ptr_f32(int elems, bool layer, int rows, int mode);
 NormFn norm_bwd_staged_ptr_bf16(int elems, bool layer, int rows, int mode);
 constexpr int kNormBwdMaxThreads = 512;
-NormFn norm_bwd_reduce_ptr();
-// The last kernel's CTA of 256 threads: `lanes` threads to a column.
+// The last kernel, `width` (4 or 1) columns to a thread, kNormReduceCols threads
+// side by side.
+NormFn norm_bwd_reduce_ptr(int width);
 constexpr int kNormReduceThreads = 256;
+constexpr int kNormReduceCols = 8;
 
 }  // namespace rmsnorm

@@ -24,7 +24,9 @@ static NormFn pick_all(int dtype, int vb, bool layer, bool cols) {
 
 NormFn norm_bwd_rows_ptr(int dtype, int vb, bool layer) { return pick_all(dtype, vb, layer, false); }
 NormFn norm_bwd_cols_ptr(int dtype, int vb, bool layer) { return pick_all(dtype, vb, layer, true); }
-NormFn norm_bwd_reduce_ptr() { return norm_bwd_reduce_kernel; }
+NormFn norm_bwd_reduce_ptr(int width) {
+    return width == 4 ? norm_bwd_reduce_kernel<4> : norm_bwd_reduce_kernel<1>;
+}
 int norm_bwd_rows_block() { return kBwdRowsThreads; }
 int norm_bwd_cols_block() { return kBwdColsThreads; }
 
