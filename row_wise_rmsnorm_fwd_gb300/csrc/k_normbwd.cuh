@@ -160,12 +160,12 @@ __global__ void __launch_bounds__(kBwdColsThreads) norm_bwd_cols_kernel(const No
 // Rows of more than 512 threads of 16 elements take 32 per thread (all of a
 // thread's 128 registers) rather than the kernels above, which read them twice.
 //
-// Measured (% of the HBM copy peak): layer norm bf16 65536 x 8192 530 us, 89,
-// 16384 x 16384 315 us, 75; fp32 32768 x 4096 245 us, 97; RMSNorm bf16 65536 x
-// 4096 243 us, 98, 65536 x 8192 497 us, 95, 16384 x 16384 247 us, 96.  What is
+// Measured (% of the HBM copy peak): layer norm bf16 65536 x 8192 526 us, 90,
+// 16384 x 16384 322 us, 74; fp32 32768 x 4096 240 us, 99; RMSNorm bf16 65536 x
+// 4096 241 us, 99, 65536 x 8192 492 us, 96, 16384 x 16384 241 us, 98.  What is
 // left in bf16 layer norm is the trips to shared memory (an access per vector
 // and pass, waited for by a quarter of the SM's warps: 126 registers each).  Rows
-// of any length: bf16 16384 x 4097 115 us, 52.  The three kernels above instead:
+// of any length: bf16 16384 x 4097 114 us, 52.  The three kernels above instead:
 // 910 us for bf16 65536 x 8192, 469 us for fp32 32768 x 4096.
 enum : int { kWhole, kPartial, kShift };
 
