@@ -46,6 +46,12 @@ CASES = {
     "far_queries": ((1, 2, 3, 100), Rule(q_offset=1 << 40)),
     "far_keys": ((1, 2, 3, 100), Rule(q_offset=-(1 << 40))),
     "many_rows": ((7, 2, 200, 48), Rule()),
+    # windows too large for the register kernels beside several short rows
+    "long_distance_few_keys": ((2, 2, 20, 64), Rule(num_buckets=64, max_distance=4096,
+                                                    q_offset=3000)),
+    "long_distance_decode": ((3, 2, 1, 70), Rule(num_buckets=128, max_distance=4096, both=False,
+                                                 causal=True, q_start=[69, 5000, 12])),
+    "many_heads": ((1, 3000, 2, 8), Rule()),
     # six vectors per thread: half a warp and a warp per row, either type
     "half_warp": ((2, 3, 20, 264), Rule(q_offset=100, kv_len=[131, 264])),
     "warp_odd": ((3, 2, 40, 601), Rule(both=False, causal=True, q_start=[561, 0, -20],
