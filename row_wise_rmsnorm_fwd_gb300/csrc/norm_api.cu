@@ -222,18 +222,22 @@ int64_t bwd_parts(const DeviceView& dv, int64_t rows, int64_t hidden, int sz) {
 // Rows staged in shared memory, read once: 16 elements of a row per thread, 32
 // where a row needs more than 512 threads otherwise; CTAs of 256 threads or one
 // row, a ring of three blocks, one wave of resident CTAs.  Two rows between
-// barriers (whole rows, 16 elements) for RMSNorm, and for layer norm, whose
-// kernel then starts more slowly, where that leaves every CTA a dozen such blocks.
-// Measured (us, one row / two): layer norm fp32 65536 x 1024 132 / 125, 16384 x
-// 4096 131 / 131, 8192 x 4096 72 / 73, 4096 x 4096 42 / 45, bf16 65536 x 8192 539 /
-// 531, 4096 x 4096 30 / 34; RMSNorm bf16 65536 x 8192 581 / 496, 131072 x 512 80 /
-// 67, 4096 x 512 9.9 / 7.1, 128 x 2048 6.5 / 5.6, fp32 32768 x 4096 258 / 246, 1024 x
-// 4096 18.3 / 18.1.  Rings of two blocks, % of the HBM copy peak: 80 against 89
-// (layer norm bf16, 8192), 84 against 97 (fp32), 61 against 95 (RMSNorm bf16,
-// 4096); of four the same as three or, where they cost a CTA per SM, 65 (layer norm
-// bf16, 4096).  8 elements per thread: bf16 rows of 4096 68, fp32 99.  32 elements
-// against two reads of the row: bf16 rows of 16384, layer norm 75 / 50, RMSNorm
-// 96 / 52.
+// barriers (16 elements; rows that fill their threads, in layer norm bf16 others
+// too) for RMSNorm, unless in bf16 that halves the resident CTAs, and for layer
+// norm, whose kernel then starts more slowly, where it leaves every CTA a dozen
+// such blocks.  Measured (us, one row / two):
+//   layer norm fp32 65536 x 1024 132 / 125, 16384 x 4096 131 / 131, 8192 x 4096 72 /
+//     73, 4096 x 4096 42 / 45, bf16 65536 x 8192 539 / 531, 4096 x 4096 30 / 34
+//   RMSNorm bf16 65536 x 8192 581 / 496, 131072 x 512 80 / 67, 4096 x 512 9.9 / 7.1,
+//     128 x 2048 6.5 / 5.6, fp32 32768 x 4096 258 / 246, 1024 x 4096 18.3 / 18.1
+//   half as many CTAs: bf16 30000 x 5120 152 / 181, fp32 15000 x 5120 146 / 150
+//   rows that leave threads idle: layer norm bf16 65536 x 1280 128 / 114, 30000 x
+//     5568 249 / 232, but fp32 65536 x 768 102 / 153, RMSNorm bf16 65536 x 1280 95 / 107
+// Rings of two blocks, % of the HBM copy peak: 80 against 89 (layer norm bf16,
+// 8192), 84 against 97 (fp32), 61 against 95 (RMSNorm bf16, 4096); of four the same
+// as three or, where they cost a CTA per SM, 65 (layer norm bf16, 4096).  8
+// elements per thread: bf16 rows of 4096 68, fp32 99.  32 elements against two
+// reads of the row: bf16 rows of 16384, layer norm 75 / 50, RMSNorm 96 / 52.
 constexpr int64_t kBwdBlock = 256;
 constexpr int64_t kBwdSlots = 3;
 constexpr int64_t kBwdMaxHidden = 32ll * kNormBwdMaxThreads;
@@ -262,31 +266,40 @@ rmsnorm_status_t plan_bwd_staged(int32_t dtype, NormCall* c, LaunchShape* s, Nor
     const int64_t weights = r.shift ? r.row_slot : 0;
     const int64_t budget = c->dv.smem_optin - 2048 - weights;
     const int64_t ctas_most = bwd_staged_ctas(c->dv, c->p.hidden);
-    // one array's share of a slot
-    auto slot_of = [&](int rows) { return rows * rpc * r.row_slot; };
-    int rows = 1;
-    if (mode == 0 && elems == 16 && 4 * slot_of(2) <= budget &&
-        (!c->layer || c->p.rows >= 2 * rpc * kBwdTwoRowBlocks * ctas_most))
-        rows = 2;
-    const int64_t slot = slot_of(rows);
-    int64_t slots = kBwdSlots;
-    while (slots > 2 && 2 * slots * slot > budget) --slots;
-    if (2 * slots * slot > budget) return RMSNORM_OK;
-    const int smem = static_cast<int>(2 * slots * slot + weights);
-    const NormFn f = bf16 ? norm_bwd_staged_ptr_bf16(elems, c->layer, rows, mode)
-                          : norm_bwd_staged_ptr_f32(elems, c->layer, rows, mode);
-    int occ = 0;
-    if (cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(f), block, smem, 1,
-                         &occ) != cudaSuccess)
-        return RMSNORM_ERR_CUDA;
-    if (occ < 1) return RMSNORM_OK;
-    int64_t ctas = static_cast<int64_t>(c->dv.sms) * occ;
+    struct Form {            // rows between barriers, and what a launch of them takes
+        int rows;
+        int64_t slots;
+        int smem, occ;
+        NormFn fn;
+    };
+    // false: a CUDA error; occ 0: does not fit
+    auto form = [&](int rows, Form* o) {
+        const int64_t slot = rows * rpc * r.row_slot;       // of one array
+        *o = Form{rows, kBwdSlots, 0, 0, nullptr};
+        while (o->slots > 2 && 2 * o->slots * slot > budget) --o->slots;
+        if (2 * o->slots * slot > budget) return true;
+        o->smem = static_cast<int>(2 * o->slots * slot + weights);
+        o->fn = bf16 ? norm_bwd_staged_ptr_bf16(elems, c->layer, rows, mode)
+                     : norm_bwd_staged_ptr_f32(elems, c->layer, rows, mode);
+        return cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(o->fn),
+                                block, o->smem, 1, &o->occ) == cudaSuccess;
+    };
+    Form f, two;
+    if (!form(1, &f)) return RMSNORM_ERR_CUDA;
+    const bool whole = mode == 0 || (mode == 1 && c->layer && bf16);
+    if (whole && elems == 16 &&
+        (!c->layer || c->p.rows >= 2 * rpc * kBwdTwoRowBlocks * ctas_most)) {
+        if (!form(2, &two)) return RMSNORM_ERR_CUDA;
+        if (two.occ > 0 && (c->layer || !bf16 || f.occ < 2 * two.occ)) f = two;
+    }
+    if (f.occ < 1) return RMSNORM_OK;
+    int64_t ctas = static_cast<int64_t>(c->dv.sms) * f.occ;
     if (ctas > ctas_most) ctas = ctas_most;
-    *s = LaunchShape{staged_grid(*c, r, rows * rpc, ctas), block, 1, smem};
-    *fn = f;
+    *s = LaunchShape{staged_grid(*c, r, f.rows * rpc, ctas), block, 1, f.smem};
+    *fn = f.fn;
     c->p.group = group;
     c->p.rows_per_cta = static_cast<int32_t>(rpc);
-    c->p.nslots = static_cast<int32_t>(slots);
+    c->p.nslots = static_cast<int32_t>(f.slots);
     c->p.row_slot = static_cast<int32_t>(r.row_slot);
     c->p.period = r.period;
     c->p.parts = s->grid;

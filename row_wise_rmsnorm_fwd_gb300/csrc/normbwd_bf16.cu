@@ -10,12 +10,12 @@ static NormFn pick(int rows, int mode) {
     if (rows == 2) {
         if constexpr (ELEMS == 16)
             if (mode == kWhole) return norm_bwd_staged_kernel<T, NV, LAYER, 2, kWhole>;
+        if constexpr (ELEMS == 16 && LAYER)
+            if (mode == kPartial) return norm_bwd_staged_kernel<T, NV, LAYER, 2, kPartial>;
         return nullptr;
     }
     switch (mode) {
-        case kWhole:             // RMSNorm, 16 elements: two rows always fit (32 KB an array)
-            if constexpr (LAYER || ELEMS == 32) return norm_bwd_staged_kernel<T, NV, LAYER, 1, kWhole>;
-            return nullptr;
+        case kWhole: return norm_bwd_staged_kernel<T, NV, LAYER, 1, kWhole>;
         case kPartial: return norm_bwd_staged_kernel<T, NV, LAYER, 1, kPartial>;
         case kShift: return norm_bwd_staged_kernel<T, NV, LAYER, 1, kShift>;
         default: return nullptr;

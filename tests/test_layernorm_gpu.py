@@ -92,7 +92,7 @@ def test_rmsnorm_backward(rows, hidden, t, options):
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,hidden", [(2000, 64), (700, 1024), (1300, 2048), (611, 130),
+@pytest.mark.parametrize("rows,hidden", [(2000, 64), (700, 1024), (1300, 2048), (611, 130), (900, 5120),
                                          (3001, 33), (2500, 255), (1999, 1001), (1500, 2050)])
 def test_many_rows_per_cta(rows, hidden, t):
     x, w, b, dy = inputs(t, rows, hidden, 9)
@@ -102,7 +102,7 @@ def test_many_rows_per_cta(rows, hidden, t):
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,hidden", [(59999, 1024), (14777, 4096)])
+@pytest.mark.parametrize("rows,hidden", [(59999, 1024), (14777, 4096), (58500, 768), (7301, 5568)])
 def test_rows_enough_for_two_between_barriers(rows, hidden, t):
     """Layer norm's backward pass with a dozen blocks of two rows for every CTA;
     the 64-bit reference runs on the GPU."""
