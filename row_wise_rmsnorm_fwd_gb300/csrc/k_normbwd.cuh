@@ -351,7 +351,9 @@ norm_bwd_staged_kernel(const NormParams p) {
             if constexpr (LAYER) {
                 k1 = -a[r] * p.inv_hidden * rstd[r];
             } else {
-                rstd[r] = rsqrtf(fmaf(a[r], p.inv_hidden, p.eps));
+                // 0 for rows behind the last one, as in layer norm: their sums are 0, whose
+                // rstd is infinite with eps = 0 and would make their share of dw NaN
+                rstd[r] = here ? rsqrtf(fmaf(a[r], p.inv_hidden, p.eps)) : 0.f;
             }
             // u * k2 = -rstd * xh * m(g * xh), m(g * xh) = rstd * b / H
             const float k2 = -(b[r] * p.inv_hidden * rstd[r]) * rstd[r] * rstd[r];
