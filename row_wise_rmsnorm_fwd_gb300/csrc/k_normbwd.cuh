@@ -149,8 +149,10 @@ __global__ void __launch_bounds__(kBwdColsThreads) norm_bwd_cols_kernel(const No
 // At 6 bytes an element (bf16) the issue slots are as scarce as the bandwidth,
 // so the arithmetic is on packed pairs and arranged for few operations: with
 // u = x - mean (RMSNorm: x), the first pass needs d * u once for both
-// m(g * xh) and dw, and dx = (d * w) * rstd + k1 + u * k2 with two constants
-// of the row.  R = 2 gives each thread two independent rows between barriers.
+// m(g * xh) and dw, and dx = (d * w + k1 + u * k2) * rstd with two constants of
+// the row, k1 = -m(g) and k2 = -m(g * xh) * rstd (which times rstd once more, for
+// rows whose squares are near fp32's smallest numbers, would overflow, though dx
+// does not).  R = 2 gives each thread two independent rows between barriers.
 // Modes: kWhole: every thread has NV whole vectors and there are weights;
 // kPartial: aligned rows of any length, with or without weights; kShift: rows
 // of any length, the weights copied to shared memory in their layout, a
@@ -358,12 +360,12 @@ norm_bwd_staged_kernel(const NormParams p) {
             if (SKIP && !here) continue;
             float k1 = 0.f;
             if constexpr (LAYER) {
-                k1 = -a[r] * p.inv_hidden * rstd[r];
+                k1 = -a[r] * p.inv_hidden;
             } else {
                 rstd[r] = rsqrtf(fmaf(a[r], p.inv_hidden, p.eps));
             }
-            // u * k2 = -rstd * xh * m(g * xh), m(g * xh) = rstd * b / H
-            const float k2 = -(b[r] * p.inv_hidden * rstd[r]) * rstd[r] * rstd[r];
+            // u * k2 = -xh * m(g * xh), m(g * xh) = rstd * b / H
+            const float k2 = -(b[r] * p.inv_hidden * rstd[r]) * rstd[r];
             const L minus = L::all(-mean[r]), q = L::all(rstd[r]);
             const L c1 = L::all(k1), c2 = L::all(k2);
             const int64_t at = (row + r * apart) * p.hidden;
@@ -378,23 +380,21 @@ norm_bwd_staged_kernel(const NormParams p) {
 #pragma unroll
                 for (int k = 0; k < PN; ++k) {
                     const L dk = lanes<T, 16>(d, k), wk = lanes<T, 16>(w, k);
-                    L u, in;
                     if constexpr (LAYER) {
-                        u = lanes_plus<T, 16>(x, k, minus);
-                        in = fma(dk * wk, q, c1);
+                        const L u = lanes_plus<T, 16>(x, k, minus);
+                        (fma(u, c2, fma(dk, wk, c1)) * q).put(o + 2 * k);
                     } else {
-                        u = lanes<T, 16>(x, k);
-                        in = dk * wk * q;
-                        aw[i * PN + k] = fma(dk * u, q, aw[i * PN + k]);
+                        const L xh = lanes<T, 16>(x, k) * q;
+                        aw[i * PN + k] = fma(dk, xh, aw[i * PN + k]);
+                        fma(xh, c2, dk * wk * q).put(o + 2 * k);
                     }
-                    fma(u, c2, in).put(o + 2 * k);
                 }
                 if (on) st_stream<16>(dst + i * G * 16, pack<T, 16>(o));
             }
             if (SHIFT && edge && here) {
                 const float d = ld_elem<T>(edge_d), u = ld_elem<T>(edge_x) - mean[r];
                 if (!LAYER) edge_aw = fmaf(d * u, rstd[r], edge_aw);
-                st_elem<T>(p.out, at + rv.edge_col(t), fmaf(u, k2, fmaf(d * edge_w, rstd[r], k1)));
+                st_elem<T>(p.out, at + rv.edge_col(t), rstd[r] * fmaf(u, k2, fmaf(d, edge_w, k1)));
             }
         }
 #pragma unroll

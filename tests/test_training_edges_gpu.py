@@ -40,3 +40,22 @@ def test_rmsnorm_backward_with_eps_zero(hidden, t, options):
         rms_bwd(dy, x, make((hidden,), t, 3, mean=1.0, std=0.1), 0.0, options)
         if rows == 3:
             rms_bwd(dy, x, None, 0.0, options)
+
+
+@pytest.mark.parametrize("options", PATHS, ids=["auto", "twopass"])
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("hidden", [64, 333, 2048, 4096, 8200])
+def test_rows_whose_squares_are_tiny(hidden, t, options):
+    """x of order 2^-62 and eps = 0: rstd is 2^62 and its square times the row's
+    m(g * xh), here about 40, is past fp32; dx, at most 2^62 * 200, is not."""
+    rows, w = 37, make((hidden,), t, 1, mean=1.0, std=0.1)
+    x = make((rows, hidden), "f32", 2)
+    dy = (40 * x + make((rows, hidden), "f32", 3)).to(TYPES[t])
+    x = (x * 2.0 ** -62).to(TYPES[t])
+    rms_bwd(dy, x, w, 0.0, options)
+    _, mean, rstd = ref.layernorm(x, w, None, 0.0)[0]
+    mean, rstd = mean.float(), rstd.float()
+    got = binding.layernorm_bwd_ex(*(v.cuda() for v in (dy, x, w, mean, rstd)), options=options)
+    want, tol = ref.layernorm_bwd(dy, x, w, mean, rstd)
+    for g, r, e, n in zip(got, want, tol, ("dx", "dw", "db")):
+        close(g, r, e, n)
