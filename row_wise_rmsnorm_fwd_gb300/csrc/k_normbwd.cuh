@@ -161,9 +161,12 @@ __global__ void __launch_bounds__(kBwdColsThreads) norm_bwd_cols_kernel(const No
 //
 // Rows of more than 512 threads of 16 elements take 32 per thread (all of a
 // thread's 128 registers) rather than the kernels above, which read them twice.
+// Layer norm's then take kPartial also where they fill their threads: its weights
+// under a predicate are not kept from pass to pass in registers that it lacks
+// (kWhole / kPartial: fp32 8192 x 12288 242 / 206 us, bf16 16384 x 16384 314 / 276).
 //
 // Measured (% of the HBM copy peak): layer norm bf16 65536 x 8192 526 us, 90,
-// 16384 x 16384 322 us, 74; fp32 32768 x 4096 240 us, 99; RMSNorm bf16 65536 x
+// 16384 x 16384 276 us, 86; fp32 32768 x 4096 241 us, 98; RMSNorm bf16 65536 x
 // 4096 241 us, 99, 65536 x 8192 492 us, 96, 16384 x 16384 241 us, 98.  What is
 // left in bf16 layer norm is the trips to shared memory (an access per vector
 // and pass, waited for by a quarter of the SM's warps: 126 registers each).  Rows
@@ -200,6 +203,9 @@ norm_bwd_staged_kernel(const NormParams p) {
     constexpr int EPV = VecTraits<T, 16>::kElems;
     constexpr int PN = PairTraits<T, 16>::N;
     constexpr bool SHIFT = MODE == kShift;
+    // 32 elements per thread are for rows of more than 8192: a CTA's block is one row, and
+    // with threads rounded up to a warp only a thread's last vector may be missing
+    constexpr bool WIDE = NV * EPV > 16;
     using L = Lanes<2>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ alignas(8) uint64_t bars[kBlockRingMaxSlots];
@@ -221,7 +227,8 @@ norm_bwd_staged_kernel(const NormParams p) {
     while (merge_width < wpg) merge_width <<= 1;
     bool valid[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) valid[i] = MODE == kWhole || i * G + t < rv.nvec;
+    for (int i = 0; i < NV; ++i)
+        valid[i] = MODE == kWhole || (WIDE && i < NV - 1) || i * G + t < rv.nvec;
     __syncthreads();
     pdl_wait();
     if (warp == 0) ring.prologue();
@@ -267,7 +274,7 @@ norm_bwd_staged_kernel(const NormParams p) {
     // pass.  Measured (us, sum of 1 / skip): fp32 65536 x 768 115 / 108, 32768 x 4096
     // (two rows) 248 / 250, bf16 65536 x 1280 96 / 99.
     constexpr bool SKIP = !LAYER && sizeof(T) == 4 && R == 1;
-    auto in_range = [&](int r) { return row + r * apart < p.rows; };
+    auto in_range = [&](int r) { return WIDE || row + r * apart < p.rows; };
     auto weights = [&](int i) {
         if constexpr (SHIFT) return ld_slot_if(ws + i * G * 16, valid[i]);
         else if constexpr (MODE == kWhole) return ld_ro<16>(wg + i * G * 16);
@@ -383,7 +390,12 @@ norm_bwd_staged_kernel(const NormParams p) {
                     if constexpr (LAYER) {
                         const L u = lanes_plus<T, 16>(x, k, minus);
                         (fma(u, c2, fma(dk, wk, c1)) * q).put(o + 2 * k);
-                    } else {
+                    } else if constexpr (WIDE) {
+                        const L u = lanes<T, 16>(x, k);
+                        aw[i * PN + k] = fma(dk * u, q, aw[i * PN + k]);
+                        (fma(u, c2, dk * wk) * q).put(o + 2 * k);
+                    } else {        // as many operations in another order: 3% less time here,
+                                    // 4% more in rows of more than 8192 elements
                         const L xh = lanes<T, 16>(x, k) * q;
                         aw[i * PN + k] = fma(dk, xh, aw[i * PN + k]);
                         fma(xh, c2, dk * wk * q).put(o + 2 * k);

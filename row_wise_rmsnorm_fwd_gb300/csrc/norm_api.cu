@@ -237,7 +237,7 @@ int64_t bwd_parts(const DeviceView& dv, int64_t rows, int64_t hidden, int sz) {
 // 8192), 84 against 97 (fp32), 61 against 95 (RMSNorm bf16, 4096); of four the same
 // as three or, where they cost a CTA per SM, 65 (layer norm bf16, 4096).  8
 // elements per thread: bf16 rows of 4096 68, fp32 99.  32 elements against two
-// reads of the row: bf16 rows of 16384, layer norm 75 / 50, RMSNorm 96 / 52.
+// reads of the row: bf16 rows of 16384, layer norm 86 / 50, RMSNorm 98 / 52.
 constexpr int64_t kBwdBlock = 256;
 constexpr int64_t kBwdSlots = 3;
 constexpr int64_t kBwdMaxHidden = 32ll * kNormBwdMaxThreads;
@@ -262,7 +262,8 @@ rmsnorm_status_t plan_bwd_staged(int32_t dtype, NormCall* c, LaunchShape* s, Nor
     const int64_t rpc = group < kBwdBlock ? kBwdBlock / group : 1;
     const int block = static_cast<int>(rpc * group);
     const bool bf16 = dtype == RMSNORM_DTYPE_BF16;
-    const int mode = r.shift ? 2 : (c->p.w && r.nvec == group * vecs ? 0 : 1);
+    const bool fills = c->p.w && r.nvec == group * vecs && !(elems == 32 && c->layer);
+    const int mode = r.shift ? 2 : (fills ? 0 : 1);
     const int64_t weights = r.shift ? r.row_slot : 0;
     const int64_t budget = c->dv.smem_optin - 2048 - weights;
     const int64_t ctas_most = bwd_staged_ctas(c->dv, c->p.hidden);

@@ -51,9 +51,9 @@ int norm_bwd_rows_block();
 NormFn norm_bwd_cols_ptr(int dtype, int vb, bool layer);
 int norm_bwd_cols_block();
 // One pass over staged rows, elems (16 or 32) elements per thread and row; mode:
-// 0 whole vectors only and weights given, 1 aligned rows, 2 rows of any length;
-// rows = rows of a thread between barriers (2: 16 elements and mode 0, layer norm
-// bf16 mode 1 too).
+// 0 whole vectors only and weights given (not layer norm with 32 elements), 1
+// aligned rows, 2 rows of any length; rows = rows of a thread between barriers (2:
+// 16 elements and mode 0, layer norm bf16 mode 1 too).
 NormFn norm_bwd_staged_ptr_f32(int elems, bool layer, int rows, int mode);
 NormFn norm_bwd_staged_ptr_bf16(int elems, bool layer, int rows, int mode);
 constexpr int kNormBwdMaxThreads = 512;

@@ -15,7 +15,9 @@ static NormFn pick(int rows, int mode) {
         return nullptr;
     }
     switch (mode) {
-        case kWhole: return norm_bwd_staged_kernel<T, NV, LAYER, 1, kWhole>;
+        case kWhole:
+            if constexpr (ELEMS == 16 || !LAYER) return norm_bwd_staged_kernel<T, NV, LAYER, 1, kWhole>;
+            else return nullptr;
         case kPartial: return norm_bwd_staged_kernel<T, NV, LAYER, 1, kPartial>;
         case kShift: return norm_bwd_staged_kernel<T, NV, LAYER, 1, kShift>;
         default: return nullptr;

@@ -29,6 +29,16 @@ def rms_bwd(dy, x, w, eps, options=None):
         close(g, r, e, f"{n} of {tuple(x.shape)}")
 
 
+def layer_bwd(dy, x, w, options=None):
+    _, mean, rstd = ref.layernorm(x, w, None, 1e-5)[0]
+    mean, rstd = mean.float(), rstd.float()
+    got = binding.layernorm_bwd_ex(*(None if v is None else v.cuda() for v in (dy, x, w, mean, rstd)),
+                                   options=options)
+    want, tol = ref.layernorm_bwd(dy, x, w, mean, rstd)
+    for g, r, e, n in zip(got, want, tol, ("dx", "dw", "db")):
+        close(g, r, e, f"{n} of {tuple(x.shape)}")
+
+
 @pytest.mark.parametrize("options", PATHS, ids=["auto", "twopass"])
 @pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("hidden", [16, 64, 333, 512, 768, 1001, 2048, 2050, 4096, 5120, 8192, 8200])
@@ -59,3 +69,14 @@ def test_rows_whose_squares_are_tiny(hidden, t, options):
     want, tol = ref.layernorm_bwd(dy, x, w, mean, rstd)
     for g, r, e, n in zip(got, want, tol, ("dx", "dw", "db")):
         close(g, r, e, n)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("hidden", [8196, 8200, 8201, 9000, 11001, 12288, 14400, 16383, 16384])
+def test_wide_rows_in_one_pass(hidden, t):
+    """Rows of more than 8192 elements: threads that lack their last vector and
+    that fill theirs, rows off the 16-byte boundaries, with and without weights."""
+    x, w, dy = make((7, hidden), t, 1, mean=0.5), make((hidden,), t, 2), make((7, hidden), t, 3)
+    for weights in (w, None):
+        rms_bwd(dy, x, weights, 1e-6)
+        layer_bwd(dy, x, weights)
