@@ -80,3 +80,29 @@ def test_wide_rows_in_one_pass(hidden, t):
     for weights in (w, None):
         rms_bwd(dy, x, weights, 1e-6)
         layer_bwd(dy, x, weights)
+
+
+@pytest.mark.parametrize("options", PATHS, ids=["auto", "twopass"])
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("hidden", [109, 448, 896, 1792, 3584, 7168])
+def test_constant_rows_at_widths_without_a_reciprocal(hidden, t, options):
+    """The mean of a constant row is the constant where its sum is exact, also at
+    widths whose fp32 reciprocal times the sum is not: the row gives b."""
+    w, b = make((hidden,), t, 1, mean=1.0), make((hidden,), t, 2)
+    x = torch.tensor([3.0, -1000.0, 0.0, 60416.0, 1.5])[:, None].repeat(1, hidden).to(TYPES[t])
+    y, mean, rstd = binding.layernorm_fwd_ex(x.cuda(), w.cuda(), b.cuda(), stats=True,
+                                             options=options)
+    assert (mean.cpu() == x[:, 0].float()).all()
+    assert (y.cpu() == b).all()
+    assert (rstd * 1e-5 ** 0.5 - 1).abs().max() < 1e-6
+
+
+@pytest.mark.parametrize("options", PATHS, ids=["auto", "twopass"])
+@pytest.mark.parametrize("hidden", [48, 448, 3584])
+def test_mean_of_a_row_with_an_infinity(hidden, options):
+    x = make((4, hidden), "f32", 5)
+    x[1, 7], x[2, 9] = float("inf"), float("-inf")
+    _, mean, rstd = binding.layernorm_fwd_ex(x.cuda(), stats=True, options=options)
+    assert rstd[1:3].isnan().all() and rstd[0].isfinite() and rstd[3].isfinite()
+    if options is None:
+        assert mean[1].item() == float("inf") and mean[2].item() == float("-inf")
