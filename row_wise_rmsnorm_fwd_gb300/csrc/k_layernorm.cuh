@@ -37,7 +37,9 @@ __device__ __forceinline__ void merge(Moments& a, const Moments& b) {
     const float n = a.n + b.n;
     const float f = n > 0.f ? b.n / n : 0.f;
     const float d = b.mean - a.mean;
-    a.m2 += b.m2 + d * d * a.n * f;
+    // nothing where one of the two is empty: its mean of 0 may be so far away that
+    // the square of the distance is infinite
+    a.m2 += b.m2 + (a.n > 0.f && b.n > 0.f ? d * d * a.n * f : 0.f);
     a.mean += d * f;
     a.n = n;
 }

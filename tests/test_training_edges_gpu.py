@@ -106,3 +106,18 @@ def test_mean_of_a_row_with_an_infinity(hidden, options):
     assert rstd[1:3].isnan().all() and rstd[0].isfinite() and rstd[3].isfinite()
     if options is None:
         assert mean[1].item() == float("inf") and mean[2].item() == float("-inf")
+
+
+@pytest.mark.parametrize("options", PATHS, ids=["auto", "twopass"])
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("hidden", [8, 109, 448, 4096, 7168, 40000])
+def test_constant_rows_whose_square_is_past_fp32(hidden, t, options):
+    """Threads without an element of the row, whose mean of nothing is 0, change
+    nothing."""
+    w, b = make((hidden,), t, 1, mean=1.0), make((hidden,), t, 2)
+    x = torch.tensor([2.0 ** 100, -2.0 ** 90, 1.0])[:, None].repeat(1, hidden).to(TYPES[t])
+    y, mean, rstd = binding.layernorm_fwd_ex(x.cuda(), w.cuda(), b.cuda(), stats=True,
+                                             options=options)
+    assert (mean.cpu() == x[:, 0].float()).all()
+    assert (y.cpu() == b).all()
+    assert (rstd * 1e-5 ** 0.5 - 1).abs().max() < 1e-6
