@@ -41,6 +41,7 @@ namespace rmsnorm {
 // Odd rows: forward fp32 (21, 25, 422, 517) 203 us, 66, backward bf16 (5, 28, 873,
 // 761) 124 us, 66.
 constexpr int kBiasFoldRows = 64;
+constexpr int kBiasFoldTurns = 256;      // the same where rows share a window in turn
 
 template <int EPV>
 __device__ __forceinline__ int bias_slot(int idx) {
@@ -786,8 +787,11 @@ __device__ __forceinline__ void bias_fold_vec(const BiasParams& p, const VecWind
 
 // Backward: y and dy of a row in registers, the row's dot product exchanged
 // behind one barrier, which also orders the rows' updates of the group's
-// window (rows_per_cta windows per CTA).
-template <typename T, int NV, bool SHIFT>
+// window (rows_per_cta windows per CTA).  TURNS, several rows to a warp: p.turns
+// neighbouring groups share a window and add to it one after the other, vector by
+// vector, with the warp in step: windows no longer decide how many warps an SM
+// holds, and the order of the additions stays fixed.
+template <typename T, int NV, bool SHIFT, bool TURNS>
 __global__ void __maxnreg__(bias_bwd_regs<NV>()) relbias_bwd_rowreg_kernel(const BiasParams p) {
     constexpr int EPV = VecTraits<T, 16>::kElems;
     constexpr int PN = PairTraits<T, 16>::N;
@@ -811,10 +815,12 @@ __global__ void __maxnreg__(bias_bwd_regs<NV>()) relbias_bwd_rowreg_kernel(const
     const int head = blockIdx.x / p.parts;
     int merge_width = 1;
     while (merge_width < wpg) merge_width <<= 1;
-    float* win = wins + g * w.floats();
-    float* total = wins + rpc * w.floats();
+    const int turns = TURNS ? p.turns : 1;
+    const int windows = TURNS ? rpc / turns : rpc;
+    float* win = wins + (TURNS ? g / turns : g) * w.floats();
+    float* total = wins + windows * w.floats();
     if (p.part) {
-        for (int i = tid; i < rpc * w.floats(); i += blockDim.x) wins[i] = 0.f;
+        for (int i = tid; i < windows * w.floats(); i += blockDim.x) wins[i] = 0.f;
         for (int k = tid; k < p.num_buckets; k += blockDim.x) sums[k] = 0.0;
     }
     int block = blockIdx.x - head * p.parts;
@@ -824,6 +830,7 @@ __global__ void __maxnreg__(bias_bwd_regs<NV>()) relbias_bwd_rowreg_kernel(const
     pdl_wait();
 
     const L scale = L::all(p.scale);
+    const int fold_every = TURNS ? max(1, min(kBiasFoldRows, kBiasFoldTurns / turns)) : kBiasFoldRows;
     float low = 0.f, high = 0.f;
     for (int it = 0; block < nblocks; block += p.parts, ++it, rows.next(p)) {
         const BiasRow info = rows.get(p, head);
@@ -910,8 +917,9 @@ __global__ void __maxnreg__(bias_bwd_regs<NV>()) relbias_bwd_rowreg_kernel(const
                 for (int k = 0; k < PN; ++k) fma(gk[k], scale, zero).put(o + 2 * k);   // -0: 0
                 if (all || is.full(i)) st_vec<T, false>(p.out, ri, false, j, pack<T, 16>(o));
                 else if (ri.here && j < ri.end) st_vec<T, SHIFT>(p.out, ri, i == 0, j, pack<T, 16>(o));
-                if (p.part && (all || j < ri.to)) {
-                    if (v > wr.vmin && v < wr.vmax) {
+                // to the window, or to the thread's sums of the sides
+                auto add = [&](bool to_window) {
+                    if (to_window) {
                         float a[EPV];
                         wr.read(win, v, a);
 #pragma unroll
@@ -923,15 +931,26 @@ __global__ void __maxnreg__(bias_bwd_regs<NV>()) relbias_bwd_rowreg_kernel(const
                         for (int k = 1; k < PN; ++k) sum = sum + gk[k];
                         if (v >= wr.vmax) high += sum.total(); else low += sum.total();
                     }
+                };
+                const bool inside = v > wr.vmin && v < wr.vmax;
+                if constexpr (TURNS) {
+                    const bool mine = all || j < ri.to;
+                    if (mine && !inside) add(false);
+                    for (int turn = 0; turn < turns; ++turn) {
+                        if (mine && inside && (g & (turns - 1)) == turn) add(true);
+                        __syncwarp();
+                    }
+                } else if (p.part && (all || j < ri.to)) {
+                    if (inside) add(true); else add(false);
                 }
             }
         };
         if (all) outputs(std::true_type()); else outputs(std::false_type());
-        if (p.part && it % kBiasFoldRows == kBiasFoldRows - 1)
-            bias_fold_vec<EPV>(p, w, wins, total, rpc, low, high, sums, fold_red);
+        if (p.part && it % fold_every == fold_every - 1)
+            bias_fold_vec<EPV>(p, w, wins, total, windows, low, high, sums, fold_red);
     }
     if (p.part) {
-        bias_fold_vec<EPV>(p, w, wins, total, rpc, low, high, sums, fold_red);
+        bias_fold_vec<EPV>(p, w, wins, total, windows, low, high, sums, fold_red);
         double* to = p.part + static_cast<int64_t>(blockIdx.x) * p.num_buckets;
         for (int k = tid; k < p.num_buckets; k += blockDim.x) to[k] = sums[k];
     }

@@ -15,6 +15,7 @@ namespace {
 constexpr int64_t kMaxOffset = 1ll << 40;
 constexpr int64_t kMaxHeadRows = 1ll << 30;    // a row's number plus a grid's stride is a 32-bit int
 constexpr int64_t kWindowBudget = 64 << 10;    // shared memory of a CTA's windows, about
+constexpr int64_t kBwdStatic = 4 << 10;        // of a backward CTA, other than windows, at most
 
 // Smallest distance of each bucket of one direction (half of them): one by one
 // up to half / 2 =: near, then where
@@ -147,8 +148,8 @@ int window_bytes(const BiasCall& c) {
 
 // Rows in registers, if they fit and the arrays start on 16-byte boundaries:
 // the launch shape and the kernel; else leaves *fn null, status OK.
-rmsnorm_status_t plan_rowreg(int32_t dtype, BiasCall* c, uintptr_t bases, bool bwd, LaunchShape* s,
-                             BiasFn* fn) {
+rmsnorm_status_t plan_rowreg(int32_t dtype, BiasCall* c, uintptr_t bases, bool bwd, bool forced,
+                             LaunchShape* s, BiasFn* fn) {
     if (bases % 16 != 0) return RMSNORM_OK;
     const int64_t epv = 16 / c->sz;
     const bool shift = c->p.k_len % epv != 0;
@@ -193,21 +194,51 @@ rmsnorm_status_t plan_rowreg(int32_t dtype, BiasCall* c, uintptr_t bases, bool b
     // causal 427 / 460, rows of 512 (16 lanes) 99 / 75.
     const int64_t threads = bwd ? (group >= 64 ? 128 : 256) : (c->sz == 2 ? 128 : 256);
     int64_t rpc = group < threads ? threads / group : 1;
-    if (sums && rpc > kWindowBudget / window) rpc = kWindowBudget / window;   // a window per row group
-    if (rpc < 1) rpc = 1;
-    if (group < 32) rpc = div_up(rpc, 32 / group) * (32 / group);              // whole warps
-    const int64_t smem = bwd ? (sums ? rpc * window + 4 * vw.size : 0) : window;
+    int64_t windows = rpc, turns = 0;
+    // Windows of sums: one for each row group that is a warp or more, as the budget
+    // allows.  Where a warp has several rows, a window for each would leave an SM one
+    // to six warps, so its rows add to one or two windows in turn (two where three CTAs
+    // of them fit an SM, as many as their registers allow), and CTAs are halved until
+    // two fit.  Measured (us, 2^25 scores, a window per row / in turn), 32 buckets up to
+    // 128: bf16 rows of 8 keys 1058 / 115, of 32 266 / 62, of 128 80 / 47, fp32 of 64 140 /
+    // 75; 64 buckets up to 500: bf16 of 8 8617 / 248, of 32 2276 / 123, of 128 303 / 68, of
+    // 512 95 / 61, fp32 of 64 547 / 105.  One window a warp against two: bf16 of 32 keys 87
+    // / 62, of 256 46 / 46; CTAs of one per SM against two, 64 buckets up to 1000: bf16 of
+    // 64 172 / 150.
+    if (sums && group < 32) {
+        const int64_t per = 32 / group;                      // rows of a warp
+        const int64_t sm = c->dv.smem_optin + 1024;          // an SM's
+        auto bytes = [&](int64_t n) { return n * window + 4 * vw.size + kBwdStatic; };
+        int64_t warps = threads / 32;
+        while (warps > 1 && 2 * bytes(warps) > sm) warps /= 2;
+        const int64_t each = 3 * bytes(2 * warps) <= sm ? 2 : 1;
+        windows = warps * each;
+        turns = per / each;
+        rpc = warps * per;
+    } else if (sums) {
+        if (rpc > kWindowBudget / window) rpc = kWindowBudget / window;
+        if (rpc < 1) rpc = 1;
+        windows = rpc;
+    }
+    const int64_t smem = bwd ? (sums ? windows * window + 4 * vw.size : 0) : window;
     if (smem > c->dv.smem_optin - 8192) return RMSNORM_OK;
     const int block = static_cast<int>(rpc * group);
-    const BiasFn f = relbias_rowreg_ptr(dtype, nv, shift, bwd);
+    const BiasFn f = relbias_rowreg_ptr(dtype, nv, shift, bwd, turns > 1);
     int occ = 0;
     if (cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(f), block,
                          static_cast<int>(smem), 1, &occ) != cudaSuccess)
         return RMSNORM_ERR_CUDA;
     if (occ < 1) return RMSNORM_OK;
+    // Windows so large that an SM holds few warps beside them: the kernel that reads
+    // rows twice, whose CTAs of 256 threads keep one of a quarter of the size.  Measured
+    // (us, 2^25 scores, in registers / read twice), 64 buckets up to 2000, 128 threads: bf16
+    // rows of 64 keys 357 / 1209, fp32 of 384 252 / 199; 128 buckets up to 4096: fp32 rows of 512 (32
+    // threads) 1714 / 205, bf16 of 2048 (64) 417 / 91, fp32 of 8192 (512) 111 / 121.
+    if (sums && !forced && occ * block < (turns > 1 ? 128 : 256)) return RMSNORM_OK;
     c->p.nvec = static_cast<int32_t>(nvec);
     c->p.group = static_cast<int32_t>(group);
     c->p.rows_per_cta = static_cast<int32_t>(rpc);
+    c->p.turns = static_cast<int32_t>(turns);
     c->p.parts = parts_per_head(*c, div_up(c->p.head_rows, rpc), occ > kCtasPerSm ? kCtasPerSm : occ);
     *s = LaunchShape{c->p.parts * c->p.heads, block, 1, static_cast<int>(smem)};
     *fn = f;
@@ -238,7 +269,7 @@ rmsnorm_status_t fwd_run(int32_t dtype, const void* x, const void* table, void* 
     LaunchShape s{0, 0, 1, 0};
     BiasFn fn = nullptr;
     if (path(opt) != RMSNORM_PATH_TWOPASS &&
-        plan_rowreg(dtype, &c, bases, false, &s, &fn) != RMSNORM_OK)
+        plan_rowreg(dtype, &c, bases, false, path(opt) == RMSNORM_PATH_ROWREG, &s, &fn) != RMSNORM_OK)
         return RMSNORM_ERR_CUDA;
     if (!fn) {
         if (path(opt) == RMSNORM_PATH_ROWREG) return RMSNORM_ERR_UNSUPPORTED;
@@ -292,7 +323,7 @@ rmsnorm_status_t bwd_run(int32_t dtype, const void* dy, const void* y, void* dx,
     LaunchShape ls{0, 0, 1, 0};
     BiasFn fn = nullptr;
     if (path(opt) != RMSNORM_PATH_TWOPASS &&
-        plan_rowreg(dtype, &c, bases, true, &ls, &fn) != RMSNORM_OK)
+        plan_rowreg(dtype, &c, bases, true, path(opt) == RMSNORM_PATH_ROWREG, &ls, &fn) != RMSNORM_OK)
         return RMSNORM_ERR_CUDA;
     if (!fn) {
         if (path(opt) == RMSNORM_PATH_ROWREG) return RMSNORM_ERR_UNSUPPORTED;

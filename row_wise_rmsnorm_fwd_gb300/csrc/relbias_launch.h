@@ -29,6 +29,7 @@ struct BiasParams {
     int32_t parts;          // CTAs per head
     int32_t group;          // threads per row
     int32_t rows_per_cta;
+    int32_t turns;          // backward: row groups that share a window in turn
     int32_t causal;
     int32_t both;           // bidirectional: positive positions in the upper half
     int32_t num_buckets;
@@ -65,7 +66,7 @@ BiasFn relbias_bwd_wide_ptr(int dtype, int vb);
 int relbias_wide_block();
 // Rows in registers: nv (4 or 6) 16-byte vectors per thread, blocks of up to kBiasMaxThreads
 // threads; shift: rows that are not a multiple of 16 bytes.
-BiasFn relbias_rowreg_ptr(int dtype, int nv, bool shift, bool bwd);
+BiasFn relbias_rowreg_ptr(int dtype, int nv, bool shift, bool bwd, bool turns);
 constexpr int kBiasMaxThreads = 512;
 BiasFn relbias_reduce_ptr();
 int relbias_reduce_block();

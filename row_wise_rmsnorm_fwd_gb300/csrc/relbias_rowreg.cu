@@ -4,16 +4,21 @@
 
 namespace rmsnorm {
 
-template <typename T, int NV>
-static BiasFn rowreg(bool shift, bool bwd) {
-    if (bwd) return shift ? relbias_bwd_rowreg_kernel<T, NV, true> : relbias_bwd_rowreg_kernel<T, NV, false>;
-    return shift ? relbias_fwd_rowreg_kernel<T, NV, true> : relbias_fwd_rowreg_kernel<T, NV, false>;
+template <typename T, int NV, bool SHIFT>
+static BiasFn rowreg(bool bwd, bool turns) {
+    if (!bwd) return relbias_fwd_rowreg_kernel<T, NV, SHIFT>;
+    return turns ? relbias_bwd_rowreg_kernel<T, NV, SHIFT, true> : relbias_bwd_rowreg_kernel<T, NV, SHIFT, false>;
 }
 
-BiasFn relbias_rowreg_ptr(int dtype, int nv, bool shift, bool bwd) {
-    if (nv == 4) return dtype == 0 ? rowreg<float, 4>(shift, bwd) : rowreg<__nv_bfloat16, 4>(shift, bwd);
-    if (nv == 6) return dtype == 0 ? rowreg<float, 6>(shift, bwd) : rowreg<__nv_bfloat16, 6>(shift, bwd);
+template <typename T>
+static BiasFn rowreg(int nv, bool shift, bool bwd, bool turns) {
+    if (nv == 4) return shift ? rowreg<T, 4, true>(bwd, turns) : rowreg<T, 4, false>(bwd, turns);
+    if (nv == 6) return shift ? rowreg<T, 6, true>(bwd, turns) : rowreg<T, 6, false>(bwd, turns);
     return nullptr;
+}
+
+BiasFn relbias_rowreg_ptr(int dtype, int nv, bool shift, bool bwd, bool turns) {
+    return dtype == 0 ? rowreg<float>(nv, shift, bwd, turns) : rowreg<__nv_bfloat16>(nv, shift, bwd, turns);
 }
 
 }  // namespace rmsnorm

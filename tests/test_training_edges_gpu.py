@@ -121,3 +121,46 @@ def test_constant_rows_whose_square_is_past_fp32(hidden, t, options):
     assert (mean.cpu() == x[:, 0].float()).all()
     assert (y.cpu() == b).all()
     assert (rstd * 1e-5 ** 0.5 - 1).abs().max() < 1e-6
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("buckets,distance", [(32, 128), (64, 500), (128, 4096)])
+@pytest.mark.parametrize("keys", [1, 8, 16, 31, 32, 64, 100])
+def test_relbias_backward_of_many_short_rows(keys, buckets, distance, t):
+    """Several rows to a warp, which add to its windows of sums in turn; the
+    register kernel also where the automatic choice reads such rows twice."""
+    shape = (3, 2, 150, keys)
+    rule = ref.Rule(buckets, distance, scale=0.5, q_start=[0, -20, 4000],
+                    kv_len=[keys, max(0, keys - 3), keys])
+    x, table = make(shape, t, 1), make((buckets, 2), t, 2)
+    y, dy = ref.relbias(x, table, rule)[0].to(TYPES[t]), make(shape, t, 3)
+    want, tol = ref.relbias_bwd(dy, y, rule)
+    for options in (None, {"path": "rowreg"}, {"path": "twopass"}):
+        got, again = (binding.rowsoftmax_relbias_bwd_ex(dy.cuda(), y.cuda(), buckets,
+                                                        options=options, **rule.kwargs())
+                      for _ in range(2))
+        for g, a, r, e, n in zip(got, again, want, tol, ("dx", "dtable")):
+            close(g, r, e, n)
+            assert torch.equal(g, a), n
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_relbias_backward_folds_windows_of_many_short_rows(t):
+    """A CTA with more short rows than it sums before it folds its windows."""
+    shape, rule = (1, 304, 5000, 8), ref.Rule(64, 500, q_start=[-2500])
+    x, table = make(shape, t, 1), make((64, 304), t, 2)
+    y, dy = ref.relbias(x, table, rule)[0].to(TYPES[t]), make(shape, t, 3)
+    want, tol = ref.relbias_bwd(dy, y, rule)
+    got = binding.rowsoftmax_relbias_bwd_ex(dy.cuda(), y.cuda(), 64, **rule.kwargs())
+    for g, r, e, n in zip(got, want, tol, ("dx", "dtable")):
+        close(g, r, e, n)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("keys", [1, 8, 32, 64])
+def test_relbias_backward_of_short_rows_in_registers(keys, t):
+    """The register kernel takes them whatever the size of the windows."""
+    y = torch.rand((2, 2, 9, keys), device="cuda").to(TYPES[t])
+    for buckets, distance in ((32, 128), (64, 500), (256, 500), (256, 4096)):
+        binding.rowsoftmax_relbias_bwd_ex(y, y, buckets, max_distance=distance,
+                                          options={"path": "rowreg"})
