@@ -17,8 +17,8 @@
  * fp32 arithmetic for both types (bf16 inputs are widened exactly, y and dx are
  * rounded once); the variance is taken about the mean, never as a difference of
  * large sums.  dw and db are fp32 for both types, as an optimiser's master
- * copy wants them.  A NaN or an infinity in a row makes that row of y and dx,
- * and through it dw and db, NaN.
+ * copy wants them.  A NaN or an infinity in a row of x makes that row of y and dx,
+ * and with it dw, NaN; db, the sum of dy alone, is not touched by it.
  *
  *  - x, dy, y, dx: DEVICE pointers, rows*hidden elements, contiguous row-major;
  *    w, b: hidden elements of the same type, NULL for ones and zeros; mean,
@@ -63,7 +63,8 @@ rmsnorm_status_t layernorm_fwd_bf16(const uint16_t* x, const uint16_t* w, const 
  * reads it twice: any width and alignment); opt->wait_timeout_ns; and in the
  * test build of the library opt->fault_inject = 1 with RMSNORM_PATH_STAGED
  * (each CTA's first copy is withheld; elsewhere RMSNORM_ERR_UNSUPPORTED).
- * Every other field must be zero, else RMSNORM_ERR_INVALID_ARG. */
+ * Every other field but epilogue_alpha, which is not read, must be zero, else
+ * RMSNORM_ERR_INVALID_ARG. */
 rmsnorm_status_t layernorm_fwd_ex(int32_t dtype, const void* x, const void* w, const void* b,
                                   void* y, float* mean, float* rstd, int64_t rows, int64_t hidden,
                                   float eps, const rmsnorm_options_t* opt,
@@ -88,9 +89,11 @@ rmsnorm_status_t layernorm_bwd_bf16(const uint16_t* dy, const uint16_t* x, const
                                     size_t workspace_bytes, rmsnorm_stream_t stream);
 
 /* Either dtype, with options as for layernorm_fwd_ex.  RMSNORM_PATH_STAGED: x
- * and dy read from HBM once (x, dy and dx on 16-byte boundaries, rows as there
- * and of at most 16384 elements); RMSNORM_PATH_TWOPASS: a pair of sums per row, then
- * dx and partial column sums, each reading x and dy once. */
+ * and dy read from HBM once (x, dy and dx on 16-byte boundaries; rows as there, of
+ * at most 16384 elements, in fp32 of 14400: two rows of x and dy, and rows off the
+ * boundaries with the weights beside them, which ends at 11517, must fit shared
+ * memory); RMSNORM_PATH_TWOPASS: a pair of sums per row, then dx and partial column
+ * sums, each reading x and dy once. */
 rmsnorm_status_t layernorm_bwd_ex(int32_t dtype, const void* dy, const void* x, const void* w,
                                   const float* mean, const float* rstd, void* dx, float* dw,
                                   float* db, int64_t rows, int64_t hidden, void* workspace,

@@ -268,12 +268,13 @@ rmsnorm_status_t rmsnorm_bwd_bf16(const uint16_t* dy, const uint16_t* x, const u
  * RMSNORM_PATH_STAGED (rows staged in shared memory by bulk copies, x and dy
  * read from HBM once: they and dx on 16-byte boundaries, rows of any length from
  * 32 bytes (16, if they and w are multiples of 16 bytes, on such boundaries) to
- * 16384 elements and what fits shared memory, else RMSNORM_ERR_UNSUPPORTED) or RMSNORM_PATH_TWOPASS (a pair of
- * sums per row, then dx and partial column sums, each reading x and dy once:
- * any width and alignment); opt->wait_timeout_ns; and in the test build of the
+ * 16384 elements, in fp32 14400 and off the boundaries 11517, for two rows of x and
+ * dy must fit shared memory; else RMSNORM_ERR_UNSUPPORTED) or RMSNORM_PATH_TWOPASS
+ * (a pair of sums per row, then dx and partial column sums, each reading x and dy
+ * once: any width and alignment); opt->wait_timeout_ns; and in the test build of the
  * library opt->fault_inject = 1 with RMSNORM_PATH_STAGED (each CTA's first copy
- * is withheld; elsewhere RMSNORM_ERR_UNSUPPORTED).  Every other field must be
- * zero, else RMSNORM_ERR_INVALID_ARG. */
+ * is withheld; elsewhere RMSNORM_ERR_UNSUPPORTED).  Every other field but
+ * epilogue_alpha, which is not read, must be zero, else RMSNORM_ERR_INVALID_ARG. */
 rmsnorm_status_t rmsnorm_bwd_ex(int32_t dtype, const void* dy, const void* x, const void* w,
                                 void* dx, float* dw, int64_t rows, int64_t hidden, float eps,
                                 void* workspace, size_t workspace_bytes,

@@ -176,7 +176,9 @@ rmsnorm_status_t rowsoftmax_relbias_fwd_bf16(const uint16_t* x, const uint16_t* 
 /* Either dtype, with options (`opt` may be NULL): opt->path RMSNORM_PATH_AUTO,
  * RMSNORM_PATH_ROWREG (rows of up to 48 KB less a few keys, held in registers; x,
  * y, dy and dx on 16-byte boundaries; else RMSNORM_ERR_UNSUPPORTED) or
- * RMSNORM_PATH_TWOPASS (rows of any width, read twice).  Every other field must be zero, else RMSNORM_ERR_INVALID_ARG. */
+ * RMSNORM_PATH_TWOPASS (rows of any width, read twice).  The kernels have no waits and
+ * no epilogue: wait_timeout_ns and epilogue_alpha are not read.  Every other field
+ * must be zero, else RMSNORM_ERR_INVALID_ARG. */
 rmsnorm_status_t rowsoftmax_relbias_fwd_ex(int32_t dtype, const void* x, const void* table,
                                            void* y, int64_t batch, int64_t heads, int64_t q_len,
                                            int64_t k_len, const rowsoftmax_relbias_t* bias,

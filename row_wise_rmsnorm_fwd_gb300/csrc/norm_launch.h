@@ -14,13 +14,13 @@ struct NormParams {
     void* out;             // y, or dx
     float* mean;           // layer norm: written forward (null: not wanted), read backward
     float* rstd;
-    float2* row_stats;     // two-kernel backward: a pair of sums per row
+    float2* row_stats;     // three-kernel backward: a pair of sums per row
     float* part_w;         // backward: [parts][hidden] partial sums of dw (null: not wanted)
     float* part_b;         // the same for db
     float* dw;
     float* db;
     int64_t rows;
-    int64_t rows_per_part; // two-kernel backward: rows of one partial sum
+    int64_t rows_per_part; // three-kernel backward: rows of one partial sum
     int32_t hidden;
     int32_t nvec;          // vectors per row
     int32_t parts;

@@ -164,3 +164,28 @@ def test_relbias_backward_of_short_rows_in_registers(keys, t):
     for buckets, distance in ((32, 128), (64, 500), (256, 500), (256, 4096)):
         binding.rowsoftmax_relbias_bwd_ex(y, y, buckets, max_distance=distance,
                                           options={"path": "rowreg"})
+
+
+def staged_norm_bwd(name, t, hidden):
+    """Whether the one-pass kernel of a backward pass takes rows of this length."""
+    x = torch.ones((2, hidden), dtype=TYPES[t], device="cuda")
+    stats = [torch.zeros(2, device="cuda"), torch.ones(2, device="cuda")]
+    args = [x, x, None] + (stats if name == "layernorm_bwd_ex" else [])
+    try:
+        getattr(binding, name)(*args, options={"path": "staged"})
+    except binding.RmsnormError as e:
+        assert e.status == binding.RMSNORM_ERR_UNSUPPORTED
+        return False
+    return True
+
+
+@pytest.mark.parametrize("name", ["layernorm_bwd_ex", "rmsnorm_bwd_ex"])
+def test_widest_rows_of_the_one_pass_backward_kernel(name):
+    """Two blocks of x and dy, of a row each, and off the 16-byte boundaries the
+    weights beside them, must fit a CTA's shared memory: in fp32 rows of 14400
+    elements, and of 11517 (2880 vectors that they touch); in both types none above
+    16384."""
+    for t, hidden, fits in (("f32", 14400, True), ("f32", 14404, False), ("f32", 16384, False),
+                            ("f32", 11517, True), ("f32", 11518, False),
+                            ("bf16", 16384, True), ("bf16", 16383, True), ("bf16", 16392, False)):
+        assert staged_norm_bwd(name, t, hidden) == fits, (t, hidden)
