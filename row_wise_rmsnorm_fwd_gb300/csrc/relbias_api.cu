@@ -8,6 +8,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <limits>
 
 namespace rmsnorm {
 namespace {
@@ -22,8 +23,12 @@ constexpr int64_t kBwdStatic = 4 << 10;        // of a backward CTA, other than 
 //     near + log(n / near) / log(max_distance / near) * (half - near)
 // reaches the bucket's number, for real logarithms: an edge that is a whole
 // number (near * (max_distance / near)^(k / (half - near)) often is) belongs to
-// the upper bucket.  powl is off by a few units of its last place (2^-63 or
-// finer); no edge below 4096 that is not whole lies within 1e-16 of one.
+// the upper bucket.  Long doubles of 64 bits and more put an edge within 1e-18 of
+// its value, relatively; over all rules that check_rule lets pass (half up to 256,
+// max_distance up to 4096) no edge that is not whole lies within 4e-12 of a whole
+// number, so what is within 1e-16 of one is one.
+static_assert(std::numeric_limits<long double>::digits >= 64,
+              "bucket edges: a long double of 64 bits or more");
 void bucket_edges(int half, int max_distance, int32_t* edges) {
     const int near = half / 2;
     for (int k = 0; k < near; ++k) edges[k] = k;
