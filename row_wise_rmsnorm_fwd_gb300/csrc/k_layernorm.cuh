@@ -169,8 +169,8 @@ layernorm_twopass_kernel(const NormParams p) {
 template <typename T, bool SHIFT>
 __global__ void __launch_bounds__(1024) layernorm_staged_kernel(const NormParams p) {
     constexpr int EPV = VecTraits<T, 16>::kElems;
-    constexpr int PN = PairTraits<T, 16>::N;
-    using L = Lanes<2>;
+    constexpr int PN = kPairs<T>;
+    using L = Lanes;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ alignas(8) uint64_t bars[kBlockRingMaxSlots];
     __shared__ float2 red[2][32];
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(1024) layernorm_staged_kernel(const NormParams
             const Vec<16> x = ld_slot(src + v * 16);
 #pragma unroll
             for (int k = 0; k < PN; ++k) {
-                if (k & 1) s1 = lanes_plus<T, 16>(x, k, s1); else s0 = lanes_plus<T, 16>(x, k, s0);
+                if (k & 1) s1 = lanes_plus<T>(x, k, s1); else s0 = lanes_plus<T>(x, k, s0);
             }
         });
         float sum = (s0 + s1).total();
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(1024) layernorm_staged_kernel(const NormParams
             const Vec<16> x = ld_slot(src + v * 16);
 #pragma unroll
             for (int k = 0; k < PN; ++k) {
-                const L d = lanes_plus<T, 16>(x, k, about);
+                const L d = lanes_plus<T>(x, k, about);
                 if (k & 1) s1 = fma(d, d, s1); else s0 = fma(d, d, s0);
             }
         });
@@ -296,13 +296,13 @@ __global__ void __launch_bounds__(1024) layernorm_staged_kernel(const NormParams
                     float o[EPV];
 #pragma unroll
                     for (int k = 0; k < PN; ++k) {
-                        L y = lanes_plus<T, 16>(x, k, minus) * r;
+                        L y = lanes_plus<T>(x, k, minus) * r;
                         if constexpr (with_w && with_b) {
-                            y = fma(y, lanes<T, 16>(wi, k), lanes<T, 16>(bi, k));
+                            y = fma(y, lanes<T>(wi, k), lanes<T>(bi, k));
                         } else if constexpr (with_w) {
-                            y = y * lanes<T, 16>(wi, k);
+                            y = y * lanes<T>(wi, k);
                         } else if constexpr (with_b) {
-                            y = y + lanes<T, 16>(bi, k);
+                            y = y + lanes<T>(bi, k);
                         }
                         y.put(o + 2 * k);
                     }

@@ -201,12 +201,12 @@ __global__ void
 __maxnreg__((norm_bwd_regs(NV * VecTraits<T, 16>::kElems, LAYER, R)))
 norm_bwd_staged_kernel(const NormParams p) {
     constexpr int EPV = VecTraits<T, 16>::kElems;
-    constexpr int PN = PairTraits<T, 16>::N;
+    constexpr int PN = kPairs<T>;
     constexpr bool SHIFT = MODE == kShift;
     // 32 elements per thread are for rows of more than 8192: a CTA's block is one row, and
     // with threads rounded up to a warp only a thread's last vector may be missing
     constexpr bool WIDE = NV * EPV > 16;
-    using L = Lanes<2>;
+    using L = Lanes;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ alignas(8) uint64_t bars[kBlockRingMaxSlots];
     __shared__ float2 red[2][R][32];
@@ -278,7 +278,7 @@ norm_bwd_staged_kernel(const NormParams p) {
     auto weights = [&](int i) {
         if constexpr (SHIFT) return ld_slot_if(ws + i * G * 16, valid[i]);
         else if constexpr (MODE == kWhole) return ld_ro<16>(wg + i * G * 16);
-        else return p.w && valid[i] ? ld_ro<16>(wg + i * G * 16) : ones_vec<T, 16>();
+        else return p.w && valid[i] ? ld_ro<16>(wg + i * G * 16) : ones_vec<T>();
     };
     RingStep step;
     int n = 0;
@@ -309,10 +309,10 @@ norm_bwd_staged_kernel(const NormParams p) {
                 const Vec<16> w = weights(i);
 #pragma unroll
                 for (int k = 0; k < PN; ++k) {
-                    const L dk = lanes<T, 16>(d, k), wk = lanes<T, 16>(w, k);
+                    const L dk = lanes<T>(d, k), wk = lanes<T>(w, k);
                     L u;
-                    if constexpr (LAYER) u = lanes_plus<T, 16>(x, k, minus);
-                    else u = lanes<T, 16>(x, k);
+                    if constexpr (LAYER) u = lanes_plus<T>(x, k, minus);
+                    else u = lanes<T>(x, k);
                     const L du = dk * u;
                     if constexpr (LAYER) {
                         sa = fma(dk, wk, sa);
@@ -386,17 +386,17 @@ norm_bwd_staged_kernel(const NormParams p) {
                 float o[EPV];
 #pragma unroll
                 for (int k = 0; k < PN; ++k) {
-                    const L dk = lanes<T, 16>(d, k), wk = lanes<T, 16>(w, k);
+                    const L dk = lanes<T>(d, k), wk = lanes<T>(w, k);
                     if constexpr (LAYER) {
-                        const L u = lanes_plus<T, 16>(x, k, minus);
+                        const L u = lanes_plus<T>(x, k, minus);
                         (fma(u, c2, fma(dk, wk, c1)) * q).put(o + 2 * k);
                     } else if constexpr (WIDE) {
-                        const L u = lanes<T, 16>(x, k);
+                        const L u = lanes<T>(x, k);
                         aw[i * PN + k] = fma(dk * u, q, aw[i * PN + k]);
                         (fma(u, c2, dk * wk) * q).put(o + 2 * k);
                     } else {        // as many operations in another order: 3% less time here,
                                     // 4% more in rows of more than 8192 elements
-                        const L xh = lanes<T, 16>(x, k) * q;
+                        const L xh = lanes<T>(x, k) * q;
                         aw[i * PN + k] = fma(dk, xh, aw[i * PN + k]);
                         fma(xh, c2, dk * wk * q).put(o + 2 * k);
                     }

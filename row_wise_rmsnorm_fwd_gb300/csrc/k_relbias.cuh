@@ -367,9 +367,9 @@ __global__ void __launch_bounds__(kBiasWideThreads) relbias_bwd_wide_kernel(cons
 // first key, `shift` elements into it, so keys have indices from `shift` on;
 // the vectors at its two ends are stored element by element.
 
-// Registers per thread: what the widest instances take without spilling and,
-// above that, no more, for resident warps (the row's loads are the only ones in
-// flight).  Measured (% of the HBM copy peak, 4 vectors): bf16 forward 96 / 112 / 128
+// Registers per thread: few enough for resident warps (the row's loads are the only
+// ones in flight), at the price of small spills: backward bf16 with 4 vectors 36 to
+// 44 bytes a thread, with 6 16, forward bf16 shifted rows 28; fp32 none or 4.  Measured (% of the HBM copy peak, 4 vectors): bf16 forward 96 / 112 / 128
 // registers 89 / 90 / 90 on rows of 2048 and 41 / 38 / 38 on a decoding step;
 // backward 64 / 72 / 80 registers, bf16 rows of 2048 90 / 94 / 96, causal 73 /
 // 75 / 71, of 512 68 / 80 / 69, fp32 rows of 1024 89 / 91 / 91.
@@ -380,11 +380,6 @@ constexpr int bias_fwd_regs() {
 template <int NV>
 constexpr int bias_bwd_regs() { return NV == 4 ? 72 : 96; }
 
-__device__ __forceinline__ float bias_max(float v, int width) {
-    for (int m = width >> 1; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
-    return v;
-}
-
 // Where the pair (m, .) stands relative to the maximum M >= m; 1 if both are -inf.
 __device__ __forceinline__ float bias_factor(float m, float M) {
     return m == M ? 1.f : exp2f((m - M) * kLog2e);
@@ -392,6 +387,7 @@ __device__ __forceinline__ float bias_factor(float m, float M) {
 
 template <int EPV>
 struct VecWindow {
+    static_assert(EPV == 4 || EPV == 8, "vectors of 16 bytes");
     BiasVecWindow s;
     int lo, hi;
     __device__ __forceinline__ explicit VecWindow(const BiasWindow& w)
@@ -399,7 +395,7 @@ struct VecWindow {
     __device__ __forceinline__ int floats() const { return s.copies * s.copy; }
     // position of relative position r, and the r of position 0
     __device__ __forceinline__ int first() const { return -lo - 2 * EPV; }
-    static constexpr int C = EPV < 4 ? EPV : 4;       // copies, and floats of a chunk
+    static constexpr int C = 4;                       // copies, and floats of a chunk
     // where copy c keeps position idx >= c
     __device__ __forceinline__ int slot(int c, int idx) const {
         const int d = idx - c, q = d / C, h = d % C;      // C is a power of two, d >= 0
@@ -412,12 +408,12 @@ struct VecWindow {
 // moved into [vmin, vmax]; vectors up to vmin are all low, from vmax on all high.
 template <int EPV>
 struct WindowRow {
-    static constexpr int C = EPV < 4 ? EPV : 4;       // floats of a chunk
+    static constexpr int C = VecWindow<EPV>::C;
     int p0, p1;                                       // float offsets
     int vmin, vmax;
     __device__ __forceinline__ WindowRow(const VecWindow<EPV>& w, int r0) {
         const int base = r0 - w.first();              // position of the row's vector 0
-        constexpr int SH = EPV == 8 ? 3 : EPV == 4 ? 2 : EPV == 2 ? 1 : 0;
+        constexpr int SH = EPV == 8 ? 3 : 2;
         const int phase = base & (EPV - 1);           // 0 .. EPV - 1
         const int v0 = base >> SH;                    // whole vectors before it
         vmin = -v0;
@@ -435,32 +431,17 @@ struct WindowRow {
     }
     __device__ __forceinline__ int moved(int v) const { return min(max(v, vmin), vmax); }
     __device__ __forceinline__ void read(const float* win, int v, float (&b)[EPV]) const {
+        const float4 x = *reinterpret_cast<const float4*>(win + p0 + v * C);
+        b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w;
         if constexpr (EPV == 8) {
-            const float4 x = *reinterpret_cast<const float4*>(win + p0 + v * C);
             const float4 y = *reinterpret_cast<const float4*>(win + p1 + v * C);
-            b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w;
             b[4] = y.x; b[5] = y.y; b[6] = y.z; b[7] = y.w;
-        } else if constexpr (EPV == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(win + p0 + v * C);
-            b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w;
-        } else if constexpr (EPV == 2) {
-            const float2 x = *reinterpret_cast<const float2*>(win + p0 + v * C);
-            b[0] = x.x; b[1] = x.y;
-        } else {
-            b[0] = win[p0 + v];
         }
     }
     __device__ __forceinline__ void write(float* win, int v, const float (&b)[EPV]) const {
-        if constexpr (EPV == 8) {
-            *reinterpret_cast<float4*>(win + p0 + v * C) = make_float4(b[0], b[1], b[2], b[3]);
+        *reinterpret_cast<float4*>(win + p0 + v * C) = make_float4(b[0], b[1], b[2], b[3]);
+        if constexpr (EPV == 8)
             *reinterpret_cast<float4*>(win + p1 + v * C) = make_float4(b[4], b[5], b[6], b[7]);
-        } else if constexpr (EPV == 4) {
-            *reinterpret_cast<float4*>(win + p0 + v * C) = make_float4(b[0], b[1], b[2], b[3]);
-        } else if constexpr (EPV == 2) {
-            *reinterpret_cast<float2*>(win + p0 + v * C) = make_float2(b[0], b[1]);
-        } else {
-            win[p0 + v] = b[0];
-        }
     }
 };
 
@@ -534,7 +515,7 @@ __device__ __forceinline__ Vec<16> ld_vec(const void* base, int64_t e, bool cut,
     constexpr int EPV = VecTraits<T, 16>::kElems;
     const char* p = static_cast<const char*>(base) + e * static_cast<int>(sizeof(T));
     if (!cut) return ld_stream<16>(p);
-    Vec<16> v = zero_vec<16>();
+    Vec<16> v = zero_vec();
 #pragma unroll
     for (int k = 0; k < EPV; ++k) {
         if (e + k < total) {
@@ -578,8 +559,8 @@ __device__ __forceinline__ void st_vec(void* base, const Row& r, bool first, int
 template <typename T, int NV, bool SHIFT>
 __global__ void __maxnreg__((bias_fwd_regs<T, NV>())) relbias_fwd_rowreg_kernel(const BiasParams p) {
     constexpr int EPV = VecTraits<T, 16>::kElems;
-    constexpr int PN = PairTraits<T, 16>::N;
-    using L = Lanes<2>;
+    constexpr int PN = kPairs<T>;
+    using L = Lanes;
     extern __shared__ __align__(16) float win[];
     __shared__ float2 red[2][32];
     __shared__ float biases[kBiasMaxBuckets];
@@ -655,7 +636,7 @@ __global__ void __maxnreg__((bias_fwd_regs<T, NV>())) relbias_fwd_rowreg_kernel(
                 wr.read(win, wr.moved(v), b);
 #pragma unroll
                 for (int k = 0; k < PN; ++k)
-                    e[i * PN + k] = fma(lanes<T, 16>(cur[i], k), scale, L::of(b + 2 * k));
+                    e[i * PN + k] = fma(lanes<T>(cur[i], k), scale, L::of(b + 2 * k));
                 if (!all && !is.full(i)) {           // masked keys
 #pragma unroll
                     for (int k = 0; k < PN; ++k) {
@@ -675,7 +656,7 @@ __global__ void __maxnreg__((bias_fwd_regs<T, NV>())) relbias_fwd_rowreg_kernel(
         };
         const bool all = is.all();
         if (all) scores(std::true_type()); else scores(std::false_type());
-        m = width == 32 ? warp_allreduce_max(m) : bias_max(m, width);
+        m = width == 32 ? warp_allreduce_max(m) : group_allreduce_max(m, width);
         const L minus = L::all(m == -INFINITY ? 0.f : -m);
         L s0 = L::all(0.f), s1 = L::all(0.f);
         auto exponentials = [&](auto all) {
@@ -702,7 +683,7 @@ __global__ void __maxnreg__((bias_fwd_regs<T, NV>())) relbias_fwd_rowreg_kernel(
             __syncthreads();
             float2 o = make_float2(-INFINITY, 0.f);
             if (lane < wpg) o = slot[gw0 + lane];
-            const float M = __shfl_sync(0xffffffffu, bias_max(o.x, merge_width), 0);
+            const float M = __shfl_sync(0xffffffffu, group_allreduce_max(o.x, merge_width), 0);
             s = group_allreduce_sum(o.y * bias_factor(o.x, M), merge_width);
             s = __shfl_sync(0xffffffffu, s, 0);
             f = bias_factor(m, M);
@@ -714,7 +695,7 @@ __global__ void __maxnreg__((bias_fwd_regs<T, NV>())) relbias_fwd_rowreg_kernel(
             for (int i = 0; i < NV; ++i) {
                 const int j = (i * G + t) * EPV;
                 if (!all && is.none(i)) {
-                    if (ri.here && j < ri.end) st_vec<T, SHIFT>(p.out, ri, i == 0, j, zero_vec<16>());
+                    if (ri.here && j < ri.end) st_vec<T, SHIFT>(p.out, ri, i == 0, j, zero_vec());
                     continue;
                 }
                 float o[EPV];
@@ -794,8 +775,8 @@ __device__ __forceinline__ void bias_fold_vec(const BiasParams& p, const VecWind
 template <typename T, int NV, bool SHIFT, bool TURNS>
 __global__ void __maxnreg__(bias_bwd_regs<NV>()) relbias_bwd_rowreg_kernel(const BiasParams p) {
     constexpr int EPV = VecTraits<T, 16>::kElems;
-    constexpr int PN = PairTraits<T, 16>::N;
-    using L = Lanes<2>;
+    constexpr int PN = kPairs<T>;
+    using L = Lanes;
     extern __shared__ __align__(16) float wins[];
     __shared__ double sums[kBiasMaxBuckets];
     __shared__ float red[2][32];
@@ -858,17 +839,17 @@ __global__ void __maxnreg__(bias_bwd_regs<NV>()) relbias_bwd_rowreg_kernel(const
                 if (!all && is.none(i)) continue;
                 if (!all && !is.full(i)) {           // clear what is not a valid key
                     const int j = (i * G + t) * EPV;
-                    clear_from<T, 16>(y[i], max(ri.to - j, 0));
-                    clear_from<T, 16>(d[i], max(ri.to - j, 0));
+                    clear_from<T>(y[i], max(ri.to - j, 0));
+                    clear_from<T>(d[i], max(ri.to - j, 0));
                     if (SHIFT && i == 0) {
-                        clear_below<T, 16>(y[i], ri.shift - j);
-                        clear_below<T, 16>(d[i], ri.shift - j);
+                        clear_below<T>(y[i], ri.shift - j);
+                        clear_below<T>(d[i], ri.shift - j);
                     }
                 }
 #pragma unroll
                 for (int k = 0; k < PN; ++k) {
-                    if (k & 1) s1 = fma(lanes<T, 16>(y[i], k), lanes<T, 16>(d[i], k), s1);
-                    else s0 = fma(lanes<T, 16>(y[i], k), lanes<T, 16>(d[i], k), s0);
+                    if (k & 1) s1 = fma(lanes<T>(y[i], k), lanes<T>(d[i], k), s1);
+                    else s0 = fma(lanes<T>(y[i], k), lanes<T>(d[i], k), s0);
                 }
             }
         };
@@ -892,13 +873,13 @@ __global__ void __maxnreg__(bias_bwd_regs<NV>()) relbias_bwd_rowreg_kernel(const
             for (int i = 0; i < NV; ++i) {
                 const int v = i * G + t, j = v * EPV;
                 if (!all && is.none(i)) {
-                    if (ri.here && j < ri.end) st_vec<T, SHIFT>(p.out, ri, i == 0, j, zero_vec<16>());
+                    if (ri.here && j < ri.end) st_vec<T, SHIFT>(p.out, ri, i == 0, j, zero_vec());
                     continue;
                 }
                 L gk[PN];
 #pragma unroll
                 for (int k = 0; k < PN; ++k)
-                    gk[k] = lanes<T, 16>(y[i], k) * (lanes<T, 16>(d[i], k) + minus);
+                    gk[k] = lanes<T>(y[i], k) * (lanes<T>(d[i], k) + minus);
                 if (!all && !sound && !is.full(i)) {
 #pragma unroll
                     for (int k = 0; k < PN; ++k) {

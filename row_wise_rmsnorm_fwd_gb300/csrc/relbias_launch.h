@@ -54,7 +54,7 @@ struct BiasVecWindow {
 constexpr BiasVecWindow bias_vec_window(int lo, int hi, int epv) {
     BiasVecWindow w{};
     w.size = lo + hi + 4 * epv;
-    w.copies = epv < 4 ? epv : 4;
+    w.copies = 4;                      // epv is 4 or 8
     const int chunks = w.size / w.copies + 1;
     w.half = (chunks + 1) / 2;
     w.copy = (epv == 8 ? 2 * w.half : chunks) * w.copies;
