@@ -369,10 +369,11 @@ __global__ void __launch_bounds__(kBiasWideThreads) relbias_bwd_wide_kernel(cons
 
 // Registers per thread: few enough for resident warps (the row's loads are the only
 // ones in flight), at the price of small spills: backward bf16 with 4 vectors 36 to
-// 44 bytes a thread, with 6 16, forward bf16 shifted rows 28; fp32 none or 4.  Measured (% of the HBM copy peak, 4 vectors): bf16 forward 96 / 112 / 128
-// registers 89 / 90 / 90 on rows of 2048 and 41 / 38 / 38 on a decoding step;
-// backward 64 / 72 / 80 registers, bf16 rows of 2048 90 / 94 / 96, causal 73 /
-// 75 / 71, of 512 68 / 80 / 69, fp32 rows of 1024 89 / 91 / 91.
+// 44 bytes a thread, with 6 16, forward bf16 shifted rows 28; fp32 none or 4.
+// Measured (% of the HBM copy peak, 4 vectors): bf16 forward 96 / 112 / 128 registers
+// 89 / 90 / 90 on rows of 2048 and 41 / 38 / 38 on a decoding step; backward 64 / 72 /
+// 80 registers, bf16 rows of 2048 90 / 94 / 96, causal 73 / 75 / 71, of 512 68 / 80 /
+// 69, fp32 rows of 1024 89 / 91 / 91.
 template <typename T, int NV>
 constexpr int bias_fwd_regs() {
     return NV == 4 ? (sizeof(T) == 2 ? 96 : 80) : (sizeof(T) == 2 ? 128 : 104);

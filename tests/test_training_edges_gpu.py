@@ -189,3 +189,24 @@ def test_widest_rows_of_the_one_pass_backward_kernel(name):
                             ("f32", 11517, True), ("f32", 11518, False),
                             ("bf16", 16384, True), ("bf16", 16383, True), ("bf16", 16392, False)):
         assert staged_norm_bwd(name, t, hidden) == fits, (t, hidden)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("with_w", [True, False])
+@pytest.mark.parametrize("hidden,groups", [(1024, 4), (4096, 1), (768, 4), (5568, 1)])
+def test_a_dozen_blocks_of_two_rows_for_every_cta(hidden, groups, with_w, t):
+    """Layer norm's backward pass with enough rows, on any number of SMs, for two
+    rows between barriers (CTAs of `groups` rows, at most four to an SM and fewer
+    for wide rows); the 64-bit reference runs on the GPU."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = 12 * 2 * groups * sms * min(4, 16384 // hidden) + 11
+    g = torch.Generator(device="cuda").manual_seed(hidden)
+    rand = lambda *shape: torch.randn(shape, generator=g, device="cuda").to(TYPES[t])  # noqa: E731
+    x, dy, w = rand(rows, hidden) * 2 + 1, rand(rows, hidden), rand(hidden) if with_w else None
+    _, mean, rstd = binding.layernorm_fwd_ex(x, w, stats=True)
+    got = binding.layernorm_bwd_ex(dy, x, w, mean, rstd)
+    if w is None:
+        w = torch.ones(hidden, device="cuda")
+    want, tol = ref.layernorm_bwd(dy, x, w, mean, rstd)
+    for a, b, e, n in zip(got, want, tol, ("dx", "dw", "db")):
+        assert ((a.double() - b).abs() <= e).all(), n
