@@ -716,8 +716,23 @@ def rmsnorm_bwd_workspace(x) -> int:
 
 # ------------------------------ row softmax with a relative position bias --
 
+def _fit(bits, **numbers):
+    """Refuse a number that a C integer of `bits` bits cannot hold: ctypes would
+    keep its lower bits."""
+    for name, v in numbers.items():
+        if not -(1 << bits - 1) <= v < 1 << bits - 1:
+            raise ValueError(f"{name} = {v} is out of range")
+
+
+_I31, _I63 = 1 << 31, 1 << 63
+
+
 def _relbias(x, index, num_buckets, max_distance, bidirectional, causal, scale, q_offset, q_start,
              kv_len):
+    if not (-_I31 <= num_buckets < _I31 and -_I31 <= max_distance < _I31
+            and -_I63 <= q_offset < _I63):
+        _fit(32, num_buckets=num_buckets, max_distance=max_distance)
+        _fit(64, q_offset=q_offset)
     if index < 0 or x.dim() != 4 or not x.is_contiguous():
         raise ValueError("scores must be a contiguous CUDA tensor [batch, heads, queries, keys]")
     if q_start is not None:
@@ -888,6 +903,8 @@ def rowsoftmax_relbias_bwd_workspace(y, num_buckets, max_distance: int = 128,
 def rowsoftmax_relbias_bucket(relative: int, num_buckets: int, max_distance: int = 128,
                               bidirectional: bool = True) -> int:
     """The bucket of a relative position (key - query); -1 for an invalid rule."""
+    _fit(32, num_buckets=num_buckets, max_distance=max_distance)
+    _fit(64, relative=relative)
     return load().rowsoftmax_relbias_bucket(relative, num_buckets, max_distance,
                                             int(bool(bidirectional)))
 
