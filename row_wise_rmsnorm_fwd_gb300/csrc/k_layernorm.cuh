@@ -161,11 +161,11 @@ layernorm_twopass_kernel(const NormParams p) {
 // the merge update above, for shares of fixed counts, with the row's mean
 // known first.
 //
-// Measured (% of the HBM copy peak): fp32 65536 x 4096 320 us, 99, bound by HBM;
-// bf16 65536 x 8192 345 us, 92, 131072 x 1024 86 us, 92: half as many bytes for
-// the same instructions.  Rows of any length, whose edges are stored element by
-// element: bf16 16384 x 4097 70 us, 56, 8191 x 2050 23.5 us, 42.  Reading the row
-// twice instead (above): 954 and, bf16 65536 x 4096, 938 us against 175.
+// Measured (launches back to back, % of the HBM copy peak): fp32 65536 x 4096 323 us,
+// 98, bound by HBM; bf16 65536 x 8192 338 us, 94, 65536 x 1024 48 us, 82: half as many
+// bytes for the same instructions.  Rows of any length, whose edges are stored
+// element by element: bf16 16384 x 4097 64 us, 62, 8191 x 2050 21.6 us, 46.  Reading
+// the row twice instead (above): 954 and, bf16 65536 x 4096, 938 us against 173.
 template <typename T, bool SHIFT>
 __global__ void __launch_bounds__(1024) layernorm_staged_kernel(const NormParams p) {
     constexpr int EPV = VecTraits<T, 16>::kElems;

@@ -165,12 +165,12 @@ __global__ void __launch_bounds__(kBwdColsThreads) norm_bwd_cols_kernel(const No
 // under a predicate are not kept from pass to pass in registers that it lacks
 // (kWhole / kPartial: fp32 8192 x 12288 242 / 206 us, bf16 16384 x 16384 314 / 276).
 //
-// Measured (% of the HBM copy peak): layer norm bf16 65536 x 8192 526 us, 90,
-// 16384 x 16384 276 us, 86; fp32 32768 x 4096 241 us, 98; RMSNorm bf16 65536 x
-// 4096 241 us, 99, 65536 x 8192 492 us, 96, 16384 x 16384 241 us, 98.  What is
-// left in bf16 layer norm is the trips to shared memory (an access per vector
-// and pass, waited for by a quarter of the SM's warps: 126 registers each).  Rows
-// of any length: bf16 16384 x 4097 114 us, 52.  The three kernels above instead:
+// Measured (calls back to back, % of the HBM copy peak): layer norm bf16 65536 x 8192
+// 531 us, 89, 16384 x 16384 276 us, 86; fp32 32768 x 4096 241 us, 98; RMSNorm bf16
+// 65536 x 4096 243 us, 98, 65536 x 8192 493 us, 96, 16384 x 16384 238 us, 100.  What
+// is left in bf16 layer norm is the trips to shared memory (an access per vector
+// and pass, waited for by a quarter of the SM's warps: 127 registers each).  Rows
+// of any length: bf16 16384 x 4097 117 us, 51.  The three kernels above instead:
 // 910 us for bf16 65536 x 8192, 469 us for fp32 32768 x 4096.
 enum : int { kWhole, kPartial, kShift };
 
@@ -478,7 +478,7 @@ norm_bwd_staged_kernel(const NormParams p) {
 // dw and db from the parts, W columns per thread (4 where the columns are a
 // multiple of 4: 16-byte loads): a CTA takes 8 * W columns, of which each of its
 // 32 lanes adds every 32nd part, ten loads in flight, then the lanes in order.
-// grid.y: 0 = dw, 1 = db.  Measured, with the writing of the parts: 3.3 of 20.7 us
+// grid.y: 0 = dw, 1 = db.  Measured, with the writing of the parts: 3.3 of 21.9 us
 // (fp32 2048 x 3584, 304 parts; through shared memory and with 4-byte loads 7.7).
 template <int W>
 static __global__ void __launch_bounds__(kNormReduceThreads)

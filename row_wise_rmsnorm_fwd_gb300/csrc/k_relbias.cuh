@@ -30,16 +30,17 @@
 
 namespace rmsnorm {
 
-// Measured (% of the HBM copy peak, bf16 unless fp32 is said): forward 256 x 512 x
-// 512 44 us, 89, 128 x 2048 x 2048 360 us, 88, causal (half as many bytes read) 360
-// us, 66, fp32 256 x 512 x 2048 323 us, 98; backward 128 x 2048 x 2048 508 us, 93,
-// causal 426 us, 74, 256 x 512 x 512 75 us, 79, fp32 256 x 512 x 2048 489 us, 97.
+// Measured (calls back to back, % of the HBM copy peak, bf16 unless fp32 is said):
+// forward 256 x 512 x 512 48 us, 82, 128 x 2048 x 2048 356 us, 89, causal (half as many
+// bytes read) 354 us, 67, fp32 128 x 2048 x 2048 648 us, 98; backward 128 x 2048 x
+// 2048 507 us, 94, causal 429 us, 74, 256 x 512 x 512 77 us, 77, fp32 128 x 2048 x 2048
+// 948 us, 100.  Rows of 128 / 32 / 8 keys: forward 87 / 72 / 33, backward 85 / 53 / 28.
 // A row costs the same instructions and the same wait for its sum whether its
 // mask leaves all or half of it, so masked rows stay further from the bandwidth:
 // forward the issue slots (64-68% busy), backward the wait for y and dy (the
 // registers of a second row in flight would cost as many resident warps).
-// Odd rows: forward fp32 (21, 25, 422, 517) 203 us, 66, backward bf16 (5, 28, 873,
-// 761) 124 us, 66.
+// Odd rows: forward fp32 (21, 25, 422, 517) 196 us, 69, backward bf16 (5, 28, 873,
+// 761) 125 us, 66.
 constexpr int kBiasFoldRows = 64;
 constexpr int kBiasFoldTurns = 256;      // the same where rows share a window in turn
 
