@@ -19,6 +19,12 @@ _BINDING_NAMES = {
     "rowsoftmax_relbias_fwd_f32", "rowsoftmax_relbias_fwd_bf16", "rowsoftmax_relbias_fwd_ex",
     "rowsoftmax_relbias_bwd_f32", "rowsoftmax_relbias_bwd_bf16", "rowsoftmax_relbias_bwd_ex",
     "rowsoftmax_relbias_bwd_workspace", "rowsoftmax_relbias_bucket",
+    "rmsnorm_block_fwd_f32", "rmsnorm_block_fwd_bf16", "rmsnorm_block_fwd_ex",
+    "rmsnorm_block_bwd_f32", "rmsnorm_block_bwd_bf16", "rmsnorm_block_bwd_ex",
+    "rmsnorm_block_bwd_workspace", "rmsnorm_rope_freqs",
+    "rmsnorm_rope_fwd_f32", "rmsnorm_rope_fwd_bf16", "rmsnorm_rope_fwd_ex",
+    "rmsnorm_rope_bwd_f32", "rmsnorm_rope_bwd_bf16", "rmsnorm_rope_bwd_ex",
+    "rmsnorm_rope_bwd_workspace",
     "make_options", "RmsnormError", "raw", "load",
 }
 

@@ -15,6 +15,7 @@ import ctypes
 import functools
 import os
 import re
+import struct
 import threading
 from types import SimpleNamespace
 
@@ -60,6 +61,38 @@ class rowsoftmax_relbias_t(ctypes.Structure):
                 ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
                 ("q_offset", ctypes.c_int64), ("q_start", ctypes.c_void_p),
                 ("kv_len", ctypes.c_void_p)]
+
+
+class rmsnorm_block_t(ctypes.Structure):
+    _fields_ = [("post_w", ctypes.c_void_p), ("pre_w", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("gate_rows", ctypes.c_int64),
+                ("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float),
+                ("post_eps", ctypes.c_float), ("pre_eps", ctypes.c_float),
+                ("post_norm", ctypes.c_int32), ("pre_norm", ctypes.c_int32)]
+
+
+class rmsnorm_view_t(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("stride", ctypes.c_int64 * 3)]
+
+
+class rmsnorm_rope_heads_t(ctypes.Structure):
+    _fields_ = [("x", rmsnorm_view_t), ("dy", rmsnorm_view_t), ("out", rmsnorm_view_t),
+                ("w", ctypes.c_void_p), ("dw", ctypes.c_void_p), ("heads", ctypes.c_int64)]
+
+
+class rmsnorm_rope_t(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("n_positions", ctypes.c_int64), ("start", ctypes.c_int64),
+                ("position_bytes", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("mscale", ctypes.c_float)]
+
+
+class rmsnorm_rope_rule_t(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("original_len", ctypes.c_int64),
+                ("divisors", ctypes.POINTER(ctypes.c_double)), ("scaling", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32)]
 
 
 class RmsnormError(RuntimeError):
@@ -139,6 +172,22 @@ def open_library(path: str):
         fn.restype = ctypes.c_int
     lib.rowsoftmax_relbias_bwd_workspace.argtypes = [i32] + shape + [ctypes.POINTER(size)]
     lib.rowsoftmax_relbias_bwd_workspace.restype = ctypes.c_int
+    # structs of these two families are passed as packed bytes or byref
+    for family, args in (("rmsnorm_block_fwd", [vp] * 4 + [i64, i64, vp]),
+                         ("rmsnorm_block_bwd", [vp] * 9 + [i64, i64, vp, vp, size]),
+                         ("rmsnorm_rope_fwd", [vp] * 2 + [i64, i64, i64, vp]),
+                         ("rmsnorm_rope_bwd", [vp] * 2 + [i64, i64, i64, vp, vp, size])):
+        for suffix, before, after in (("_f32", [], []), ("_bf16", [], []), ("_ex", [i32], [opt])):
+            fn = getattr(lib, family + suffix)
+            fn.argtypes = before + args + after + [vp]
+            fn.restype = ctypes.c_int
+    lib.rmsnorm_block_bwd_workspace.argtypes = [i32, i64, i64, vp, ctypes.POINTER(size)]
+    lib.rmsnorm_rope_bwd_workspace.argtypes = [i32, i64, i64, i64, i64, ctypes.POINTER(size)]
+    lib.rmsnorm_rope_freqs.argtypes = [ctypes.POINTER(rmsnorm_rope_rule_t), vp,
+                                       ctypes.POINTER(f32)]
+    for name in ("rmsnorm_block_bwd_workspace", "rmsnorm_rope_bwd_workspace",
+                 "rmsnorm_rope_freqs"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.rowsoftmax_relbias_bucket.argtypes = [i64, i32, i32, i32]
     lib.rowsoftmax_relbias_bucket.restype = ctypes.c_int32
     return lib
@@ -907,6 +956,590 @@ def rowsoftmax_relbias_bucket(relative: int, num_buckets: int, max_distance: int
     _fit(64, relative=relative)
     return load().rowsoftmax_relbias_bucket(relative, num_buckets, max_distance,
                                             int(bool(bidirectional)))
+
+
+# ------------------------------------------------ the boundary of two blocks --
+
+_PACK_BLOCK = struct.Struct("4q4f2i").pack        # rmsnorm_block_t
+_PACK_HEADS = struct.Struct("15q").pack           # rmsnorm_rope_heads_t
+_PACK_ROPE = struct.Struct("4q4i2f").pack         # rmsnorm_rope_t
+
+
+def _packed(pack, *numbers):
+    """A struct's bytes; numbers that its fields cannot hold are refused."""
+    try:
+        return pack(*numbers)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"a number is out of range: {e}") from None
+
+
+def _gate_rows(gate, x, shape, hidden, index):
+    """How many rows share a row of the gate, which is one row, or has the leading
+    dims of x up to some dim (and ones for those behind it)."""
+    _require("gate", gate, x.dtype, gate.shape, index)
+    lead = gate.shape[:-1]
+    if gate.dim() == 0 or gate.shape[-1] != hidden or gate.dim() > len(shape):
+        raise ValueError(f"gate must end in {hidden} and have at most {len(shape)} dims, got "
+                         f"{tuple(gate.shape)}")
+    n = gate.numel() // hidden
+    if n == 1:
+        return max(1, x.numel() // hidden)
+    k = len(lead)
+    while k and lead[k - 1] == 1:
+        k -= 1
+    if lead[:k] != shape[:k]:
+        raise ValueError(f"gate must have the leading dims of x {tuple(shape)}, got "
+                         f"{tuple(gate.shape)}")
+    rows = 1
+    for v in shape[k:-1]:
+        rows *= v
+    return max(1, rows)
+
+
+def _block_rule(x, shape, hidden, index, post_w, pre_w, gate, post_norm, pre_norm, residual_scale,
+                branch_scale, post_eps, pre_eps):
+    dt = x.dtype
+    if post_w is not None:
+        if not post_norm:
+            raise ValueError("post_w without post_norm")
+        _require("post_w", post_w, dt, (hidden,), index)
+    if pre_w is not None:
+        if not pre_norm:
+            raise ValueError("pre_w without pre_norm")
+        _require("pre_w", pre_w, dt, (hidden,), index)
+    rows = 1 if gate is None else _gate_rows(gate, x, shape, hidden, index)
+    return _packed(_PACK_BLOCK, post_w.data_ptr() if post_w is not None else 0,
+                   pre_w.data_ptr() if pre_w is not None else 0,
+                   gate.data_ptr() if gate is not None else 0, rows, residual_scale, branch_scale,
+                   post_eps, pre_eps, bool(post_norm), bool(pre_norm))
+
+
+def _block_fwd(name, want, x, residual, post_w, pre_w, gate, h, y, post_norm, pre_norm,
+               residual_scale, branch_scale, post_eps, pre_eps, options, stream):
+    if _T is None:
+        _warm()
+    code = _code(x, want)
+    dt, shape, index = x.dtype, x.shape, x.get_device()
+    if index < 0 or not shape or not shape[-1] or not x.is_contiguous():
+        _input(x)
+    hidden = shape[-1]
+    _require("residual", residual, dt, shape, index)
+    if h is not None:
+        _require("h", h, dt, shape, index)
+    if y is not None:
+        if not pre_norm:
+            raise ValueError("y without pre_norm")
+        _require("y", y, dt, shape, index)
+    rule = _block_rule(x, shape, hidden, index, post_w, pre_w, gate, post_norm, pre_norm,
+                       residual_scale, branch_scale, post_eps, pre_eps)
+    if stream is None and index == _current_device():
+        return _block_fwd_on(_raw_stream(index), name, code, x, residual, h, y, hidden, rule,
+                             pre_norm, options)
+    return _elsewhere(index, stream, _block_fwd_on, name, code, x, residual, h, y, hidden, rule,
+                      pre_norm, options)
+
+
+def _block_fwd_on(handle, name, code, x, residual, h, y, hidden, rule, pre_norm, options):
+    if h is None:
+        h = _T.empty_like(x)
+    if y is None and pre_norm:
+        y = _T.empty_like(x)
+    st = (_lib or load()).rmsnorm_block_fwd_ex(
+        code, x.data_ptr(), residual.data_ptr(), h.data_ptr(),
+        y.data_ptr() if y is not None else None, x.numel() // hidden, hidden, rule,
+        _opt(options) if options is not None else None, handle) if x.numel() else 0
+    if st:
+        raise RmsnormError(st, name)
+    return h, y
+
+
+def rmsnorm_block_fwd_f32(x, residual, post_w=None, pre_w=None, gate=None, h=None, y=None, *,
+                          post_norm: bool = True, pre_norm: bool = True,
+                          residual_scale: float = 1.0, branch_scale: float = 1.0,
+                          post_eps: float = 1e-6, pre_eps: float = 1e-6, stream=None):
+    """(h, y): h = residual_scale * residual + branch_scale * gate * RMSNorm(x) * post_w,
+    the residual stream behind a block whose branch is x, and y = RMSNorm(h) * pre_w, the
+    next block's input, for float32 CUDA tensors (last dim = hidden).  post_norm=False adds
+    x itself, pre_norm=False gives no y (None).  Weights and gate may be None (ones); the
+    gate is [hidden], or has the leading dims of x up to some dim, and ones for those
+    behind it: [batch, hidden] or [batch, 1, hidden] for x [batch, seq, hidden] is a gate
+    for each sequence.  h and y may be x or residual (in place)."""
+    return _block_fwd("rmsnorm_block_fwd_f32", RMSNORM_DTYPE_F32, x, residual, post_w, pre_w, gate,
+                      h, y, post_norm, pre_norm, residual_scale, branch_scale, post_eps, pre_eps,
+                      None, stream)
+
+
+def rmsnorm_block_fwd_bf16(x, residual, post_w=None, pre_w=None, gate=None, h=None, y=None, *,
+                           post_norm: bool = True, pre_norm: bool = True,
+                           residual_scale: float = 1.0, branch_scale: float = 1.0,
+                           post_eps: float = 1e-6, pre_eps: float = 1e-6, stream=None):
+    """The same for bfloat16 CUDA tensors (fp32 arithmetic; y from the unrounded h)."""
+    return _block_fwd("rmsnorm_block_fwd_bf16", RMSNORM_DTYPE_BF16, x, residual, post_w, pre_w,
+                      gate, h, y, post_norm, pre_norm, residual_scale, branch_scale, post_eps,
+                      pre_eps, None, stream)
+
+
+def rmsnorm_block_fwd_ex(x, residual, post_w=None, pre_w=None, gate=None, h=None, y=None, *,
+                         post_norm: bool = True, pre_norm: bool = True,
+                         residual_scale: float = 1.0, branch_scale: float = 1.0,
+                         post_eps: float = 1e-6, pre_eps: float = 1e-6, options=None, stream=None):
+    """Either dtype, with options (path auto or twopass)."""
+    return _block_fwd("rmsnorm_block_fwd_ex", None, x, residual, post_w, pre_w, gate, h, y,
+                      post_norm, pre_norm, residual_scale, branch_scale, post_eps, pre_eps,
+                      options, stream)
+
+
+def _block_bwd(name, want, dy, dh, x, h, post_w, pre_w, gate, dx, dresidual, dpost_w, dpre_w,
+               dgate, post_norm, pre_norm, residual_scale, branch_scale, post_eps, pre_eps,
+               weight_grads, workspace, options, stream):
+    torch = _T or _warm()
+    code = _code(x, want)
+    dt, shape, index = x.dtype, x.shape, x.get_device()
+    if index < 0 or not shape or not shape[-1] or not x.is_contiguous():
+        _input(x)
+    hidden, f32 = shape[-1], torch.float32
+    if pre_norm:
+        _require("dy", dy, dt, shape, index)
+        _require("h", h, dt, shape, index)
+    elif dy is not None:
+        raise ValueError("dy without pre_norm")
+    if dh is not None:
+        _require("dh", dh, dt, shape, index)
+    if dx is not None:
+        _require("dx", dx, dt, shape, index)
+    if dresidual is not None:
+        _require("dresidual", dresidual, dt, shape, index)
+    if dpost_w is not None:
+        if not post_norm:
+            raise ValueError("dpost_w without post_norm")
+        _require("dpost_w", dpost_w, f32, (hidden,), index)
+    if dpre_w is not None:
+        if not pre_norm:
+            raise ValueError("dpre_w without pre_norm")
+        _require("dpre_w", dpre_w, f32, (hidden,), index)
+    if dgate is not None:
+        if gate is None:
+            raise ValueError("dgate without a gate")
+        _require("dgate", dgate, f32, gate.shape, index)
+    rule = _block_rule(x, shape, hidden, index, post_w, pre_w, gate, post_norm, pre_norm,
+                       residual_scale, branch_scale, post_eps, pre_eps)
+    grads = (weight_grads and post_w is not None, weight_grads and pre_w is not None,
+             gate.shape if weight_grads and gate is not None else None)
+    args = (name, code, dy, dh, x, h if pre_norm else None, dx, dresidual, dpost_w, dpre_w, dgate,
+            grads, hidden, rule, workspace, options, index)
+    if stream is None and index == _current_device():
+        return _block_bwd_on(_raw_stream(index), *args)
+    return _elsewhere(index, stream, _block_bwd_on, *args)
+
+
+@functools.lru_cache(maxsize=1024)
+def _block_workspace(code, rows, hidden, gate_rows, index):
+    """Bytes of workspace (with device `index` current); gate_rows 0: no gate."""
+    rule = _PACK_BLOCK(0, 0, 1 if gate_rows else 0, gate_rows, 1.0, 1.0, 0.0, 0.0, 0, 0)
+    size = ctypes.c_size_t()
+    st = load().rmsnorm_block_bwd_workspace(code, rows, hidden, rule, ctypes.byref(size))
+    if st != RMSNORM_OK:
+        raise RmsnormError(st, "rmsnorm_block_bwd_workspace")
+    return size.value
+
+
+def _block_bwd_on(handle, name, code, dy, dh, x, h, dx, dresidual, dpost_w, dpre_w, dgate, grads,
+                  hidden, rule, workspace, options, index):
+    empty, f32, dev = _T.empty, _T.float32, x.device
+    if dx is None:
+        dx = _T.empty_like(x)
+    if dresidual is None:
+        dresidual = _T.empty_like(x)
+    if dpost_w is None and grads[0]:
+        dpost_w = empty(hidden, dtype=f32, device=dev)
+    if dpre_w is None and grads[1]:
+        dpre_w = empty(hidden, dtype=f32, device=dev)
+    if dgate is None and grads[2] is not None:
+        dgate = empty(grads[2], dtype=f32, device=dev)
+    rows = x.numel() // hidden
+    if rows == 0:
+        for t in (dpost_w, dpre_w, dgate):
+            if t is not None:
+                t.zero_()
+        return dx, dresidual, dpost_w, dpre_w, dgate
+    gate_rows = _BLOCK_GATE(rule)
+    ws, n = _room(workspace, _block_workspace(code, rows, hidden, gate_rows, index), x)
+    st = (_lib or load()).rmsnorm_block_bwd_ex(
+        code, dy.data_ptr() if dy is not None else None, dh.data_ptr() if dh is not None else None,
+        x.data_ptr(), h.data_ptr() if h is not None else None, dx.data_ptr(),
+        dresidual.data_ptr(), _ptr(dpost_w), _ptr(dpre_w), _ptr(dgate), rows, hidden, rule,
+        ws.data_ptr(), n, _opt(options) if options is not None else None, handle)
+    if st:
+        raise RmsnormError(st, name)
+    return dx, dresidual, dpost_w, dpre_w, dgate
+
+
+def _BLOCK_GATE(rule):
+    """gate_rows of a packed rule, 0 without a gate."""
+    gate, rows = _UNPACK_GATE(rule, 16)
+    return rows if gate else 0
+
+
+_UNPACK_GATE = struct.Struct("2q").unpack_from
+
+
+def rmsnorm_block_bwd_f32(dy, dh, x, h, post_w=None, pre_w=None, gate=None, dx=None,
+                          dresidual=None, dpost_w=None, dpre_w=None, dgate=None, *,
+                          post_norm: bool = True, pre_norm: bool = True,
+                          residual_scale: float = 1.0, branch_scale: float = 1.0,
+                          post_eps: float = 1e-6, pre_eps: float = 1e-6,
+                          weight_grads: bool = True, workspace=None, stream=None):
+    """(dx, dresidual, dpost_w, dpre_w, dgate) from dy, what comes to h from everything
+    else (dh, None: nothing), x and the h of the forward pass, float32 CUDA tensors; the
+    rest as there (pre_norm=False: dy is None, h not needed).  dpost_w, dpre_w
+    and dgate (the gate's shape) are float32, computed for the weights that are given, or
+    if they are given themselves; weight_grads=False computes only those, the others are
+    None.  dx and dresidual may be one of dy, dh, x and h each (in place).  workspace: at
+    least rmsnorm_block_bwd_workspace(x, gate) bytes, else one is allocated."""
+    return _block_bwd("rmsnorm_block_bwd_f32", RMSNORM_DTYPE_F32, dy, dh, x, h, post_w, pre_w,
+                      gate, dx, dresidual, dpost_w, dpre_w, dgate, post_norm, pre_norm,
+                      residual_scale, branch_scale, post_eps, pre_eps, weight_grads, workspace,
+                      None, stream)
+
+
+def rmsnorm_block_bwd_bf16(dy, dh, x, h, post_w=None, pre_w=None, gate=None, dx=None,
+                           dresidual=None, dpost_w=None, dpre_w=None, dgate=None, *,
+                           post_norm: bool = True, pre_norm: bool = True,
+                           residual_scale: float = 1.0, branch_scale: float = 1.0,
+                           post_eps: float = 1e-6, pre_eps: float = 1e-6,
+                           weight_grads: bool = True, workspace=None, stream=None):
+    """The same for bfloat16 arrays, weights and gate (their gradients are float32)."""
+    return _block_bwd("rmsnorm_block_bwd_bf16", RMSNORM_DTYPE_BF16, dy, dh, x, h, post_w, pre_w,
+                      gate, dx, dresidual, dpost_w, dpre_w, dgate, post_norm, pre_norm,
+                      residual_scale, branch_scale, post_eps, pre_eps, weight_grads, workspace,
+                      None, stream)
+
+
+def rmsnorm_block_bwd_ex(dy, dh, x, h, post_w=None, pre_w=None, gate=None, dx=None,
+                         dresidual=None, dpost_w=None, dpre_w=None, dgate=None, *,
+                         post_norm: bool = True, pre_norm: bool = True,
+                         residual_scale: float = 1.0, branch_scale: float = 1.0,
+                         post_eps: float = 1e-6, pre_eps: float = 1e-6,
+                         weight_grads: bool = True, workspace=None, options=None, stream=None):
+    """Either dtype, with options (path auto or twopass)."""
+    return _block_bwd("rmsnorm_block_bwd_ex", None, dy, dh, x, h, post_w, pre_w, gate, dx,
+                      dresidual, dpost_w, dpre_w, dgate, post_norm, pre_norm, residual_scale,
+                      branch_scale, post_eps, pre_eps, weight_grads, workspace, options, stream)
+
+
+def rmsnorm_block_bwd_workspace(x, gate=None) -> int:
+    """Bytes of workspace of rmsnorm_block_bwd_* for a tensor of x's shape and type."""
+    torch = _T or _warm()
+    _input(x)
+    hidden, index = x.shape[-1], x.get_device()
+    rows = 0 if gate is None else _gate_rows(gate, x, x.shape, hidden, index)
+    with torch.cuda.device(index):
+        return _block_workspace(_code(x, None), x.numel() // hidden, hidden, rows, index)
+
+
+# ------------------------------------------ rotary positions with head norms --
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
+_TURNS = {"ramp": (1.0, 32.0), "bands": (1.0, 4.0)}       # low, high unless given
+
+
+def rmsnorm_rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none",
+                       factor: float = 1.0, original_len: int = 0, low: float = None,
+                       high: float = None, divisors=None, device=None):
+    """(freqs, mscale) for rmsnorm_rope_fwd_* and _bwd_*: rot_dim / 2 frequencies
+    base^(-2i / rot_dim) as an int64 tensor of 2^-64 turns per position on `device`
+    (default: the current CUDA device).  scaling for contexts longer than the
+    original_len positions of training: "linear" divides all by factor, "base" raises
+    the base so that the slowest is divided by it, "ramp" keeps pairs that make more than
+    `high` (32) turns over original_len, divides those below `low` (1), in proportion to the
+    pair's number between them, and gives mscale 0.1 ln(factor) + 1, "bands" the same by
+    turns (low 1, high 4).  divisors: a number for each frequency that it is divided by."""
+    torch = _T or _warm()
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    _fit(32, rot_dim=rot_dim)
+    _fit(64, original_len=original_len)
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError(f"rot_dim must be even and at least 2, got {rot_dim}")
+    half = rot_dim // 2
+    turns = _TURNS.get(scaling, (0.0, 0.0))
+    each = None
+    if divisors is not None:
+        if len(divisors) != half:
+            raise ValueError(f"divisors must be {half} numbers, got {len(divisors)}")
+        each = (ctypes.c_double * half)(*map(float, divisors))
+    rule = rmsnorm_rope_rule_t(base, factor, turns[0] if low is None else low,
+                               turns[1] if high is None else high, original_len, each,
+                               ROPE_SCALINGS[scaling], rot_dim)
+    freqs, mscale = torch.empty(half, dtype=torch.int64), ctypes.c_float()
+    st = load().rmsnorm_rope_freqs(ctypes.byref(rule), freqs.data_ptr(), ctypes.byref(mscale))
+    if st != RMSNORM_OK:
+        raise RmsnormError(st, "rmsnorm_rope_freqs")
+    return freqs.to("cuda" if device is None else device), mscale.value
+
+
+def _heads(name, t, dtype, shape, index):
+    """Refuse `t` unless it is of this type, shape and device with contiguous heads."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"the elements of a head of {name} must be contiguous")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on device cuda:{index}, got {t.device}")
+
+
+def _view(t):
+    """Pointer and strides of batch, token and head; tokens alone: one batch."""
+    if t is None:
+        return 0, 0, 0, 0
+    s = t.stride()
+    return (t.data_ptr(), *s[:3]) if len(s) == 4 else (t.data_ptr(), 0, s[0], s[1])
+
+
+def _rope_rule(lead, dim, index, freqs, positions, norm, interleaved, start, mscale, eps):
+    torch = _T
+    half = freqs.shape[0] if freqs.dim() == 1 else 0
+    if freqs.dtype != torch.int64 or not half or 2 * half > dim or not freqs.is_contiguous():
+        raise ValueError(f"freqs must be the contiguous int64 tensor that rmsnorm_rope_freqs gives "
+                         f"for a rot_dim of at most {dim}")
+    if freqs.get_device() != index:
+        raise ValueError(f"freqs must be on device cuda:{index}, got {freqs.device}")
+    at = n = size = 0
+    if positions is not None:
+        size = 8 if positions.dtype == torch.int64 else 4 if positions.dtype == torch.int32 else 0
+        if not size:
+            raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
+        shape = positions.shape
+        if shape != lead and shape != lead[-1:] and shape != (1, *lead[-1:]):
+            raise ValueError(f"positions must have shape {tuple(lead)} or {tuple(lead[-1:])}, got "
+                             f"{tuple(shape)}")
+        if positions.get_device() != index or not positions.is_contiguous():
+            raise ValueError(f"positions must be contiguous, on device cuda:{index}")
+        at, n = positions.data_ptr(), max(1, positions.numel())
+    return _packed(_PACK_ROPE, freqs.data_ptr(), at, n, start, size, 2 * half, bool(interleaved),
+                   bool(norm), eps, mscale)
+
+
+def _rope_shapes(first, other):
+    """Leading dims and head_dim of two tensors [..., heads, head_dim]; other may be None."""
+    shape, index = first.shape, first.get_device()
+    if index < 0:
+        raise ValueError("q must be a CUDA tensor")
+    if len(shape) not in (3, 4):
+        raise ValueError("q must be [batch, seq, heads, head_dim] or [tokens, heads, head_dim], "
+                         f"got {tuple(shape)}")
+    if other is not None and (other.shape[:-2] != shape[:-2] or other.shape[-1:] != shape[-1:]):
+        raise ValueError(f"k must be like q {tuple(shape)} but for its heads, got "
+                         f"{tuple(other.shape)}")
+    return shape, index
+
+
+def _rope_fwd(name, want, q, k, freqs, positions, q_w, k_w, q_out, k_out, norm, interleaved, start,
+              mscale, eps, options, stream):
+    if _T is None:
+        _warm()
+    code = _code(q, want)
+    shape, index = _rope_shapes(q, k)
+    dt, dim = q.dtype, shape[-1]
+    _heads("q", q, dt, shape, index)
+    if q_out is not None:
+        _heads("q_out", q_out, dt, shape, index)
+    if k is not None:
+        _heads("k", k, dt, k.shape, index)
+        if k_out is not None:
+            _heads("k_out", k_out, dt, k.shape, index)
+    elif k_out is not None or k_w is not None:
+        raise ValueError("k_out and k_w need a k")
+    for n, w in (("q_w", q_w), ("k_w", k_w)):
+        if w is not None:
+            if not norm:
+                raise ValueError(f"{n} without norm")
+            _require(n, w, dt, (dim,), index)
+    rule = _rope_rule(shape[:-2], dim, index, freqs, positions, norm, interleaved, start, mscale,
+                      eps)
+    if stream is None and index == _current_device():
+        return _rope_fwd_on(_raw_stream(index), name, code, q, k, q_w, k_w, q_out, k_out, shape,
+                            rule, options)
+    return _elsewhere(index, stream, _rope_fwd_on, name, code, q, k, q_w, k_w, q_out, k_out, shape,
+                      rule, options)
+
+
+def _rope_fwd_on(handle, name, code, q, k, q_w, k_w, q_out, k_out, shape, rule, options):
+    if q_out is None:
+        q_out = _T.empty(shape, dtype=q.dtype, device=q.device)
+    hq = _PACK_HEADS(*_view(q), 0, 0, 0, 0, *_view(q_out),
+                     q_w.data_ptr() if q_w is not None else 0, 0, shape[-2])
+    hk = None
+    if k is not None:
+        if k_out is None:
+            k_out = _T.empty(k.shape, dtype=k.dtype, device=k.device)
+        hk = _PACK_HEADS(*_view(k), 0, 0, 0, 0, *_view(k_out),
+                         k_w.data_ptr() if k_w is not None else 0, 0, k.shape[-2])
+    batch, seq = shape[:2] if len(shape) == 4 else (1, shape[0])
+    if batch * seq:
+        st = (_lib or load()).rmsnorm_rope_fwd_ex(
+            code, hq, hk, batch, seq, shape[-1], rule,
+            _opt(options) if options is not None else None, handle)
+        if st:
+            raise RmsnormError(st, name)
+    return q_out, k_out
+
+
+def rmsnorm_rope_fwd_f32(q, k, freqs, positions=None, q_w=None, k_w=None, q_out=None, k_out=None, *,
+                         norm: bool = True, interleaved: bool = False, start: int = 0,
+                         mscale: float = 1.0, eps: float = 1e-6, stream=None):
+    """(q_out, k_out): each head of the float32 CUDA tensors q and k [batch, seq, heads,
+    head_dim] or [tokens, heads, head_dim] normed (RMSNorm over head_dim times q_w or k_w,
+    None: ones; norm=False: not normed) and its first 2 * len(freqs) elements turned to its
+    token's position: pairs (i, i + half), or neighbours if interleaved.  k may be None.
+    freqs and mscale from rmsnorm_rope_freqs.  Token s of a sequence stands at start +
+    positions[..., s] (int32 or int64, [batch, seq] or [seq]), or start + s without
+    positions.  q and k may be strided views with contiguous heads, and q_out and k_out the
+    views q and k themselves (in place)."""
+    return _rope_fwd("rmsnorm_rope_fwd_f32", RMSNORM_DTYPE_F32, q, k, freqs, positions, q_w, k_w,
+                     q_out, k_out, norm, interleaved, start, mscale, eps, None, stream)
+
+
+def rmsnorm_rope_fwd_bf16(q, k, freqs, positions=None, q_w=None, k_w=None, q_out=None, k_out=None,
+                          *, norm: bool = True, interleaved: bool = False, start: int = 0,
+                          mscale: float = 1.0, eps: float = 1e-6, stream=None):
+    """The same for bfloat16 q, k, q_w and k_w (fp32 arithmetic)."""
+    return _rope_fwd("rmsnorm_rope_fwd_bf16", RMSNORM_DTYPE_BF16, q, k, freqs, positions, q_w, k_w,
+                     q_out, k_out, norm, interleaved, start, mscale, eps, None, stream)
+
+
+def rmsnorm_rope_fwd_ex(q, k, freqs, positions=None, q_w=None, k_w=None, q_out=None, k_out=None, *,
+                        norm: bool = True, interleaved: bool = False, start: int = 0,
+                        mscale: float = 1.0, eps: float = 1e-6, options=None, stream=None):
+    """Either dtype, with options (path auto or twopass)."""
+    return _rope_fwd("rmsnorm_rope_fwd_ex", None, q, k, freqs, positions, q_w, k_w, q_out, k_out,
+                     norm, interleaved, start, mscale, eps, options, stream)
+
+
+def _rope_bwd(name, want, dq, dk, freqs, positions, q, k, q_w, k_w, dq_in, dk_in, dq_w, dk_w, norm,
+              interleaved, start, mscale, eps, weight_grads, workspace, options, stream):
+    torch = _T or _warm()
+    if norm is None:
+        norm = q is not None
+    code = _code(dq, want)
+    shape, index = _rope_shapes(dq, dk)
+    dt, dim = dq.dtype, shape[-1]
+    both = [("q", dq, q, q_w, dq_in, dq_w)]
+    if dk is not None:
+        both.append(("k", dk, k, k_w, dk_in, dk_w))
+    elif any(t is not None for t in (k, k_w, dk_in, dk_w)):
+        raise ValueError("k, k_w, dk_in and dk_w need a dk")
+    for n, dy, x, w, dx, dw in both:
+        _heads("d" + n, dy, dt, dy.shape, index)
+        if dx is not None:
+            _heads(f"d{n}_in", dx, dt, dy.shape, index)
+        if norm:
+            _heads(n, x, dt, dy.shape, index)
+            if w is not None:
+                _require(n + "_w", w, dt, (dim,), index)
+            if dw is not None:
+                _require(f"d{n}_w", dw, torch.float32, (dim,), index)
+        elif w is not None or dw is not None:
+            raise ValueError(f"{n}_w and d{n}_w need the norm")
+    rule = _rope_rule(shape[:-2], dim, index, freqs, positions, norm, interleaved, start, mscale,
+                      eps)
+    args = (name, code, both, norm, weight_grads, workspace, shape, rule, options, index)
+    if stream is None and index == _current_device():
+        return _rope_bwd_on(_raw_stream(index), *args)
+    return _elsewhere(index, stream, _rope_bwd_on, *args)
+
+
+@functools.lru_cache(maxsize=1024)
+def _rope_workspace(code, batch, seq, heads, dim, index):
+    """Bytes of workspace (with device `index` current)."""
+    size = ctypes.c_size_t()
+    st = load().rmsnorm_rope_bwd_workspace(code, batch, seq, heads, dim, ctypes.byref(size))
+    if st != RMSNORM_OK:
+        raise RmsnormError(st, "rmsnorm_rope_bwd_workspace")
+    return size.value
+
+
+def _rope_bwd_on(handle, name, code, both, norm, weight_grads, workspace, shape, rule, options,
+                 index):
+    batch, seq = shape[:2] if len(shape) == 4 else (1, shape[0])
+    dxs, dws, packed, heads = [None, None], [None, None], [None, None], 0
+    for i, (n, dy, x, w, dx, dw) in enumerate(both):
+        if dx is None:
+            dx = _T.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+        if dw is None and weight_grads and w is not None:
+            dw = _T.empty(shape[-1], dtype=_T.float32, device=dy.device)
+        dxs[i], dws[i] = dx, dw
+        heads += dy.shape[-2]
+        packed[i] = _PACK_HEADS(*_view(x if norm else None), *_view(dy), *_view(dx),
+                                w.data_ptr() if w is not None else 0,
+                                dw.data_ptr() if dw is not None else 0, dy.shape[-2])
+    if batch * seq == 0:
+        for dw in dws:
+            if dw is not None:
+                dw.zero_()
+        return (*dxs, *dws)
+    ws, size = None, 0
+    if dws[0] is not None or dws[1] is not None:
+        ws, size = _room(workspace, _rope_workspace(code, batch, seq, heads, shape[-1], index),
+                         dxs[0])
+    st = (_lib or load()).rmsnorm_rope_bwd_ex(
+        code, packed[0], packed[1], batch, seq, shape[-1], rule, _ptr(ws), size,
+        _opt(options) if options is not None else None, handle)
+    if st:
+        raise RmsnormError(st, name)
+    return (*dxs, *dws)
+
+
+def rmsnorm_rope_bwd_f32(dq, dk, freqs, positions=None, q=None, k=None, q_w=None, k_w=None,
+                         dq_in=None, dk_in=None, dq_w=None, dk_w=None, *, norm: bool = None,
+                         interleaved: bool = False, start: int = 0, mscale: float = 1.0,
+                         eps: float = 1e-6, weight_grads: bool = True, workspace=None, stream=None):
+    """(dq_in, dk_in, dq_w, dk_w): the gradients of q, k, q_w and k_w of rmsnorm_rope_fwd_f32
+    from those of its outputs, dq and dk (dk may be None); the rest as there.  With the norm
+    (the default if q is given) q and k are read again.  dq_w and dk_w are float32, computed
+    for the weights that are given, or if they are given themselves; weight_grads=False
+    computes only those, the others are None.  dq_in may be dq or q, and dk_in dk or k (in
+    place).  workspace: at least rmsnorm_rope_bwd_workspace(dq, dk) bytes, else one is
+    allocated."""
+    return _rope_bwd("rmsnorm_rope_bwd_f32", RMSNORM_DTYPE_F32, dq, dk, freqs, positions, q, k,
+                     q_w, k_w, dq_in, dk_in, dq_w, dk_w, norm, interleaved, start, mscale, eps,
+                     weight_grads, workspace, None, stream)
+
+
+def rmsnorm_rope_bwd_bf16(dq, dk, freqs, positions=None, q=None, k=None, q_w=None, k_w=None,
+                          dq_in=None, dk_in=None, dq_w=None, dk_w=None, *, norm: bool = None,
+                          interleaved: bool = False, start: int = 0, mscale: float = 1.0,
+                          eps: float = 1e-6, weight_grads: bool = True, workspace=None,
+                          stream=None):
+    """The same for bfloat16 tensors and weights (dq_w and dk_w are float32)."""
+    return _rope_bwd("rmsnorm_rope_bwd_bf16", RMSNORM_DTYPE_BF16, dq, dk, freqs, positions, q, k,
+                     q_w, k_w, dq_in, dk_in, dq_w, dk_w, norm, interleaved, start, mscale, eps,
+                     weight_grads, workspace, None, stream)
+
+
+def rmsnorm_rope_bwd_ex(dq, dk, freqs, positions=None, q=None, k=None, q_w=None, k_w=None,
+                        dq_in=None, dk_in=None, dq_w=None, dk_w=None, *, norm: bool = None,
+                        interleaved: bool = False, start: int = 0, mscale: float = 1.0,
+                        eps: float = 1e-6, weight_grads: bool = True, workspace=None, options=None,
+                        stream=None):
+    """Either dtype, with options (path auto or twopass)."""
+    return _rope_bwd("rmsnorm_rope_bwd_ex", None, dq, dk, freqs, positions, q, k, q_w, k_w, dq_in,
+                     dk_in, dq_w, dk_w, norm, interleaved, start, mscale, eps, weight_grads,
+                     workspace, options, stream)
+
+
+def rmsnorm_rope_bwd_workspace(q, k=None) -> int:
+    """Bytes of workspace of rmsnorm_rope_bwd_* for tensors of these shapes and type."""
+    torch = _T or _warm()
+    shape, index = _rope_shapes(q, k)
+    batch, seq = shape[:2] if len(shape) == 4 else (1, shape[0])
+    heads = shape[-2] + (k.shape[-2] if k is not None else 0)
+    with torch.cuda.device(index):
+        return _rope_workspace(_code(q, None), batch, seq, heads, shape[-1], index)
 
 
 def rmsnorm_last_device_status(stream=None) -> int:

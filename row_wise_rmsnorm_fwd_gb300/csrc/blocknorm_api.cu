@@ -1,0 +1,313 @@
+// blocknorm_api.cu -- C ABI of the boundary between two blocks
+// (include/rmsnorm_block.h): validation, kernel choice and launch.  Shares the
+// library's per-device state (device.h) and status conventions with the other entry
+// points.
+#include "rmsnorm_block.h"
+#include "blocknorm_launch.h"
+#include "checks.h"
+#include "device.h"
+
+#include <cmath>
+#include <cstring>
+
+namespace rmsnorm {
+namespace {
+
+constexpr int64_t kMaxHidden = 1 << 20;
+
+struct BlockCall {
+    int dtype = 0;
+    int sz = 0;
+    BlockParams p;
+    int32_t path = RMSNORM_PATH_AUTO;
+    DeviceView dv;
+};
+
+rmsnorm_status_t check_shape(int32_t dtype, int64_t rows, int64_t hidden, const rmsnorm_block_t* b,
+                             BlockCall* c) {
+    if (dtype != RMSNORM_DTYPE_F32 && dtype != RMSNORM_DTYPE_BF16) return RMSNORM_ERR_INVALID_ARG;
+    if (!b) return RMSNORM_ERR_INVALID_ARG;
+    std::memset(&c->p, 0, sizeof(c->p));
+    c->dtype = dtype;
+    c->sz = dtype == RMSNORM_DTYPE_F32 ? 4 : 2;
+    if (rows < 0 || hidden <= 0 || hidden > kMaxHidden) return RMSNORM_ERR_INVALID_ARG;
+    // every array, the fp32 sums of each row and gate row included, has a size in 63 bits
+    if (rows > (INT64_MAX / 64) / (hidden + 16)) return RMSNORM_ERR_INVALID_ARG;
+    if (b->gate && b->gate_rows < 1) return RMSNORM_ERR_INVALID_ARG;
+    BlockParams& p = c->p;
+    p.rows = rows;
+    p.hidden = static_cast<int32_t>(hidden);
+    p.inv_hidden = 1.0f / static_cast<float>(hidden);
+    p.gate_rows = b->gate && b->gate_rows < rows ? b->gate_rows : (rows > 0 ? rows : 1);
+    p.gates = rows > 0 ? div_up(rows, p.gate_rows) : 1;
+    return RMSNORM_OK;
+}
+
+// The rule and the options, once the shape is known to be good.
+rmsnorm_status_t check_rule(const rmsnorm_block_t& b, const rmsnorm_options_t* opt, BlockCall* c) {
+    if (b.post_norm < 0 || b.post_norm > 1 || b.pre_norm < 0 || b.pre_norm > 1 ||
+        !std::isfinite(b.residual_scale) || !std::isfinite(b.branch_scale) ||
+        !std::isfinite(b.post_eps) || b.post_eps < 0.f || !std::isfinite(b.pre_eps) || b.pre_eps < 0.f)
+        return RMSNORM_ERR_INVALID_ARG;
+    const uintptr_t sz = static_cast<uintptr_t>(c->sz);
+    if (!aligned(b.post_w, sz) || !aligned(b.pre_w, sz) || !aligned(b.gate, sz))
+        return RMSNORM_ERR_INVALID_ARG;
+    BlockParams& p = c->p;
+    p.post_w = b.post_norm ? b.post_w : nullptr;
+    p.pre_w = b.pre_norm ? b.pre_w : nullptr;
+    p.gate = b.gate;
+    p.post = b.post_norm;
+    p.pre = b.pre_norm;
+    p.residual_scale = b.residual_scale;
+    p.branch_scale = b.branch_scale;
+    p.post_eps = b.post_eps;
+    p.pre_eps = b.pre_eps;
+    if (!opt) return RMSNORM_OK;
+    const rmsnorm_options_t& o = *opt;
+    if (o.cluster || o.threads || o.grid || o.vec_bytes || o.chunk_bytes || o.stages || o.weights ||
+        o.reserved || o.epilogue || o.fault_inject)
+        return RMSNORM_ERR_INVALID_ARG;
+    if (o.path != RMSNORM_PATH_AUTO && o.path != RMSNORM_PATH_TWOPASS) return RMSNORM_ERR_INVALID_ARG;
+    c->path = o.path;
+    return RMSNORM_OK;
+}
+
+uintptr_t bits(const void* a) { return reinterpret_cast<uintptr_t>(a); }
+
+rmsnorm_status_t launch(const BlockCall& c, BlockFn fn, const LaunchShape& s, cudaStream_t stream) {
+    return note(launch_ex(fn, s, stream, c.p)) == cudaSuccess ? RMSNORM_OK : RMSNORM_ERR_CUDA;
+}
+
+int at_most(int64_t want, int64_t most) { return static_cast<int>(want < most ? want : most); }
+
+// ------------------------------------------------------------------- forward --
+
+rmsnorm_status_t fwd_run(int32_t dtype, const void* x, const void* residual, void* h, void* y,
+                         int64_t rows, int64_t hidden, const rmsnorm_block_t* b,
+                         const rmsnorm_options_t* opt, cudaStream_t stream) {
+    BlockCall c;
+    rmsnorm_status_t st = check_shape(dtype, rows, hidden, b, &c);
+    if (st != RMSNORM_OK) return st;
+    if (!x || !residual || !h) return RMSNORM_ERR_INVALID_ARG;
+    st = check_rule(*b, opt, &c);
+    if (st != RMSNORM_OK) return st;
+    const uintptr_t sz = static_cast<uintptr_t>(c.sz);
+    if ((c.p.pre != 0) != (y != nullptr) || !aligned(x, sz) || !aligned(residual, sz) ||
+        !aligned(h, sz) || !aligned(y, sz))
+        return RMSNORM_ERR_INVALID_ARG;
+    const uint64_t n = static_cast<uint64_t>(rows) * hidden * sz, nh = static_cast<uint64_t>(hidden) * sz;
+    const Span a[] = {span(x, n), span(residual, n), span(b->post_w, nh), span(b->pre_w, nh),
+                      span(b->gate, static_cast<uint64_t>(c.p.gates) * nh), span(h, n)};
+    if (clashes(a[5], a, 5, 2) || clashes(span(y, n), a, 5, 2) || overlaps(span(y, n), a[5]))
+        return RMSNORM_ERR_INVALID_ARG;
+    if (rows == 0) return RMSNORM_OK;
+    if (current_device(&c.dv) != cudaSuccess) return RMSNORM_ERR_CUDA;
+    c.p.x = x;
+    c.p.residual = residual;
+    c.p.h = h;
+    c.p.y = y;
+    const int vb = widest_vector(bits(x) | bits(residual) | bits(h) | bits(y) | bits(c.p.post_w) |
+                                 bits(c.p.pre_w) | bits(c.p.gate), hidden * c.sz, c.sz);
+    c.p.nvec = static_cast<int32_t>(hidden / (vb / c.sz));
+    const LaunchShape s{at_most(rows, 8ll * c.dv.sms), blocknorm_rows_block(), 1, 0};
+    return launch(c, blocknorm_fwd_any_ptr(dtype, vb), s, stream);
+}
+
+// ------------------------------------------------------------------ backward --
+
+constexpr int64_t kColsWaves = 8;      // CTAs per SM the column kernel aims at
+constexpr int64_t kMaxGridParts = 512; // of them side by side in the rows' direction
+
+struct BwdSpace {
+    int64_t parts_per_gate, parts, grid_parts;     // any-width kernels
+    uint64_t row_stats, part_pre, part_gate, gate_sums, bytes;
+};
+
+// Parts of the any-width kernels: enough CTAs to fill the GPU, at least four rows
+// each, none across gate rows.  Whatever the vectors' width, so that the workspace is
+// the same.
+BwdSpace bwd_space(const BlockCall& c) {
+    const BlockParams& p = c.p;
+    BwdSpace s;
+    auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
+    const int64_t col_ctas = div_up(static_cast<int64_t>(p.hidden) * c.sz, 16ll * blocknorm_cols_block());
+    int64_t want = div_up(kColsWaves * c.dv.sms, col_ctas);
+    if (want > kMaxGridParts) want = kMaxGridParts;
+    s.parts_per_gate = div_up(want, p.gates);
+    const int64_t most = div_up(p.gate_rows, 4);
+    if (s.parts_per_gate > most) s.parts_per_gate = most;
+    s.parts = p.gates * s.parts_per_gate;
+    s.grid_parts = s.parts < kMaxGridParts ? s.parts : kMaxGridParts;
+    const uint64_t row = static_cast<uint64_t>(p.hidden) * 4;
+    s.row_stats = 0;
+    s.part_pre = up(static_cast<uint64_t>(p.rows) * sizeof(float4));
+    s.part_gate = s.part_pre + up(s.grid_parts * row);
+    s.gate_sums = s.part_gate + up(s.parts * row);
+    s.bytes = s.gate_sums + (p.gates > 1 ? up(p.gates * row) : 0);
+    return s;
+}
+
+rmsnorm_status_t launch_reduce(const BlockCall& c, cudaStream_t stream) {
+    const BlockParams& p = c.p;
+    const int width = p.hidden % 4 == 0 ? 4 : 1;
+    LaunchShape s{static_cast<int>(div_up(p.hidden, kBlockReduceCols * width)), kBlockReduceThreads, 1, 0};
+    if (p.part_pre || p.part_gate) {
+        s.grid_y = p.part_gate ? 1 + at_most(p.gates, 65534) : 1;
+        const rmsnorm_status_t st = launch(c, blocknorm_reduce_ptr(c.dtype, width, true), s, stream);
+        if (st != RMSNORM_OK) return st;
+    }
+    if (!p.gate_sums) return RMSNORM_OK;
+    s.grid_y = 1;
+    return launch(c, blocknorm_reduce_ptr(c.dtype, width, false), s, stream);
+}
+
+rmsnorm_status_t bwd_workspace(int32_t dtype, int64_t rows, int64_t hidden, const rmsnorm_block_t* b,
+                               size_t* bytes) {
+    BlockCall c;
+    if (!bytes) return RMSNORM_ERR_INVALID_ARG;
+    const rmsnorm_status_t st = check_shape(dtype, rows, hidden, b, &c);
+    if (st != RMSNORM_OK) return st;
+    *bytes = 0;
+    if (rows == 0) return RMSNORM_OK;
+    if (current_device(&c.dv) != cudaSuccess) return RMSNORM_ERR_CUDA;
+    *bytes = bwd_space(c).bytes;
+    return RMSNORM_OK;
+}
+
+rmsnorm_status_t bwd_run(int32_t dtype, const void* dy, const void* dh, const void* x, const void* h,
+                         void* dx, void* dres, float* dpost_w, float* dpre_w, float* dgate,
+                         int64_t rows, int64_t hidden, const rmsnorm_block_t* b, void* workspace,
+                         size_t workspace_bytes, const rmsnorm_options_t* opt, cudaStream_t stream) {
+    BlockCall c;
+    rmsnorm_status_t st = check_shape(dtype, rows, hidden, b, &c);
+    if (st != RMSNORM_OK) return st;
+    if (!x || !dx || !dres) return RMSNORM_ERR_INVALID_ARG;
+    st = check_rule(*b, opt, &c);
+    if (st != RMSNORM_OK) return st;
+    if (c.p.pre ? !dy || !h : dy != nullptr) return RMSNORM_ERR_INVALID_ARG;
+    if ((dpost_w && !c.p.post) || (dpre_w && !c.p.pre) || (dgate && !b->gate))
+        return RMSNORM_ERR_INVALID_ARG;
+    if (!c.p.pre) h = nullptr;                   // not read
+    const uintptr_t sz = static_cast<uintptr_t>(c.sz);
+    if (!aligned(dy, sz) || !aligned(dh, sz) || !aligned(x, sz) || !aligned(h, sz) || !aligned(dx, sz) ||
+        !aligned(dres, sz) || !aligned(dpost_w, 4) || !aligned(dpre_w, 4) || !aligned(dgate, 4) ||
+        !aligned(workspace, 16))
+        return RMSNORM_ERR_INVALID_ARG;
+    const uint64_t n = static_cast<uint64_t>(rows) * hidden * sz, nh = static_cast<uint64_t>(hidden);
+    const uint64_t ng = static_cast<uint64_t>(c.p.gates) * nh;
+    const Span a[] = {span(dy, n),  span(dh, n),           span(x, n),           span(h, n),
+                      span(b->post_w, nh * sz), span(b->pre_w, nh * sz), span(b->gate, ng * sz),
+                      span(dx, n),  span(dres, n),         span(dpost_w, nh * 4), span(dpre_w, nh * 4),
+                      span(dgate, ng * 4)};
+    if (clashes(a[7], a, 7, 4) || clashes(a[8], a, 7, 4) || overlaps(a[7], a[8]) ||
+        clashes(a[9], a, 9, 0) || clashes(a[10], a, 10, 0) || clashes(a[11], a, 11, 0) ||
+        clashes(span(workspace, workspace_bytes), a, 12, 0))
+        return RMSNORM_ERR_INVALID_ARG;
+    if (rows == 0) {            // sums over no rows
+        float* sums[] = {dpost_w, dpre_w, dgate};
+        for (float* d : sums)
+            if (d && note(cudaMemsetAsync(d, 0, nh * 4, stream)) != cudaSuccess) return RMSNORM_ERR_CUDA;
+        return RMSNORM_OK;
+    }
+    if (!workspace) return RMSNORM_ERR_INVALID_ARG;
+    if (current_device(&c.dv) != cudaSuccess) return RMSNORM_ERR_CUDA;
+    const BwdSpace ws = bwd_space(c);
+    if (workspace_bytes < ws.bytes) return RMSNORM_ERR_INVALID_ARG;
+    char* base = static_cast<char*>(workspace);
+    BlockParams& p = c.p;
+    p.x = x;
+    p.dy = dy;
+    p.dh = dh;
+    p.h_in = h;
+    p.dx = dx;
+    p.dres = dres;
+    p.dpost_w = dpost_w;
+    p.dpre_w = dpre_w;
+    p.dgate = dgate;
+    p.row_stats = reinterpret_cast<float4*>(base + ws.row_stats);
+    p.part_pre = dpre_w ? reinterpret_cast<float*>(base + ws.part_pre) : nullptr;
+    p.part_gate = dpost_w || dgate ? reinterpret_cast<float*>(base + ws.part_gate) : nullptr;
+    p.gate_sums = dpost_w && p.gates > 1 ? reinterpret_cast<float*>(base + ws.gate_sums) : nullptr;
+    p.parts_per_gate = ws.parts_per_gate;
+    p.parts = ws.parts;
+    p.rows_per_part = div_up(p.gate_rows, ws.parts_per_gate);
+    p.pre_parts = static_cast<int32_t>(ws.grid_parts);
+    const int vb = widest_vector(bits(dy) | bits(dh) | bits(x) | bits(h) | bits(dx) | bits(dres) |
+                                 bits(p.post_w) | bits(p.pre_w) | bits(p.gate), hidden * c.sz, c.sz);
+    p.nvec = static_cast<int32_t>(hidden / (vb / c.sz));
+    const LaunchShape rs{at_most(rows, 8ll * c.dv.sms), blocknorm_rows_block(), 1, 0};
+    st = launch(c, blocknorm_bwd_rows_ptr(dtype, vb), rs, stream);
+    if (st != RMSNORM_OK) return st;
+    LaunchShape cs{static_cast<int>(div_up(p.nvec, blocknorm_cols_block())), blocknorm_cols_block(), 1, 0};
+    cs.grid_y = static_cast<int>(ws.grid_parts);
+    st = launch(c, blocknorm_bwd_cols_ptr(dtype, vb), cs, stream);
+    if (st != RMSNORM_OK) return st;
+    return launch_reduce(c, stream);
+}
+
+}  // namespace
+}  // namespace rmsnorm
+
+using namespace rmsnorm;
+
+extern "C" {
+
+rmsnorm_status_t rmsnorm_block_fwd_f32(const float* x, const float* residual, float* h, float* y,
+                                       int64_t rows, int64_t hidden, const rmsnorm_block_t* block,
+                                       rmsnorm_stream_t stream) {
+    return fwd_run(RMSNORM_DTYPE_F32, x, residual, h, y, rows, hidden, block, nullptr,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+rmsnorm_status_t rmsnorm_block_fwd_bf16(const uint16_t* x, const uint16_t* residual, uint16_t* h,
+                                        uint16_t* y, int64_t rows, int64_t hidden,
+                                        const rmsnorm_block_t* block, rmsnorm_stream_t stream) {
+    return fwd_run(RMSNORM_DTYPE_BF16, x, residual, h, y, rows, hidden, block, nullptr,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+rmsnorm_status_t rmsnorm_block_fwd_ex(int32_t dtype, const void* x, const void* residual, void* h,
+                                      void* y, int64_t rows, int64_t hidden,
+                                      const rmsnorm_block_t* block, const rmsnorm_options_t* opt,
+                                      rmsnorm_stream_t stream) {
+    return fwd_run(dtype, x, residual, h, y, rows, hidden, block, opt,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+rmsnorm_status_t rmsnorm_block_bwd_workspace(int32_t dtype, int64_t rows, int64_t hidden,
+                                             const rmsnorm_block_t* block, size_t* bytes) {
+    return bwd_workspace(dtype, rows, hidden, block, bytes);
+}
+
+rmsnorm_status_t rmsnorm_block_bwd_f32(const float* dy, const float* dh, const float* x,
+                                       const float* h, float* dx, float* dresidual, float* dpost_w,
+                                       float* dpre_w, float* dgate, int64_t rows, int64_t hidden,
+                                       const rmsnorm_block_t* block, void* workspace,
+                                       size_t workspace_bytes, rmsnorm_stream_t stream) {
+    return bwd_run(RMSNORM_DTYPE_F32, dy, dh, x, h, dx, dresidual, dpost_w, dpre_w, dgate, rows,
+                   hidden, block, workspace, workspace_bytes, nullptr,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+rmsnorm_status_t rmsnorm_block_bwd_bf16(const uint16_t* dy, const uint16_t* dh, const uint16_t* x,
+                                        const uint16_t* h, uint16_t* dx, uint16_t* dresidual,
+                                        float* dpost_w, float* dpre_w, float* dgate, int64_t rows,
+                                        int64_t hidden, const rmsnorm_block_t* block,
+                                        void* workspace, size_t workspace_bytes,
+                                        rmsnorm_stream_t stream) {
+    return bwd_run(RMSNORM_DTYPE_BF16, dy, dh, x, h, dx, dresidual, dpost_w, dpre_w, dgate, rows,
+                   hidden, block, workspace, workspace_bytes, nullptr,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+rmsnorm_status_t rmsnorm_block_bwd_ex(int32_t dtype, const void* dy, const void* dh, const void* x,
+                                      const void* h, void* dx, void* dresidual, float* dpost_w,
+                                      float* dpre_w, float* dgate, int64_t rows, int64_t hidden,
+                                      const rmsnorm_block_t* block, void* workspace,
+                                      size_t workspace_bytes, const rmsnorm_options_t* opt,
+                                      rmsnorm_stream_t stream) {
+    return bwd_run(dtype, dy, dh, x, h, dx, dresidual, dpost_w, dpre_w, dgate, rows, hidden, block,
+                   workspace, workspace_bytes, opt, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,61 @@
+// blocknorm_launch.h -- parameter block and kernel getters of the boundary between
+// two blocks (include/rmsnorm_block.h).  Internal to the library.
+#pragma once
+#include "launch.h"
+
+namespace rmsnorm {
+
+// Everything a kernel of this family needs; passed by value.
+struct BlockParams {
+    const void* x;
+    const void* residual;  // forward
+    const void* dy;        // backward
+    const void* dh;        // null: zeros
+    const void* h_in;      // backward: the forward pass's h
+    const void* post_w;    // null: ones
+    const void* pre_w;
+    const void* gate;
+    void* h;               // forward outputs; y null: not wanted
+    void* y;
+    void* dx;              // backward outputs
+    void* dres;
+    float4* row_stats;     // any-width backward: the four factors of each row
+    float* part_pre;       // partial sums of dpre_w (null: not wanted)
+    float* part_gate;      // partial sums of D * xh, from which dpost_w and dgate are made
+    float* gate_sums;      // [gates][hidden], their sums (several gate rows and dpost_w)
+    float* dpost_w;
+    float* dpre_w;
+    float* dgate;
+    int64_t rows;
+    int64_t gate_rows;     // rows of a gate row; without a gate: rows
+    int64_t gates;         // rows of the gate, 1 without one
+    int64_t rows_per_part; // any-width backward: rows of a part
+    int64_t parts_per_gate;
+    int64_t parts;         // any-width backward: gates * parts_per_gate
+    int32_t pre_parts;     // parts of dpre_w
+    int32_t hidden;
+    int32_t nvec;          // vectors per row
+    int32_t post;          // the branch is normed
+    int32_t pre;           // y is wanted
+    float inv_hidden;
+    float residual_scale;
+    float branch_scale;
+    float post_eps;
+    float pre_eps;
+};
+
+using BlockFn = void (*)(BlockParams);
+
+// dtype: 0 = fp32, 1 = bf16; vb = bytes per vector.  Any width.
+BlockFn blocknorm_fwd_any_ptr(int dtype, int vb);
+BlockFn blocknorm_bwd_rows_ptr(int dtype, int vb);
+BlockFn blocknorm_bwd_cols_ptr(int dtype, int vb);
+int blocknorm_rows_block();
+int blocknorm_cols_block();
+// Sums over the parts, `width` (4 or 1) columns to a thread.  gates: one grid row (y) for
+// dpre_w and one for each gate row; else dpost_w from the sums of several gate rows.
+BlockFn blocknorm_reduce_ptr(int dtype, int width, bool gates);
+constexpr int kBlockReduceThreads = 256;
+constexpr int kBlockReduceCols = 8;
+
+}  // namespace rmsnorm
