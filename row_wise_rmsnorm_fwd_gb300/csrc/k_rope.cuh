@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(32 * kRopeAnyWarps) rope_any_kernel(const Rope
             float v = 0.f;
 #pragma unroll
             for (int w = 0; w < kRopeAnyWarps; ++w) v += sums[w][j];
-            p.part[static_cast<int64_t>(blockIdx.x) * 2 * p.dim + j] = v;
+            p.part[static_cast<int64_t>(blockIdx.x) * p.part_stride + j] = v;
         }
     }
 }
@@ -194,9 +194,10 @@ static __global__ void __launch_bounds__(kRopeReduceThreads) rope_reduce_kernel(
     if (!t.dw) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = blockIdx.x * 32 + lane;
-    const float* from = p.part + static_cast<int64_t>(blockIdx.y) * p.dim + (col < p.dim ? col : 0);
+    const float* from = p.part + p.part_at[blockIdx.y] + (col < p.dim ? col : 0);
+    const int n = p.part_n[blockIdx.y];
     float s = 0.f;
-    for (int k = warp; k < p.parts; k += WARPS) s += from[static_cast<int64_t>(k) * 2 * p.dim];
+    for (int k = warp; k < n; k += WARPS) s += from[static_cast<int64_t>(k) * p.part_stride];
     red[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && col < p.dim) {

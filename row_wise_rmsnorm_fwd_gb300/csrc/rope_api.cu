@@ -73,6 +73,7 @@ rmsnorm_status_t freqs_of(const rmsnorm_rope_rule_t* r, uint64_t* freqs, float* 
 // ---------------------------------------------------------------------- checks --
 
 constexpr int64_t kMaxItems = 1ll << 40;
+constexpr int64_t kAngleRounds = 4;     // rounds of heads that a token's angles cost
 
 struct RopeCall {
     int dtype = 0;
@@ -276,16 +277,112 @@ rmsnorm_status_t launch(const RopeCall& c, RopeFn fn, const LaunchShape& s, cuda
     return note(launch_ex(fn, s, stream, c.p)) == cudaSuccess ? RMSNORM_OK : RMSNORM_ERR_CUDA;
 }
 
-// CTAs of the any kernel, and so its parts.
+// CTAs of the any kernel, and of the vector kernel, at most: what a workspace has parts for.
 int64_t any_ctas(const DeviceView& dv, int64_t items) {
     const int64_t ctas = div_up(items, kRopeAnyWarps), most = 8ll * dv.sms;
     return ctas < most ? ctas : most;
 }
+constexpr int64_t kVecCtasPerSm = 8;
 
-rmsnorm_status_t launch_any(const RopeCall& c, bool interleaved, bool back, cudaStream_t stream) {
-    const int64_t items = c.p.tokens * (c.p.t[0].heads + c.p.t[1].heads);
-    const LaunchShape s{static_cast<int>(any_ctas(c.dv, items)), 32 * kRopeAnyWarps, 1, 0};
-    return launch(c, rope_any_ptr(c.dtype, interleaved, back), s, stream);
+rmsnorm_status_t launch_any(RopeCall* c, bool interleaved, bool back, cudaStream_t stream) {
+    RopeParams& p = c->p;
+    const int ctas = static_cast<int>(any_ctas(c->dv, p.tokens * (p.t[0].heads + p.t[1].heads)));
+    p.part_stride = 2 * p.dim;
+    p.part_at[1] = p.dim;
+    p.part_n[0] = p.part_n[1] = ctas;
+    const LaunchShape s{ctas, 32 * kRopeAnyWarps, 1, 0};
+    return launch(*c, rope_any_ptr(c->dtype, interleaved, back), s, stream);
+}
+
+// Widest vector that the views, the head and its turned part (whole units) allow.
+int vec_bytes(const RopeCall& c, bool back) {
+    const RopeParams& p = c.p;
+    const uint64_t sz = static_cast<uint64_t>(c.sz);
+    uint64_t bits = static_cast<uint64_t>(p.dim | (p.rot / 2)) * sz;
+    for (const RopeHeads& t : p.t) {
+        bits |= reinterpret_cast<uintptr_t>(t.w);
+        const RopeView* views[] = {&t.x, &t.out, &t.dy};
+        for (int i = 0; i < (back ? 3 : 2); ++i) {
+            bits |= reinterpret_cast<uintptr_t>(views[i]->p);
+            // a dim of one element has a stride that is not used
+            if (c.batch > 1) bits |= static_cast<uint64_t>(views[i]->batch) * sz;
+            if (p.seq > 1) bits |= static_cast<uint64_t>(views[i]->token) * sz;
+            if (t.heads > 1) bits |= static_cast<uint64_t>(views[i]->head) * sz;
+        }
+    }
+    int v = 16;
+    while (v > c.sz && bits % v) v >>= 1;
+    return v;
+}
+
+int pow2_ceil(int v) {
+    int p = 1;
+    while (p < v) p <<= 1;
+    return p;
+}
+
+// Heads in vectors; *done stays false where a head has more than 32 units.
+rmsnorm_status_t launch_vec(RopeCall* c, bool interleaved, int kind, bool* done, cudaStream_t stream) {
+    RopeParams& p = c->p;
+    const int vb = vec_bytes(*c, kind != kRopeTurn);
+    const int epv = vb / c->sz;
+    p.units = static_cast<int32_t>(div_up(p.dim / epv, 2));
+    if (p.units > 32) return RMSNORM_OK;
+    p.lanes = pow2_ceil(p.units);
+    RopeFn fn = kind == kRopeTurn ? rope_vec_ptr_turn(c->dtype, vb, interleaved)
+                : kind == kRopeTurnBack ? rope_vec_ptr_back(c->dtype, vb, interleaved)
+                                        : rope_vec_ptr_grad(c->dtype, vb, interleaved);
+    int occ = 0;
+    if (cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(fn), 32 * kRopeVecWarps, 0,
+                         1, &occ) != cudaSuccess)
+        return RMSNORM_ERR_CUDA;
+    const int64_t most = c->dv.sms * (occ < kVecCtasPerSm ? occ : kVecCtasPerSm);
+    // A token's heads are shared by as many warps as it takes to have a warp for each of
+    // the GPU's warp slots, of one round of heads at least.
+    const int groups = 32 / p.lanes;
+    int64_t want[2] = {0, 0}, cost[2] = {0, 0};
+    for (int i = 0; i < 2; ++i) {
+        p.split[i] = 1;
+        if (!p.t[i].heads) continue;
+        const int64_t rounds = div_up(p.t[i].heads, groups);
+        int64_t split = div_up(most * kRopeVecWarps, p.tokens);
+        if (split > rounds) split = rounds;
+        p.split[i] = static_cast<int32_t>(split);
+        want[i] = div_up(p.tokens * split, kRopeVecWarps);
+        cost[i] = rounds + kAngleRounds;
+    }
+    int64_t q = want[0], k = want[1];
+    if (q + k > most) {           // shares of what they cost
+        q = most * cost[0] / (cost[0] + cost[1]);
+        if (q < 1) q = 1;
+        if (q > want[0]) q = want[0];
+        k = most - q;
+        if (k > want[1]) {
+            k = want[1];
+            q = most - k < want[0] ? most - k : want[0];
+        }
+        if (want[1] && k < 1) {
+            k = 1;
+            q = most - 1;
+        }
+    }
+    p.q_ctas = static_cast<int32_t>(q);
+    p.part_stride = p.dim;
+    p.part_at[1] = q * p.dim;
+    p.part_n[0] = static_cast<int32_t>(q);
+    p.part_n[1] = static_cast<int32_t>(k);
+    *done = true;
+    const LaunchShape s{static_cast<int>(q + k), 32 * kRopeVecWarps, 1, 0};
+    return launch(*c, fn, s, stream);
+}
+
+rmsnorm_status_t launch_rope(RopeCall* c, bool interleaved, int kind, cudaStream_t stream) {
+    if (c->path != RMSNORM_PATH_TWOPASS) {
+        bool done = false;
+        const rmsnorm_status_t st = launch_vec(c, interleaved, kind, &done, stream);
+        if (st != RMSNORM_OK || done) return st;
+    }
+    return launch_any(c, interleaved, kind != kRopeTurn, stream);
 }
 
 rmsnorm_status_t fwd_run(int32_t dtype, const rmsnorm_rope_heads_t* q, const rmsnorm_rope_heads_t* k,
@@ -295,7 +392,7 @@ rmsnorm_status_t fwd_run(int32_t dtype, const rmsnorm_rope_heads_t* q, const rms
     const rmsnorm_status_t st = check_call(dtype, q, k, batch, seq, dim, r, false, nullptr, 0, opt, &c);
     if (st != RMSNORM_OK || c.p.tokens == 0) return st;
     if (current_device(&c.dv) != cudaSuccess) return RMSNORM_ERR_CUDA;
-    return launch_any(c, r->interleaved != 0, false, stream);
+    return launch_rope(&c, r->interleaved != 0, kRopeTurn, stream);
 }
 
 rmsnorm_status_t bwd_workspace(int32_t dtype, int64_t batch, int64_t seq, int64_t heads, int64_t dim,
@@ -311,7 +408,9 @@ rmsnorm_status_t bwd_workspace(int32_t dtype, int64_t batch, int64_t seq, int64_
     if (items == 0) return RMSNORM_OK;
     DeviceView dv;
     if (current_device(&dv) != cudaSuccess) return RMSNORM_ERR_CUDA;
-    *bytes = static_cast<size_t>(any_ctas(dv, items)) * 2 * dim * 4;
+    // the any kernel has rows for q and k in each part, the vector kernel one
+    const int64_t any = 2 * any_ctas(dv, items), vec = kVecCtasPerSm * dv.sms;
+    *bytes = static_cast<size_t>(any > vec ? any : vec) * dim * 4;
     return RMSNORM_OK;
 }
 
@@ -339,9 +438,8 @@ rmsnorm_status_t bwd_run(int32_t dtype, const rmsnorm_rope_heads_t* q, const rms
         if (st != RMSNORM_OK) return st;
         if (workspace_bytes < need) return RMSNORM_ERR_INVALID_ARG;
         c.p.part = static_cast<float*>(workspace);
-        c.p.parts = static_cast<int32_t>(any_ctas(c.dv, c.p.tokens * (c.p.t[0].heads + c.p.t[1].heads)));
     }
-    st = launch_any(c, r->interleaved != 0, true, stream);
+    st = launch_rope(&c, r->interleaved != 0, r->norm ? kRopeGrad : kRopeTurnBack, stream);
     if (st != RMSNORM_OK || !sums) return st;
     LaunchShape s{static_cast<int>(div_up(dim, 32)), kRopeReduceThreads, 1, 0};
     s.grid_y = 2;

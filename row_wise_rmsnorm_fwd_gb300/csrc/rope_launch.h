@@ -27,8 +27,14 @@ struct RopeParams {
     int64_t start;
     int64_t seq;
     int64_t tokens;        // batch * seq
-    float* part;           // partial sums of dw, [parts][2][dim]
-    int32_t parts;
+    float* part;           // partial sums of dw: of q (0) and k (1), part_n[i] of them from
+    int64_t part_at[2];    // part + part_at[i] on, part_stride apart
+    int32_t part_n[2];
+    int32_t part_stride;
+    int32_t lanes;         // vector kernel: lanes per head (a power of two)
+    int32_t units;         // pairs of vectors per head, at most lanes
+    int32_t q_ctas;        // CTAs that work on q, the others on k
+    int32_t split[2];      // warps that share a token's heads of q, of k
     int32_t wide;          // positions are 64-bit
     int32_t dim;
     int32_t rot;
@@ -44,6 +50,13 @@ using RopeFn = void (*)(RopeParams);
 // p.norm the norm's gradient.
 RopeFn rope_any_ptr(int dtype, bool interleaved, bool back);
 constexpr int kRopeAnyWarps = 4;
+// Heads in vectors of vb bytes, a few lanes per head: forward, backward without a norm, and
+// with one.
+enum : int { kRopeTurn, kRopeTurnBack, kRopeGrad };
+RopeFn rope_vec_ptr_turn(int dtype, int vb, bool interleaved);
+RopeFn rope_vec_ptr_back(int dtype, int vb, bool interleaved);
+RopeFn rope_vec_ptr_grad(int dtype, int vb, bool interleaved);
+constexpr int kRopeVecWarps = 4;
 // Sums of the parts: grid (columns / 32, 2).
 RopeFn rope_reduce_ptr();
 constexpr int kRopeReduceThreads = 1024;
