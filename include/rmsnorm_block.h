@@ -85,10 +85,16 @@ rmsnorm_status_t rmsnorm_block_fwd_bf16(const uint16_t* x, const uint16_t* resid
                                         uint16_t* y, int64_t rows, int64_t hidden,
                                         const rmsnorm_block_t* block, rmsnorm_stream_t stream);
 
-/* Either dtype, with options (`opt` may be NULL): opt->path RMSNORM_PATH_AUTO or
+/* Either dtype, with options (`opt` may be NULL): opt->path RMSNORM_PATH_AUTO,
+ * RMSNORM_PATH_STAGED (rows staged in shared memory by bulk copies, read from HBM once:
+ * every array and row a multiple of 16 bytes on 16-byte boundaries, rows of at most 512
+ * KB, backward 256 KB, split over a thread-block cluster above 32 KB, backward 16 KB;
+ * else RMSNORM_ERR_UNSUPPORTED; opt->cluster = 2, 4, 8 or 16 forces that split) or
  * RMSNORM_PATH_TWOPASS (a CTA per row that reads it again for each sum: any width and
- * alignment).  Every other field but wait_timeout_ns and epilogue_alpha, which are
- * not read, must be zero, else RMSNORM_ERR_INVALID_ARG. */
+ * alignment); opt->wait_timeout_ns; and in the test build of the library
+ * opt->fault_inject with RMSNORM_PATH_STAGED: 1 = each CTA's first copy is withheld, 2 =
+ * with opt->cluster, rank 0's first sums are (elsewhere RMSNORM_ERR_UNSUPPORTED).  Every other
+ * field but epilogue_alpha, which is not read, must be zero, else RMSNORM_ERR_INVALID_ARG. */
 rmsnorm_status_t rmsnorm_block_fwd_ex(int32_t dtype, const void* x, const void* residual, void* h,
                                       void* y, int64_t rows, int64_t hidden,
                                       const rmsnorm_block_t* block, const rmsnorm_options_t* opt,

@@ -14,12 +14,14 @@ namespace rmsnorm {
 namespace {
 
 constexpr int64_t kMaxHidden = 1 << 20;
+constexpr int kMaxCluster = 16;
 
 struct BlockCall {
     int dtype = 0;
     int sz = 0;
     BlockParams p;
     int32_t path = RMSNORM_PATH_AUTO;
+    int32_t cluster = 0;         // forced; 0: automatic
     DeviceView dv;
 };
 
@@ -64,11 +66,20 @@ rmsnorm_status_t check_rule(const rmsnorm_block_t& b, const rmsnorm_options_t* o
     p.pre_eps = b.pre_eps;
     if (!opt) return RMSNORM_OK;
     const rmsnorm_options_t& o = *opt;
-    if (o.cluster || o.threads || o.grid || o.vec_bytes || o.chunk_bytes || o.stages || o.weights ||
-        o.reserved || o.epilogue || o.fault_inject)
+    if (o.cluster < 0 || o.cluster > kMaxCluster || (o.cluster & (o.cluster - 1)) || o.threads || o.grid ||
+        o.vec_bytes || o.chunk_bytes || o.stages || o.weights || o.reserved || o.epilogue ||
+        o.fault_inject < 0 || o.fault_inject > 2)
         return RMSNORM_ERR_INVALID_ARG;
-    if (o.path != RMSNORM_PATH_AUTO && o.path != RMSNORM_PATH_TWOPASS) return RMSNORM_ERR_INVALID_ARG;
+    if (o.path != RMSNORM_PATH_AUTO && o.path != RMSNORM_PATH_STAGED && o.path != RMSNORM_PATH_TWOPASS)
+        return RMSNORM_ERR_INVALID_ARG;
+    if (o.cluster && o.path != RMSNORM_PATH_STAGED) return RMSNORM_ERR_INVALID_ARG;
+    if (o.fault_inject && (!RMSNORM_FAULT_INJECT || o.path != RMSNORM_PATH_STAGED ||
+                           (o.fault_inject == 2 && o.cluster < 2)))
+        return RMSNORM_ERR_UNSUPPORTED;
     c->path = o.path;
+    c->cluster = o.cluster;
+    p.fault = o.fault_inject;
+    p.timeout_ns = o.wait_timeout_ns;
     return RMSNORM_OK;
 }
 
@@ -79,6 +90,92 @@ rmsnorm_status_t launch(const BlockCall& c, BlockFn fn, const LaunchShape& s, cu
 }
 
 int at_most(int64_t want, int64_t most) { return static_cast<int>(want < most ? want : most); }
+
+// --------------------------------------------------------------- staged rows --
+
+constexpr int64_t kBlockThreads = 256;        // threads that narrow rows share a CTA of
+constexpr int64_t kBwdCtasPerSm = 4;          // at most, so that there are few parts
+
+int64_t pow2_ceil(int64_t v) {
+    int64_t p = 1;
+    while (p < v) p <<= 1;
+    return p;
+}
+
+// Threads for a row, or a slice, of nvec vectors.
+int64_t group_of(int64_t nvec) {
+    const int64_t g = div_up(nvec, kBlockStagedBytes / 16);
+    return g <= 32 ? pow2_ceil(g) : div_up(g, 32) * 32;
+}
+
+using PickFn = BlockFn (*)(int dtype, bool post, bool pre, bool cluster);
+
+// Rows staged in shared memory.  bits: of the addresses of the arrays, weights and gate;
+// narr: arrays with a place in a slot.  Leaves s->grid 0, status OK, where rows cannot be
+// staged.
+rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t address_bits, int narr, bool back, PickFn pick,
+                             LaunchShape* s, BlockFn* fn) {
+    BlockParams& p = c->p;
+    const int64_t row_bytes = static_cast<int64_t>(p.hidden) * c->sz;
+    s->grid = 0;
+    if (address_bits % 16 || row_bytes % 16) return RMSNORM_OK;
+    const int64_t nvec = row_bytes / 16;
+    const int64_t max_threads = back ? kBlockBwdMaxThreads : kBlockFwdMaxThreads;
+    const int64_t budget = c->dv.smem_optin - 6 * 1024;             // static shared memory beside it
+    for (int64_t cluster = c->cluster ? c->cluster : 1; cluster <= kMaxCluster; cluster *= 2) {
+        const int64_t slice = div_up(nvec, cluster);
+        // a split row's CTA is one group of whole warps, with a thread for each rank to send to
+        const int64_t narrow = group_of(slice), group = cluster > 1 && narrow < 32 ? 32 : narrow;
+        const bool last = c->cluster != 0;
+        // every rank has at least one vector
+        if (group <= max_threads && (cluster == 1 || (cluster - 1) * slice < nvec)) {
+            // Several narrow rows to a CTA, fewer where that leaves SMs without one or
+            // more than a gate row has.
+            int64_t rows = cluster == 1 && group < kBlockThreads ? kBlockThreads / group : 1;
+            while (rows > 1 && rows * group > 32 &&
+                   (div_up(p.rows, rows) < c->dv.sms || rows / 2 >= p.gate_rows))
+                rows /= 2;
+            const int block = static_cast<int>(rows * group);
+            const int64_t slot = narr * rows * slice * 16;
+            const int64_t scratch = back && rows > 1 ? rows * row_bytes * 4 / c->sz : 0;
+            *fn = pick(c->dtype, p.post != 0, p.pre != 0, cluster > 1);
+            int best = 0;
+            for (int64_t slots = 3; slots >= 2; --slots) {
+                const int64_t smem = slots * slot + scratch;
+                if (smem > budget) continue;
+                int occ = 0;
+                if (cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(*fn), block,
+                                     static_cast<int>(smem), static_cast<int>(cluster), &occ) != cudaSuccess)
+                    return RMSNORM_ERR_CUDA;
+                if (occ <= best) continue;
+                best = occ;
+                s->smem = static_cast<int>(smem);
+                p.nslots = static_cast<int32_t>(slots);
+            }
+            if (best > 0) {
+                const int64_t last_rows = p.rows - (p.gates - 1) * p.gate_rows;
+                p.block_rows = static_cast<int32_t>(rows);
+                p.blocks_per_gate = div_up(p.gate_rows, rows);
+                p.blocks = (p.gates - 1) * p.blocks_per_gate + div_up(last_rows, rows);
+                p.group = static_cast<int32_t>(group);
+                p.cluster = static_cast<int32_t>(cluster);
+                p.slice_vecs = static_cast<int32_t>(slice);
+                p.status = c->dv.status;
+                if (!p.timeout_ns) p.timeout_ns = kDefaultTimeoutNs;
+                if (back && best > kBwdCtasPerSm && cluster == 1) best = kBwdCtasPerSm;
+                int64_t units = cluster > 1 ? best : static_cast<int64_t>(c->dv.sms) * best;
+                if (units > p.blocks) units = p.blocks;
+                p.units = units;
+                s->grid = static_cast<int>(units * cluster);
+                s->block = block;
+                s->cluster = static_cast<int>(cluster);
+                return RMSNORM_OK;
+            }
+        }
+        if (last) break;
+    }
+    return RMSNORM_OK;
+}
 
 // ------------------------------------------------------------------- forward --
 
@@ -106,8 +203,17 @@ rmsnorm_status_t fwd_run(int32_t dtype, const void* x, const void* residual, voi
     c.p.residual = residual;
     c.p.h = h;
     c.p.y = y;
-    const int vb = widest_vector(bits(x) | bits(residual) | bits(h) | bits(y) | bits(c.p.post_w) |
-                                 bits(c.p.pre_w) | bits(c.p.gate), hidden * c.sz, c.sz);
+    const uintptr_t all = bits(x) | bits(residual) | bits(h) | bits(y) | bits(c.p.post_w) |
+                          bits(c.p.pre_w) | bits(c.p.gate);
+    if (c.path != RMSNORM_PATH_TWOPASS) {
+        LaunchShape s{0, 0, 1, 0};
+        BlockFn fn = nullptr;
+        st = plan_staged(&c, all, 2, false, blocknorm_fwd_staged_ptr, &s, &fn);
+        if (st != RMSNORM_OK) return st;
+        if (s.grid) return launch(c, fn, s, stream);
+        if (c.path == RMSNORM_PATH_STAGED) return RMSNORM_ERR_UNSUPPORTED;
+    }
+    const int vb = widest_vector(all, hidden * c.sz, c.sz);
     c.p.nvec = static_cast<int32_t>(hidden / (vb / c.sz));
     const LaunchShape s{at_most(rows, 8ll * c.dv.sms), blocknorm_rows_block(), 1, 0};
     return launch(c, blocknorm_fwd_any_ptr(dtype, vb), s, stream);
@@ -138,11 +244,14 @@ BwdSpace bwd_space(const BlockCall& c) {
     if (s.parts_per_gate > most) s.parts_per_gate = most;
     s.parts = p.gates * s.parts_per_gate;
     s.grid_parts = s.parts < kMaxGridParts ? s.parts : kMaxGridParts;
+    // the staged kernel's: a part for each unit, and one more for each gate row but the first
+    const int64_t units = p.rows < kBwdCtasPerSm * c.dv.sms ? p.rows : kBwdCtasPerSm * c.dv.sms;
+    const int64_t gate_parts = units + p.gates - 1;
     const uint64_t row = static_cast<uint64_t>(p.hidden) * 4;
     s.row_stats = 0;
     s.part_pre = up(static_cast<uint64_t>(p.rows) * sizeof(float4));
-    s.part_gate = s.part_pre + up(s.grid_parts * row);
-    s.gate_sums = s.part_gate + up(s.parts * row);
+    s.part_gate = s.part_pre + up((s.grid_parts > units ? s.grid_parts : units) * row);
+    s.gate_sums = s.part_gate + up((s.parts > gate_parts ? s.parts : gate_parts) * row);
     s.bytes = s.gate_sums + (p.gates > 1 ? up(p.gates * row) : 0);
     return s;
 }
@@ -228,12 +337,25 @@ rmsnorm_status_t bwd_run(int32_t dtype, const void* dy, const void* dh, const vo
     p.part_pre = dpre_w ? reinterpret_cast<float*>(base + ws.part_pre) : nullptr;
     p.part_gate = dpost_w || dgate ? reinterpret_cast<float*>(base + ws.part_gate) : nullptr;
     p.gate_sums = dpost_w && p.gates > 1 ? reinterpret_cast<float*>(base + ws.gate_sums) : nullptr;
+    const uintptr_t all = bits(dy) | bits(dh) | bits(x) | bits(h) | bits(dx) | bits(dres) |
+                          bits(p.post_w) | bits(p.pre_w) | bits(p.gate);
+    if (c.path != RMSNORM_PATH_TWOPASS) {
+        LaunchShape s{0, 0, 1, 0};
+        BlockFn fn = nullptr;
+        st = plan_staged(&c, all, p.pre ? 4 : 2, true, blocknorm_bwd_staged_ptr, &s, &fn);
+        if (st != RMSNORM_OK) return st;
+        if (s.grid) {
+            p.pre_parts = static_cast<int32_t>(p.units);
+            st = launch(c, fn, s, stream);
+            return st == RMSNORM_OK ? launch_reduce(c, stream) : st;
+        }
+        if (c.path == RMSNORM_PATH_STAGED) return RMSNORM_ERR_UNSUPPORTED;
+    }
     p.parts_per_gate = ws.parts_per_gate;
     p.parts = ws.parts;
     p.rows_per_part = div_up(p.gate_rows, ws.parts_per_gate);
     p.pre_parts = static_cast<int32_t>(ws.grid_parts);
-    const int vb = widest_vector(bits(dy) | bits(dh) | bits(x) | bits(h) | bits(dx) | bits(dres) |
-                                 bits(p.post_w) | bits(p.pre_w) | bits(p.gate), hidden * c.sz, c.sz);
+    const int vb = widest_vector(all, hidden * c.sz, c.sz);
     p.nvec = static_cast<int32_t>(hidden / (vb / c.sz));
     const LaunchShape rs{at_most(rows, 8ll * c.dv.sms), blocknorm_rows_block(), 1, 0};
     st = launch(c, blocknorm_bwd_rows_ptr(dtype, vb), rs, stream);

@@ -32,9 +32,22 @@ struct BlockParams {
     int64_t rows_per_part; // any-width backward: rows of a part
     int64_t parts_per_gate;
     int64_t parts;         // any-width backward: gates * parts_per_gate
+    int64_t units;         // staged backward: CTAs or clusters, unit u's sums of gate row s
+                           // being part u + s; 0: the parts are the any-width kernel's
     int32_t pre_parts;     // parts of dpre_w
     int32_t hidden;
     int32_t nvec;          // vectors per row
+    // staged kernels
+    int64_t blocks;        // blocks of rows, of all gate rows
+    int64_t blocks_per_gate;
+    int32_t block_rows;    // rows of a block: row groups of a CTA
+    int32_t group;         // threads per row (cluster > 1: per slice)
+    int32_t cluster;       // CTAs per row
+    int32_t slice_vecs;    // vectors of a CTA's slice of a row
+    int32_t nslots;        // ring slots
+    int32_t fault;         // failure-detection test builds only (else always 0)
+    unsigned* status;
+    uint64_t timeout_ns;
     int32_t post;          // the branch is normed
     int32_t pre;           // y is wanted
     float inv_hidden;
@@ -55,6 +68,13 @@ int blocknorm_cols_block();
 // Sums over the parts, `width` (4 or 1) columns to a thread.  gates: one grid row (y) for
 // dpre_w and one for each gate row; else dpost_w from the sums of several gate rows.
 BlockFn blocknorm_reduce_ptr(int dtype, int width, bool gates);
+// Rows staged in shared memory, read once.  post, pre: the norms; cluster: rows split over
+// a thread-block cluster.
+BlockFn blocknorm_fwd_staged_ptr(int dtype, bool post, bool pre, bool cluster);
+BlockFn blocknorm_bwd_staged_ptr(int dtype, bool post, bool pre, bool cluster);
+constexpr int kBlockStagedBytes = 32;       // bytes of a row to a thread
+constexpr int kBlockFwdMaxThreads = 1024;
+constexpr int kBlockBwdMaxThreads = 512;
 constexpr int kBlockReduceThreads = 256;
 constexpr int kBlockReduceCols = 8;
 

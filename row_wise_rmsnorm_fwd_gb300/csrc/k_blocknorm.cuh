@@ -378,8 +378,15 @@ __global__ void __launch_bounds__(kBlockReduceThreads) blocknorm_reduce_kernel(c
     if (!p.part_gate) return;
     const T* post_w = p.post ? static_cast<const T*>(p.post_w) : nullptr;
     for (int64_t s = blockIdx.y - 1; s < p.gates; s += gridDim.y - 1) {
-        const float v = sum_parts<T, W>(p.part_gate + s * p.parts_per_gate * p.hidden,
-                                        p.parts_per_gate, p.hidden, nullptr);
+        int64_t from = s * p.parts_per_gate, count = p.parts_per_gate;
+        if (p.units) {          // the units that the gate row's blocks were dealt to
+            const int64_t b0 = s * p.blocks_per_gate;
+            const int64_t b1 = min(b0 + p.blocks_per_gate, p.blocks) - 1;
+            const int64_t u0 = ((b0 + 1) * p.units - 1) / p.blocks;
+            from = u0 + s;
+            count = ((b1 + 1) * p.units - 1) / p.blocks - u0 + 1;
+        }
+        const float v = sum_parts<T, W>(p.part_gate + from * p.hidden, count, p.hidden, nullptr);
         if (!mine) continue;
         const int64_t at = s * p.hidden + col;
         if (p.dgate) p.dgate[at] = p.branch_scale * v * (post_w ? static_cast<float>(post_w[col]) : 1.f);

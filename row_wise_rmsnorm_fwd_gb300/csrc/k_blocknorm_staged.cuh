@@ -1,0 +1,472 @@
+// k_blocknorm_staged.cuh -- the boundary between two blocks (formulas in
+// include/rmsnorm_block.h): rows staged in shared memory and read from HBM once.
+//
+// A group of p.group threads takes a row (with a cluster: a slice of it), 32 bytes of
+// each array to a thread, which it holds in registers, packed, from the sums to the
+// outputs.  The ring's slot is free again behind the block barrier of the sums.
+#pragma once
+#include "k_blocknorm.cuh"
+#include "k_blockring.cuh"
+#include "k_rowblocks.cuh"
+#include "pairs.cuh"
+
+namespace rmsnorm {
+
+// A cluster's exchange of N sums per row: two sets of slots and two mbarriers, used in
+// turn.  A phase takes one local arrival, which expects the bytes of all ranks.  A peer
+// sends a row's sums only behind its block barrier of that row, by when all its threads have
+// read the row before: it is never two rows ahead of a slot that is still read.
+struct BlockExchange {
+    alignas(16) float slot[2][16][8];
+    alignas(8) uint64_t bar[2];
+};
+
+// Sums of all ranks in rank order; false once the bounded wait has run out.
+template <int N>
+__device__ __forceinline__ bool exchange_sums(BlockExchange* ex, float (&v)[8], int ncta, uint32_t rank,
+                                              uint32_t it, const BlockParams& p) {
+    const uint32_t b = it & 1u;
+    const uint32_t bar = smem_addr(&ex->bar[b]);
+    const int tid = threadIdx.x;
+    if (tid == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(ncta * N * 4));
+    bool send = tid < ncta;
+#if RMSNORM_FAULT_INJECT
+    if (p.fault == kFaultClusterWithholdPartial && rank == 0 && it == 0) send = false;
+#endif
+    if (send) {
+        const uint32_t to = map_to_rank(smem_addr(&ex->slot[b][rank][0]), static_cast<uint32_t>(tid));
+        const uint32_t peer_bar = map_to_rank(bar, static_cast<uint32_t>(tid));
+        if constexpr (N == 1) {
+            st_async_f32(to, v[0], peer_bar);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; k += 2) st_async_v2_f32(to + 4 * k, v[k], v[k + 1], peer_bar);
+        }
+    }
+    const bool ok = mbar_wait_bounded<true>(bar, (it >> 1) & 1u, p.timeout_ns);
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = 0.f;
+    if (ok) {
+        for (int c = 0; c < ncta; ++c) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] += ex->slot[b][c][k];
+        }
+    } else if (tid == 0) {
+        report_timeout(p.status, kSiteClusterExchange);
+    }
+    return ok;
+}
+
+__device__ __forceinline__ void exchange_init(BlockExchange* ex) {
+    if (threadIdx.x == 0) {
+        mbar_init(smem_addr(&ex->bar[0]), 1);
+        mbar_init(smem_addr(&ex->bar[1]), 1);
+        fence_mbarrier_init_cluster();
+    }
+    __syncthreads();
+    cluster_sync_all();
+}
+
+// A thread's place: its row of a block and its vectors.
+struct RowPlace {
+    int g, t, G, width, wpg, gw0;
+    __device__ __forceinline__ explicit RowPlace(int group) : G(group) {
+        width = G < 32 ? G : 32;
+        g = static_cast<int>(threadIdx.x) / G;
+        t = static_cast<int>(threadIdx.x) - g * G;
+        wpg = G >> 5;
+        gw0 = g * wpg;
+    }
+};
+
+constexpr int kBlockVecs = kBlockStagedBytes / 16;
+
+// A vector of a row of weights (or of the gate), ones where there are none.  Volatile: read
+// again from L1 where it is used again, instead of being kept from the sums to the outputs
+// in registers that the backward kernel lacks.
+template <typename T>
+__device__ __forceinline__ Vec<16> weight_vec(const char* from, bool on) {
+    Vec<16> v = ones_vec<T>();
+    if (from && on)
+        asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3]) : "l"(from));
+    return v;
+}
+
+// Keep vectors packed from here on: widened before, they would be held widened.
+template <int N>
+__device__ __forceinline__ void stay_packed(Vec<16> (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) opaque(v[i].u[k]);
+    }
+}
+
+// ------------------------------------------------------------------- forward --
+
+template <typename T, bool POST, bool PRE, bool CL>
+__global__ void __launch_bounds__(kBlockFwdMaxThreads, 1) blocknorm_fwd_staged_kernel(const BlockParams p) {
+    constexpr int NV = kBlockVecs, PN = kPairs<T>, EPV = VecTraits<T, 16>::kElems;
+    using L = Lanes;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ alignas(8) uint64_t bars[kRowBlocksMaxSlots];
+    __shared__ float red[2][2][32 * 8];
+    __shared__ BlockExchange ex[CL ? 2 : 1];
+    pdl_trigger();
+    const RowPlace at(p.group);
+    const uint32_t rank = CL ? cluster_ctarank() : 0;
+    const void* const arrays[2] = {p.x, p.residual};
+    const RowBlocks<2> ring(p, arrays, sizeof(T), rank, static_cast<int>(CL ? cluster_id_x() : blockIdx.x),
+                            static_cast<int>(CL ? cluster_count_x() : gridDim.x), smem, bars);
+    if constexpr (CL) {
+        exchange_init(&ex[0]);
+        exchange_init(&ex[1]);
+    } else {
+        __syncthreads();
+    }
+    pdl_wait();
+    if (threadIdx.x == 0) ring.prologue();
+    bool valid[NV];
+    int col[NV];                       // bytes from the row's start
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = i * at.G + at.t;
+        valid[i] = v * 16 < ring.bytes;
+        col[i] = ring.at + v * 16;
+    }
+    const char* post_w = static_cast<const char*>(p.post_w);
+    const char* pre_w = static_cast<const char*>(p.pre_w);
+    const L rs = L::all(p.residual_scale);
+    int slot = 0;
+    uint32_t use = 0;
+    bool bad = false;
+    int64_t n = 0;
+    for (; n < ring.count; ++n) {
+        int64_t gate_row, row;
+        int rows;
+        ring.where(n, gate_row, row, rows);
+        row += at.g;
+        const bool here = at.g < rows;
+        const char* gate = at_or_null(p.gate, gate_row * ring.row_bytes);
+        const bool ok = ring.wait(slot, use) && !bad;
+        Vec<16> x[NV], r[NV];
+        RowSums<1> s;
+        L acc = L::all(0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const uint32_t in = static_cast<uint32_t>(at.g * ring.slot_row + (i * at.G + at.t) * 16);
+            x[i] = ld_slot_if(ring.base(slot, 0) + in, here && valid[i]);
+            r[i] = ld_slot_if(ring.base(slot, 1) + in, here && valid[i]);
+            if constexpr (POST) {
+#pragma unroll
+                for (int k = 0; k < PN; ++k) acc = fma(lanes<T>(x[i], k), lanes<T>(x[i], k), acc);
+            }
+        }
+        float rx = p.branch_scale;
+        if constexpr (POST) {
+            s.v[0] = acc.total();
+            s.gather(red[0][n & 1], at.width);
+        }
+        if (__syncthreads_or(!ok)) break;                     // uniform
+        if (threadIdx.x == 0 && n + p.nslots < ring.count) ring.issue(slot, n + p.nslots);
+        if constexpr (POST) {
+            s.totals(red[0][n & 1], at.width, at.gw0, at.wpg);
+            if (CL && !exchange_sums<1>(&ex[0], s.v, p.cluster, rank, static_cast<uint32_t>(n), p)) bad = true;
+            rx = rsqrtf(fmaf(s.v[0], p.inv_hidden, p.post_eps));
+        }
+        L h[NV * PN];
+        acc = L::all(0.f);
+        const L rx2 = L::all(rx), bs = L::all(p.branch_scale);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Vec<16> w = weight_vec<T>(POST && post_w ? post_w + col[i] : nullptr, valid[i]);
+            const Vec<16> g = weight_vec<T>(gate ? gate + col[i] : nullptr, valid[i]);
+            float o[EPV];
+#pragma unroll
+            for (int k = 0; k < PN; ++k) {
+                L b = lanes<T>(x[i], k);
+                if constexpr (POST) b = b * rx2 * lanes<T>(w, k);
+                b = lanes<T>(g, k) * b * bs;
+                const L v = fma(rs, lanes<T>(r[i], k), b);
+                h[i * PN + k] = v;
+                acc = fma(v, v, acc);
+                v.put(o + 2 * k);
+            }
+            if (here && valid[i])
+                st_stream<16>(static_cast<char*>(p.h) + row * ring.row_bytes + col[i], pack<T, 16>(o));
+        }
+        if constexpr (PRE) {
+            s.v[0] = acc.total();
+            s.gather(red[1][n & 1], at.width);
+            if (at.wpg > 1) __syncthreads();
+            else __syncwarp();
+            s.totals(red[1][n & 1], at.width, at.gw0, at.wpg);
+            if (CL && !exchange_sums<1>(&ex[1], s.v, p.cluster, rank, static_cast<uint32_t>(n), p)) bad = true;
+            const L rh = L::all(rsqrtf(fmaf(s.v[0], p.inv_hidden, p.pre_eps)));
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const Vec<16> w = weight_vec<T>(pre_w ? pre_w + col[i] : nullptr, valid[i]);
+                float o[EPV];
+#pragma unroll
+                for (int k = 0; k < PN; ++k) (h[i * PN + k] * rh * lanes<T>(w, k)).put(o + 2 * k);
+                if (here && valid[i])
+                    st_stream<16>(static_cast<char*>(p.y) + row * ring.row_bytes + col[i], pack<T, 16>(o));
+            }
+        }
+        if (++slot == p.nslots) {
+            slot = 0;
+            ++use;
+        }
+    }
+    if (n < ring.count && threadIdx.x == 0) {
+        if (!bad) report_timeout(p.status, kSiteStagedFull);
+        ring.drain(n, slot, use);
+    }
+    if constexpr (CL) {
+        __syncthreads();
+        cluster_sync_all();
+    }
+}
+
+// ------------------------------------------------------------------ backward --
+
+// Column sums of a CTA's vectors, written to `to` (one row of a part).  Several row groups:
+// added in order through shared memory.
+template <typename T, int NV>
+__device__ __forceinline__ void write_part(const Lanes (&acc)[NV * kPairs<T>], float* to, const RowPlace& at,
+                                           int groups, const int (&col)[NV], const bool (&valid)[NV],
+                                           float* scratch, int slice_elems, int first_elem) {
+    constexpr int EPV = VecTraits<T, 16>::kElems, PN = kPairs<T>;
+    auto put = [&](float* row, int i) {
+        float f[EPV];
+#pragma unroll
+        for (int k = 0; k < PN; ++k) acc[i * PN + k].put(f + 2 * k);
+#pragma unroll
+        for (int k = 0; k < EPV; k += 4)
+            *reinterpret_cast<float4*>(row + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+    };
+    if (groups == 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (valid[i]) put(to + col[i] / static_cast<int>(sizeof(T)), i);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (valid[i]) put(scratch + at.g * slice_elems + (i * at.G + at.t) * EPV, i);
+    __syncthreads();
+    for (int c = threadIdx.x * 4; c < slice_elems; c += blockDim.x * 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int g = 0; g < groups; ++g) {
+            const float4 f = *reinterpret_cast<const float4*>(scratch + g * slice_elems + c);
+            v.x += f.x;
+            v.y += f.y;
+            v.z += f.z;
+            v.w += f.w;
+        }
+        *reinterpret_cast<float4*>(to + first_elem + c) = v;
+    }
+    __syncthreads();
+}
+
+template <typename T, bool POST, bool PRE, bool CL>
+__global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_kernel(const BlockParams p) {
+    constexpr int NV = kBlockVecs, PN = kPairs<T>, EPV = VecTraits<T, 16>::kElems;
+    constexpr int NARR = PRE ? 4 : 2;
+    constexpr int NS = PRE && POST ? 6 : (PRE || POST ? 2 : 0);
+    using L = Lanes;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ alignas(8) uint64_t bars[kRowBlocksMaxSlots];
+    __shared__ float red[2][32 * 8];
+    __shared__ BlockExchange ex[1];
+    pdl_trigger();
+    const RowPlace at(p.group);
+    const uint32_t rank = CL ? cluster_ctarank() : 0;
+    const int unit = static_cast<int>(CL ? cluster_id_x() : blockIdx.x);
+    const int units = static_cast<int>(CL ? cluster_count_x() : gridDim.x);
+    auto make_ring = [&]() {
+        if constexpr (PRE) {
+            const void* const arrays[4] = {p.x, p.dh, p.dy, p.h_in};
+            return RowBlocks<4>(p, arrays, sizeof(T), rank, unit, units, smem, bars);
+        } else {
+            const void* const arrays[2] = {p.x, p.dh};
+            return RowBlocks<2>(p, arrays, sizeof(T), rank, unit, units, smem, bars);
+        }
+    };
+    const RowBlocks<NARR> ring = make_ring();
+    if constexpr (CL) exchange_init(ex);
+    else __syncthreads();
+    pdl_wait();
+    if (threadIdx.x == 0) ring.prologue();
+    bool valid[NV];
+    int col[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = i * at.G + at.t;
+        valid[i] = v * 16 < ring.bytes;
+        col[i] = ring.at + v * 16;
+    }
+    float* scratch = reinterpret_cast<float*>(smem + (ring.base(p.nslots, 0) - ring.base(0, 0)));
+    const int slice_elems = ring.bytes / static_cast<int>(sizeof(T));
+    const int first_elem = ring.at / static_cast<int>(sizeof(T));
+    const char* post_w = static_cast<const char*>(p.post_w);
+    const char* pre_w = static_cast<const char*>(p.pre_w);
+    const bool have_dh = p.dh != nullptr;
+    L acc[NV * PN], pre[PRE ? NV * PN : 1];     // sums of D * xh and of dy * h * rh
+#pragma unroll
+    for (int k = 0; k < NV * PN; ++k) acc[k] = L::all(0.f);
+#pragma unroll
+    for (int k = 0; k < (PRE ? NV * PN : 1); ++k) pre[k] = L::all(0.f);
+    // The CTA's sums of gate row s are part unit + s: both only grow along the units'
+    // ranges of blocks, and one of them does from each part to the next.
+    auto write_gate = [&](int64_t s) {
+        if (p.part_gate)
+            write_part<T, NV>(acc, p.part_gate + (unit + s) * p.hidden, at, p.block_rows, col, valid, scratch,
+                              slice_elems, first_elem);
+    };
+    int slot = 0;
+    uint32_t use = 0;
+    bool bad = false;
+    int64_t n = 0, last_gate = -1;
+    for (; n < ring.count; ++n) {
+        int64_t gate_row, row;
+        int rows;
+        ring.where(n, gate_row, row, rows);
+        if (gate_row != last_gate) {
+            if (last_gate >= 0) {
+                write_gate(last_gate);
+#pragma unroll
+                for (int k = 0; k < NV * PN; ++k) acc[k] = L::all(0.f);
+            }
+            last_gate = gate_row;
+        }
+        row += at.g;
+        const bool here = at.g < rows;
+        const char* gate = at_or_null(p.gate, gate_row * ring.row_bytes);
+        const bool ok = ring.wait(slot, use) && !bad;
+        Vec<16> x[NV], d[NV], y[PRE ? NV : 1], h[PRE ? NV : 1];
+        RowSums<NS> s;
+        L a[6];
+#pragma unroll
+        for (int k = 0; k < 6; ++k) a[k] = L::all(0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool on = here && valid[i];
+            const uint32_t in = static_cast<uint32_t>(at.g * ring.slot_row + (i * at.G + at.t) * 16);
+            x[i] = ld_slot_if(ring.base(slot, 0) + in, on);
+            d[i] = ld_slot_if(ring.base(slot, 1) + in, on && have_dh);
+            Vec<16> pw, w, g;
+            if constexpr (PRE) {
+                y[i] = ld_slot_if(ring.base(slot, 2) + in, on);
+                h[i] = ld_slot_if(ring.base(slot, 3) + in, on);
+                pw = weight_vec<T>(pre_w ? pre_w + col[i] : nullptr, valid[i]);
+            }
+            if constexpr (POST) {
+                w = weight_vec<T>(post_w ? post_w + col[i] : nullptr, valid[i]);
+                g = weight_vec<T>(gate ? gate + col[i] : nullptr, valid[i]);
+            }
+#pragma unroll
+            for (int k = 0; k < PN; ++k) {
+                L q, gy;
+                if constexpr (POST) {
+                    const L xk = lanes<T>(x[i], k);
+                    q = lanes<T>(w, k) * lanes<T>(g, k) * xk;
+                    a[2] = fma(xk, xk, a[2]);
+                    a[3] = fma(q, lanes<T>(d[i], k), a[3]);
+                }
+                if constexpr (PRE) {
+                    const L hk = lanes<T>(h[i], k);
+                    gy = lanes<T>(y[i], k) * lanes<T>(pw, k);
+                    a[0] = fma(hk, hk, a[0]);
+                    a[1] = fma(gy, hk, a[1]);
+                    if constexpr (POST) {
+                        a[4] = fma(q, gy, a[4]);
+                        a[5] = fma(q, hk, a[5]);
+                    }
+                }
+            }
+        }
+        // the sums that there are, in the order of block_factors
+        constexpr int FIRST = PRE ? 0 : 2;
+#pragma unroll
+        for (int k = 0; k < NS; ++k) s.v[k] = a[FIRST + k].total();
+        if constexpr (NS > 0) s.gather(red[n & 1], at.width);
+        if (__syncthreads_or(!ok)) break;                     // uniform
+        if (threadIdx.x == 0 && n + p.nslots < ring.count) ring.issue(slot, n + p.nslots);
+        if constexpr (NS > 0) {
+            s.totals(red[n & 1], at.width, at.gw0, at.wpg);
+            if (CL && !exchange_sums<NS>(ex, s.v, p.cluster, rank, static_cast<uint32_t>(n), p)) bad = true;
+        }
+        stay_packed(x);
+        stay_packed(d);
+        if constexpr (PRE) {
+            stay_packed(y);
+            stay_packed(h);
+        }
+        float six[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < NS; ++k) six[FIRST + k] = s.v[k];
+        BlockFactors f = block_factors(six, p);
+        if (!here) f = BlockFactors{0.f, 0.f, 0.f, 0.f};      // rows of zeros: 0 * an infinite factor
+        const L rh = L::all(f.rh), kh = L::all(-f.kh), rx = L::all(f.rx), kx = L::all(-f.kx);
+        const L bs = L::all(p.branch_scale), rs = L::all(p.residual_scale);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            Vec<16> pw;
+            if constexpr (PRE) pw = weight_vec<T>(pre_w ? pre_w + col[i] : nullptr, valid[i]);
+            const Vec<16> w = weight_vec<T>(POST && post_w ? post_w + col[i] : nullptr, valid[i]);
+            const Vec<16> g = weight_vec<T>(gate ? gate + col[i] : nullptr, valid[i]);
+            float ox[EPV], od[EPV];
+#pragma unroll
+            for (int k = 0; k < PN; ++k) {
+                const L xk = lanes<T>(x[i], k);
+                L D = lanes<T>(d[i], k);
+                if constexpr (PRE) {
+                    const L hk = lanes<T>(h[i], k), yk = lanes<T>(y[i], k);
+                    D = fma(rh, fma(hk, kh, yk * lanes<T>(pw, k)), D);
+                    pre[i * PN + k] = fma(yk, hk * rh, pre[i * PN + k]);
+                }
+                (D * rs).put(od + 2 * k);
+                L u = lanes<T>(g, k);
+                if constexpr (POST) {
+                    u = u * lanes<T>(w, k);
+                    acc[i * PN + k] = fma(D, xk * rx, acc[i * PN + k]);
+                    (fma(xk, kx, D * bs * u) * rx).put(ox + 2 * k);
+                } else {
+                    acc[i * PN + k] = fma(D, xk, acc[i * PN + k]);
+                    (D * bs * u).put(ox + 2 * k);
+                }
+            }
+            if (here && valid[i]) {
+                const int64_t to = row * ring.row_bytes + col[i];
+                st_stream<16>(static_cast<char*>(p.dx) + to, pack<T, 16>(ox));
+                st_stream<16>(static_cast<char*>(p.dres) + to, pack<T, 16>(od));
+            }
+        }
+        if (++slot == p.nslots) {
+            slot = 0;
+            ++use;
+        }
+    }
+    if (n < ring.count || bad) {
+        if (threadIdx.x == 0) {
+            if (!bad) report_timeout(p.status, kSiteStagedFull);
+            ring.drain(n, slot, use);
+        }
+        __syncthreads();
+    } else if (ring.count > 0) {
+        write_gate(last_gate);
+        if constexpr (PRE) {
+            if (p.part_pre)
+                write_part<T, NV>(pre, p.part_pre + static_cast<int64_t>(unit) * p.hidden, at, p.block_rows, col,
+                                  valid, scratch, slice_elems, first_elem);
+        }
+    }
+    if constexpr (CL) {
+        __syncthreads();
+        cluster_sync_all();
+    }
+}
+
+}  // namespace rmsnorm

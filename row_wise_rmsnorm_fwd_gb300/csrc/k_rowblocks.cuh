@@ -1,0 +1,176 @@
+// k_rowblocks.cuh -- blocks of consecutive rows of several arrays brought into shared
+// memory by 1-D bulk copies, a ring of them in flight, for kernels that take a block
+// into registers at once: its slot is refilled behind the block barrier that every
+// kernel has for the rows' sums, so a ring of two keeps a whole block under way at all
+// times.
+//
+// Rows are whole 16-byte vectors, arrays on 16-byte boundaries.  Blocks lie within the
+// rows of a gate row and are dealt out in contiguous ranges, so that a CTA meets few
+// gate rows, in order.  With a cluster each CTA takes its slice of every row (one row to a
+// block).
+#pragma once
+#include "blocknorm_launch.h"
+#include "common.cuh"
+
+namespace rmsnorm {
+
+constexpr int kRowBlocksMaxSlots = 4;
+
+template <int NARR>
+struct RowBlocks {
+    const BlockParams& p;
+    const char* src[NARR];       // null: absent
+    int narr;                    // arrays present
+    uint32_t slots, bars;        // shared-memory addresses
+    int64_t first, count;        // the unit's blocks
+    int unit;                    // number of the CTA, or of the cluster
+    int row_bytes, at, bytes;    // a row, and the CTA's slice of it
+    int slot_row;                // bytes of a row in a slot
+
+    __device__ __forceinline__ RowBlocks(const BlockParams& p_, const void* const (&arrays)[NARR],
+                                         int sz, uint32_t rank, int unit_, int units,
+                                         unsigned char* smem, uint64_t* barriers)
+        : p(p_), narr(0), slots(smem_addr(smem)), bars(smem_addr(barriers)), unit(unit_) {
+#pragma unroll
+        for (int a = 0; a < NARR; ++a) {
+            src[a] = static_cast<const char*>(arrays[a]);
+            narr += src[a] != nullptr;
+        }
+        first = p.blocks * unit / units;
+        count = p.blocks * (unit + 1) / units - first;
+        row_bytes = p.hidden * sz;
+        slot_row = p.slice_vecs * 16;
+        at = static_cast<int>(rank) * slot_row;
+        bytes = row_bytes - at;
+        if (bytes > slot_row) bytes = slot_row;
+        if (threadIdx.x == 0) {
+            for (int k = 0; k < p.nslots; ++k) mbar_init(bars + 8 * k, 1);
+            fence_mbarrier_init_cluster();
+        }
+    }
+
+    // Gate row, first row and number of rows of the unit's n-th block.
+    __device__ __forceinline__ void where(int64_t n, int64_t& gate, int64_t& row, int& rows) const {
+        const int64_t b = first + n;
+        gate = p.gates == 1 ? 0 : b / p.blocks_per_gate;
+        row = gate * p.gate_rows + (b - gate * p.blocks_per_gate) * p.block_rows;
+        int64_t end = (gate + 1) * p.gate_rows;
+        if (end > p.rows) end = p.rows;
+        rows = static_cast<int>(end - row < p.block_rows ? end - row : p.block_rows);
+    }
+
+    // Shared-memory address of array a (counted with the absent ones) in a slot.
+    __device__ __forceinline__ uint32_t base(int slot, int a) const {
+        return slots + static_cast<uint32_t>((slot * NARR + a) * p.block_rows * slot_row);
+    }
+
+    // One thread: start the copies of block n into `slot`.
+    __device__ __forceinline__ void issue(int slot, int64_t n) const {
+        const uint32_t bar = bars + 8 * slot;
+#if RMSNORM_FAULT_INJECT
+        if (p.fault == kFaultStagedWithholdCopy && n == 0) {   // armed for bytes that never come
+            mbar_arrive_expect_tx(bar, 16);
+            return;
+        }
+#endif
+        int64_t gate, row;
+        int rows;
+        where(n, gate, row, rows);
+        // one row of a slice, or whole rows, which follow one another
+        const uint32_t n_bytes = static_cast<uint32_t>(p.cluster > 1 ? bytes : rows * row_bytes);
+        mbar_arrive_expect_tx(bar, n_bytes * narr);
+        const int64_t from = row * row_bytes + at;
+#pragma unroll
+        for (int a = 0; a < NARR; ++a)
+            if (src[a]) bulk_g2s_plain(base(slot, a), src[a] + from, n_bytes, bar);
+    }
+
+    __device__ __forceinline__ void prologue() const {
+        for (int k = 0; k < p.nslots && k < count; ++k) issue(k, k);
+    }
+
+    // Wait (bounded) for block n.
+    __device__ __forceinline__ bool wait(int slot, uint32_t use) const {
+        return mbar_wait_bounded<false>(bars + 8 * slot, use & 1u, p.timeout_ns);
+    }
+
+    // One thread, after the wait for block n has run out and every thread has left the
+    // loop: wait (bounded) for what is under way.
+    __device__ __forceinline__ void drain(int64_t n, int slot, uint32_t use) const {
+        for (int k = 0; k < p.nslots && n + k < count; ++k) {
+            wait(slot, use);
+            if (++slot == p.nslots) {
+                slot = 0;
+                ++use;
+            }
+        }
+    }
+};
+
+// ------------------------------------------------------------ sums of a row --
+
+// Eight values summed over a warp in nine exchanges: lanes hand over the half of the values
+// that they do not keep.  Lane L ends with the sum of value L / 4.
+__device__ __forceinline__ float warp_sum8(const float (&v)[8]) {
+    const int lane = threadIdx.x & 31;
+    float a[4], b[2], c;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float keep = lane & 16 ? v[k + 4] : v[k], give = lane & 16 ? v[k] : v[k + 4];
+        a[k] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float keep = lane & 8 ? a[k + 2] : a[k], give = lane & 8 ? a[k] : a[k + 2];
+        b[k] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
+    }
+    {
+        const float keep = lane & 4 ? b[1] : b[0], give = lane & 4 ? b[0] : b[1];
+        c = keep + __shfl_xor_sync(0xffffffffu, give, 4);
+    }
+    c += __shfl_xor_sync(0xffffffffu, c, 2);
+    return c + __shfl_xor_sync(0xffffffffu, c, 1);
+}
+
+// N sums of each row group, in three steps around the block barrier of an iteration.
+// red: [2][32][8] floats, the halves used in turn.
+//   gather: before the barrier; group_totals: behind it.  Groups of less than a warp need no
+//   shared memory: `width` lanes hold their totals already.
+template <int N>
+struct RowSums {
+    float v[8];
+    __device__ __forceinline__ RowSums() {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = 0.f;
+    }
+    __device__ __forceinline__ void gather(float* red, int width) {
+        const int lane = threadIdx.x & 31;
+        if (width < 32) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = group_allreduce_sum(v[k], width);
+        } else if constexpr (N > 2) {
+            const float s = warp_sum8(v);
+            if ((lane & 3) == 0) red[(threadIdx.x >> 5) * 8 + (lane >> 2)] = s;
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const float s = warp_allreduce_sum(v[k]);
+                if (lane == 0) red[(threadIdx.x >> 5) * 8 + k] = s;
+            }
+        }
+    }
+    // warps first .. first + n - 1 are the group's
+    __device__ __forceinline__ void totals(const float* red, int width, int first, int n) {
+        if (width < 32) return;
+        const int lane = threadIdx.x & 31, k = lane & 7;
+        float s = 0.f;
+        if (k < N)
+            for (int w = lane >> 3; w < n; w += 4) s += red[(first + w) * 8 + k];
+        s += __shfl_xor_sync(0xffffffffu, s, 8);
+        s += __shfl_xor_sync(0xffffffffu, s, 16);
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = __shfl_sync(0xffffffffu, s, j);
+    }
+};
+
+}  // namespace rmsnorm

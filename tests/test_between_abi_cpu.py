@@ -50,8 +50,8 @@ NAN, INF = float("nan"), float("inf")
 BAD_RULES = [dict(gate_rows=0), dict(gate_rows=-3), dict(residual_scale=NAN), dict(branch_scale=INF),
              dict(post_eps=-1e-9), dict(pre_eps=NAN), dict(post_eps=INF), dict(post_norm=2),
              dict(pre_norm=-1), dict(post_w=POST + 2), dict(pre_w=PRE + 1), dict(gate=GATE + 3)]
-BAD_OPTIONS = [dict(path="staged"), dict(path="cluster"), dict(threads=64), dict(epilogue="relu"),
-               dict(fault_inject=1), dict(grid=3)]
+BAD_OPTIONS = [dict(path="rowreg"), dict(path="cluster"), dict(threads=64), dict(epilogue="relu"),
+               dict(fault_inject=3), dict(grid=3), dict(cluster=2), dict(cluster=3, path="staged")]
 
 
 def test_block_forward_refuses(lib):
@@ -69,6 +69,8 @@ def test_block_forward_refuses(lib):
         assert f(**kw) == INVALID, kw
     for o in BAD_OPTIONS:
         assert f(opt=options(**o)) == INVALID, o
+    for o in (dict(fault_inject=1), dict(fault_inject=2, path="staged", cluster=2)):
+        assert f(opt=options(**o)) == UNSUPPORTED, o          # the test build's
     for h, y in ((H, Y), (X, RES), (RES, X), (X, Y)):
         assert f(rows=0, h=h, y=y) == OK
     assert f(rows=0, pre_norm=0, y=0) == OK

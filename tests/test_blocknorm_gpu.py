@@ -133,6 +133,32 @@ def test_gates_of_many_lengths(lead, t, path):
 
 
 @pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("cluster", [2, 4, 8, 16])
+@pytest.mark.parametrize("n", [136, 1024, 4104, 16384, 65536, 131072])
+def test_rows_over_a_cluster(n, cluster, t):
+    """Forced splits, uneven ones among them, agree with the references, several blocks of
+    rows to a cluster; what cannot be split so is refused."""
+    options = {"path": "staged", "cluster": cluster}
+    v = inputs((3, 5), n, t, RULES["scaled"], "sequence")
+    g = on(v)
+    per = -(-n * v["x"].element_size() // 16 // cluster)
+    threads = -(-per // 2)
+    vectors = n * v["x"].element_size() // 16
+    for run, check_it, most in ((forward, check_forward, 1024), (backward, check_backward, 512)):
+        if threads > most or (cluster - 1) * per >= vectors:
+            with pytest.raises(binding.RmsnormError) as e:
+                run(g, RULES["scaled"], options=options)
+            assert e.value.status == binding.RMSNORM_ERR_UNSUPPORTED
+            continue
+        check_it(v, RULES["scaled"], run(g, RULES["scaled"], options=options))
+    if n == 1024:
+        for rule in RULES.values():
+            v = inputs((301, 3), n, t, rule, "sequence")
+            check_forward(v, rule, forward(on(v), rule, options=options))
+            check_backward(v, rule, backward(on(v), rule, options=options))
+
+
+@pytest.mark.parametrize("t", TYPES)
 def test_gate_shapes(t):
     """[hidden], [1, hidden], [batch, hidden], [batch, 1, hidden], [batch, seq, hidden]."""
     rule = RULES["scaled"]
