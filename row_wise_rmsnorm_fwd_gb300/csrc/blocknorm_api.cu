@@ -108,13 +108,16 @@ int64_t group_of(int64_t nvec) {
     return g <= 32 ? pow2_ceil(g) : div_up(g, 32) * 32;
 }
 
-using PickFn = BlockFn (*)(int dtype, bool post, bool pre, bool cluster);
+BlockFn staged_ptr(const BlockVariant& v) {
+    if (v.dtype == RMSNORM_DTYPE_F32) return v.back ? blocknorm_bwd_staged_f32(v) : blocknorm_fwd_staged_f32(v);
+    return v.back ? blocknorm_bwd_staged_bf16(v) : blocknorm_fwd_staged_bf16(v);
+}
 
 // Rows staged in shared memory.  bits: of the addresses of the arrays, weights and gate;
 // narr: arrays with a place in a slot.  Leaves s->grid 0, status OK, where rows cannot be
 // staged.
-rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t address_bits, int narr, bool back, PickFn pick,
-                             LaunchShape* s, BlockFn* fn) {
+rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t address_bits, int narr, bool back, LaunchShape* s,
+                             BlockFn* fn) {
     BlockParams& p = c->p;
     const int64_t row_bytes = static_cast<int64_t>(p.hidden) * c->sz;
     s->grid = 0;
@@ -138,7 +141,9 @@ rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t address_bits, int narr, boo
             const int block = static_cast<int>(rows * group);
             const int64_t slot = narr * rows * slice * 16;
             const int64_t scratch = back && rows > 1 ? rows * row_bytes * 4 / c->sz : 0;
-            *fn = pick(c->dtype, p.post != 0, p.pre != 0, cluster > 1);
+            const bool whole = nvec == cluster * group * (kBlockStagedBytes / 16) && (!p.post || p.post_w) &&
+                               (!p.pre || p.pre_w) && (p.post || p.pre);
+            *fn = staged_ptr({c->dtype, back, p.post != 0, p.pre != 0, cluster > 1, whole, p.gate != nullptr});
             int best = 0;
             for (int64_t slots = 3; slots >= 2; --slots) {
                 const int64_t smem = slots * slot + scratch;
@@ -208,7 +213,7 @@ rmsnorm_status_t fwd_run(int32_t dtype, const void* x, const void* residual, voi
     if (c.path != RMSNORM_PATH_TWOPASS) {
         LaunchShape s{0, 0, 1, 0};
         BlockFn fn = nullptr;
-        st = plan_staged(&c, all, 2, false, blocknorm_fwd_staged_ptr, &s, &fn);
+        st = plan_staged(&c, all, 2, false, &s, &fn);
         if (st != RMSNORM_OK) return st;
         if (s.grid) return launch(c, fn, s, stream);
         if (c.path == RMSNORM_PATH_STAGED) return RMSNORM_ERR_UNSUPPORTED;
@@ -342,7 +347,7 @@ rmsnorm_status_t bwd_run(int32_t dtype, const void* dy, const void* dh, const vo
     if (c.path != RMSNORM_PATH_TWOPASS) {
         LaunchShape s{0, 0, 1, 0};
         BlockFn fn = nullptr;
-        st = plan_staged(&c, all, p.pre ? 4 : 2, true, blocknorm_bwd_staged_ptr, &s, &fn);
+        st = plan_staged(&c, all, p.pre ? 4 : 2, true, &s, &fn);
         if (st != RMSNORM_OK) return st;
         if (s.grid) {
             p.pre_parts = static_cast<int32_t>(p.units);

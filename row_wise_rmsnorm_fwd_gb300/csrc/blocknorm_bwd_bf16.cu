@@ -1,0 +1,8 @@
+// blocknorm_bwd_bf16.cu -- instances of the block boundary's staged kernel, backward, bf16.
+#include "blocknorm_pick.cuh"
+
+namespace rmsnorm {
+
+BlockFn blocknorm_bwd_staged_bf16(const BlockVariant& v) { return blocknorm_pick_all<__nv_bfloat16, true>(v); }
+
+}  // namespace rmsnorm

@@ -69,9 +69,16 @@ int blocknorm_cols_block();
 // dpre_w and one for each gate row; else dpost_w from the sums of several gate rows.
 BlockFn blocknorm_reduce_ptr(int dtype, int width, bool gates);
 // Rows staged in shared memory, read once.  post, pre: the norms; cluster: rows split over
-// a thread-block cluster.
-BlockFn blocknorm_fwd_staged_ptr(int dtype, bool post, bool pre, bool cluster);
-BlockFn blocknorm_bwd_staged_ptr(int dtype, bool post, bool pre, bool cluster);
+// a thread-block cluster; whole: every thread has all its vectors, there are weights for
+// the norms (one at least), and a gate as `gate` says.
+struct BlockVariant {
+    int dtype;
+    bool back, post, pre, cluster, whole, gate;
+};
+BlockFn blocknorm_fwd_staged_f32(const BlockVariant& v);
+BlockFn blocknorm_fwd_staged_bf16(const BlockVariant& v);
+BlockFn blocknorm_bwd_staged_f32(const BlockVariant& v);
+BlockFn blocknorm_bwd_staged_bf16(const BlockVariant& v);
 constexpr int kBlockStagedBytes = 32;       // bytes of a row to a thread
 constexpr int kBlockFwdMaxThreads = 1024;
 constexpr int kBlockBwdMaxThreads = 512;

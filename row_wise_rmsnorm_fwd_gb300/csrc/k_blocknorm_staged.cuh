@@ -81,16 +81,59 @@ struct RowPlace {
 
 constexpr int kBlockVecs = kBlockStagedBytes / 16;
 
-// A vector of a row of weights (or of the gate), ones where there are none.  Volatile: read
-// again from L1 where it is used again, instead of being kept from the sums to the outputs
-// in registers that the backward kernel lacks.
-template <typename T>
+// What a kernel may take for granted of its rows and weights.
+//   kBlockSome: nothing: a thread may lack vectors, and weights may be absent (ones)
+//   kBlockPlain: every thread has all its vectors, the norms' weights are there, no gate
+//   kBlockGated: the same with a gate
+enum : int { kBlockSome, kBlockPlain, kBlockGated };
+
+// A vector of a slot; zeros where it is missing.
+template <int MODE>
+__device__ __forceinline__ Vec<16> slot_vec(uint32_t at, bool on) {
+    return MODE == kBlockSome ? ld_slot_if(at, on) : ld_slot(at);
+}
+
+// A vector of weights.  Volatile: read where it stands, from L1, and not kept.
+template <typename T, int MODE>
 __device__ __forceinline__ Vec<16> weight_vec(const char* from, bool on) {
-    Vec<16> v = ones_vec<T>();
-    if (from && on)
-        asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3]) : "l"(from));
+    Vec<16> v;
+    if (MODE == kBlockSome) {
+        v = ones_vec<T>();
+        if (!from || !on) return v;
+    }
+    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3]) : "l"(from));
     return v;
+}
+
+// Pair k of two vectors' product: for bf16 the mixed-precision product, which widens its
+// operands by itself (added to -0, which changes no product).
+template <typename T>
+__device__ __forceinline__ Lanes product(const Vec<16>& a, const Vec<16>& b, int k) {
+    if constexpr (sizeof(T) == 2) {
+        float c, d;
+        asm("{\n\t.reg .b16 l, h, m, n;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 {m, n}, %3;\n\t"
+            "fma.rn.f32.bf16 %0, l, m, %4;\n\tfma.rn.f32.bf16 %1, h, n, %4;\n\t}"
+            : "=f"(c), "=f"(d) : "r"(a.u[k]), "r"(b.u[k]), "f"(-0.0f));
+        return {pack_x2(c, d)};
+    } else {
+        return lanes<T>(a, k) * lanes<T>(b, k);
+    }
+}
+
+// The same of a vector with itself, added to a pair.
+template <typename T>
+__device__ __forceinline__ Lanes add_square(const Vec<16>& a, int k, Lanes to) {
+    if constexpr (sizeof(T) == 2) {
+        float c, d, e, f;
+        unpack_x2(to.v, e, f);
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "fma.rn.f32.bf16 %0, l, l, %3;\n\tfma.rn.f32.bf16 %1, h, h, %4;\n\t}"
+            : "=f"(c), "=f"(d) : "r"(a.u[k]), "f"(e), "f"(f));
+        return {pack_x2(c, d)};
+    } else {
+        return fma(lanes<T>(a, k), lanes<T>(a, k), to);
+    }
 }
 
 // Keep vectors packed from here on: widened before, they would be held widened.
@@ -105,9 +148,10 @@ __device__ __forceinline__ void stay_packed(Vec<16> (&v)[N]) {
 
 // ------------------------------------------------------------------- forward --
 
-template <typename T, bool POST, bool PRE, bool CL>
+template <typename T, bool POST, bool PRE, bool CL, int MODE>
 __global__ void __launch_bounds__(kBlockFwdMaxThreads, 1) blocknorm_fwd_staged_kernel(const BlockParams p) {
     constexpr int NV = kBlockVecs, PN = kPairs<T>, EPV = VecTraits<T, 16>::kElems;
+    constexpr bool GATE = MODE != kBlockPlain;
     using L = Lanes;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ alignas(8) uint64_t bars[kRowBlocksMaxSlots];
@@ -132,9 +176,10 @@ __global__ void __launch_bounds__(kBlockFwdMaxThreads, 1) blocknorm_fwd_staged_k
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = i * at.G + at.t;
-        valid[i] = v * 16 < ring.bytes;
+        valid[i] = MODE != kBlockSome || v * 16 < ring.bytes;
         col[i] = ring.at + v * 16;
     }
+    const uint32_t in_slot = static_cast<uint32_t>(at.g * ring.slot_row + at.t * 16);
     const char* post_w = static_cast<const char*>(p.post_w);
     const char* pre_w = static_cast<const char*>(p.pre_w);
     const L rs = L::all(p.residual_scale);
@@ -147,23 +192,28 @@ __global__ void __launch_bounds__(kBlockFwdMaxThreads, 1) blocknorm_fwd_staged_k
         int rows;
         ring.where(n, gate_row, row, rows);
         row += at.g;
+        // rows that the block lacks: sums of what the slot held before, not used
         const bool here = at.g < rows;
-        const char* gate = at_or_null(p.gate, gate_row * ring.row_bytes);
+        Vec<16> x[NV], r[NV], w[NV], g[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if constexpr (POST) w[i] = weight_vec<T, MODE>(post_w ? post_w + col[i] : nullptr, valid[i]);
+            if constexpr (GATE)
+                g[i] = weight_vec<T, MODE>(at_or_null(p.gate, gate_row * ring.row_bytes + col[i]), valid[i]);
+        }
         const bool ok = ring.wait(slot, use) && !bad;
-        Vec<16> x[NV], r[NV];
         RowSums<1> s;
         L acc = L::all(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const uint32_t in = static_cast<uint32_t>(at.g * ring.slot_row + (i * at.G + at.t) * 16);
-            x[i] = ld_slot_if(ring.base(slot, 0) + in, here && valid[i]);
-            r[i] = ld_slot_if(ring.base(slot, 1) + in, here && valid[i]);
+            x[i] = slot_vec<MODE>(ring.base(slot, 0) + in_slot + i * at.G * 16, valid[i]);
+            r[i] = slot_vec<MODE>(ring.base(slot, 1) + in_slot + i * at.G * 16, valid[i]);
             if constexpr (POST) {
 #pragma unroll
-                for (int k = 0; k < PN; ++k) acc = fma(lanes<T>(x[i], k), lanes<T>(x[i], k), acc);
+                for (int k = 0; k < PN; ++k) acc = add_square<T>(x[i], k, acc);
             }
         }
-        float rx = p.branch_scale;
+        float scale = p.branch_scale;
         if constexpr (POST) {
             s.v[0] = acc.total();
             s.gather(red[0][n & 1], at.width);
@@ -173,30 +223,31 @@ __global__ void __launch_bounds__(kBlockFwdMaxThreads, 1) blocknorm_fwd_staged_k
         if constexpr (POST) {
             s.totals(red[0][n & 1], at.width, at.gw0, at.wpg);
             if (CL && !exchange_sums<1>(&ex[0], s.v, p.cluster, rank, static_cast<uint32_t>(n), p)) bad = true;
-            rx = rsqrtf(fmaf(s.v[0], p.inv_hidden, p.post_eps));
+            scale *= rsqrtf(fmaf(s.v[0], p.inv_hidden, p.post_eps));
         }
         L h[NV * PN];
         acc = L::all(0.f);
-        const L rx2 = L::all(rx), bs = L::all(p.branch_scale);
+        const L sc = L::all(scale);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const Vec<16> w = weight_vec<T>(POST && post_w ? post_w + col[i] : nullptr, valid[i]);
-            const Vec<16> g = weight_vec<T>(gate ? gate + col[i] : nullptr, valid[i]);
             float o[EPV];
 #pragma unroll
             for (int k = 0; k < PN; ++k) {
-                L b = lanes<T>(x[i], k);
-                if constexpr (POST) b = b * rx2 * lanes<T>(w, k);
-                b = lanes<T>(g, k) * b * bs;
+                L b = lanes<T>(x[i], k) * sc;
+                if constexpr (POST && GATE) b = b * product<T>(w[i], g[i], k);
+                else if constexpr (POST) b = b * lanes<T>(w[i], k);
+                else if constexpr (GATE) b = b * lanes<T>(g[i], k);
                 const L v = fma(rs, lanes<T>(r[i], k), b);
                 h[i * PN + k] = v;
-                acc = fma(v, v, acc);
+                if constexpr (PRE) acc = fma(v, v, acc);
                 v.put(o + 2 * k);
             }
             if (here && valid[i])
                 st_stream<16>(static_cast<char*>(p.h) + row * ring.row_bytes + col[i], pack<T, 16>(o));
         }
         if constexpr (PRE) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) w[i] = weight_vec<T, MODE>(pre_w ? pre_w + col[i] : nullptr, valid[i]);
             s.v[0] = acc.total();
             s.gather(red[1][n & 1], at.width);
             if (at.wpg > 1) __syncthreads();
@@ -206,10 +257,9 @@ __global__ void __launch_bounds__(kBlockFwdMaxThreads, 1) blocknorm_fwd_staged_k
             const L rh = L::all(rsqrtf(fmaf(s.v[0], p.inv_hidden, p.pre_eps)));
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const Vec<16> w = weight_vec<T>(pre_w ? pre_w + col[i] : nullptr, valid[i]);
                 float o[EPV];
 #pragma unroll
-                for (int k = 0; k < PN; ++k) (h[i * PN + k] * rh * lanes<T>(w, k)).put(o + 2 * k);
+                for (int k = 0; k < PN; ++k) (h[i * PN + k] * rh * lanes<T>(w[i], k)).put(o + 2 * k);
                 if (here && valid[i])
                     st_stream<16>(static_cast<char*>(p.y) + row * ring.row_bytes + col[i], pack<T, 16>(o));
             }
@@ -270,10 +320,14 @@ __device__ __forceinline__ void write_part(const Lanes (&acc)[NV * kPairs<T>], f
     __syncthreads();
 }
 
-template <typename T, bool POST, bool PRE, bool CL>
+template <typename T, bool POST, bool PRE, bool CL, int MODE>
 __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_kernel(const BlockParams p) {
     constexpr int NV = kBlockVecs, PN = kPairs<T>, EPV = VecTraits<T, 16>::kElems;
     constexpr int NARR = PRE ? 4 : 2;
+    constexpr bool GATE = MODE != kBlockPlain;
+    // weights read again in each pass (from L1) rather than kept: with both norms in bf16 they
+    // would not fit beside the column sums
+    constexpr bool REREAD = PRE && POST && sizeof(T) == 2;
     constexpr int NS = PRE && POST ? 6 : (PRE || POST ? 2 : 0);
     using L = Lanes;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -304,7 +358,7 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = i * at.G + at.t;
-        valid[i] = v * 16 < ring.bytes;
+        valid[i] = MODE != kBlockSome || v * 16 < ring.bytes;
         col[i] = ring.at + v * 16;
     }
     float* scratch = reinterpret_cast<float*>(smem + (ring.base(p.nslots, 0) - ring.base(0, 0)));
@@ -313,6 +367,20 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
     const char* post_w = static_cast<const char*>(p.post_w);
     const char* pre_w = static_cast<const char*>(p.pre_w);
     const bool have_dh = p.dh != nullptr;
+    const uint32_t in_slot = static_cast<uint32_t>(at.g * ring.slot_row + at.t * 16);
+    // weights, and the gate of the rows at hand, packed
+    Vec<16> w[NV], pw[NV], gt[NV];
+    auto read_weights = [&](int i) {
+        if constexpr (POST) w[i] = weight_vec<T, MODE>(post_w ? post_w + col[i] : nullptr, valid[i]);
+        if constexpr (PRE) pw[i] = weight_vec<T, MODE>(pre_w ? pre_w + col[i] : nullptr, valid[i]);
+    };
+    auto read_gate = [&](int i, int64_t row) {
+        if constexpr (GATE) gt[i] = weight_vec<T, MODE>(at_or_null(p.gate, row * ring.row_bytes + col[i]), valid[i]);
+    };
+    if constexpr (!REREAD) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) read_weights(i);
+    }
     L acc[NV * PN], pre[PRE ? NV * PN : 1];     // sums of D * xh and of dy * h * rh
 #pragma unroll
     for (int k = 0; k < NV * PN; ++k) acc[k] = L::all(0.f);
@@ -340,44 +408,55 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
                 for (int k = 0; k < NV * PN; ++k) acc[k] = L::all(0.f);
             }
             last_gate = gate_row;
+            if constexpr (!REREAD) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) read_gate(i, gate_row);
+            }
+        }
+        if constexpr (!REREAD) {
+            if constexpr (POST) stay_packed(w);
+            if constexpr (PRE) stay_packed(pw);
+            if constexpr (GATE) stay_packed(gt);
         }
         row += at.g;
         const bool here = at.g < rows;
-        const char* gate = at_or_null(p.gate, gate_row * ring.row_bytes);
         const bool ok = ring.wait(slot, use) && !bad;
         Vec<16> x[NV], d[NV], y[PRE ? NV : 1], h[PRE ? NV : 1];
         RowSums<NS> s;
         L a[6];
 #pragma unroll
         for (int k = 0; k < 6; ++k) a[k] = L::all(0.f);
+        // post_w * gate
+        auto factor = [&](int i, int k) {
+            if constexpr (POST && GATE) return product<T>(w[i], gt[i], k);
+            else if constexpr (POST) return lanes<T>(w[i], k);
+            else if constexpr (GATE) return lanes<T>(gt[i], k);
+            else return L::all(1.f);
+        };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const bool on = here && valid[i];
-            const uint32_t in = static_cast<uint32_t>(at.g * ring.slot_row + (i * at.G + at.t) * 16);
-            x[i] = ld_slot_if(ring.base(slot, 0) + in, on);
-            d[i] = ld_slot_if(ring.base(slot, 1) + in, on && have_dh);
-            Vec<16> pw, w, g;
-            if constexpr (PRE) {
-                y[i] = ld_slot_if(ring.base(slot, 2) + in, on);
-                h[i] = ld_slot_if(ring.base(slot, 3) + in, on);
-                pw = weight_vec<T>(pre_w ? pre_w + col[i] : nullptr, valid[i]);
+            const uint32_t in = in_slot + i * at.G * 16;
+            if constexpr (REREAD) {
+                read_weights(i);
+                read_gate(i, gate_row);
             }
-            if constexpr (POST) {
-                w = weight_vec<T>(post_w ? post_w + col[i] : nullptr, valid[i]);
-                g = weight_vec<T>(gate ? gate + col[i] : nullptr, valid[i]);
+            x[i] = slot_vec<MODE>(ring.base(slot, 0) + in, valid[i]);
+            d[i] = have_dh ? slot_vec<MODE>(ring.base(slot, 1) + in, valid[i]) : zero_vec();
+            if constexpr (PRE) {
+                y[i] = slot_vec<MODE>(ring.base(slot, 2) + in, valid[i]);
+                h[i] = slot_vec<MODE>(ring.base(slot, 3) + in, valid[i]);
             }
 #pragma unroll
             for (int k = 0; k < PN; ++k) {
                 L q, gy;
                 if constexpr (POST) {
-                    const L xk = lanes<T>(x[i], k);
-                    q = lanes<T>(w, k) * lanes<T>(g, k) * xk;
-                    a[2] = fma(xk, xk, a[2]);
+                    q = factor(i, k) * lanes<T>(x[i], k);
+                    a[2] = add_square<T>(x[i], k, a[2]);
                     a[3] = fma(q, lanes<T>(d[i], k), a[3]);
                 }
                 if constexpr (PRE) {
                     const L hk = lanes<T>(h[i], k);
-                    gy = lanes<T>(y[i], k) * lanes<T>(pw, k);
+                    gy = product<T>(y[i], pw[i], k);
                     a[0] = fma(hk, hk, a[0]);
                     a[1] = fma(gy, hk, a[1]);
                     if constexpr (POST) {
@@ -407,41 +486,42 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
         float six[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < NS; ++k) six[FIRST + k] = s.v[k];
-        BlockFactors f = block_factors(six, p);
-        if (!here) f = BlockFactors{0.f, 0.f, 0.f, 0.f};      // rows of zeros: 0 * an infinite factor
+        const BlockFactors f = block_factors(six, p);
         const L rh = L::all(f.rh), kh = L::all(-f.kh), rx = L::all(f.rx), kx = L::all(-f.kx);
         const L bs = L::all(p.branch_scale), rs = L::all(p.residual_scale);
+        // rows that the block lacks have sums of what the slot held before, and add nothing
+        if (here) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            Vec<16> pw;
-            if constexpr (PRE) pw = weight_vec<T>(pre_w ? pre_w + col[i] : nullptr, valid[i]);
-            const Vec<16> w = weight_vec<T>(POST && post_w ? post_w + col[i] : nullptr, valid[i]);
-            const Vec<16> g = weight_vec<T>(gate ? gate + col[i] : nullptr, valid[i]);
-            float ox[EPV], od[EPV];
+            for (int i = 0; i < NV; ++i) {
+                float ox[EPV], od[EPV];
+                if constexpr (REREAD) {
+                    read_weights(i);
+                    read_gate(i, gate_row);
+                }
 #pragma unroll
-            for (int k = 0; k < PN; ++k) {
-                const L xk = lanes<T>(x[i], k);
-                L D = lanes<T>(d[i], k);
-                if constexpr (PRE) {
-                    const L hk = lanes<T>(h[i], k), yk = lanes<T>(y[i], k);
-                    D = fma(rh, fma(hk, kh, yk * lanes<T>(pw, k)), D);
-                    pre[i * PN + k] = fma(yk, hk * rh, pre[i * PN + k]);
+                for (int k = 0; k < PN; ++k) {
+                    const L xk = lanes<T>(x[i], k);
+                    L D = lanes<T>(d[i], k);
+                    if constexpr (PRE) {
+                        const L hk = lanes<T>(h[i], k);
+                        D = fma(rh, fma(hk, kh, product<T>(y[i], pw[i], k)), D);
+                        pre[i * PN + k] = fma(lanes<T>(y[i], k), hk * rh, pre[i * PN + k]);
+                    }
+                    (D * rs).put(od + 2 * k);
+                    const L e = D * bs * factor(i, k);
+                    if constexpr (POST) {
+                        acc[i * PN + k] = fma(D, xk * rx, acc[i * PN + k]);
+                        (fma(xk, kx, e) * rx).put(ox + 2 * k);
+                    } else {
+                        acc[i * PN + k] = fma(D, xk, acc[i * PN + k]);
+                        e.put(ox + 2 * k);
+                    }
                 }
-                (D * rs).put(od + 2 * k);
-                L u = lanes<T>(g, k);
-                if constexpr (POST) {
-                    u = u * lanes<T>(w, k);
-                    acc[i * PN + k] = fma(D, xk * rx, acc[i * PN + k]);
-                    (fma(xk, kx, D * bs * u) * rx).put(ox + 2 * k);
-                } else {
-                    acc[i * PN + k] = fma(D, xk, acc[i * PN + k]);
-                    (D * bs * u).put(ox + 2 * k);
+                if (valid[i]) {
+                    const int64_t to = row * ring.row_bytes + col[i];
+                    st_stream<16>(static_cast<char*>(p.dx) + to, pack<T, 16>(ox));
+                    st_stream<16>(static_cast<char*>(p.dres) + to, pack<T, 16>(od));
                 }
-            }
-            if (here && valid[i]) {
-                const int64_t to = row * ring.row_bytes + col[i];
-                st_stream<16>(static_cast<char*>(p.dx) + to, pack<T, 16>(ox));
-                st_stream<16>(static_cast<char*>(p.dres) + to, pack<T, 16>(od));
             }
         }
         if (++slot == p.nslots) {
