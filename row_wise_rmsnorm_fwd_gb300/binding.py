@@ -965,14 +965,6 @@ _PACK_HEADS = struct.Struct("15q").pack           # rmsnorm_rope_heads_t
 _PACK_ROPE = struct.Struct("4q4i2f").pack         # rmsnorm_rope_t
 
 
-def _packed(pack, *numbers):
-    """A struct's bytes; numbers that its fields cannot hold are refused."""
-    try:
-        return pack(*numbers)
-    except (struct.error, OverflowError) as e:
-        raise ValueError(f"a number is out of range: {e}") from None
-
-
 def _gate_rows(gate, x, shape, hidden, index):
     """How many rows share a row of the gate, which is one row, or has the leading
     dims of x up to some dim (and ones for those behind it)."""
@@ -998,20 +990,26 @@ def _gate_rows(gate, x, shape, hidden, index):
 
 def _block_rule(x, shape, hidden, index, post_w, pre_w, gate, post_norm, pre_norm, residual_scale,
                 branch_scale, post_eps, pre_eps):
-    dt = x.dtype
+    dt, one = x.dtype, shape[-1:]
+    post = pre = at = 0
+    rows = 1
     if post_w is not None:
         if not post_norm:
             raise ValueError("post_w without post_norm")
-        _require("post_w", post_w, dt, (hidden,), index)
+        _require("post_w", post_w, dt, one, index)
+        post = post_w.data_ptr()
     if pre_w is not None:
         if not pre_norm:
             raise ValueError("pre_w without pre_norm")
-        _require("pre_w", pre_w, dt, (hidden,), index)
-    rows = 1 if gate is None else _gate_rows(gate, x, shape, hidden, index)
-    return _packed(_PACK_BLOCK, post_w.data_ptr() if post_w is not None else 0,
-                   pre_w.data_ptr() if pre_w is not None else 0,
-                   gate.data_ptr() if gate is not None else 0, rows, residual_scale, branch_scale,
-                   post_eps, pre_eps, bool(post_norm), bool(pre_norm))
+        _require("pre_w", pre_w, dt, one, index)
+        pre = pre_w.data_ptr()
+    if gate is not None:
+        rows, at = _gate_rows(gate, x, shape, hidden, index), gate.data_ptr()
+    try:
+        return _PACK_BLOCK(post, pre, at, rows, residual_scale, branch_scale, post_eps, pre_eps,
+                           bool(post_norm), bool(pre_norm)), rows if at else 0
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"a number is out of range: {e}") from None
 
 
 def _block_fwd(name, want, x, residual, post_w, pre_w, gate, h, y, post_norm, pre_norm,
@@ -1031,7 +1029,7 @@ def _block_fwd(name, want, x, residual, post_w, pre_w, gate, h, y, post_norm, pr
             raise ValueError("y without pre_norm")
         _require("y", y, dt, shape, index)
     rule = _block_rule(x, shape, hidden, index, post_w, pre_w, gate, post_norm, pre_norm,
-                       residual_scale, branch_scale, post_eps, pre_eps)
+                       residual_scale, branch_scale, post_eps, pre_eps)[0]
     if stream is None and index == _current_device():
         return _block_fwd_on(_raw_stream(index), name, code, x, residual, h, y, hidden, rule,
                              pre_norm, options)
@@ -1121,12 +1119,12 @@ def _block_bwd(name, want, dy, dh, x, h, post_w, pre_w, gate, dx, dresidual, dpo
         if gate is None:
             raise ValueError("dgate without a gate")
         _require("dgate", dgate, f32, gate.shape, index)
-    rule = _block_rule(x, shape, hidden, index, post_w, pre_w, gate, post_norm, pre_norm,
-                       residual_scale, branch_scale, post_eps, pre_eps)
-    grads = (weight_grads and post_w is not None, weight_grads and pre_w is not None,
-             gate.shape if weight_grads and gate is not None else None)
+    rule, gate_rows = _block_rule(x, shape, hidden, index, post_w, pre_w, gate, post_norm,
+                                  pre_norm, residual_scale, branch_scale, post_eps, pre_eps)
+    if not weight_grads:
+        post_w = pre_w = gate = None
     args = (name, code, dy, dh, x, h if pre_norm else None, dx, dresidual, dpost_w, dpre_w, dgate,
-            grads, hidden, rule, workspace, options, index)
+            post_w, pre_w, gate, hidden, rule, gate_rows, workspace, options, index)
     if stream is None and index == _current_device():
         return _block_bwd_on(_raw_stream(index), *args)
     return _elsewhere(index, stream, _block_bwd_on, *args)
@@ -1143,44 +1141,37 @@ def _block_workspace(code, rows, hidden, gate_rows, index):
     return size.value
 
 
-def _block_bwd_on(handle, name, code, dy, dh, x, h, dx, dresidual, dpost_w, dpre_w, dgate, grads,
-                  hidden, rule, workspace, options, index):
-    empty, f32, dev = _T.empty, _T.float32, x.device
+def _block_bwd_on(handle, name, code, dy, dh, x, h, dx, dresidual, dpost_w, dpre_w, dgate, post_w,
+                  pre_w, gate, hidden, rule, gate_rows, workspace, options, index):
+    empty_like, f32 = _T.empty_like, _T.float32
     if dx is None:
-        dx = _T.empty_like(x)
+        dx = empty_like(x)
     if dresidual is None:
-        dresidual = _T.empty_like(x)
-    if dpost_w is None and grads[0]:
-        dpost_w = empty(hidden, dtype=f32, device=dev)
-    if dpre_w is None and grads[1]:
-        dpre_w = empty(hidden, dtype=f32, device=dev)
-    if dgate is None and grads[2] is not None:
-        dgate = empty(grads[2], dtype=f32, device=dev)
+        dresidual = empty_like(x)
+    # gradients of the weights that are given
+    if dpost_w is None and post_w is not None:
+        dpost_w = empty_like(post_w, dtype=f32)
+    if dpre_w is None and pre_w is not None:
+        dpre_w = empty_like(pre_w, dtype=f32)
+    if dgate is None and gate is not None:
+        dgate = empty_like(gate, dtype=f32)
     rows = x.numel() // hidden
     if rows == 0:
         for t in (dpost_w, dpre_w, dgate):
             if t is not None:
                 t.zero_()
         return dx, dresidual, dpost_w, dpre_w, dgate
-    gate_rows = _BLOCK_GATE(rule)
     ws, n = _room(workspace, _block_workspace(code, rows, hidden, gate_rows, index), x)
     st = (_lib or load()).rmsnorm_block_bwd_ex(
-        code, dy.data_ptr() if dy is not None else None, dh.data_ptr() if dh is not None else None,
-        x.data_ptr(), h.data_ptr() if h is not None else None, dx.data_ptr(),
-        dresidual.data_ptr(), _ptr(dpost_w), _ptr(dpre_w), _ptr(dgate), rows, hidden, rule,
-        ws.data_ptr(), n, _opt(options) if options is not None else None, handle)
+        code, None if dy is None else dy.data_ptr(), None if dh is None else dh.data_ptr(),
+        x.data_ptr(), None if h is None else h.data_ptr(), dx.data_ptr(), dresidual.data_ptr(),
+        None if dpost_w is None else dpost_w.data_ptr(),
+        None if dpre_w is None else dpre_w.data_ptr(),
+        None if dgate is None else dgate.data_ptr(), rows, hidden, rule, ws.data_ptr(), n,
+        _opt(options) if options is not None else None, handle)
     if st:
         raise RmsnormError(st, name)
     return dx, dresidual, dpost_w, dpre_w, dgate
-
-
-def _BLOCK_GATE(rule):
-    """gate_rows of a packed rule, 0 without a gate."""
-    gate, rows = _UNPACK_GATE(rule, 16)
-    return rows if gate else 0
-
-
-_UNPACK_GATE = struct.Struct("2q").unpack_from
 
 
 def rmsnorm_block_bwd_f32(dy, dh, x, h, post_w=None, pre_w=None, gate=None, dx=None,
@@ -1297,35 +1288,11 @@ def _view(t):
     if t is None:
         return 0, 0, 0, 0
     s = t.stride()
-    return (t.data_ptr(), *s[:3]) if len(s) == 4 else (t.data_ptr(), 0, s[0], s[1])
-
-
-def _rope_rule(lead, dim, index, freqs, positions, norm, interleaved, start, mscale, eps):
-    torch = _T
-    half = freqs.shape[0] if freqs.dim() == 1 else 0
-    if freqs.dtype != torch.int64 or not half or 2 * half > dim or not freqs.is_contiguous():
-        raise ValueError(f"freqs must be the contiguous int64 tensor that rmsnorm_rope_freqs gives "
-                         f"for a rot_dim of at most {dim}")
-    if freqs.get_device() != index:
-        raise ValueError(f"freqs must be on device cuda:{index}, got {freqs.device}")
-    at = n = size = 0
-    if positions is not None:
-        size = 8 if positions.dtype == torch.int64 else 4 if positions.dtype == torch.int32 else 0
-        if not size:
-            raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
-        shape = positions.shape
-        if shape != lead and shape != lead[-1:] and shape != (1, *lead[-1:]):
-            raise ValueError(f"positions must have shape {tuple(lead)} or {tuple(lead[-1:])}, got "
-                             f"{tuple(shape)}")
-        if positions.get_device() != index or not positions.is_contiguous():
-            raise ValueError(f"positions must be contiguous, on device cuda:{index}")
-        at, n = positions.data_ptr(), max(1, positions.numel())
-    return _packed(_PACK_ROPE, freqs.data_ptr(), at, n, start, size, 2 * half, bool(interleaved),
-                   bool(norm), eps, mscale)
+    return (t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else (t.data_ptr(), 0, s[0], s[1])
 
 
 def _rope_shapes(first, other):
-    """Leading dims and head_dim of two tensors [..., heads, head_dim]; other may be None."""
+    """Shape and device of two tensors [..., heads, head_dim]; other may be None."""
     shape, index = first.shape, first.get_device()
     if index < 0:
         raise ValueError("q must be a CUDA tensor")
@@ -1338,52 +1305,114 @@ def _rope_shapes(first, other):
     return shape, index
 
 
+def _sig(t):
+    """All of a tensor that the checks of a call look at."""
+    return None if t is None else (t.dtype, t.shape, t.stride(), t.get_device())
+
+
+# What the checks of a call of these signatures came to: small calls are bound by the host, and
+# the checks of up to eight tensors are most of what it does.
+_ROPE_PLANS = {}
+
+
+def _rope_plan(key, want, norm, first, other, freqs, positions, xs, ws):
+    """Check a call and keep (dtype code, device, batch, seq, head_dim, rot_dim, number of
+    positions, their bytes, heads, shapes of q and k, whether contiguous).  first and other:
+    q and k, or their gradients; xs: q and k where they are read beside those, else None."""
+    torch = _T
+    code = _code(first, want)
+    shape, index = _rope_shapes(first, other)
+    dt, dim, lead = first.dtype, shape[-1], shape[:-2]
+    pre = "" if xs is None else "d"
+    _heads(pre + "q", first, dt, shape, index)
+    if other is not None:
+        _heads(pre + "k", other, dt, other.shape, index)
+    elif ws[1] is not None or (xs is not None and xs[1] is not None):
+        raise ValueError("k and k_w need a " + pre + "k")
+    for n, x, y, w in zip("qk", xs or (None, None), (first, other), ws):
+        if xs is not None and norm and y is not None:
+            _heads(n, x, dt, y.shape, index)
+        if w is not None:
+            if not norm:
+                raise ValueError(f"{n}_w without norm")
+            _require(n + "_w", w, dt, (dim,), index)
+    half = freqs.shape[0] if freqs.dim() == 1 else 0
+    if freqs.dtype != torch.int64 or not half or 2 * half > dim or not freqs.is_contiguous():
+        raise ValueError(f"freqs must be the contiguous int64 tensor that rmsnorm_rope_freqs gives "
+                         f"for a rot_dim of at most {dim}")
+    if freqs.get_device() != index:
+        raise ValueError(f"freqs must be on device cuda:{index}, got {freqs.device}")
+    n = size = 0
+    if positions is not None:
+        size = 8 if positions.dtype == torch.int64 else 4 if positions.dtype == torch.int32 else 0
+        if not size:
+            raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
+        if positions.shape not in (lead, lead[-1:], (1, *lead[-1:])):
+            raise ValueError(f"positions must have shape {tuple(lead)} or {tuple(lead[-1:])}, got "
+                             f"{tuple(positions.shape)}")
+        if positions.get_device() != index or not positions.is_contiguous():
+            raise ValueError(f"positions must be contiguous, on device cuda:{index}")
+        n = max(1, positions.numel())
+    batch, seq = lead if len(lead) == 2 else (1, lead[0])
+    plan = (code, index, batch, seq, dim, 2 * half, n, size,
+            (shape[-2], 0 if other is None else other.shape[-2]),
+            (shape, None if other is None else other.shape),
+            (first.is_contiguous(), other is not None and other.is_contiguous()))
+    if len(_ROPE_PLANS) >= 1024:
+        _ROPE_PLANS.clear()
+    _ROPE_PLANS[key] = plan
+    return plan
+
+
+def _rope_rule(plan, freqs, positions, norm, interleaved, start, mscale, eps):
+    try:
+        return _PACK_ROPE(freqs.data_ptr(), 0 if positions is None else positions.data_ptr(), plan[6],
+                          start, plan[7], plan[5], bool(interleaved), norm, eps, mscale)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"a number is out of range: {e}") from None
+
+
 def _rope_fwd(name, want, q, k, freqs, positions, q_w, k_w, q_out, k_out, norm, interleaved, start,
               mscale, eps, options, stream):
     if _T is None:
         _warm()
-    code = _code(q, want)
-    shape, index = _rope_shapes(q, k)
-    dt, dim = q.dtype, shape[-1]
-    _heads("q", q, dt, shape, index)
+    norm = bool(norm)
+    key = (want, norm, _sig(q), _sig(k), _sig(freqs), _sig(positions), _sig(q_w), _sig(k_w))
+    plan = _ROPE_PLANS.get(key) or _rope_plan(key, want, norm, q, k, freqs, positions, None,
+                                              (q_w, k_w))
+    index = plan[1]
     if q_out is not None:
-        _heads("q_out", q_out, dt, shape, index)
-    if k is not None:
-        _heads("k", k, dt, k.shape, index)
-        if k_out is not None:
-            _heads("k_out", k_out, dt, k.shape, index)
-    elif k_out is not None or k_w is not None:
-        raise ValueError("k_out and k_w need a k")
-    for n, w in (("q_w", q_w), ("k_w", k_w)):
-        if w is not None:
-            if not norm:
-                raise ValueError(f"{n} without norm")
-            _require(n, w, dt, (dim,), index)
-    rule = _rope_rule(shape[:-2], dim, index, freqs, positions, norm, interleaved, start, mscale,
-                      eps)
+        _heads("q_out", q_out, q.dtype, plan[9][0], index)
+    if k_out is not None:
+        if k is None:
+            raise ValueError("k_out needs a k")
+        _heads("k_out", k_out, q.dtype, plan[9][1], index)
+    rule = _rope_rule(plan, freqs, positions, norm, interleaved, start, mscale, eps)
     if stream is None and index == _current_device():
-        return _rope_fwd_on(_raw_stream(index), name, code, q, k, q_w, k_w, q_out, k_out, shape,
-                            rule, options)
-    return _elsewhere(index, stream, _rope_fwd_on, name, code, q, k, q_w, k_w, q_out, k_out, shape,
-                      rule, options)
+        return _rope_fwd_on(_raw_stream(index), name, plan, q, k, q_w, k_w, q_out, k_out, rule, options)
+    return _elsewhere(index, stream, _rope_fwd_on, name, plan, q, k, q_w, k_w, q_out, k_out, rule,
+                      options)
 
 
-def _rope_fwd_on(handle, name, code, q, k, q_w, k_w, q_out, k_out, shape, rule, options):
+def _like(t, shape, contiguous):
+    return _T.empty_like(t) if contiguous else _T.empty(shape, dtype=t.dtype, device=t.device)
+
+
+def _rope_fwd_on(handle, name, plan, q, k, q_w, k_w, q_out, k_out, rule, options):
+    code, _, batch, seq, dim, _, _, _, heads, shapes, dense = plan
     if q_out is None:
-        q_out = _T.empty(shape, dtype=q.dtype, device=q.device)
-    hq = _PACK_HEADS(*_view(q), 0, 0, 0, 0, *_view(q_out),
-                     q_w.data_ptr() if q_w is not None else 0, 0, shape[-2])
+        q_out = _like(q, shapes[0], dense[0])
+    hq = _PACK_HEADS(*_view(q), 0, 0, 0, 0, *_view(q_out), 0 if q_w is None else q_w.data_ptr(), 0,
+                     heads[0])
     hk = None
     if k is not None:
         if k_out is None:
-            k_out = _T.empty(k.shape, dtype=k.dtype, device=k.device)
-        hk = _PACK_HEADS(*_view(k), 0, 0, 0, 0, *_view(k_out),
-                         k_w.data_ptr() if k_w is not None else 0, 0, k.shape[-2])
-    batch, seq = shape[:2] if len(shape) == 4 else (1, shape[0])
-    if batch * seq:
+            k_out = _like(k, shapes[1], dense[1])
+        hk = _PACK_HEADS(*_view(k), 0, 0, 0, 0, *_view(k_out), 0 if k_w is None else k_w.data_ptr(),
+                         0, heads[1])
+    if batch and seq:
         st = (_lib or load()).rmsnorm_rope_fwd_ex(
-            code, hq, hk, batch, seq, shape[-1], rule,
-            _opt(options) if options is not None else None, handle)
+            code, hq, hk, batch, seq, dim, rule, None if options is None else _opt(options), handle)
         if st:
             raise RmsnormError(st, name)
     return q_out, k_out
@@ -1422,32 +1451,26 @@ def rmsnorm_rope_fwd_ex(q, k, freqs, positions=None, q_w=None, k_w=None, q_out=N
 
 def _rope_bwd(name, want, dq, dk, freqs, positions, q, k, q_w, k_w, dq_in, dk_in, dq_w, dk_w, norm,
               interleaved, start, mscale, eps, weight_grads, workspace, options, stream):
-    torch = _T or _warm()
-    if norm is None:
-        norm = q is not None
-    code = _code(dq, want)
-    shape, index = _rope_shapes(dq, dk)
-    dt, dim = dq.dtype, shape[-1]
-    both = [("q", dq, q, q_w, dq_in, dq_w)]
-    if dk is not None:
-        both.append(("k", dk, k, k_w, dk_in, dk_w))
-    elif any(t is not None for t in (k, k_w, dk_in, dk_w)):
-        raise ValueError("k, k_w, dk_in and dk_w need a dk")
-    for n, dy, x, w, dx, dw in both:
-        _heads("d" + n, dy, dt, dy.shape, index)
+    if _T is None:
+        _warm()
+    norm = q is not None if norm is None else bool(norm)
+    key = (want, norm, _sig(dq), _sig(dk), _sig(freqs), _sig(positions), _sig(q_w), _sig(k_w),
+           _sig(q), _sig(k))
+    plan = _ROPE_PLANS.get(key) or _rope_plan(key, want, norm, dq, dk, freqs, positions, (q, k),
+                                              (q_w, k_w))
+    index = plan[1]
+    if dk is None and (dk_in is not None or dk_w is not None):
+        raise ValueError("dk_in and dk_w need a dk")
+    for n, i, dx, dw in (("q", 0, dq_in, dq_w), ("k", 1, dk_in, dk_w)):
         if dx is not None:
-            _heads(f"d{n}_in", dx, dt, dy.shape, index)
-        if norm:
-            _heads(n, x, dt, dy.shape, index)
-            if w is not None:
-                _require(n + "_w", w, dt, (dim,), index)
-            if dw is not None:
-                _require(f"d{n}_w", dw, torch.float32, (dim,), index)
-        elif w is not None or dw is not None:
-            raise ValueError(f"{n}_w and d{n}_w need the norm")
-    rule = _rope_rule(shape[:-2], dim, index, freqs, positions, norm, interleaved, start, mscale,
-                      eps)
-    args = (name, code, both, norm, weight_grads, workspace, shape, rule, options, index)
+            _heads(f"d{n}_in", dx, dq.dtype, plan[9][i], index)
+        if dw is not None:
+            if not norm:
+                raise ValueError(f"d{n}_w without norm")
+            _require(f"d{n}_w", dw, _T.float32, (plan[4],), index)
+    rule = _rope_rule(plan, freqs, positions, norm, interleaved, start, mscale, eps)
+    args = (name, plan, dq, dk, q if norm else None, k if norm else None, q_w, k_w, dq_in, dk_in,
+            dq_w, dk_w, weight_grads, workspace, rule, options)
     if stream is None and index == _current_device():
         return _rope_bwd_on(_raw_stream(index), *args)
     return _elsewhere(index, stream, _rope_bwd_on, *args)
@@ -1463,35 +1486,39 @@ def _rope_workspace(code, batch, seq, heads, dim, index):
     return size.value
 
 
-def _rope_bwd_on(handle, name, code, both, norm, weight_grads, workspace, shape, rule, options,
-                 index):
-    batch, seq = shape[:2] if len(shape) == 4 else (1, shape[0])
-    dxs, dws, packed, heads = [None, None], [None, None], [None, None], 0
-    for i, (n, dy, x, w, dx, dw) in enumerate(both):
-        if dx is None:
-            dx = _T.empty(dy.shape, dtype=dy.dtype, device=dy.device)
-        if dw is None and weight_grads and w is not None:
-            dw = _T.empty(shape[-1], dtype=_T.float32, device=dy.device)
-        dxs[i], dws[i] = dx, dw
-        heads += dy.shape[-2]
-        packed[i] = _PACK_HEADS(*_view(x if norm else None), *_view(dy), *_view(dx),
-                                w.data_ptr() if w is not None else 0,
-                                dw.data_ptr() if dw is not None else 0, dy.shape[-2])
-    if batch * seq == 0:
-        for dw in dws:
+def _rope_bwd_on(handle, name, plan, dq, dk, q, k, q_w, k_w, dq_in, dk_in, dq_w, dk_w, weight_grads,
+                 workspace, rule, options):
+    code, index, batch, seq, dim, _, _, _, heads, shapes, dense = plan
+    f32 = _T.float32
+    if dq_in is None:
+        dq_in = _like(dq, shapes[0], dense[0])
+    if dq_w is None and weight_grads and q_w is not None:
+        dq_w = _T.empty_like(q_w, dtype=f32)
+    hq = _PACK_HEADS(*_view(q), *_view(dq), *_view(dq_in), 0 if q_w is None else q_w.data_ptr(),
+                     0 if dq_w is None else dq_w.data_ptr(), heads[0])
+    hk = None
+    if dk is not None:
+        if dk_in is None:
+            dk_in = _like(dk, shapes[1], dense[1])
+        if dk_w is None and weight_grads and k_w is not None:
+            dk_w = _T.empty_like(k_w, dtype=f32)
+        hk = _PACK_HEADS(*_view(k), *_view(dk), *_view(dk_in), 0 if k_w is None else k_w.data_ptr(),
+                         0 if dk_w is None else dk_w.data_ptr(), heads[1])
+    if not batch or not seq:
+        for dw in (dq_w, dk_w):
             if dw is not None:
                 dw.zero_()
-        return (*dxs, *dws)
-    ws, size = None, 0
-    if dws[0] is not None or dws[1] is not None:
-        ws, size = _room(workspace, _rope_workspace(code, batch, seq, heads, shape[-1], index),
-                         dxs[0])
-    st = (_lib or load()).rmsnorm_rope_bwd_ex(
-        code, packed[0], packed[1], batch, seq, shape[-1], rule, _ptr(ws), size,
-        _opt(options) if options is not None else None, handle)
+        return dq_in, dk_in, dq_w, dk_w
+    at, size = None, 0
+    if dq_w is not None or dk_w is not None:
+        ws, size = _room(workspace, _rope_workspace(code, batch, seq, heads[0] + heads[1], dim, index),
+                         dq)
+        at = ws.data_ptr()
+    st = (_lib or load()).rmsnorm_rope_bwd_ex(code, hq, hk, batch, seq, dim, rule, at, size,
+                                              None if options is None else _opt(options), handle)
     if st:
         raise RmsnormError(st, name)
-    return (*dxs, *dws)
+    return dq_in, dk_in, dq_w, dk_w
 
 
 def rmsnorm_rope_bwd_f32(dq, dk, freqs, positions=None, q=None, k=None, q_w=None, k_w=None,

@@ -379,7 +379,9 @@ __global__ void __launch_bounds__(kBlockReduceThreads) blocknorm_reduce_kernel(c
     const T* post_w = p.post ? static_cast<const T*>(p.post_w) : nullptr;
     for (int64_t s = blockIdx.y - 1; s < p.gates; s += gridDim.y - 1) {
         int64_t from = s * p.parts_per_gate, count = p.parts_per_gate;
-        if (p.units) {          // the units that the gate row's blocks were dealt to
+        if (p.units && p.gates == 1) {
+            count = p.units;
+        } else if (p.units) {   // the units that the gate row's blocks were dealt to
             const int64_t b0 = s * p.blocks_per_gate;
             const int64_t b1 = min(b0 + p.blocks_per_gate, p.blocks) - 1;
             const int64_t u0 = ((b0 + 1) * p.units - 1) / p.blocks;

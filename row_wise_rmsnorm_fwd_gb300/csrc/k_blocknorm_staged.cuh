@@ -451,7 +451,8 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
                 L q, gy;
                 if constexpr (POST) {
                     q = factor(i, k) * lanes<T>(x[i], k);
-                    a[2] = add_square<T>(x[i], k, a[2]);
+                    const L xk = lanes<T>(x[i], k);
+                    a[2] = fma(xk, xk, a[2]);
                     a[3] = fma(q, lanes<T>(d[i], k), a[3]);
                 }
                 if constexpr (PRE) {

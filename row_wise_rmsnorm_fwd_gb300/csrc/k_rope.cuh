@@ -5,7 +5,7 @@
 // the integer product with a position, modulo 2^64, is the angle modulo a turn with
 // nothing lost for any position.  Of its upper 32 bits the nearest quarter turn is taken
 // away in integers, which leaves at most an eighth of a turn for fp32 to hold: the angle
-// is off by at most 2^-24 of that (without, of half a turn).
+// is off by at most 2^-23 of that (without, of half a turn).
 // No fp64, and no table in memory.
 #pragma once
 #include "common.cuh"
@@ -13,13 +13,23 @@
 
 namespace rmsnorm {
 
-// (cos, sin) * mscale of pair i at a position.
+// (cos, sin) * mscale at a position.  Within an eighth of a turn the Taylor series of sine and
+// cosine end at x^9 / 9! and x^10 / 10!: the next terms are below 2^-29 of either.
 __device__ __forceinline__ float2 rope_turn(uint64_t freq, int64_t position, float mscale) {
     const uint32_t turns = static_cast<uint32_t>((freq * static_cast<uint64_t>(position)) >> 32);
     const uint32_t quarter = (turns + 0x20000000u) >> 30;
-    const float half = static_cast<float>(static_cast<int32_t>(turns - (quarter << 30))) * 0x1p-31f;
-    float s, c;
-    sincospif(half, &s, &c);
+    const float x = static_cast<float>(static_cast<int32_t>(turns - (quarter << 30))) *
+                    1.4629180792671596e-9f;                        // 2 pi / 2^32
+    const float q = x * x;
+    float s = fmaf(q, 1.f / 362880.f, -1.f / 5040.f);
+    s = fmaf(q, s, 1.f / 120.f);
+    s = fmaf(q, s, -1.f / 6.f);
+    s = fmaf(x * q, s, x);
+    float c = fmaf(q, -1.f / 3628800.f, 1.f / 40320.f);
+    c = fmaf(q, c, -1.f / 720.f);
+    c = fmaf(q, c, 1.f / 24.f);
+    c = fmaf(q, c, -0.5f);
+    c = fmaf(q, c, 1.f);
     const float a = quarter & 1 ? -s : c, b = quarter & 1 ? c : s;
     const float scale = quarter & 2 ? -mscale : mscale;
     return make_float2(a * scale, b * scale);
@@ -55,7 +65,7 @@ __device__ __forceinline__ void rope_put(void* p, int64_t at, float v) {
 }
 
 // Any head_dim, strides and alignment: a warp per head, which reads it twice, element
-// by element, and forms every angle for itself (about forty instructions each: they
+// by element, and forms every angle for itself (about thirty instructions each: they
 // bound it).  Lane l has the pairs, and behind rot the elements, l, l + 32, ...; both
 // elements of a pair are read before either is written, so the heads may be turned in
 // place.  BACK: turned the other way, then the norm's gradient; a lane's columns are

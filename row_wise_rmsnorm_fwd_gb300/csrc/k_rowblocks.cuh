@@ -22,7 +22,7 @@ struct RowBlocks {
     const char* src[NARR];       // null: absent
     int narr;                    // arrays present
     uint32_t slots, bars;        // shared-memory addresses
-    int64_t first, count;        // the unit's blocks
+    int64_t first, step, count;  // the unit's blocks
     int unit;                    // number of the CTA, or of the cluster
     int row_bytes, at, bytes;    // a row, and the CTA's slice of it
     int slot_row;                // bytes of a row in a slot
@@ -36,8 +36,15 @@ struct RowBlocks {
             src[a] = static_cast<const char*>(arrays[a]);
             narr += src[a] != nullptr;
         }
-        first = p.blocks * unit / units;
-        count = p.blocks * (unit + 1) / units - first;
+        if (p.gates == 1) {
+            first = unit;
+            step = units;
+            count = (p.blocks - unit + units - 1) / units;
+        } else {
+            first = p.blocks * unit / units;
+            step = 1;
+            count = p.blocks * (unit + 1) / units - first;
+        }
         row_bytes = p.hidden * sz;
         slot_row = p.slice_vecs * 16;
         at = static_cast<int>(rank) * slot_row;
@@ -51,7 +58,7 @@ struct RowBlocks {
 
     // Gate row, first row and number of rows of the unit's n-th block.
     __device__ __forceinline__ void where(int64_t n, int64_t& gate, int64_t& row, int& rows) const {
-        const int64_t b = first + n;
+        const int64_t b = first + n * step;
         gate = p.gates == 1 ? 0 : b / p.blocks_per_gate;
         row = gate * p.gate_rows + (b - gate * p.blocks_per_gate) * p.block_rows;
         int64_t end = (gate + 1) * p.gate_rows;
