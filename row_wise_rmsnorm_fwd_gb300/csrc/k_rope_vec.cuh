@@ -3,9 +3,10 @@
 // A head is taken as units of two vectors of EPV elements: where it is turned, the unit
 // holds EPV whole pairs (vectors i and i + rot/2, or two neighbours if interleaved), behind
 // that two neighbours.  `lanes` lanes (a power of two) share a head, a unit each, so a
-// warp has 32 / lanes heads of a token at a time, walks over the token's heads, and its
-// lanes keep the cosines and sines of their pairs for all of them: an angle is formed once
-// for a warp's share of a token's heads, by one of the lanes that need it.  A CTA works on q alone or on k alone, so a lane's
+// warp has 32 / lanes heads at a time: of one token, or, where a token has fewer, of
+// several.  It walks over its tokens' heads, and its lanes keep the cosines and sines of their
+// pairs for all of them: an angle is formed once for a warp's share of a token's heads, by
+// one of the lanes that need it.  A CTA works on q alone or on k alone, so a lane's
 // weights, and backward its column sums, stay in registers for all its tokens.
 #pragma once
 #include <type_traits>
@@ -24,6 +25,12 @@ struct RopeOne {
     __device__ __forceinline__ float total() const { return v; }
     __device__ __forceinline__ void put(float* f) const { f[0] = v; }
 };
+__device__ __forceinline__ RopeOne minus(RopeOne a, RopeOne b) { return {a.v - b.v}; }
+__device__ __forceinline__ Lanes minus(Lanes a, Lanes b) {
+    Lanes r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
 __device__ __forceinline__ RopeOne fma(RopeOne a, RopeOne b, RopeOne c) { return {fmaf(a.v, b.v, c.v)}; }
 
 // A vector of EPV fp32 elements as pairs.
@@ -60,42 +67,37 @@ struct RopeAngles {
     float c[EPV], s[EPV];
 };
 
-// The lane groups of a warp share the work: of NG groups group g forms every NG-th pair from g
-// on, and hands it to the others.
+// The lane groups of a token share the work: of NG groups group g (0, 1, ...) forms every NG-th
+// pair from g on, and hands it to the others.  first, second: numbers of the two halves of the
+// unit's pairs; base: the lane of group 0 that has this lane's unit.
 template <int EPV, int NG>
 __device__ __forceinline__ void rope_share_angles(RopeAngles<EPV>& t, const uint64_t* freqs, int first,
                                                   int second, int64_t position, float mscale, int lanes,
-                                                  int sub, int l) {
+                                                  int group, int base) {
     constexpr int STEPS = (EPV + NG - 1) / NG;
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) {
-        int k = j * NG + sub % NG;
-        if (k >= EPV) k = EPV - 1;
+        const int k = j * NG + group;
         const int i = k < EPV / 2 || EPV == 1 ? first + k : second + k - EPV / 2;
         const float2 cs = rope_turn(__ldg(freqs + i), position, mscale);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            if (j * NG + g < EPV) {
-                t.c[j * NG + g] = NG == 1 ? cs.x : __shfl_sync(0xffffffffu, cs.x, g * lanes + l);
-                t.s[j * NG + g] = NG == 1 ? cs.y : __shfl_sync(0xffffffffu, cs.y, g * lanes + l);
-            }
+            t.c[j * NG + g] = NG == 1 ? cs.x : __shfl_sync(0xffffffffu, cs.x, base + g * lanes);
+            t.s[j * NG + g] = NG == 1 ? cs.y : __shfl_sync(0xffffffffu, cs.y, base + g * lanes);
         }
     }
 }
 
-// All lanes of the warp.  first, second: pair numbers of the two halves of the unit's pairs.
+// All lanes of the warp; `share` groups (a power of two) work on the token.
 template <int EPV>
 __device__ __forceinline__ void rope_angles(RopeAngles<EPV>& t, const uint64_t* freqs, int first, int second,
-                                            int64_t position, float mscale, int lanes, int sub, int l) {
-    if (lanes <= 4 && EPV >= 8) {
-        rope_share_angles<EPV, (EPV < 8 ? EPV : 8)>(t, freqs, first, second, position, mscale, lanes, sub, l);
-    } else if (lanes <= 8 && EPV >= 4) {
-        rope_share_angles<EPV, (EPV < 4 ? EPV : 4)>(t, freqs, first, second, position, mscale, lanes, sub, l);
-    } else if (lanes <= 16 && EPV >= 2) {
-        rope_share_angles<EPV, (EPV < 2 ? EPV : 2)>(t, freqs, first, second, position, mscale, lanes, sub, l);
-    } else {
-        rope_share_angles<EPV, 1>(t, freqs, first, second, position, mscale, lanes, sub, l);
-    }
+                                            int64_t position, float mscale, int lanes, int share, int group,
+                                            int base) {
+    constexpr int N8 = EPV < 8 ? EPV : 8, N4 = EPV < 4 ? EPV : 4, N2 = EPV < 2 ? EPV : 2;
+    if (share >= 8) rope_share_angles<EPV, N8>(t, freqs, first, second, position, mscale, lanes, group % N8, base);
+    else if (share == 4) rope_share_angles<EPV, N4>(t, freqs, first, second, position, mscale, lanes, group % N4, base);
+    else if (share == 2) rope_share_angles<EPV, N2>(t, freqs, first, second, position, mscale, lanes, group % N2, base);
+    else rope_share_angles<EPV, 1>(t, freqs, first, second, position, mscale, lanes, 0, base);
 }
 
 // Two vectors turned by their pairs' angles (BACK: the other way).  NEAR: pairs are neighbours.
@@ -117,14 +119,17 @@ __device__ __forceinline__ void rope_apply(RopeVec<EPV>& a, RopeVec<EPV>& b, con
             turn(b.e[k], t.c[EPV / 2 + k], t.s[EPV / 2 + k]);
         }
     } else {
-        const L minus = L::all(-1.f);
 #pragma unroll
         for (int k = 0; k < RopeVec<EPV>::N; ++k) {
             const L c = L::of(t.c + k * RopeVec<EPV>::PER), s = L::of(t.s + k * RopeVec<EPV>::PER);
             const L x = a.e[k], y = b.e[k];
-            const L xs = x * s, ys = y * s;
-            a.e[k] = fma(x, c, BACK ? ys : ys * minus);
-            b.e[k] = fma(y, c, BACK ? xs * minus : xs);
+            if constexpr (BACK) {
+                a.e[k] = fma(y, s, x * c);
+                b.e[k] = minus(y * c, x * s);
+            } else {
+                a.e[k] = minus(x * c, y * s);
+                b.e[k] = fma(x, s, y * c);
+            }
         }
     }
 }
@@ -132,7 +137,9 @@ __device__ __forceinline__ void rope_apply(RopeVec<EPV>& a, RopeVec<EPV>& b, con
 // Registers: enough CTAs to an SM for the loads under way to cover HBM's latency.
 constexpr int rope_ctas(int kind) { return kind == kRopeGrad ? 4 : 6; }
 
-template <typename T, int VB, bool INTER, int KIND>
+// LANES > 0: that many lanes to a head, each with a whole unit; 0: p.lanes, of which some may
+// have none or half of one.
+template <typename T, int VB, bool INTER, int KIND, int LANES>
 __global__ void __launch_bounds__(32 * kRopeVecWarps, rope_ctas(KIND)) rope_vec_kernel(const RopeParams p) {
     constexpr int EPV = VecTraits<T, VB>::kElems;
     constexpr bool NEAR = INTER && EPV > 1;
@@ -146,11 +153,14 @@ __global__ void __launch_bounds__(32 * kRopeVecWarps, rope_ctas(KIND)) rope_vec_
     const int cta = static_cast<int>(blockIdx.x) - (which ? p.q_ctas : 0);
     const int ctas = which ? static_cast<int>(gridDim.x) - p.q_ctas : p.q_ctas;
     const RopeHeads& t = p.t[which];
-    const int lanes = p.lanes, groups = 32 / lanes;
+    const int lanes = LANES ? LANES : p.lanes;
     const int sub = lane / lanes, l = lane - sub * lanes;
+    // the warp's lane groups by token, and the token's groups
+    const int share = p.share[which], mine = sub % share, token_of_warp = sub / share;
+    const int tokens_per_warp = 32 / lanes / share;
     const int half = p.rot / 2;
     const int turned = half / EPV;                  // units that are turned
-    const bool on = l < p.units, turns = l < turned;
+    const bool on = LANES || l < p.units, turns = l < turned;
     int ja, jb;                                     // first columns of the two vectors
     if (turns) {
         ja = INTER ? 2 * l * EPV : l * EPV;
@@ -159,28 +169,27 @@ __global__ void __launch_bounds__(32 * kRopeVecWarps, rope_ctas(KIND)) rope_vec_
         ja = p.rot + 2 * (l - turned) * EPV;
         jb = ja + EPV;
     }
-    const bool on_b = on && jb < p.dim;
-    // pair numbers of the two halves of the unit's pairs; lanes that turn nothing take any
+    const bool on_b = LANES || (on && jb < p.dim);
+    // numbers of the two halves of the unit's pairs; lanes that turn nothing take any
     const int unit = turns ? l : 0;
     const int first_pair = unit * EPV, second_pair = first_pair + EPV / 2;
-    auto load = [&](const void* base, int64_t at, bool yes) {
+    const bool all_turn = turned >= lanes;
+    auto load = [&](const T* at, bool yes) {
         Vec<VB> v;
         if constexpr (VB == 2) v.h = 0;
         else {
 #pragma unroll
             for (int k = 0; k < Vec<VB>::kWords; ++k) v.u[k] = 0u;
         }
-        if (yes) v = ld_stream<VB>(static_cast<const T*>(base) + at);
+        if (yes) v = ld_stream<VB>(at);
         return v;
     };
     pdl_wait();
-    V wa, wb;
-    if (t.w) {
-        wa.template widen<T, VB>(load(t.w, ja, on));
-        wb.template widen<T, VB>(load(t.w, jb, on_b));
-    } else {
-#pragma unroll
-        for (int k = 0; k < V::N; ++k) wa.e[k] = wb.e[k] = L::all(1.f);
+    Vec<VB> wa, wb;                                 // weights, packed
+    const bool weights = t.w != nullptr;
+    if (weights) {
+        wa = load(static_cast<const T*>(t.w) + ja, on);
+        wb = load(static_cast<const T*>(t.w) + jb, on_b);
     }
     V da, db;                                       // column sums
 #pragma unroll
@@ -190,38 +199,51 @@ __global__ void __launch_bounds__(32 * kRopeVecWarps, rope_ctas(KIND)) rope_vec_
     struct Loads {
         Vec<VB> a, b, xa, xb;
     };
-    const int split = p.split[which];
-    const int step = split * groups;
-    const int64_t items = p.tokens * split;
+    const int heads = t.heads, split = p.split[which];
+    const int step = split * share;
+    const int ab = jb - ja;
+    const RopeView& from = BACK ? t.dy : t.x;
+    const int64_t src_step = step * from.head, x_step = GRAD ? step * t.x.head : 0, out_step = step * t.out.head;
+    const int64_t items = (p.tokens + tokens_per_warp - 1) / tokens_per_warp * split;
     for (int64_t item = static_cast<int64_t>(cta) * kRopeVecWarps + warp; item < items;
          item += static_cast<int64_t>(ctas) * kRopeVecWarps) {
-        const int64_t token = item / split;
-        const RopeToken tk(p, token);
-        const RopeView& from = BACK ? t.dy : t.x;
-        const T* src = static_cast<const T*>(from.p) + tk.at(from, 0);
-        const T* xs = GRAD ? static_cast<const T*>(t.x.p) + tk.at(t.x, 0) : nullptr;
-        T* dst = static_cast<T*>(t.out.p) + tk.at(t.out, 0);
-        int head = static_cast<int>(item - token * split) * groups + sub;
-        auto read = [&](int h) {
+        const int64_t place = item / split;
+        const int64_t token = place * tokens_per_warp + token_of_warp;
+        const bool there = token < p.tokens;
+        const RopeToken tk(p, there ? token : 0);
+        const int first = static_cast<int>(item - place * split) * share;
+        int head = first + mine;
+        const T* src = static_cast<const T*>(from.p) + tk.at(from, head) + ja;
+        const T* xs = GRAD ? static_cast<const T*>(t.x.p) + tk.at(t.x, head) + ja : nullptr;
+        T* dst = static_cast<T*>(t.out.p) + tk.at(t.out, head) + ja;
+        auto read = [&](bool here) {
             Loads r;
-            const bool here = h < t.heads;
-            const int64_t at = h * from.head;
-            r.a = load(src, at + ja, here && on);
-            r.b = load(src, at + jb, here && on_b);
+            r.a = load(src, here && on);
+            r.b = load(src + ab, here && on_b);
+            src += src_step;
             if constexpr (GRAD) {
-                const int64_t ax = h * t.x.head;
-                r.xa = load(xs, ax + ja, here && on);
-                r.xb = load(xs, ax + jb, here && on_b);
+                r.xa = load(xs, here && on);
+                r.xb = load(xs + ab, here && on_b);
+                xs += x_step;
             }
             return r;
         };
-        Loads next = read(head);
+        Loads next = read(there && head < heads);
         RopeAngles<EPV> angle;
-        rope_angles<EPV>(angle, p.freqs, first_pair, second_pair, tk.position, p.mscale, lanes, sub, l);
-        for (int rest = t.heads - (head - sub); rest > 0; rest -= step, head += step) {
+        rope_angles<EPV>(angle, p.freqs, first_pair, second_pair, tk.position, p.mscale, lanes, share, mine,
+                         token_of_warp * share * lanes + l);
+        for (int rest = heads - first; rest > 0; rest -= step, head += step) {
             const Loads v = next;
-            const bool here = head < t.heads;
-            if (rest > step) next = read(head + step);
+            const bool here = there && head < heads;
+            // widened where they are used: widened once, they would be held so
+            if constexpr (VB > 2) {
+#pragma unroll
+                for (int k = 0; k < Vec<VB>::kWords; ++k) {
+                    opaque(wa.u[k]);
+                    opaque(wb.u[k]);
+                }
+            }
+            if (rest > step) next = read(there && head + step < heads);
             V a, b;
             a.template widen<T, VB>(v.a);
             b.template widen<T, VB>(v.b);
@@ -232,23 +254,44 @@ __global__ void __launch_bounds__(32 * kRopeVecWarps, rope_ctas(KIND)) rope_vec_
                     for (int k = 0; k < V::N; ++k) s = fma(b.e[k], b.e[k], fma(a.e[k], a.e[k], s));
                     const float sum = group_allreduce_sum(s.total(), lanes);
                     const L r = L::all(rsqrtf(fmaf(sum, p.inv_dim, p.eps)));
+                    V ua, ub;
+                    if (weights) {
+                        ua.template widen<T, VB>(wa);
+                        ub.template widen<T, VB>(wb);
+                    }
 #pragma unroll
                     for (int k = 0; k < V::N; ++k) {
-                        a.e[k] = a.e[k] * r * wa.e[k];
-                        b.e[k] = b.e[k] * r * wb.e[k];
+                        a.e[k] = a.e[k] * r;
+                        b.e[k] = b.e[k] * r;
+                        if (weights) {
+                            a.e[k] = a.e[k] * ua.e[k];
+                            b.e[k] = b.e[k] * ub.e[k];
+                        }
                     }
                 }
-                if (turns) rope_apply<EPV, NEAR, BACK>(a, b, angle);
+                if (all_turn || turns) rope_apply<EPV, NEAR, BACK>(a, b, angle);
             } else {
-                if (turns) rope_apply<EPV, NEAR, true>(a, b, angle);
-                V x, y;
+                if (all_turn || turns) rope_apply<EPV, NEAR, true>(a, b, angle);
+                V x, y, ua, ub;
                 x.template widen<T, VB>(v.xa);
                 y.template widen<T, VB>(v.xb);
+                // what the weights multiply, beside what dw is summed from
+                ua = a;
+                ub = b;
+                if (weights) {
+                    V u;
+                    u.template widen<T, VB>(wa);
+#pragma unroll
+                    for (int k = 0; k < V::N; ++k) ua.e[k] = ua.e[k] * u.e[k];
+                    u.template widen<T, VB>(wb);
+#pragma unroll
+                    for (int k = 0; k < V::N; ++k) ub.e[k] = ub.e[k] * u.e[k];
+                }
                 L s2 = L::all(0.f), s1 = L::all(0.f);
 #pragma unroll
                 for (int k = 0; k < V::N; ++k) {
                     s2 = fma(y.e[k], y.e[k], fma(x.e[k], x.e[k], s2));
-                    s1 = fma(b.e[k] * wb.e[k], y.e[k], fma(a.e[k] * wa.e[k], x.e[k], s1));
+                    s1 = fma(ub.e[k], y.e[k], fma(ua.e[k], x.e[k], s1));
                 }
                 float ss = group_allreduce_sum(s2.total(), lanes);
                 const float dot = group_allreduce_sum(s1.total(), lanes);
@@ -256,21 +299,21 @@ __global__ void __launch_bounds__(32 * kRopeVecWarps, rope_ctas(KIND)) rope_vec_
                 // zeros is infinite with eps = 0
                 if (!here) ss = 1.f;
                 const float rstd = rsqrtf(fmaf(ss, p.inv_dim, p.eps));
-                const L r = L::all(rstd), minus = L::all(-(dot * p.inv_dim * rstd) * rstd);
+                const L r = L::all(rstd), less = L::all(-(dot * p.inv_dim * rstd) * rstd);
 #pragma unroll
                 for (int k = 0; k < V::N; ++k) {
                     da.e[k] = fma(a.e[k], x.e[k] * r, da.e[k]);
                     db.e[k] = fma(b.e[k], y.e[k] * r, db.e[k]);
-                    a.e[k] = fma(x.e[k], minus, a.e[k] * wa.e[k]) * r;
-                    b.e[k] = fma(y.e[k], minus, b.e[k] * wb.e[k]) * r;
+                    a.e[k] = fma(x.e[k], less, ua.e[k]) * r;
+                    b.e[k] = fma(y.e[k], less, ub.e[k]) * r;
                 }
             }
-            T* to = dst + head * t.out.head;
             float f[EPV];
             a.put(f);
-            if (here && on) st_stream<VB>(to + ja, pack<T, VB>(f));
+            if (here && on) st_stream<VB>(dst, pack<T, VB>(f));
             b.put(f);
-            if (here && on_b) st_stream<VB>(to + jb, pack<T, VB>(f));
+            if (here && on_b) st_stream<VB>(dst + ab, pack<T, VB>(f));
+            dst += out_step;
         }
     }
     if constexpr (GRAD) {

@@ -73,7 +73,7 @@ rmsnorm_status_t freqs_of(const rmsnorm_rope_rule_t* r, uint64_t* freqs, float* 
 // ---------------------------------------------------------------------- checks --
 
 constexpr int64_t kMaxItems = 1ll << 40;
-constexpr int64_t kAngleRounds = 4;     // rounds of heads that a token's angles cost
+constexpr int64_t kAngleRounds = 2;     // rounds of heads that a token's angles cost
 
 struct RopeCall {
     int dtype = 0;
@@ -329,27 +329,39 @@ rmsnorm_status_t launch_vec(RopeCall* c, bool interleaved, int kind, bool* done,
     p.units = static_cast<int32_t>(div_up(p.dim / epv, 2));
     if (p.units > 32) return RMSNORM_OK;
     p.lanes = pow2_ceil(p.units);
-    RopeFn fn = kind == kRopeTurn ? rope_vec_ptr_turn(c->dtype, vb, interleaved)
-                : kind == kRopeTurnBack ? rope_vec_ptr_back(c->dtype, vb, interleaved)
-                                        : rope_vec_ptr_grad(c->dtype, vb, interleaved);
+    const int whole = p.lanes == p.units && p.dim / epv == 2 * p.units ? p.lanes : 0;
+    RopeFn fn;
+    if (c->dtype == RMSNORM_DTYPE_F32)
+        fn = kind == kRopeTurn ? rope_vec_f32_turn(vb, interleaved, whole)
+             : kind == kRopeTurnBack ? rope_vec_f32_back(vb, interleaved, whole)
+                                     : rope_vec_f32_grad(vb, interleaved, whole);
+    else
+        fn = kind == kRopeTurn ? rope_vec_bf16_turn(vb, interleaved, whole)
+             : kind == kRopeTurnBack ? rope_vec_bf16_back(vb, interleaved, whole)
+                                     : rope_vec_bf16_grad(vb, interleaved, whole);
     int occ = 0;
     if (cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(fn), 32 * kRopeVecWarps, 0,
                          1, &occ) != cudaSuccess)
         return RMSNORM_ERR_CUDA;
     const int64_t most = c->dv.sms * (occ < kVecCtasPerSm ? occ : kVecCtasPerSm);
     // A token's heads are shared by as many warps as it takes to have a warp for each of
-    // the GPU's warp slots, of one round of heads at least.
+    // the GPU's warp slots, of one round of heads at least; fewer heads than a warp has lane
+    // groups leave groups for other tokens.
     const int groups = 32 / p.lanes;
     int64_t want[2] = {0, 0}, cost[2] = {0, 0};
     for (int i = 0; i < 2; ++i) {
-        p.split[i] = 1;
+        p.split[i] = p.share[i] = 1;
         if (!p.t[i].heads) continue;
-        const int64_t rounds = div_up(p.t[i].heads, groups);
-        int64_t split = div_up(most * kRopeVecWarps, p.tokens);
+        const int64_t share = pow2_ceil(p.t[i].heads < groups ? p.t[i].heads : groups);
+        const int64_t places = div_up(p.tokens, groups / share);
+        const int64_t rounds = div_up(p.t[i].heads, share);
+        int64_t split = div_up(most * kRopeVecWarps, places);
         if (split > rounds) split = rounds;
         p.split[i] = static_cast<int32_t>(split);
-        want[i] = div_up(p.tokens * split, kRopeVecWarps);
-        cost[i] = rounds + kAngleRounds;
+        p.share[i] = static_cast<int32_t>(share);
+        want[i] = div_up(places * split, kRopeVecWarps);
+        // what a token's heads cost, and its angles
+        cost[i] = (rounds + kAngleRounds) * share;
     }
     int64_t q = want[0], k = want[1];
     if (q + k > most) {           // shares of what they cost

@@ -35,6 +35,7 @@ struct RopeParams {
     int32_t units;         // pairs of vectors per head, at most lanes
     int32_t q_ctas;        // CTAs that work on q, the others on k
     int32_t split[2];      // warps that share a token's heads of q, of k
+    int32_t share[2];      // lane groups of a warp that work on one token (a power of two)
     int32_t wide;          // positions are 64-bit
     int32_t dim;
     int32_t rot;
@@ -51,11 +52,14 @@ using RopeFn = void (*)(RopeParams);
 RopeFn rope_any_ptr(int dtype, bool interleaved, bool back);
 constexpr int kRopeAnyWarps = 4;
 // Heads in vectors of vb bytes, a few lanes per head: forward, backward without a norm, and
-// with one.
+// with one.  lanes: those of heads that are whole units for each of them, else 0.
 enum : int { kRopeTurn, kRopeTurnBack, kRopeGrad };
-RopeFn rope_vec_ptr_turn(int dtype, int vb, bool interleaved);
-RopeFn rope_vec_ptr_back(int dtype, int vb, bool interleaved);
-RopeFn rope_vec_ptr_grad(int dtype, int vb, bool interleaved);
+RopeFn rope_vec_f32_turn(int vb, bool interleaved, int lanes);
+RopeFn rope_vec_bf16_turn(int vb, bool interleaved, int lanes);
+RopeFn rope_vec_f32_back(int vb, bool interleaved, int lanes);
+RopeFn rope_vec_bf16_back(int vb, bool interleaved, int lanes);
+RopeFn rope_vec_f32_grad(int vb, bool interleaved, int lanes);
+RopeFn rope_vec_bf16_grad(int vb, bool interleaved, int lanes);
 constexpr int kRopeVecWarps = 4;
 // Sums of the parts: grid (columns / 32, 2).
 RopeFn rope_reduce_ptr();

@@ -1,27 +1,29 @@
-// rope_vec_pick.cuh -- instances of the vector kernel of one kind.
+// rope_vec_pick.cuh -- instances of the vector kernel of one type and kind.
 #pragma once
 #include "k_rope_vec.cuh"
 
 namespace rmsnorm {
 
+// Numbers of lanes of their own: heads of 64, 128 and 256 elements in bf16 vectors of 16
+// bytes, of 32 to 128 in fp32.
 template <typename T, int KIND, bool INTER>
-static RopeFn rope_pick_vec(int vb) {
+static RopeFn rope_pick_vec(int vb, int lanes) {
+    if (vb == 16 && lanes == 4) return rope_vec_kernel<T, 16, INTER, KIND, 4>;
+    if (vb == 16 && lanes == 8) return rope_vec_kernel<T, 16, INTER, KIND, 8>;
+    if (vb == 16 && lanes == 16) return rope_vec_kernel<T, 16, INTER, KIND, 16>;
     switch (vb) {
-        case 16: return rope_vec_kernel<T, 16, INTER, KIND>;
-        case 8: return rope_vec_kernel<T, 8, INTER, KIND>;
-        case 4: return rope_vec_kernel<T, 4, INTER, KIND>;
+        case 16: return rope_vec_kernel<T, 16, INTER, KIND, 0>;
+        case 8: return rope_vec_kernel<T, 8, INTER, KIND, 0>;
+        case 4: return rope_vec_kernel<T, 4, INTER, KIND, 0>;
         default:
-            if constexpr (sizeof(T) == 2) return rope_vec_kernel<T, 2, INTER, KIND>;
+            if constexpr (sizeof(T) == 2) return rope_vec_kernel<T, 2, INTER, KIND, 0>;
             return nullptr;
     }
 }
 
-template <int KIND>
-static RopeFn rope_pick_vec_all(int dtype, int vb, bool interleaved) {
-    if (dtype == 0)
-        return interleaved ? rope_pick_vec<float, KIND, true>(vb) : rope_pick_vec<float, KIND, false>(vb);
-    return interleaved ? rope_pick_vec<__nv_bfloat16, KIND, true>(vb)
-                       : rope_pick_vec<__nv_bfloat16, KIND, false>(vb);
+template <typename T, int KIND>
+static RopeFn rope_pick_vec_all(int vb, bool interleaved, int lanes) {
+    return interleaved ? rope_pick_vec<T, KIND, true>(vb, lanes) : rope_pick_vec<T, KIND, false>(vb, lanes);
 }
 
 }  // namespace rmsnorm
