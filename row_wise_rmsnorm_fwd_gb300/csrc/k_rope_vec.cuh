@@ -1,8 +1,9 @@
 // k_rope_vec.cuh -- rotary positions with head norms, heads in vectors.
 //
-// A head is taken as units of two vectors of EPV elements: where it is turned, the unit
-// holds EPV whole pairs (vectors i and i + rot/2, or two neighbours if interleaved), behind
-// that two neighbours.  `lanes` lanes (a power of two) share a head, a unit each, so a
+// A head is taken as units of two vectors of EPV elements, half of the turned part apart, so
+// that the unit holds EPV whole pairs (interleaved: each vector half of them; vectors of
+// one element: neighbours), and behind that half of the rest apart: neighbouring lanes have
+// neighbouring vectors, so that no sector of memory is asked for twice.  `lanes` lanes (a power of two) share a head, a unit each, so a
 // warp has 32 / lanes heads at a time: of one token, or, where a token has fewer, of
 // several.  It walks over its tokens' heads, and its lanes keep the cosines and sines of their
 // pairs for all of them: an angle is formed once for a warp's share of a token's heads, by
@@ -134,8 +135,40 @@ __device__ __forceinline__ void rope_apply(RopeVec<EPV>& a, RopeVec<EPV>& b, con
     }
 }
 
-// Registers: enough CTAs to an SM for the loads under way to cover HBM's latency.
-constexpr int rope_ctas(int kind) { return kind == kRopeGrad ? 4 : 6; }
+// A lane's own vectors of the heads to come, in shared memory: copied there without passing
+// through registers, kRopeStages rounds of heads ahead of the one at work and across tokens.
+// Nothing is shared among threads, so a thread waits for its own copies and no barrier is
+// needed.  Vectors of 2 bytes, which such copies cannot move, are read when their turn comes.
+constexpr int kRopeStages = 3;
+
+template <int VB>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool yes) {
+    const uint32_t n = yes ? VB : 0;            // what is not read is filled with zeros
+    if constexpr (VB == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(to), "l"(from), "r"(n) : "memory");
+    else if constexpr (VB == 8)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" :: "r"(to), "l"(from), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(to), "l"(from), "r"(n) : "memory");
+}
+
+template <int VB>
+__device__ __forceinline__ Vec<VB> staged_vec(uint32_t at) {
+    Vec<VB> v;
+    if constexpr (VB == 16)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3]) : "r"(at) : "memory");
+    else if constexpr (VB == 8)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.u[0]), "=r"(v.u[1]) : "r"(at) : "memory");
+    else
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v.u[0]) : "r"(at) : "memory");
+    return v;
+}
+
+// CTAs to an SM that the registers have to allow: more of them spill.  Measured (us, bf16
+// 65536 tokens, 32 + 8 heads of 128): forward 4 / 5 / 6 CTAs and 4 slots 228 / 230 / 245, 3
+// slots and 5 CTAs 224; with the norm's gradient 3 / 4 CTAs 314 / 335, 3 slots 316 / 318.
+constexpr int rope_ctas(int kind) { return kind == kRopeGrad ? 3 : 4; }
 
 // LANES > 0: that many lanes to a head, each with a whole unit; 0: p.lanes, of which some may
 // have none or half of one.
@@ -144,9 +177,13 @@ __global__ void __launch_bounds__(32 * kRopeVecWarps, rope_ctas(KIND)) rope_vec_
     constexpr int EPV = VecTraits<T, VB>::kElems;
     constexpr bool NEAR = INTER && EPV > 1;
     constexpr bool GRAD = KIND == kRopeGrad, BACK = KIND != kRopeTurn;
+    constexpr int VECS = GRAD ? 4 : 2, THREADS = 32 * kRopeVecWarps;
+    constexpr bool ASYNC = VB > 2;
+    constexpr int STAGE = VECS * THREADS * VB, SUMS = GRAD ? kRopeVecWarps * 64 * EPV * 4 : 0;
     using V = RopeVec<EPV>;
     using L = typename V::L;
-    __shared__ float sums[GRAD ? kRopeVecWarps : 1][GRAD ? 64 * EPV : 1];
+    constexpr int STAGED = ASYNC ? kRopeStages * STAGE : 16;
+    __shared__ alignas(16) unsigned char smem[STAGED > SUMS ? STAGED : SUMS];
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int which = static_cast<int>(blockIdx.x) >= p.q_ctas;
@@ -163,16 +200,17 @@ __global__ void __launch_bounds__(32 * kRopeVecWarps, rope_ctas(KIND)) rope_vec_
     const bool on = LANES || l < p.units, turns = l < turned;
     int ja, jb;                                     // first columns of the two vectors
     if (turns) {
-        ja = INTER ? 2 * l * EPV : l * EPV;
-        jb = INTER ? ja + EPV : ja + half;
+        ja = INTER && !NEAR ? 2 * l : l * EPV;
+        jb = INTER && !NEAR ? ja + 1 : ja + half;
     } else {
-        ja = p.rot + 2 * (l - turned) * EPV;
-        jb = ja + EPV;
+        ja = p.rot + (l - turned) * EPV;
+        jb = ja + (p.units - turned) * EPV;
     }
     const bool on_b = LANES || (on && jb < p.dim);
     // numbers of the two halves of the unit's pairs; lanes that turn nothing take any
     const int unit = turns ? l : 0;
-    const int first_pair = unit * EPV, second_pair = first_pair + EPV / 2;
+    const int first_pair = NEAR ? unit * EPV / 2 : unit * EPV;
+    const int second_pair = first_pair + (NEAR ? half / 2 : EPV / 2);
     const bool all_turn = turned >= lanes;
     auto load = [&](const T* at, bool yes) {
         Vec<VB> v;
@@ -195,46 +233,100 @@ __global__ void __launch_bounds__(32 * kRopeVecWarps, rope_ctas(KIND)) rope_vec_
 #pragma unroll
     for (int k = 0; k < V::N; ++k) da.e[k] = db.e[k] = L::all(0.f);
 
-    // What a lane reads of a head, the next one under way while one is worked on.
-    struct Loads {
-        Vec<VB> a, b, xa, xb;
-    };
     const int heads = t.heads, split = p.split[which];
     const int step = split * share;
     const int ab = jb - ja;
     const RopeView& from = BACK ? t.dy : t.x;
     const int64_t src_step = step * from.head, x_step = GRAD ? step * t.x.head : 0, out_step = step * t.out.head;
     const int64_t items = (p.tokens + tokens_per_warp - 1) / tokens_per_warp * split;
-    for (int64_t item = static_cast<int64_t>(cta) * kRopeVecWarps + warp; item < items;
-         item += static_cast<int64_t>(ctas) * kRopeVecWarps) {
-        const int64_t place = item / split;
+    const int64_t item_step = static_cast<int64_t>(ctas) * kRopeVecWarps;
+    const int64_t item0 = static_cast<int64_t>(cta) * kRopeVecWarps + warp;
+
+    // What is read: a round of heads of the warp's tokens at a time.
+    struct {
+        int64_t item;
+        const T *src, *xs;
+        int head, rest;              // the lane group's head, and heads from the warp's first on
+        bool there;
+    } ahead;
+    auto enter = [&](int64_t item) {
+        ahead.item = item;
+        if (item >= items) return;
+        const int64_t place = split == 1 ? item : rope_div(item, split);
+        const int64_t token = place * tokens_per_warp + token_of_warp;
+        ahead.there = token < p.tokens;
+        const int first = static_cast<int>(item - place * split) * share;
+        ahead.head = first + mine;
+        ahead.rest = heads - first;
+        const int64_t tok = ahead.there ? token : 0, b = rope_div(tok, p.seq), s = tok - b * p.seq;
+        ahead.src = static_cast<const T*>(from.p) + b * from.batch + s * from.token + ahead.head * from.head + ja;
+        if constexpr (GRAD)
+            ahead.xs = static_cast<const T*>(t.x.p) + b * t.x.batch + s * t.x.token + ahead.head * t.x.head + ja;
+    };
+    const uint32_t my_slot = smem_addr(smem) + threadIdx.x * VB;
+    auto fetch = [&](int stage) {                    // the next round into `stage`
+        if (ahead.item < items) {
+            const bool here = ahead.there && ahead.head < heads;
+            const uint32_t to = my_slot + stage * STAGE;
+            copy_async<VB>(to, ahead.src, here && on);
+            copy_async<VB>(to + THREADS * VB, ahead.src + ab, here && on_b);
+            ahead.src += src_step;
+            if constexpr (GRAD) {
+                copy_async<VB>(to + 2 * THREADS * VB, ahead.xs, here && on);
+                copy_async<VB>(to + 3 * THREADS * VB, ahead.xs + ab, here && on_b);
+                ahead.xs += x_step;
+            }
+            ahead.head += step;
+            ahead.rest -= step;
+            if (ahead.rest <= 0) enter(ahead.item + item_step);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    enter(item0);
+    if constexpr (ASYNC) {
+#pragma unroll
+        for (int k = 0; k < kRopeStages - 1; ++k) fetch(k);
+    }
+    int stage = 0;
+    for (int64_t item = item0; item < items; item += item_step) {
+        const int64_t place = split == 1 ? item : rope_div(item, split);
         const int64_t token = place * tokens_per_warp + token_of_warp;
         const bool there = token < p.tokens;
         const RopeToken tk(p, there ? token : 0);
         const int first = static_cast<int>(item - place * split) * share;
         int head = first + mine;
-        const T* src = static_cast<const T*>(from.p) + tk.at(from, head) + ja;
-        const T* xs = GRAD ? static_cast<const T*>(t.x.p) + tk.at(t.x, head) + ja : nullptr;
         T* dst = static_cast<T*>(t.out.p) + tk.at(t.out, head) + ja;
-        auto read = [&](bool here) {
-            Loads r;
-            r.a = load(src, here && on);
-            r.b = load(src + ab, here && on_b);
-            src += src_step;
-            if constexpr (GRAD) {
-                r.xa = load(xs, here && on);
-                r.xb = load(xs + ab, here && on_b);
-                xs += x_step;
-            }
-            return r;
-        };
-        Loads next = read(there && head < heads);
         RopeAngles<EPV> angle;
         rope_angles<EPV>(angle, p.freqs, first_pair, second_pair, tk.position, p.mscale, lanes, share, mine,
                          token_of_warp * share * lanes + l);
         for (int rest = heads - first; rest > 0; rest -= step, head += step) {
-            const Loads v = next;
             const bool here = there && head < heads;
+            struct {
+                Vec<VB> a, b, xa, xb;
+            } v;
+            if constexpr (ASYNC) {
+                asm volatile("cp.async.wait_group %0;" :: "n"(kRopeStages - 2) : "memory");
+                const uint32_t at = my_slot + stage * STAGE;
+                v.a = staged_vec<VB>(at);
+                v.b = staged_vec<VB>(at + THREADS * VB);
+                if constexpr (GRAD) {
+                    v.xa = staged_vec<VB>(at + 2 * THREADS * VB);
+                    v.xb = staged_vec<VB>(at + 3 * THREADS * VB);
+                }
+                // the slot that the round before this one was in
+                fetch(stage == 0 ? kRopeStages - 1 : stage - 1);
+                stage = stage == kRopeStages - 1 ? 0 : stage + 1;
+            } else {
+                v.a = load(ahead.src, here && on);
+                v.b = load(ahead.src + ab, here && on_b);
+                ahead.src += src_step;
+                if constexpr (GRAD) {
+                    v.xa = load(ahead.xs, here && on);
+                    v.xb = load(ahead.xs + ab, here && on_b);
+                    ahead.xs += x_step;
+                }
+                if (rest <= step) enter(item + item_step);
+            }
             // widened where they are used: widened once, they would be held so
             if constexpr (VB > 2) {
 #pragma unroll
@@ -243,7 +335,6 @@ __global__ void __launch_bounds__(32 * kRopeVecWarps, rope_ctas(KIND)) rope_vec_
                     opaque(wb.u[k]);
                 }
             }
-            if (rest > step) next = read(there && head + step < heads);
             V a, b;
             a.template widen<T, VB>(v.a);
             b.template widen<T, VB>(v.b);
@@ -319,6 +410,8 @@ __global__ void __launch_bounds__(32 * kRopeVecWarps, rope_ctas(KIND)) rope_vec_
     if constexpr (GRAD) {
         // the CTA's part: the warp's lane groups, then the warps, in order
         if (!t.dw) return;
+        float (*sums)[64 * EPV] = reinterpret_cast<float (*)[64 * EPV]>(smem);
+        __syncthreads();                             // every thread is done with its slots
         float fa[EPV], fb[EPV];
         da.put(fa);
         db.put(fb);
