@@ -86,12 +86,15 @@ rmsnorm_status_t rmsnorm_block_fwd_bf16(const uint16_t* x, const uint16_t* resid
                                         const rmsnorm_block_t* block, rmsnorm_stream_t stream);
 
 /* Either dtype, with options (`opt` may be NULL): opt->path RMSNORM_PATH_AUTO,
- * RMSNORM_PATH_STAGED (rows staged in shared memory by bulk copies, read from HBM once:
- * every array and row a multiple of 16 bytes on 16-byte boundaries, rows of at most 512
- * KB, backward 256 KB, split over a thread-block cluster above 32 KB, backward 16 KB;
- * else RMSNORM_ERR_UNSUPPORTED; opt->cluster = 2, 4, 8 or 16 forces that split) or
- * RMSNORM_PATH_TWOPASS (a CTA per row that reads it again for each sum: any width and
- * alignment); opt->wait_timeout_ns; and in the test build of the library
+ * RMSNORM_PATH_STAGED (rows staged in shared memory by bulk copies, read from HBM once: x and
+ * residual, backward dy, dh, x and h, on 16-byte boundaries; if rows, weights, gate and
+ * outputs are multiples of 16 bytes on such boundaries too, rows of at most 512 KB, backward
+ * 256 KB, split over a thread-block cluster above 32 KB, backward 16 KB, which
+ * opt->cluster = 2, 4, 8 or 16 forces; else rows of 16 bytes to 24 KB, backward to about 14;
+ * RMSNORM_ERR_UNSUPPORTED otherwise), RMSNORM_PATH_ROWREG (forward; rows of 8-byte vectors
+ * held in registers: what 8 is the widest vector for, rows of at most 32 KB; else
+ * RMSNORM_ERR_UNSUPPORTED) or RMSNORM_PATH_TWOPASS (a CTA per row that reads it again for each
+ * sum: any width and alignment); opt->wait_timeout_ns; and in the test build of the library
  * opt->fault_inject with RMSNORM_PATH_STAGED: 1 = each CTA's first copy is withheld, 2 =
  * with opt->cluster, rank 0's first sums are (elsewhere RMSNORM_ERR_UNSUPPORTED).  Every other
  * field but epilogue_alpha, which is not read, must be zero, else RMSNORM_ERR_INVALID_ARG. */
@@ -121,7 +124,8 @@ rmsnorm_status_t rmsnorm_block_bwd_bf16(const uint16_t* dy, const uint16_t* dh, 
                                         void* workspace, size_t workspace_bytes,
                                         rmsnorm_stream_t stream);
 
-/* Either dtype, with options as for rmsnorm_block_fwd_ex (RMSNORM_PATH_TWOPASS: the
+/* Either dtype, with options as for rmsnorm_block_fwd_ex (no RMSNORM_PATH_ROWREG;
+ * RMSNORM_PATH_TWOPASS: the
  * sums of each row, then the outputs and partial column sums, each reading the arrays
  * once: any width and alignment). */
 rmsnorm_status_t rmsnorm_block_bwd_ex(int32_t dtype, const void* dy, const void* dh, const void* x,

@@ -1081,7 +1081,7 @@ def rmsnorm_block_fwd_ex(x, residual, post_w=None, pre_w=None, gate=None, h=None
                          post_norm: bool = True, pre_norm: bool = True,
                          residual_scale: float = 1.0, branch_scale: float = 1.0,
                          post_eps: float = 1e-6, pre_eps: float = 1e-6, options=None, stream=None):
-    """Either dtype, with options (path auto or twopass)."""
+    """Either dtype, with options (path auto, staged, rowreg or twopass)."""
     return _block_fwd("rmsnorm_block_fwd_ex", None, x, residual, post_w, pre_w, gate, h, y,
                       post_norm, pre_norm, residual_scale, branch_scale, post_eps, pre_eps,
                       options, stream)
@@ -1212,7 +1212,7 @@ def rmsnorm_block_bwd_ex(dy, dh, x, h, post_w=None, pre_w=None, gate=None, dx=No
                          residual_scale: float = 1.0, branch_scale: float = 1.0,
                          post_eps: float = 1e-6, pre_eps: float = 1e-6,
                          weight_grads: bool = True, workspace=None, options=None, stream=None):
-    """Either dtype, with options (path auto or twopass)."""
+    """Either dtype, with options (path auto, staged or twopass)."""
     return _block_bwd("rmsnorm_block_bwd_ex", None, dy, dh, x, h, post_w, pre_w, gate, dx,
                       dresidual, dpost_w, dpre_w, dgate, post_norm, pre_norm, residual_scale,
                       branch_scale, post_eps, pre_eps, weight_grads, workspace, options, stream)

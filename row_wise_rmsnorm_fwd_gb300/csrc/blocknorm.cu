@@ -37,6 +37,9 @@ static BlockFn pick_reduce(int width, bool gates) {
 }
 
 BlockFn blocknorm_fwd_any_ptr(int dtype, int vb) { return pick_all(dtype, vb, kFwd); }
+BlockFn blocknorm_fwd_regs_ptr(int dtype) {
+    return dtype == 0 ? blocknorm_fwd_regs_kernel<float> : blocknorm_fwd_regs_kernel<__nv_bfloat16>;
+}
 BlockFn blocknorm_bwd_rows_ptr(int dtype, int vb) { return pick_all(dtype, vb, kRows); }
 BlockFn blocknorm_bwd_cols_ptr(int dtype, int vb) { return pick_all(dtype, vb, kCols); }
 BlockFn blocknorm_reduce_ptr(int dtype, int width, bool gates) {

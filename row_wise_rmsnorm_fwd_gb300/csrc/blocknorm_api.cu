@@ -46,7 +46,7 @@ rmsnorm_status_t check_shape(int32_t dtype, int64_t rows, int64_t hidden, const 
 }
 
 // The rule and the options, once the shape is known to be good.
-rmsnorm_status_t check_rule(const rmsnorm_block_t& b, const rmsnorm_options_t* opt, BlockCall* c) {
+rmsnorm_status_t check_rule(const rmsnorm_block_t& b, const rmsnorm_options_t* opt, bool back, BlockCall* c) {
     if (b.post_norm < 0 || b.post_norm > 1 || b.pre_norm < 0 || b.pre_norm > 1 ||
         !std::isfinite(b.residual_scale) || !std::isfinite(b.branch_scale) ||
         !std::isfinite(b.post_eps) || b.post_eps < 0.f || !std::isfinite(b.pre_eps) || b.pre_eps < 0.f)
@@ -70,7 +70,8 @@ rmsnorm_status_t check_rule(const rmsnorm_block_t& b, const rmsnorm_options_t* o
         o.vec_bytes || o.chunk_bytes || o.stages || o.weights || o.reserved || o.epilogue ||
         o.fault_inject < 0 || o.fault_inject > 2)
         return RMSNORM_ERR_INVALID_ARG;
-    if (o.path != RMSNORM_PATH_AUTO && o.path != RMSNORM_PATH_STAGED && o.path != RMSNORM_PATH_TWOPASS)
+    if (o.path != RMSNORM_PATH_AUTO && o.path != RMSNORM_PATH_STAGED && o.path != RMSNORM_PATH_TWOPASS &&
+        !(o.path == RMSNORM_PATH_ROWREG && !back))
         return RMSNORM_ERR_INVALID_ARG;
     if (o.cluster && o.path != RMSNORM_PATH_STAGED) return RMSNORM_ERR_INVALID_ARG;
     if (o.fault_inject && (!RMSNORM_FAULT_INJECT || o.path != RMSNORM_PATH_STAGED ||
@@ -109,23 +110,31 @@ int64_t group_of(int64_t nvec) {
 }
 
 BlockFn staged_ptr(const BlockVariant& v) {
+    if (v.vb < 16) {
+        if (v.dtype == RMSNORM_DTYPE_F32) return v.back ? blocknorm_bwd_ragged_f32(v) : blocknorm_fwd_ragged_f32(v);
+        return v.back ? blocknorm_bwd_ragged_bf16(v) : blocknorm_fwd_ragged_bf16(v);
+    }
     if (v.dtype == RMSNORM_DTYPE_F32) return v.back ? blocknorm_bwd_staged_f32(v) : blocknorm_fwd_staged_f32(v);
     return v.back ? blocknorm_bwd_staged_bf16(v) : blocknorm_fwd_staged_bf16(v);
 }
 
-// Rows staged in shared memory.  bits: of the addresses of the arrays, weights and gate;
-// narr: arrays with a place in a slot.  Leaves s->grid 0, status OK, where rows cannot be
-// staged.
-rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t address_bits, int narr, bool back, LaunchShape* s,
-                             BlockFn* fn) {
+// Rows staged in shared memory.  read_bits: of the addresses of the arrays that are staged;
+// other_bits: of the outputs, weights and gate; narr: arrays with a place in a slot.  Leaves
+// s->grid 0, status OK, where rows cannot be staged.
+rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t read_bits, uintptr_t other_bits, int narr, bool back,
+                             LaunchShape* s, BlockFn* fn) {
     BlockParams& p = c->p;
     const int64_t row_bytes = static_cast<int64_t>(p.hidden) * c->sz;
     s->grid = 0;
-    if (address_bits % 16 || row_bytes % 16) return RMSNORM_OK;
-    const int64_t nvec = row_bytes / 16;
-    const int64_t max_threads = back ? kBlockBwdMaxThreads : kBlockFwdMaxThreads;
+    if (read_bits % 16) return RMSNORM_OK;
+    const int vb = widest_vector(other_bits, row_bytes, c->sz);
+    // what lies behind a ragged array's last boundary has to be within its last row
+    if (vb < 16 && (c->cluster > 1 || row_bytes < 16)) return RMSNORM_OK;
+    const int64_t nvec = div_up(row_bytes, 16);
+    const int64_t max_threads = back ? kBlockBwdMaxThreads
+                                : vb < 16 ? kBlockFwdRaggedMaxThreads : kBlockFwdMaxThreads;
     const int64_t budget = c->dv.smem_optin - 6 * 1024;             // static shared memory beside it
-    for (int64_t cluster = c->cluster ? c->cluster : 1; cluster <= kMaxCluster; cluster *= 2) {
+    for (int64_t cluster = c->cluster ? c->cluster : 1; cluster <= (vb < 16 ? 1 : kMaxCluster); cluster *= 2) {
         const int64_t slice = div_up(nvec, cluster);
         // a split row's CTA is one group of whole warps, with a thread for each rank to send to
         const int64_t narrow = group_of(slice), group = cluster > 1 && narrow < 32 ? 32 : narrow;
@@ -139,11 +148,13 @@ rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t address_bits, int narr, boo
                    (div_up(p.rows, rows) < c->dv.sms || rows / 2 >= p.gate_rows))
                 rows /= 2;
             const int block = static_cast<int>(rows * group);
-            const int64_t slot = narr * rows * slice * 16;
+            // a ragged row's window starts less than 16 bytes before it
+            const int64_t row_slot = vb < 16 ? div_up(row_bytes + 16 - vb, 16) * 16 : slice * 16;
+            const int64_t slot = narr * rows * row_slot;
             const int64_t scratch = back && rows > 1 ? rows * row_bytes * 4 / c->sz : 0;
-            const bool whole = nvec == cluster * group * (kBlockStagedBytes / 16) && (!p.post || p.post_w) &&
+            const bool whole = vb == 16 && nvec == cluster * group * (kBlockStagedBytes / 16) && (!p.post || p.post_w) &&
                                (!p.pre || p.pre_w) && (p.post || p.pre);
-            *fn = staged_ptr({c->dtype, back, p.post != 0, p.pre != 0, cluster > 1, whole, p.gate != nullptr});
+            *fn = staged_ptr({c->dtype, vb, back, p.post != 0, p.pre != 0, cluster > 1, whole, p.gate != nullptr});
             int best = 0;
             for (int64_t slots = 3; slots >= 2; --slots) {
                 const int64_t smem = slots * slot + scratch;
@@ -165,6 +176,7 @@ rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t address_bits, int narr, boo
                 p.group = static_cast<int32_t>(group);
                 p.cluster = static_cast<int32_t>(cluster);
                 p.slice_vecs = static_cast<int32_t>(slice);
+                p.row_slot = static_cast<int32_t>(row_slot);
                 p.status = c->dv.status;
                 if (!p.timeout_ns) p.timeout_ns = kDefaultTimeoutNs;
                 if (back && best > kBwdCtasPerSm && cluster == 1) best = kBwdCtasPerSm;
@@ -184,6 +196,25 @@ rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t address_bits, int narr, boo
 
 // ------------------------------------------------------------------- forward --
 
+constexpr int64_t kRegsRowBytes = 1024;       // narrower rows would leave a CTA few threads
+
+// Rows of 8-byte vectors held in registers, a CTA to a row.  Leaves s->grid 0, status OK, where
+// rows are of other vectors or a CTA cannot hold one.
+rmsnorm_status_t plan_regs(BlockCall* c, int vb, LaunchShape* s, BlockFn* fn) {
+    s->grid = 0;
+    const int64_t block = div_up(div_up(c->p.nvec, kBlockRegsVecs), 32) * 32;
+    if (vb != 8 || block > kBlockRegsMaxThreads) return RMSNORM_OK;
+    *fn = blocknorm_fwd_regs_ptr(c->dtype);
+    int occ = 0;
+    if (cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(*fn),
+                         static_cast<int>(block), 0, 1, &occ) != cudaSuccess)
+        return RMSNORM_ERR_CUDA;
+    if (occ < 1) return RMSNORM_OK;
+    s->grid = at_most(c->p.rows, static_cast<int64_t>(c->dv.sms) * occ);
+    s->block = static_cast<int>(block);
+    return RMSNORM_OK;
+}
+
 rmsnorm_status_t fwd_run(int32_t dtype, const void* x, const void* residual, void* h, void* y,
                          int64_t rows, int64_t hidden, const rmsnorm_block_t* b,
                          const rmsnorm_options_t* opt, cudaStream_t stream) {
@@ -191,7 +222,7 @@ rmsnorm_status_t fwd_run(int32_t dtype, const void* x, const void* residual, voi
     rmsnorm_status_t st = check_shape(dtype, rows, hidden, b, &c);
     if (st != RMSNORM_OK) return st;
     if (!x || !residual || !h) return RMSNORM_ERR_INVALID_ARG;
-    st = check_rule(*b, opt, &c);
+    st = check_rule(*b, opt, false, &c);
     if (st != RMSNORM_OK) return st;
     const uintptr_t sz = static_cast<uintptr_t>(c.sz);
     if ((c.p.pre != 0) != (y != nullptr) || !aligned(x, sz) || !aligned(residual, sz) ||
@@ -208,18 +239,26 @@ rmsnorm_status_t fwd_run(int32_t dtype, const void* x, const void* residual, voi
     c.p.residual = residual;
     c.p.h = h;
     c.p.y = y;
-    const uintptr_t all = bits(x) | bits(residual) | bits(h) | bits(y) | bits(c.p.post_w) |
-                          bits(c.p.pre_w) | bits(c.p.gate);
+    const uintptr_t read = bits(x) | bits(residual);
+    const uintptr_t other = bits(h) | bits(y) | bits(c.p.post_w) | bits(c.p.pre_w) | bits(c.p.gate);
+    const int vb = widest_vector(read | other, hidden * c.sz, c.sz);
+    c.p.nvec = static_cast<int32_t>(hidden / (vb / c.sz));
+    if (c.path == RMSNORM_PATH_ROWREG || (c.path == RMSNORM_PATH_AUTO && vb == 8 && hidden * c.sz >= kRegsRowBytes)) {
+        LaunchShape s{0, 0, 1, 0};
+        BlockFn fn = nullptr;
+        st = plan_regs(&c, vb, &s, &fn);
+        if (st != RMSNORM_OK) return st;
+        if (s.grid) return launch(c, fn, s, stream);
+        if (c.path == RMSNORM_PATH_ROWREG) return RMSNORM_ERR_UNSUPPORTED;
+    }
     if (c.path != RMSNORM_PATH_TWOPASS) {
         LaunchShape s{0, 0, 1, 0};
         BlockFn fn = nullptr;
-        st = plan_staged(&c, all, 2, false, &s, &fn);
+        st = plan_staged(&c, read, other, 2, false, &s, &fn);
         if (st != RMSNORM_OK) return st;
         if (s.grid) return launch(c, fn, s, stream);
         if (c.path == RMSNORM_PATH_STAGED) return RMSNORM_ERR_UNSUPPORTED;
     }
-    const int vb = widest_vector(all, hidden * c.sz, c.sz);
-    c.p.nvec = static_cast<int32_t>(hidden / (vb / c.sz));
     const LaunchShape s{at_most(rows, 8ll * c.dv.sms), blocknorm_rows_block(), 1, 0};
     return launch(c, blocknorm_fwd_any_ptr(dtype, vb), s, stream);
 }
@@ -296,7 +335,7 @@ rmsnorm_status_t bwd_run(int32_t dtype, const void* dy, const void* dh, const vo
     rmsnorm_status_t st = check_shape(dtype, rows, hidden, b, &c);
     if (st != RMSNORM_OK) return st;
     if (!x || !dx || !dres) return RMSNORM_ERR_INVALID_ARG;
-    st = check_rule(*b, opt, &c);
+    st = check_rule(*b, opt, true, &c);
     if (st != RMSNORM_OK) return st;
     if (c.p.pre ? !dy || !h : dy != nullptr) return RMSNORM_ERR_INVALID_ARG;
     if ((dpost_w && !c.p.post) || (dpre_w && !c.p.pre) || (dgate && !b->gate))
@@ -342,12 +381,12 @@ rmsnorm_status_t bwd_run(int32_t dtype, const void* dy, const void* dh, const vo
     p.part_pre = dpre_w ? reinterpret_cast<float*>(base + ws.part_pre) : nullptr;
     p.part_gate = dpost_w || dgate ? reinterpret_cast<float*>(base + ws.part_gate) : nullptr;
     p.gate_sums = dpost_w && p.gates > 1 ? reinterpret_cast<float*>(base + ws.gate_sums) : nullptr;
-    const uintptr_t all = bits(dy) | bits(dh) | bits(x) | bits(h) | bits(dx) | bits(dres) |
-                          bits(p.post_w) | bits(p.pre_w) | bits(p.gate);
+    const uintptr_t read = bits(dy) | bits(dh) | bits(x) | bits(h);
+    const uintptr_t other = bits(dx) | bits(dres) | bits(p.post_w) | bits(p.pre_w) | bits(p.gate);
     if (c.path != RMSNORM_PATH_TWOPASS) {
         LaunchShape s{0, 0, 1, 0};
         BlockFn fn = nullptr;
-        st = plan_staged(&c, all, p.pre ? 4 : 2, true, &s, &fn);
+        st = plan_staged(&c, read, other, p.pre ? 4 : 2, true, &s, &fn);
         if (st != RMSNORM_OK) return st;
         if (s.grid) {
             p.pre_parts = static_cast<int32_t>(p.units);
@@ -360,7 +399,7 @@ rmsnorm_status_t bwd_run(int32_t dtype, const void* dy, const void* dh, const vo
     p.parts = ws.parts;
     p.rows_per_part = div_up(p.gate_rows, ws.parts_per_gate);
     p.pre_parts = static_cast<int32_t>(ws.grid_parts);
-    const int vb = widest_vector(all, hidden * c.sz, c.sz);
+    const int vb = widest_vector(read | other, hidden * c.sz, c.sz);
     p.nvec = static_cast<int32_t>(hidden / (vb / c.sz));
     const LaunchShape rs{at_most(rows, 8ll * c.dv.sms), blocknorm_rows_block(), 1, 0};
     st = launch(c, blocknorm_bwd_rows_ptr(dtype, vb), rs, stream);

@@ -45,6 +45,7 @@ struct BlockParams {
     int32_t cluster;       // CTAs per row
     int32_t slice_vecs;    // vectors of a CTA's slice of a row
     int32_t nslots;        // ring slots
+    int32_t row_slot;      // ragged rows: bytes of a row in a slot
     int32_t fault;         // failure-detection test builds only (else always 0)
     unsigned* status;
     uint64_t timeout_ns;
@@ -61,6 +62,10 @@ using BlockFn = void (*)(BlockParams);
 
 // dtype: 0 = fp32, 1 = bf16; vb = bytes per vector.  Any width.
 BlockFn blocknorm_fwd_any_ptr(int dtype, int vb);
+// Rows of 8-byte vectors, kBlockRegsVecs to a thread.
+BlockFn blocknorm_fwd_regs_ptr(int dtype);
+constexpr int kBlockRegsVecs = 4;
+constexpr int kBlockRegsMaxThreads = 1024;
 BlockFn blocknorm_bwd_rows_ptr(int dtype, int vb);
 BlockFn blocknorm_bwd_cols_ptr(int dtype, int vb);
 int blocknorm_rows_block();
@@ -73,14 +78,20 @@ BlockFn blocknorm_reduce_ptr(int dtype, int width, bool gates);
 // the norms (one at least), and a gate as `gate` says.
 struct BlockVariant {
     int dtype;
+    int vb;               // bytes of a vector; less than 16: ragged rows
     bool back, post, pre, cluster, whole, gate;
 };
 BlockFn blocknorm_fwd_staged_f32(const BlockVariant& v);
 BlockFn blocknorm_fwd_staged_bf16(const BlockVariant& v);
 BlockFn blocknorm_bwd_staged_f32(const BlockVariant& v);
 BlockFn blocknorm_bwd_staged_bf16(const BlockVariant& v);
+BlockFn blocknorm_fwd_ragged_f32(const BlockVariant& v);
+BlockFn blocknorm_fwd_ragged_bf16(const BlockVariant& v);
+BlockFn blocknorm_bwd_ragged_f32(const BlockVariant& v);
+BlockFn blocknorm_bwd_ragged_bf16(const BlockVariant& v);
 constexpr int kBlockStagedBytes = 32;       // bytes of a row to a thread
 constexpr int kBlockFwdMaxThreads = 1024;
+constexpr int kBlockFwdRaggedMaxThreads = 768;   // their pieces take more registers
 constexpr int kBlockBwdMaxThreads = 512;
 constexpr int kBlockReduceThreads = 256;
 constexpr int kBlockReduceCols = 8;

@@ -114,6 +114,85 @@ __global__ void __launch_bounds__(kBlockRowsThreads) blocknorm_fwd_any_kernel(co
     }
 }
 
+// Forward, rows of 8-byte vectors that are wide enough for a CTA of their own: as above, but
+// the row is held in registers, kBlockRegsVecs vectors to a thread, and read once.  Measured
+// (us, this / the kernel above / staged in pieces, k_blocknorm_staged.cuh): fp32 32768 x 2050
+// 218 / 225 / 261, 65536 x 514 110 / 238 / 148, 2555 x 2050 21.4 / 24.5 / 24.4, bf16 32768 x
+// 4100 257 / 296 / 292.  With vectors of 4 and 2 bytes the pieces win: bf16 65536 x 2050 376 /
+// 427 / 338, 65536 x 1027 288 / 334 / 262, fp32 65536 x 1027 315 / 302 / 304.
+template <typename T>
+__global__ void __launch_bounds__(kBlockRegsMaxThreads, 1) blocknorm_fwd_regs_kernel(const BlockParams p) {
+    constexpr int VB = 8, EPV = VecTraits<T, VB>::kElems, NV = kBlockRegsVecs;
+    __shared__ float red[2][2][32];
+    pdl_trigger();
+    pdl_wait();
+    const int64_t row_bytes = static_cast<int64_t>(p.hidden) * sizeof(T);
+    const int n = static_cast<int>(blockDim.x);
+    const int count = (p.nvec - static_cast<int>(threadIdx.x) + n - 1) / n;      // vectors of this thread
+    const int64_t mine = static_cast<int64_t>(threadIdx.x) * VB;
+    const int apart = n * VB;
+    int it = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, it ^= 1) {
+        const char* xs = static_cast<const char*>(p.x) + row * row_bytes + mine;
+        const char* rs = static_cast<const char*>(p.residual) + row * row_bytes + mine;
+        const char* gate = at_or_null(p.gate, row / p.gate_rows * row_bytes + mine);
+        const char* post_w = at_or_null(p.post ? p.post_w : nullptr, mine);
+        const char* pre_w = at_or_null(p.pre_w, mine);
+        Vec<VB> x[NV], r[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (i < count) {
+                x[i] = ld_stream<VB>(xs + i * apart);
+                r[i] = ld_stream<VB>(rs + i * apart);
+            }
+        }
+        float scale = p.branch_scale;
+        if (p.post) {
+            float s[1] = {0.f};
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (i < count) {
+#pragma unroll
+                    for (int k = 0; k < EPV; ++k) s[0] = fmaf(get<T, VB>(x[i], k), get<T, VB>(x[i], k), s[0]);
+                }
+            }
+            block_sums<1>(s, red[it][0]);
+            scale *= rsqrtf(fmaf(s[0], p.inv_hidden, p.post_eps));
+        }
+        float h[NV][EPV];
+        float s[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (i < count) {
+                float w[EPV], g[EPV];
+                widen_ro<T, VB>(w, post_w ? post_w + i * apart : nullptr);
+                widen_ro<T, VB>(g, gate ? gate + i * apart : nullptr);
+#pragma unroll
+                for (int k = 0; k < EPV; ++k) {
+                    const float b = get<T, VB>(x[i], k) * scale * (w[k] * g[k]);
+                    h[i][k] = fmaf(p.residual_scale, get<T, VB>(r[i], k), b);
+                    s[0] = fmaf(h[i][k], h[i][k], s[0]);
+                }
+                st_stream<VB>(static_cast<char*>(p.h) + row * row_bytes + mine + i * apart, pack<T, VB>(h[i]));
+            }
+        }
+        if (p.pre) {
+            block_sums<1>(s, red[it][1]);
+            const float rh = rsqrtf(fmaf(s[0], p.inv_hidden, p.pre_eps));
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (i < count) {
+                    float w[EPV];
+                    widen_ro<T, VB>(w, pre_w ? pre_w + i * apart : nullptr);
+#pragma unroll
+                    for (int k = 0; k < EPV; ++k) w[k] = h[i][k] * rh * w[k];
+                    st_stream<VB>(static_cast<char*>(p.y) + row * row_bytes + mine + i * apart, pack<T, VB>(w));
+                }
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------------ backward --
 //
 // With u = post_w * gate and q = u * x, D = dh + rh * (g - h * kh), the row's last sum

@@ -4,6 +4,10 @@
 // A group of p.group threads takes a row (with a cluster: a slice of it), 32 bytes of
 // each array to a thread, which it holds in registers, packed, from the sums to the
 // outputs.  The ring's slot is free again behind the block barrier of the sums.
+//
+// Rows that are not whole 16-byte vectors, or weights or outputs off the boundaries: a
+// thread's 16 bytes are pieces of VB bytes each, taken G pieces apart, so that accesses stay
+// side by side; everything between load and store is the same.
 #pragma once
 #include "k_blocknorm.cuh"
 #include "k_blockring.cuh"
@@ -87,23 +91,137 @@ constexpr int kBlockVecs = kBlockStagedBytes / 16;
 //   kBlockGated: the same with a gate
 enum : int { kBlockSome, kBlockPlain, kBlockGated };
 
-// A vector of a slot; zeros where it is missing.
-template <int MODE>
-__device__ __forceinline__ Vec<16> slot_vec(uint32_t at, bool on) {
-    return MODE == kBlockSome ? ld_slot_if(at, on) : ld_slot(at);
+// Pieces of VB bytes that make up 16.
+template <int VB>
+constexpr int kPieces = 16 / VB;
+template <int VB>
+constexpr uint32_t kAllPieces = (1u << kPieces<VB>) - 1;
+
+// Piece j of a vector put in, and taken out.
+template <int VB>
+__device__ __forceinline__ void put_piece(Vec<16>& v, int j, const Vec<VB>& w) {
+    if constexpr (VB == 2) {
+        const uint32_t h = w.h;
+        v.u[j / 2] = j % 2 ? (v.u[j / 2] & 0xFFFFu) | (h << 16) : h;
+    } else {
+#pragma unroll
+        for (int k = 0; k < VB / 4; ++k) v.u[j * (VB / 4) + k] = w.u[k];
+    }
+}
+template <int VB>
+__device__ __forceinline__ Vec<VB> take_piece(const Vec<16>& v, int j) {
+    Vec<VB> w;
+    if constexpr (VB == 2) {
+        w.h = static_cast<uint16_t>(j % 2 ? v.u[j / 2] >> 16 : v.u[j / 2]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < VB / 4; ++k) w.u[k] = v.u[j * (VB / 4) + k];
+    }
+    return w;
+}
+
+// FAST: a branch for threads that have all pieces (all of a row but its last ones).  Measured
+// (us, with / without): forward bf16 65536 x 1027 261 / 464, 65536 x 2050 337 / 378, but fp32
+// 32768 x 2050 284 / 261, backward 500 / 464, bf16 65536 x 2050 709 / 608.
+//
+// A vector of a slot; zeros where (bit j of `on`: piece j) it is missing.  apart: bytes from
+// piece to piece.
+template <int VB, int MODE, bool FAST>
+__device__ __forceinline__ Vec<16> slot_vec(uint32_t at, int apart, uint32_t on) {
+    if constexpr (VB == 16) {
+        return MODE == kBlockSome ? ld_slot_if(at, on) : ld_slot(at);
+    } else {
+        Vec<16> v;
+        auto piece = [&](int j, bool yes) {
+            Vec<VB> w;
+            const uint32_t q = yes, a = at + j * apart;
+            if constexpr (VB == 8) {
+                asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+                             "@p ld.shared.v2.u32 {%0,%1}, [%2];\n\t}"
+                             : "=&r"(w.u[0]), "=&r"(w.u[1]) : "r"(a), "r"(q));
+            } else if constexpr (VB == 4) {
+                asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t"
+                             "@p ld.shared.u32 %0, [%1];\n\t}" : "=&r"(w.u[0]) : "r"(a), "r"(q));
+            } else {
+                asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t"
+                             "@p ld.shared.u16 %0, [%1];\n\t}" : "=&h"(w.h) : "r"(a), "r"(q));
+            }
+            put_piece<VB>(v, j, w);
+        };
+        auto whole_piece = [&](int j) {
+            Vec<VB> w;
+            const uint32_t a = at + j * apart;
+            if constexpr (VB == 8)
+                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w.u[0]), "=r"(w.u[1]) : "r"(a));
+            else if constexpr (VB == 4)
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w.u[0]) : "r"(a));
+            else
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w.h) : "r"(a));
+            put_piece<VB>(v, j, w);
+        };
+        if (FAST && on == kAllPieces<VB>) {
+#pragma unroll
+            for (int j = 0; j < kPieces<VB>; ++j) whole_piece(j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPieces<VB>; ++j) piece(j, on >> j & 1u);
+        }
+        return v;
+    }
 }
 
 // A vector of weights.  Volatile: read where it stands, from L1, and not kept.
-template <typename T, int MODE>
-__device__ __forceinline__ Vec<16> weight_vec(const char* from, bool on) {
+template <typename T, int VB, int MODE, bool FAST>
+__device__ __forceinline__ Vec<16> weight_vec(const char* from, int apart, uint32_t on) {
     Vec<16> v;
     if (MODE == kBlockSome) {
         v = ones_vec<T>();
-        if (!from || !on) return v;
+        if (!from) return v;
     }
-    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3]) : "l"(from));
+    if constexpr (VB == 16) {
+        if (MODE == kBlockSome && !on) return v;
+        asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3]) : "l"(from));
+    } else if (FAST && on == kAllPieces<VB>) {
+#pragma unroll
+        for (int j = 0; j < kPieces<VB>; ++j) put_piece<VB>(v, j, ld_ro<VB>(from + j * apart));
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPieces<VB>; ++j)
+            if (on >> j & 1u) put_piece<VB>(v, j, ld_ro<VB>(from + j * apart));
+    }
     return v;
+}
+
+// A vector stored, the pieces that there are.
+template <int VB, bool FAST>
+__device__ __forceinline__ void store_vec(char* to, int apart, uint32_t on, const Vec<16>& v) {
+    if constexpr (VB == 16) {
+        if (on) st_stream<16>(to, v);
+    } else if (FAST && on == kAllPieces<VB>) {
+#pragma unroll
+        for (int j = 0; j < kPieces<VB>; ++j) st_stream<VB>(to + j * apart, take_piece<VB>(v, j));
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPieces<VB>; ++j)
+            if (on >> j & 1u) st_stream<VB>(to + j * apart, take_piece<VB>(v, j));
+    }
+}
+
+// The pieces that a thread has of a row of `bytes`: column of its vector i (bytes from the
+// row's start on) and the bits.
+template <int VB, int MODE>
+__device__ __forceinline__ void row_columns(const RowPlace& at, int first, int bytes, int (&col)[kBlockVecs],
+                                            uint32_t (&valid)[kBlockVecs]) {
+#pragma unroll
+    for (int i = 0; i < kBlockVecs; ++i) {
+        const int c = (i * kPieces<VB> * at.G + at.t) * VB;
+        col[i] = first + c;
+        valid[i] = 0;
+#pragma unroll
+        for (int j = 0; j < kPieces<VB>; ++j)
+            if (MODE != kBlockSome || c + j * at.G * VB < bytes) valid[i] |= 1u << j;
+    }
 }
 
 // Pair k of two vectors' product: for bf16 the mixed-precision product, which widens its
@@ -148,8 +266,9 @@ __device__ __forceinline__ void stay_packed(Vec<16> (&v)[N]) {
 
 // ------------------------------------------------------------------- forward --
 
-template <typename T, bool POST, bool PRE, bool CL, int MODE>
-__global__ void __launch_bounds__(kBlockFwdMaxThreads, 1) blocknorm_fwd_staged_kernel(const BlockParams p) {
+template <typename T, bool POST, bool PRE, bool CL, int MODE, int VB>
+__global__ void __launch_bounds__(VB == 16 ? kBlockFwdMaxThreads : kBlockFwdRaggedMaxThreads, 1)
+blocknorm_fwd_staged_kernel(const BlockParams p) {
     constexpr int NV = kBlockVecs, PN = kPairs<T>, EPV = VecTraits<T, 16>::kElems;
     constexpr bool GATE = MODE != kBlockPlain;
     using L = Lanes;
@@ -161,7 +280,7 @@ __global__ void __launch_bounds__(kBlockFwdMaxThreads, 1) blocknorm_fwd_staged_k
     const RowPlace at(p.group);
     const uint32_t rank = CL ? cluster_ctarank() : 0;
     const void* const arrays[2] = {p.x, p.residual};
-    const RowBlocks<2> ring(p, arrays, sizeof(T), rank, static_cast<int>(CL ? cluster_id_x() : blockIdx.x),
+    const RowBlocks<2, VB != 16> ring(p, arrays, sizeof(T), rank, static_cast<int>(CL ? cluster_id_x() : blockIdx.x),
                             static_cast<int>(CL ? cluster_count_x() : gridDim.x), smem, bars);
     if constexpr (CL) {
         exchange_init(&ex[0]);
@@ -170,16 +289,12 @@ __global__ void __launch_bounds__(kBlockFwdMaxThreads, 1) blocknorm_fwd_staged_k
         __syncthreads();
     }
     pdl_wait();
-    if (threadIdx.x == 0) ring.prologue();
-    bool valid[NV];
-    int col[NV];                       // bytes from the row's start
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int v = i * at.G + at.t;
-        valid[i] = MODE != kBlockSome || v * 16 < ring.bytes;
-        col[i] = ring.at + v * 16;
-    }
-    const uint32_t in_slot = static_cast<uint32_t>(at.g * ring.slot_row + at.t * 16);
+    if (threadIdx.x < 32) ring.prologue();
+    uint32_t valid[NV];
+    int col[NV];
+    row_columns<VB, MODE>(at, ring.at, ring.bytes, col, valid);
+    const int apart = at.G * VB;           // bytes from piece to piece, kPieces of them a vector
+    const uint32_t in_slot = static_cast<uint32_t>(at.g * ring.slot_row + at.t * VB);
     const char* post_w = static_cast<const char*>(p.post_w);
     const char* pre_w = static_cast<const char*>(p.pre_w);
     const L rs = L::all(p.residual_scale);
@@ -191,23 +306,28 @@ __global__ void __launch_bounds__(kBlockFwdMaxThreads, 1) blocknorm_fwd_staged_k
         int64_t gate_row, row;
         int rows;
         ring.where(n, gate_row, row, rows);
+        const int64_t row0 = row;
         row += at.g;
         // rows that the block lacks: sums of what the slot held before, not used
         const bool here = at.g < rows;
         Vec<16> x[NV], r[NV], w[NV], g[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if constexpr (POST) w[i] = weight_vec<T, MODE>(post_w ? post_w + col[i] : nullptr, valid[i]);
+            if constexpr (POST)
+                w[i] = weight_vec<T, VB, MODE, (VB < 8)>(post_w ? post_w + col[i] : nullptr, apart, valid[i]);
             if constexpr (GATE)
-                g[i] = weight_vec<T, MODE>(at_or_null(p.gate, gate_row * ring.row_bytes + col[i]), valid[i]);
+                g[i] = weight_vec<T, VB, MODE, (VB < 8)>(at_or_null(p.gate, gate_row * ring.row_bytes + col[i]), apart,
+                                               valid[i]);
         }
         const bool ok = ring.wait(slot, use) && !bad;
+        ring.template finish<T>(slot, row0, rows);
         RowSums<1> s;
         L acc = L::all(0.f);
+        const uint32_t in = in_slot + static_cast<uint32_t>(ring.skip(row));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            x[i] = slot_vec<MODE>(ring.base(slot, 0) + in_slot + i * at.G * 16, valid[i]);
-            r[i] = slot_vec<MODE>(ring.base(slot, 1) + in_slot + i * at.G * 16, valid[i]);
+            x[i] = slot_vec<VB, MODE, (VB < 8)>(ring.base(slot, 0) + in + i * kPieces<VB> * apart, apart, valid[i]);
+            r[i] = slot_vec<VB, MODE, (VB < 8)>(ring.base(slot, 1) + in + i * kPieces<VB> * apart, apart, valid[i]);
             if constexpr (POST) {
 #pragma unroll
                 for (int k = 0; k < PN; ++k) acc = add_square<T>(x[i], k, acc);
@@ -219,7 +339,7 @@ __global__ void __launch_bounds__(kBlockFwdMaxThreads, 1) blocknorm_fwd_staged_k
             s.gather(red[0][n & 1], at.width);
         }
         if (__syncthreads_or(!ok)) break;                     // uniform
-        if (threadIdx.x == 0 && n + p.nslots < ring.count) ring.issue(slot, n + p.nslots);
+        if (threadIdx.x < 32 && n + p.nslots < ring.count) ring.issue(slot, n + p.nslots);
         if constexpr (POST) {
             s.totals(red[0][n & 1], at.width, at.gw0, at.wpg);
             if (CL && !exchange_sums<1>(&ex[0], s.v, p.cluster, rank, static_cast<uint32_t>(n), p)) bad = true;
@@ -242,12 +362,14 @@ __global__ void __launch_bounds__(kBlockFwdMaxThreads, 1) blocknorm_fwd_staged_k
                 if constexpr (PRE) acc = fma(v, v, acc);
                 v.put(o + 2 * k);
             }
-            if (here && valid[i])
-                st_stream<16>(static_cast<char*>(p.h) + row * ring.row_bytes + col[i], pack<T, 16>(o));
+            if (here)
+                store_vec<VB, (VB < 8)>(static_cast<char*>(p.h) + row * ring.row_bytes + col[i], apart, valid[i],
+                              pack<T, 16>(o));
         }
         if constexpr (PRE) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) w[i] = weight_vec<T, MODE>(pre_w ? pre_w + col[i] : nullptr, valid[i]);
+            for (int i = 0; i < NV; ++i)
+                w[i] = weight_vec<T, VB, MODE, (VB < 8)>(pre_w ? pre_w + col[i] : nullptr, apart, valid[i]);
             s.v[0] = acc.total();
             s.gather(red[1][n & 1], at.width);
             if (at.wpg > 1) __syncthreads();
@@ -260,8 +382,9 @@ __global__ void __launch_bounds__(kBlockFwdMaxThreads, 1) blocknorm_fwd_staged_k
                 float o[EPV];
 #pragma unroll
                 for (int k = 0; k < PN; ++k) (h[i * PN + k] * rh * lanes<T>(w[i], k)).put(o + 2 * k);
-                if (here && valid[i])
-                    st_stream<16>(static_cast<char*>(p.y) + row * ring.row_bytes + col[i], pack<T, 16>(o));
+                if (here)
+                    store_vec<VB, (VB < 8)>(static_cast<char*>(p.y) + row * ring.row_bytes + col[i], apart, valid[i],
+                                  pack<T, 16>(o));
             }
         }
         if (++slot == p.nslots) {
@@ -281,46 +404,74 @@ __global__ void __launch_bounds__(kBlockFwdMaxThreads, 1) blocknorm_fwd_staged_k
 
 // ------------------------------------------------------------------ backward --
 
+// N floats (a power of two) at a time.
+template <int N>
+__device__ __forceinline__ void put_floats(float* to, const float* f) {
+    if constexpr (N >= 4) {
+#pragma unroll
+        for (int k = 0; k < N; k += 4) *reinterpret_cast<float4*>(to + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+    } else if constexpr (N == 2) {
+        *reinterpret_cast<float2*>(to) = make_float2(f[0], f[1]);
+    } else {
+        *to = *f;
+    }
+}
+
 // Column sums of a CTA's vectors, written to `to` (one row of a part).  Several row groups:
 // added in order through shared memory.
-template <typename T, int NV>
-__device__ __forceinline__ void write_part(const Lanes (&acc)[NV * kPairs<T>], float* to, const RowPlace& at,
-                                           int groups, const int (&col)[NV], const bool (&valid)[NV],
-                                           float* scratch, int slice_elems, int first_elem) {
-    constexpr int EPV = VecTraits<T, 16>::kElems, PN = kPairs<T>;
-    auto put = [&](float* row, int i) {
+template <typename T, int VB>
+__device__ __forceinline__ void write_part(const Lanes (&acc)[kBlockVecs * kPairs<T>], float* to,
+                                           const RowPlace& at, int groups, const int (&col)[kBlockVecs],
+                                           const uint32_t (&valid)[kBlockVecs], float* scratch, int slice_elems,
+                                           int first_elem) {
+    constexpr int EPV = VecTraits<T, 16>::kElems, PN = kPairs<T>, SZ = static_cast<int>(sizeof(T));
+    constexpr int EPP = VB / SZ;                          // elements of a piece
+    auto put = [&](float* row, int i) {                   // row: of column 0
         float f[EPV];
 #pragma unroll
         for (int k = 0; k < PN; ++k) acc[i * PN + k].put(f + 2 * k);
 #pragma unroll
-        for (int k = 0; k < EPV; k += 4)
-            *reinterpret_cast<float4*>(row + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+        for (int j = 0; j < kPieces<VB>; ++j)
+            if (valid[i] >> j & 1u) put_floats<EPP>(row + (col[i] + j * at.G * VB) / SZ, f + j * EPP);
     };
     if (groups == 1) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (valid[i]) put(to + col[i] / static_cast<int>(sizeof(T)), i);
+        for (int i = 0; i < kBlockVecs; ++i) put(to, i);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (valid[i]) put(scratch + at.g * slice_elems + (i * at.G + at.t) * EPV, i);
+    for (int i = 0; i < kBlockVecs; ++i) put(scratch + at.g * slice_elems - first_elem, i);
     __syncthreads();
-    for (int c = threadIdx.x * 4; c < slice_elems; c += blockDim.x * 4) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int W = EPP < 4 ? EPP : 4;
+    for (int c = threadIdx.x * W; c < slice_elems; c += blockDim.x * W) {
+        float v[W];
+#pragma unroll
+        for (int k = 0; k < W; ++k) v[k] = 0.f;
         for (int g = 0; g < groups; ++g) {
-            const float4 f = *reinterpret_cast<const float4*>(scratch + g * slice_elems + c);
-            v.x += f.x;
-            v.y += f.y;
-            v.z += f.z;
-            v.w += f.w;
+            const float* from = scratch + g * slice_elems + c;
+            float f[W];
+            if constexpr (W == 4) {
+                const float4 q = *reinterpret_cast<const float4*>(from);
+                f[0] = q.x;
+                f[1] = q.y;
+                f[2] = q.z;
+                f[3] = q.w;
+            } else if constexpr (W == 2) {
+                const float2 q = *reinterpret_cast<const float2*>(from);
+                f[0] = q.x;
+                f[1] = q.y;
+            } else {
+                f[0] = *from;
+            }
+#pragma unroll
+            for (int k = 0; k < W; ++k) v[k] += f[k];
         }
-        *reinterpret_cast<float4*>(to + first_elem + c) = v;
+        put_floats<W>(to + first_elem + c, v);
     }
     __syncthreads();
 }
 
-template <typename T, bool POST, bool PRE, bool CL, int MODE>
+template <typename T, bool POST, bool PRE, bool CL, int MODE, int VB>
 __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_kernel(const BlockParams p) {
     constexpr int NV = kBlockVecs, PN = kPairs<T>, EPV = VecTraits<T, 16>::kElems;
     constexpr int NARR = PRE ? 4 : 2;
@@ -342,40 +493,37 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
     auto make_ring = [&]() {
         if constexpr (PRE) {
             const void* const arrays[4] = {p.x, p.dh, p.dy, p.h_in};
-            return RowBlocks<4>(p, arrays, sizeof(T), rank, unit, units, smem, bars);
+            return RowBlocks<4, VB != 16>(p, arrays, sizeof(T), rank, unit, units, smem, bars);
         } else {
             const void* const arrays[2] = {p.x, p.dh};
-            return RowBlocks<2>(p, arrays, sizeof(T), rank, unit, units, smem, bars);
+            return RowBlocks<2, VB != 16>(p, arrays, sizeof(T), rank, unit, units, smem, bars);
         }
     };
-    const RowBlocks<NARR> ring = make_ring();
+    const RowBlocks<NARR, VB != 16> ring = make_ring();
     if constexpr (CL) exchange_init(ex);
     else __syncthreads();
     pdl_wait();
-    if (threadIdx.x == 0) ring.prologue();
-    bool valid[NV];
+    if (threadIdx.x < 32) ring.prologue();
+    uint32_t valid[NV];
     int col[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int v = i * at.G + at.t;
-        valid[i] = MODE != kBlockSome || v * 16 < ring.bytes;
-        col[i] = ring.at + v * 16;
-    }
+    row_columns<VB, MODE>(at, ring.at, ring.bytes, col, valid);
+    const int apart = at.G * VB;
     float* scratch = reinterpret_cast<float*>(smem + (ring.base(p.nslots, 0) - ring.base(0, 0)));
     const int slice_elems = ring.bytes / static_cast<int>(sizeof(T));
     const int first_elem = ring.at / static_cast<int>(sizeof(T));
     const char* post_w = static_cast<const char*>(p.post_w);
     const char* pre_w = static_cast<const char*>(p.pre_w);
     const bool have_dh = p.dh != nullptr;
-    const uint32_t in_slot = static_cast<uint32_t>(at.g * ring.slot_row + at.t * 16);
+    const uint32_t in_slot = static_cast<uint32_t>(at.g * ring.slot_row + at.t * VB);
     // weights, and the gate of the rows at hand, packed
     Vec<16> w[NV], pw[NV], gt[NV];
     auto read_weights = [&](int i) {
-        if constexpr (POST) w[i] = weight_vec<T, MODE>(post_w ? post_w + col[i] : nullptr, valid[i]);
-        if constexpr (PRE) pw[i] = weight_vec<T, MODE>(pre_w ? pre_w + col[i] : nullptr, valid[i]);
+        if constexpr (POST) w[i] = weight_vec<T, VB, MODE, false>(post_w ? post_w + col[i] : nullptr, apart, valid[i]);
+        if constexpr (PRE) pw[i] = weight_vec<T, VB, MODE, false>(pre_w ? pre_w + col[i] : nullptr, apart, valid[i]);
     };
     auto read_gate = [&](int i, int64_t row) {
-        if constexpr (GATE) gt[i] = weight_vec<T, MODE>(at_or_null(p.gate, row * ring.row_bytes + col[i]), valid[i]);
+        if constexpr (GATE)
+            gt[i] = weight_vec<T, VB, MODE, false>(at_or_null(p.gate, row * ring.row_bytes + col[i]), apart, valid[i]);
     };
     if constexpr (!REREAD) {
 #pragma unroll
@@ -390,7 +538,7 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
     // ranges of blocks, and one of them does from each part to the next.
     auto write_gate = [&](int64_t s) {
         if (p.part_gate)
-            write_part<T, NV>(acc, p.part_gate + (unit + s) * p.hidden, at, p.block_rows, col, valid, scratch,
+            write_part<T, VB>(acc, p.part_gate + (unit + s) * p.hidden, at, p.block_rows, col, valid, scratch,
                               slice_elems, first_elem);
     };
     int slot = 0;
@@ -418,9 +566,12 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
             if constexpr (PRE) stay_packed(pw);
             if constexpr (GATE) stay_packed(gt);
         }
+        const int64_t row0 = row;
         row += at.g;
         const bool here = at.g < rows;
         const bool ok = ring.wait(slot, use) && !bad;
+        ring.template finish<T>(slot, row0, rows);
+        const uint32_t in_row = in_slot + static_cast<uint32_t>(ring.skip(row));
         Vec<16> x[NV], d[NV], y[PRE ? NV : 1], h[PRE ? NV : 1];
         RowSums<NS> s;
         L a[6];
@@ -435,16 +586,16 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
         };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const uint32_t in = in_slot + i * at.G * 16;
+            const uint32_t in = in_row + i * kPieces<VB> * apart;
             if constexpr (REREAD) {
                 read_weights(i);
                 read_gate(i, gate_row);
             }
-            x[i] = slot_vec<MODE>(ring.base(slot, 0) + in, valid[i]);
-            d[i] = have_dh ? slot_vec<MODE>(ring.base(slot, 1) + in, valid[i]) : zero_vec();
+            x[i] = slot_vec<VB, MODE, false>(ring.base(slot, 0) + in, apart, valid[i]);
+            d[i] = have_dh ? slot_vec<VB, MODE, false>(ring.base(slot, 1) + in, apart, valid[i]) : zero_vec();
             if constexpr (PRE) {
-                y[i] = slot_vec<MODE>(ring.base(slot, 2) + in, valid[i]);
-                h[i] = slot_vec<MODE>(ring.base(slot, 3) + in, valid[i]);
+                y[i] = slot_vec<VB, MODE, false>(ring.base(slot, 2) + in, apart, valid[i]);
+                h[i] = slot_vec<VB, MODE, false>(ring.base(slot, 3) + in, apart, valid[i]);
             }
 #pragma unroll
             for (int k = 0; k < PN; ++k) {
@@ -473,7 +624,7 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
         for (int k = 0; k < NS; ++k) s.v[k] = a[FIRST + k].total();
         if constexpr (NS > 0) s.gather(red[n & 1], at.width);
         if (__syncthreads_or(!ok)) break;                     // uniform
-        if (threadIdx.x == 0 && n + p.nslots < ring.count) ring.issue(slot, n + p.nslots);
+        if (threadIdx.x < 32 && n + p.nslots < ring.count) ring.issue(slot, n + p.nslots);
         if constexpr (NS > 0) {
             s.totals(red[n & 1], at.width, at.gw0, at.wpg);
             if (CL && !exchange_sums<NS>(ex, s.v, p.cluster, rank, static_cast<uint32_t>(n), p)) bad = true;
@@ -518,11 +669,9 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
                         e.put(ox + 2 * k);
                     }
                 }
-                if (valid[i]) {
-                    const int64_t to = row * ring.row_bytes + col[i];
-                    st_stream<16>(static_cast<char*>(p.dx) + to, pack<T, 16>(ox));
-                    st_stream<16>(static_cast<char*>(p.dres) + to, pack<T, 16>(od));
-                }
+                const int64_t to = row * ring.row_bytes + col[i];
+                store_vec<VB, false>(static_cast<char*>(p.dx) + to, apart, valid[i], pack<T, 16>(ox));
+                store_vec<VB, false>(static_cast<char*>(p.dres) + to, apart, valid[i], pack<T, 16>(od));
             }
         }
         if (++slot == p.nslots) {
@@ -540,7 +689,7 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
         write_gate(last_gate);
         if constexpr (PRE) {
             if (p.part_pre)
-                write_part<T, NV>(pre, p.part_pre + static_cast<int64_t>(unit) * p.hidden, at, p.block_rows, col,
+                write_part<T, VB>(pre, p.part_pre + static_cast<int64_t>(unit) * p.hidden, at, p.block_rows, col,
                                   valid, scratch, slice_elems, first_elem);
         }
     }

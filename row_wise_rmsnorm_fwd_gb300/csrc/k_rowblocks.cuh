@@ -4,10 +4,14 @@
 // kernel has for the rows' sums, so a ring of two keeps a whole block under way at all
 // times.
 //
-// Rows are whole 16-byte vectors, arrays on 16-byte boundaries.  Blocks lie within the
-// rows of a gate row and are dealt out in contiguous ranges, so that a CTA meets few
-// gate rows, in order.  With a cluster each CTA takes its slice of every row (one row to a
-// block).
+// Arrays are on 16-byte boundaries.  Rows of whole 16-byte vectors come many to a copy; RAGGED,
+// rows of any length, each by itself, from the boundary at or before its start to the one at
+// or after its end (the bytes around it belong to its neighbours).  Behind the arrays'
+// last boundary nothing may be read by such copies: what the last row has there is copied by
+// threads (finish).  With one gate row the blocks are dealt out in turn, so that the CTAs
+// read side by side; else they lie within the rows of a gate row and are dealt out in
+// contiguous ranges, so that a CTA meets few gate rows, in order.  With a cluster each CTA
+// takes its slice of every row (one row to a block).
 #pragma once
 #include "blocknorm_launch.h"
 #include "common.cuh"
@@ -16,7 +20,7 @@ namespace rmsnorm {
 
 constexpr int kRowBlocksMaxSlots = 4;
 
-template <int NARR>
+template <int NARR, bool RAGGED>
 struct RowBlocks {
     const BlockParams& p;
     const char* src[NARR];       // null: absent
@@ -46,10 +50,10 @@ struct RowBlocks {
             count = p.blocks * (unit + 1) / units - first;
         }
         row_bytes = p.hidden * sz;
-        slot_row = p.slice_vecs * 16;
-        at = static_cast<int>(rank) * slot_row;
+        slot_row = RAGGED ? p.row_slot : p.slice_vecs * 16;
+        at = RAGGED ? 0 : static_cast<int>(rank) * slot_row;
         bytes = row_bytes - at;
-        if (bytes > slot_row) bytes = slot_row;
+        if (!RAGGED && bytes > slot_row) bytes = slot_row;
         if (threadIdx.x == 0) {
             for (int k = 0; k < p.nslots; ++k) mbar_init(bars + 8 * k, 1);
             fence_mbarrier_init_cluster();
@@ -71,29 +75,91 @@ struct RowBlocks {
         return slots + static_cast<uint32_t>((slot * NARR + a) * p.block_rows * slot_row);
     }
 
-    // One thread: start the copies of block n into `slot`.
+    // Bytes of an array before its last boundary.
+    __device__ __forceinline__ int64_t inside() const { return p.rows * row_bytes / 16 * 16; }
+    // Bytes of a row's slot before the row.
+    __device__ __forceinline__ int skip(int64_t row) const {
+        return RAGGED ? static_cast<int>(row * row_bytes % 16) : 0;
+    }
+
+    // One warp: start the copies of block n into `slot`.
     __device__ __forceinline__ void issue(int slot, int64_t n) const {
+        const int lane = threadIdx.x & 31;
         const uint32_t bar = bars + 8 * slot;
 #if RMSNORM_FAULT_INJECT
         if (p.fault == kFaultStagedWithholdCopy && n == 0) {   // armed for bytes that never come
-            mbar_arrive_expect_tx(bar, 16);
+            if (lane == 0) mbar_arrive_expect_tx(bar, 16);
             return;
         }
 #endif
         int64_t gate, row;
         int rows;
         where(n, gate, row, rows);
-        // one row of a slice, or whole rows, which follow one another
-        const uint32_t n_bytes = static_cast<uint32_t>(p.cluster > 1 ? bytes : rows * row_bytes);
-        mbar_arrive_expect_tx(bar, n_bytes * narr);
-        const int64_t from = row * row_bytes + at;
+        if constexpr (!RAGGED) {
+            if (lane != 0) return;
+            // one row of a slice, or whole rows, which follow one another
+            const uint32_t n_bytes = static_cast<uint32_t>(p.cluster > 1 ? bytes : rows * row_bytes);
+            mbar_arrive_expect_tx(bar, n_bytes * narr);
+            const int64_t from = row * row_bytes + at;
 #pragma unroll
-        for (int a = 0; a < NARR; ++a)
-            if (src[a]) bulk_g2s_plain(base(slot, a), src[a] + from, n_bytes, bar);
+            for (int a = 0; a < NARR; ++a)
+                if (src[a]) bulk_g2s_plain(base(slot, a), src[a] + from, n_bytes, bar);
+        } else {
+            // a row's window: as large as any row needs, but not past the last boundary
+            auto window = [&](int r, int64_t& from) {
+                from = (row + r) * row_bytes / 16 * 16;
+                const int64_t left = inside() - from;
+                return static_cast<uint32_t>(left < slot_row ? left : slot_row);
+            };
+            uint32_t total = 0;
+            int64_t from;
+            for (int r = lane; r < rows; r += 32) total += window(r, from);
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
+            if (lane == 0) mbar_arrive_expect_tx(bar, total * narr);
+            __syncwarp();
+            for (int r = lane; r < rows; r += 32) {
+                const uint32_t n_bytes = window(r, from);
+                if (n_bytes == 0) continue;                 // a last row of less than 16 bytes
+#pragma unroll
+                for (int a = 0; a < NARR; ++a)
+                    if (src[a])
+                        bulk_g2s_plain(base(slot, a) + static_cast<uint32_t>(r * slot_row), src[a] + from,
+                                       n_bytes, bar);
+            }
+        }
     }
 
     __device__ __forceinline__ void prologue() const {
         for (int k = 0; k < p.nslots && k < count; ++k) issue(k, k);
+    }
+
+    // All threads, after a block has landed: what the arrays' last row, if it is the
+    // block's last, has behind their last boundary.  Ends with a barrier if there is any.
+    template <typename T>
+    __device__ __forceinline__ void finish(int slot, int64_t row0, int rows) const {
+        if constexpr (RAGGED) {
+            const int64_t end = inside();
+            const int tail = static_cast<int>((p.rows * row_bytes - end) / static_cast<int>(sizeof(T)));
+            if (tail == 0 || row0 + rows != p.rows) return;      // uniform
+            const int64_t from = (p.rows - 1) * row_bytes / 16 * 16;
+            if (static_cast<int>(threadIdx.x) < tail) {
+                const uint32_t to = static_cast<uint32_t>((rows - 1) * slot_row) +
+                                    static_cast<uint32_t>(end - from) + threadIdx.x * static_cast<uint32_t>(sizeof(T));
+#pragma unroll
+                for (int a = 0; a < NARR; ++a) {
+                    if (!src[a]) continue;
+                    const char* v = src[a] + end + threadIdx.x * sizeof(T);
+                    if constexpr (sizeof(T) == 4)
+                        asm volatile("st.shared.u32 [%0], %1;" :: "r"(base(slot, a) + to),
+                                     "r"(*reinterpret_cast<const uint32_t*>(v)) : "memory");
+                    else
+                        asm volatile("st.shared.u16 [%0], %1;" :: "r"(base(slot, a) + to),
+                                     "h"(*reinterpret_cast<const uint16_t*>(v)) : "memory");
+                }
+            }
+            __syncthreads();
+        }
     }
 
     // Wait (bounded) for block n.

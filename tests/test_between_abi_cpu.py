@@ -50,7 +50,7 @@ NAN, INF = float("nan"), float("inf")
 BAD_RULES = [dict(gate_rows=0), dict(gate_rows=-3), dict(residual_scale=NAN), dict(branch_scale=INF),
              dict(post_eps=-1e-9), dict(pre_eps=NAN), dict(post_eps=INF), dict(post_norm=2),
              dict(pre_norm=-1), dict(post_w=POST + 2), dict(pre_w=PRE + 1), dict(gate=GATE + 3)]
-BAD_OPTIONS = [dict(path="rowreg"), dict(path="cluster"), dict(threads=64), dict(epilogue="relu"),
+BAD_OPTIONS = [dict(path="ringreg"), dict(path="cluster"), dict(threads=64), dict(epilogue="relu"),
                dict(fault_inject=3), dict(grid=3), dict(cluster=2), dict(cluster=3, path="staged")]
 
 

@@ -195,6 +195,46 @@ def test_unaligned_pointers(t, path):
     check_backward(v, rule, backward(g, rule, dx=out[0], dresidual=out[1], options={"path": path}))
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("lead,n", [((3, 21), 1024), ((400,), 72), ((5, 7), 2051), ((2,), 3), ((1,), 5),
+                                    ((2000,), 33), ((3, 100), 1030), ((7,), 4095), ((4, 3), 6004)])
+def test_weights_and_outputs_off_the_boundaries(lead, n, t):
+    """Inputs on their boundaries, the weights, the gate and the outputs not; ragged rows,
+    the arrays' last bytes among them."""
+    rule = RULES["scaled"]
+    for by in (1, 2, 4):
+        for gate in ("sequence", "channel"):
+            v = inputs(lead, n, t, rule, gate, seed=by)
+            g = on(v)
+            off = lambda a: torch.empty(a.numel() + 16, dtype=a.dtype, device="cuda")[by:by + a.numel()].view(a.shape)  # noqa: E731
+            for k in ("post_w", "pre_w", "gate"):
+                g[k] = off(v[k]).copy_(v[k])
+            one, two = off(v["x"]), off(v["x"])
+            check_forward(v, rule, forward(g, rule, h=one, y=two))
+            check_backward(v, rule, backward(g, rule, dx=one, dresidual=two))
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("n", [5, 33, 1027, 2050, 4097, 6004])
+def test_nothing_behind_the_arrays(n, t):
+    """Arrays that end where their memory does hold NaN from there on: nothing of it is
+    used, and nothing there is written."""
+    rule = RULES["scaled"]
+    v = inputs((3, 3), n, t, rule, "channel")
+    rooms = {}
+    g = {}
+    for k, a in v.items():
+        rooms[k] = torch.full((a.numel() + 64,), float("nan"), dtype=a.dtype, device="cuda")
+        g[k] = rooms[k][:a.numel()].view(a.shape)
+        g[k].copy_(a)
+    outs = [torch.full((v["x"].numel() + 64,), 7.0, dtype=v["x"].dtype, device="cuda") for _ in range(2)]
+    one, two = (o[:v["x"].numel()].view(v["x"].shape) for o in outs)
+    check_forward(v, rule, forward(g, rule, h=one, y=two))
+    check_backward(v, rule, backward(g, rule, dx=one, dresidual=two))
+    for o in outs:
+        assert (o[v["x"].numel():] == 7.0).all()
+
+
 @pytest.mark.parametrize("path", PATHS)
 @pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("n", [64, 1030, 4096, 9001, 16384])
