@@ -476,8 +476,10 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
     constexpr int NV = kBlockVecs, PN = kPairs<T>, EPV = VecTraits<T, 16>::kElems;
     constexpr int NARR = PRE ? 4 : 2;
     constexpr bool GATE = MODE != kBlockPlain;
-    // weights read again in each pass (from L1) rather than kept: with both norms in bf16 they
-    // would not fit beside the column sums
+    // With both norms in bf16 not all weights fit beside the column sums: pre_w is read again in
+    // each pass.  post_w and the gate are kept, their product in fp32: the ring leaves L1 too
+    // little for all three.  Measured (us, bf16 32768 x 8192 with a gate, all three read again /
+    // so): 577 / 505.
     constexpr bool REREAD = PRE && POST && sizeof(T) == 2;
     constexpr int NS = PRE && POST ? 6 : (PRE || POST ? 2 : 0);
     using L = Lanes;
@@ -515,20 +517,34 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
     const char* pre_w = static_cast<const char*>(p.pre_w);
     const bool have_dh = p.dh != nullptr;
     const uint32_t in_slot = static_cast<uint32_t>(at.g * ring.slot_row + at.t * VB);
-    // weights, and the gate of the rows at hand, packed
-    Vec<16> w[NV], pw[NV], gt[NV];
-    auto read_weights = [&](int i) {
-        if constexpr (POST) w[i] = weight_vec<T, VB, MODE, false>(post_w ? post_w + col[i] : nullptr, apart, valid[i]);
-        if constexpr (PRE) pw[i] = weight_vec<T, VB, MODE, false>(pre_w ? pre_w + col[i] : nullptr, apart, valid[i]);
+    // pre_w and, without the post norm, the gate of the rows at hand, packed; post_w times the
+    // gate in fp32
+    Vec<16> pw[NV], gt[NV];
+    L u[POST ? NV * PN : 1];
+    auto read_pre = [&](int i) {
+        if constexpr (PRE)
+            pw[i] = weight_vec<T, VB, MODE, false>(pre_w ? pre_w + col[i] : nullptr, apart, valid[i]);
     };
-    auto read_gate = [&](int i, int64_t row) {
-        if constexpr (GATE)
-            gt[i] = weight_vec<T, VB, MODE, false>(at_or_null(p.gate, row * ring.row_bytes + col[i]), apart, valid[i]);
+    auto read_post = [&](int64_t gate_row) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if constexpr (GATE)
+                gt[i] = weight_vec<T, VB, MODE, false>(at_or_null(p.gate, gate_row * ring.row_bytes + col[i]),
+                                                       apart, valid[i]);
+            if constexpr (POST) {
+                const Vec<16> w =
+                    weight_vec<T, VB, MODE, false>(post_w ? post_w + col[i] : nullptr, apart, valid[i]);
+#pragma unroll
+                for (int k = 0; k < PN; ++k)
+                    u[i * PN + k] = GATE ? product<T>(w, gt[i], k) : lanes<T>(w, k);
+            }
+        }
     };
     if constexpr (!REREAD) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) read_weights(i);
+        for (int i = 0; i < NV; ++i) read_pre(i);
     }
+    if constexpr (!GATE) read_post(0);
     L acc[NV * PN], pre[PRE ? NV * PN : 1];     // sums of D * xh and of dy * h * rh
 #pragma unroll
     for (int k = 0; k < NV * PN; ++k) acc[k] = L::all(0.f);
@@ -556,16 +572,10 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
                 for (int k = 0; k < NV * PN; ++k) acc[k] = L::all(0.f);
             }
             last_gate = gate_row;
-            if constexpr (!REREAD) {
-#pragma unroll
-                for (int i = 0; i < NV; ++i) read_gate(i, gate_row);
-            }
+            if constexpr (GATE) read_post(gate_row);
         }
-        if constexpr (!REREAD) {
-            if constexpr (POST) stay_packed(w);
-            if constexpr (PRE) stay_packed(pw);
-            if constexpr (GATE) stay_packed(gt);
-        }
+        if constexpr (GATE && !POST) stay_packed(gt);
+        if constexpr (PRE && !REREAD) stay_packed(pw);
         const int64_t row0 = row;
         row += at.g;
         const bool here = at.g < rows;
@@ -579,18 +589,14 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
         for (int k = 0; k < 6; ++k) a[k] = L::all(0.f);
         // post_w * gate
         auto factor = [&](int i, int k) {
-            if constexpr (POST && GATE) return product<T>(w[i], gt[i], k);
-            else if constexpr (POST) return lanes<T>(w[i], k);
+            if constexpr (POST) return u[i * PN + k];
             else if constexpr (GATE) return lanes<T>(gt[i], k);
             else return L::all(1.f);
         };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const uint32_t in = in_row + i * kPieces<VB> * apart;
-            if constexpr (REREAD) {
-                read_weights(i);
-                read_gate(i, gate_row);
-            }
+            if constexpr (REREAD) read_pre(i);
             x[i] = slot_vec<VB, MODE, false>(ring.base(slot, 0) + in, apart, valid[i]);
             d[i] = have_dh ? slot_vec<VB, MODE, false>(ring.base(slot, 1) + in, apart, valid[i]) : zero_vec();
             if constexpr (PRE) {
@@ -646,10 +652,7 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float ox[EPV], od[EPV];
-                if constexpr (REREAD) {
-                    read_weights(i);
-                    read_gate(i, gate_row);
-                }
+                if constexpr (REREAD) read_pre(i);
 #pragma unroll
                 for (int k = 0; k < PN; ++k) {
                     const L xk = lanes<T>(x[i], k);

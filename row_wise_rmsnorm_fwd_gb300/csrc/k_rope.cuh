@@ -35,17 +35,11 @@ __device__ __forceinline__ float2 rope_turn(uint64_t freq, int64_t position, flo
     return make_float2(a * scale, b * scale);
 }
 
-// a / b for a >= 0, b > 0; numbers of 32 bits, as most are, in a quarter of the instructions.
-__device__ __forceinline__ int64_t rope_div(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
 // Position of a token, and where it lies in a view.
 struct RopeToken {
     int64_t b, s, position;
     __device__ __forceinline__ RopeToken(const RopeParams& p, int64_t token) {
-        b = rope_div(token, p.seq);
+        b = div_nonneg(token, p.seq);
         s = token - b * p.seq;
         position = p.start;
         if (!p.positions) {

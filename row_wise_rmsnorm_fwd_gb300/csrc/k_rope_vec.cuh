@@ -252,13 +252,13 @@ __global__ void __launch_bounds__(32 * kRopeVecWarps, rope_ctas(KIND)) rope_vec_
     auto enter = [&](int64_t item) {
         ahead.item = item;
         if (item >= items) return;
-        const int64_t place = split == 1 ? item : rope_div(item, split);
+        const int64_t place = split == 1 ? item : div_nonneg(item, split);
         const int64_t token = place * tokens_per_warp + token_of_warp;
         ahead.there = token < p.tokens;
         const int first = static_cast<int>(item - place * split) * share;
         ahead.head = first + mine;
         ahead.rest = heads - first;
-        const int64_t tok = ahead.there ? token : 0, b = rope_div(tok, p.seq), s = tok - b * p.seq;
+        const int64_t tok = ahead.there ? token : 0, b = div_nonneg(tok, p.seq), s = tok - b * p.seq;
         ahead.src = static_cast<const T*>(from.p) + b * from.batch + s * from.token + ahead.head * from.head + ja;
         if constexpr (GRAD)
             ahead.xs = static_cast<const T*>(t.x.p) + b * t.x.batch + s * t.x.token + ahead.head * t.x.head + ja;
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(32 * kRopeVecWarps, rope_ctas(KIND)) rope_vec_
     }
     int stage = 0;
     for (int64_t item = item0; item < items; item += item_step) {
-        const int64_t place = split == 1 ? item : rope_div(item, split);
+        const int64_t place = split == 1 ? item : div_nonneg(item, split);
         const int64_t token = place * tokens_per_warp + token_of_warp;
         const bool there = token < p.tokens;
         const RopeToken tk(p, there ? token : 0);

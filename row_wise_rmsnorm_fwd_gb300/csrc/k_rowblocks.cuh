@@ -63,7 +63,7 @@ struct RowBlocks {
     // Gate row, first row and number of rows of the unit's n-th block.
     __device__ __forceinline__ void where(int64_t n, int64_t& gate, int64_t& row, int& rows) const {
         const int64_t b = first + n * step;
-        gate = p.gates == 1 ? 0 : b / p.blocks_per_gate;
+        gate = p.gates == 1 ? 0 : div_nonneg(b, p.blocks_per_gate);
         row = gate * p.gate_rows + (b - gate * p.blocks_per_gate) * p.block_rows;
         int64_t end = (gate + 1) * p.gate_rows;
         if (end > p.rows) end = p.rows;
