@@ -35,6 +35,7 @@ struct BlockParams {
     int64_t units;         // staged backward: CTAs or clusters, unit u's sums of gate row s
                            // being part u + s; 0: the parts are the any-width kernel's
     int32_t pre_parts;     // parts of dpre_w
+    int32_t few_parts;     // several gate rows of few parts each
     int32_t hidden;
     int32_t nvec;          // vectors per row
     // staged kernels

@@ -371,7 +371,9 @@ __global__ void __launch_bounds__(kBlockColsThreads) blocknorm_bwd_cols_kernel(c
 // Gate row s has A[s] = the sum of its parts:
 //   dgate[s] = branch_scale * post_w * A[s],   dpost_w = branch_scale * sum_s gate[s] * A[s]
 // With one gate row both come from here; with several A is kept, and dpost_w
-// is formed from it by a second launch (GATES false).
+// is formed from it by a second launch (GATES false).  Where the gate rows have few parts
+// each, lanes for 32 parts would be idle (32 gate rows of 5 parts, 8192 wide: 38 us), and a
+// thread adds its columns' by itself.
 
 template <int W>
 __device__ __forceinline__ void load_cols(float (&v)[W], const float* from) {
@@ -456,17 +458,58 @@ __global__ void __launch_bounds__(kBlockReduceThreads) blocknorm_reduce_kernel(c
     }
     if (!p.part_gate) return;
     const T* post_w = p.post ? static_cast<const T*>(p.post_w) : nullptr;
-    for (int64_t s = blockIdx.y - 1; s < p.gates; s += gridDim.y - 1) {
-        int64_t from = s * p.parts_per_gate, count = p.parts_per_gate;
+    auto parts_of = [&](int64_t s, int64_t& from, int64_t& count) {
+        from = s * p.parts_per_gate;
+        count = p.parts_per_gate;
         if (p.units && p.gates == 1) {
             count = p.units;
         } else if (p.units) {   // the units that the gate row's blocks were dealt to
             const int64_t b0 = s * p.blocks_per_gate;
             const int64_t b1 = min(b0 + p.blocks_per_gate, p.blocks) - 1;
-            const int64_t u0 = ((b0 + 1) * p.units - 1) / p.blocks;
+            const int64_t u0 = div_nonneg((b0 + 1) * p.units - 1, p.blocks);
             from = u0 + s;
-            count = ((b1 + 1) * p.units - 1) / p.blocks - u0 + 1;
+            count = div_nonneg((b1 + 1) * p.units - 1, p.blocks) - u0 + 1;
         }
+    };
+    if (p.few_parts) {          // a thread for W columns of a gate row
+        const int64_t per_gate = (p.hidden + kBlockReduceThreads * W - 1) / (kBlockReduceThreads * W);
+        const int64_t ctas = static_cast<int64_t>(gridDim.x) * (gridDim.y - 1);
+        for (int64_t task = blockIdx.x + static_cast<int64_t>(gridDim.x) * (blockIdx.y - 1);
+             task < per_gate * p.gates; task += ctas) {
+            const int64_t s = div_nonneg(task, per_gate);
+            const int64_t c = ((task - s * per_gate) * kBlockReduceThreads + threadIdx.x) * W;
+            if (c >= p.hidden) continue;
+            int64_t from, count;
+            parts_of(s, from, count);
+            float v[W];
+#pragma unroll
+            for (int w = 0; w < W; ++w) v[w] = 0.f;
+            for (int64_t k = 0; k < count; k += 4) {
+                float f[4][W];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)      // past the last part it again, not added
+                    load_cols<W>(f[u], p.part_gate + (from + min(k + u, count - 1)) * p.hidden + c);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (k + u < count) {
+#pragma unroll
+                        for (int w = 0; w < W; ++w) v[w] += f[u][w];
+                    }
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const int64_t at = s * p.hidden + c + w;
+                if (p.dgate)
+                    p.dgate[at] = p.branch_scale * v[w] * (post_w ? static_cast<float>(post_w[c + w]) : 1.f);
+                if (p.gate_sums) p.gate_sums[at] = v[w];
+            }
+        }
+        return;
+    }
+    for (int64_t s = blockIdx.y - 1; s < p.gates; s += gridDim.y - 1) {
+        int64_t from, count;
+        parts_of(s, from, count);
         const float v = sum_parts<T, W>(p.part_gate + from * p.hidden, count, p.hidden, nullptr);
         if (!mine) continue;
         const int64_t at = s * p.hidden + col;

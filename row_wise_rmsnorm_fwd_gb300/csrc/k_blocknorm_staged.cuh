@@ -289,7 +289,8 @@ blocknorm_fwd_staged_kernel(const BlockParams p) {
         __syncthreads();
     }
     pdl_wait();
-    if (threadIdx.x < 32) ring.prologue();
+    auto now = ring.start(), ahead = now;        // the block at work, and the next to be copied
+    if (threadIdx.x < 32) ring.prologue(ahead);
     uint32_t valid[NV];
     int col[NV];
     row_columns<VB, MODE>(at, ring.at, ring.bytes, col, valid);
@@ -303,11 +304,10 @@ blocknorm_fwd_staged_kernel(const BlockParams p) {
     bool bad = false;
     int64_t n = 0;
     for (; n < ring.count; ++n) {
-        int64_t gate_row, row;
-        int rows;
-        ring.where(n, gate_row, row, rows);
-        const int64_t row0 = row;
-        row += at.g;
+        const int64_t gate_row = now.gate, row0 = now.row;
+        const int rows = now.rows;
+        ring.advance(now);
+        const int64_t row = row0 + at.g;
         // rows that the block lacks: sums of what the slot held before, not used
         const bool here = at.g < rows;
         Vec<16> x[NV], r[NV], w[NV], g[NV];
@@ -339,7 +339,7 @@ blocknorm_fwd_staged_kernel(const BlockParams p) {
             s.gather(red[0][n & 1], at.width);
         }
         if (__syncthreads_or(!ok)) break;                     // uniform
-        if (threadIdx.x < 32 && n + p.nslots < ring.count) ring.issue(slot, n + p.nslots);
+        if (threadIdx.x < 32 && n + p.nslots < ring.count) ring.issue(slot, n + p.nslots, ahead);
         if constexpr (POST) {
             s.totals(red[0][n & 1], at.width, at.gw0, at.wpg);
             if (CL && !exchange_sums<1>(&ex[0], s.v, p.cluster, rank, static_cast<uint32_t>(n), p)) bad = true;
@@ -505,7 +505,8 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
     if constexpr (CL) exchange_init(ex);
     else __syncthreads();
     pdl_wait();
-    if (threadIdx.x < 32) ring.prologue();
+    auto now = ring.start(), ahead = now;        // the block at work, and the next to be copied
+    if (threadIdx.x < 32) ring.prologue(ahead);
     uint32_t valid[NV];
     int col[NV];
     row_columns<VB, MODE>(at, ring.at, ring.bytes, col, valid);
@@ -562,9 +563,9 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
     bool bad = false;
     int64_t n = 0, last_gate = -1;
     for (; n < ring.count; ++n) {
-        int64_t gate_row, row;
-        int rows;
-        ring.where(n, gate_row, row, rows);
+        const int64_t gate_row = now.gate, row0 = now.row;
+        const int rows = now.rows;
+        ring.advance(now);
         if (gate_row != last_gate) {
             if (last_gate >= 0) {
                 write_gate(last_gate);
@@ -576,8 +577,7 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
         }
         if constexpr (GATE && !POST) stay_packed(gt);
         if constexpr (PRE && !REREAD) stay_packed(pw);
-        const int64_t row0 = row;
-        row += at.g;
+        const int64_t row = row0 + at.g;
         const bool here = at.g < rows;
         const bool ok = ring.wait(slot, use) && !bad;
         ring.template finish<T>(slot, row0, rows);
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
         for (int k = 0; k < NS; ++k) s.v[k] = a[FIRST + k].total();
         if constexpr (NS > 0) s.gather(red[n & 1], at.width);
         if (__syncthreads_or(!ok)) break;                     // uniform
-        if (threadIdx.x < 32 && n + p.nslots < ring.count) ring.issue(slot, n + p.nslots);
+        if (threadIdx.x < 32 && n + p.nslots < ring.count) ring.issue(slot, n + p.nslots, ahead);
         if constexpr (NS > 0) {
             s.totals(red[n & 1], at.width, at.gw0, at.wpg);
             if (CL && !exchange_sums<NS>(ex, s.v, p.cluster, rank, static_cast<uint32_t>(n), p)) bad = true;

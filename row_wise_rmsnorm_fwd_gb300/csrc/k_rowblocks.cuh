@@ -60,14 +60,31 @@ struct RowBlocks {
         }
     }
 
-    // Gate row, first row and number of rows of the unit's n-th block.
-    __device__ __forceinline__ void where(int64_t n, int64_t& gate, int64_t& row, int& rows) const {
-        const int64_t b = first + n * step;
-        gate = p.gates == 1 ? 0 : div_nonneg(b, p.blocks_per_gate);
-        row = gate * p.gate_rows + (b - gate * p.blocks_per_gate) * p.block_rows;
-        int64_t end = (gate + 1) * p.gate_rows;
+    // The unit's blocks in order: gate row, block within it, first row and number of rows.
+    struct Cursor {
+        int64_t gate, j, row;
+        int rows;
+    };
+    __device__ __forceinline__ void locate(Cursor& c) const {
+        c.row = c.gate * p.gate_rows + c.j * p.block_rows;
+        int64_t end = (c.gate + 1) * p.gate_rows;
         if (end > p.rows) end = p.rows;
-        rows = static_cast<int>(end - row < p.block_rows ? end - row : p.block_rows);
+        c.rows = static_cast<int>(end - c.row < p.block_rows ? end - c.row : p.block_rows);
+    }
+    __device__ __forceinline__ Cursor start() const {
+        Cursor c;
+        c.gate = p.gates == 1 ? 0 : div_nonneg(first, p.blocks_per_gate);
+        c.j = first - c.gate * p.blocks_per_gate;
+        locate(c);
+        return c;
+    }
+    __device__ __forceinline__ void advance(Cursor& c) const {
+        c.j += step;
+        if (p.gates > 1 && c.j == p.blocks_per_gate) {     // step is 1 then
+            c.j = 0;
+            ++c.gate;
+        }
+        locate(c);
     }
 
     // Shared-memory address of array a (counted with the absent ones) in a slot.
@@ -82,19 +99,20 @@ struct RowBlocks {
         return RAGGED ? static_cast<int>(row * row_bytes % 16) : 0;
     }
 
-    // One warp: start the copies of block n into `slot`.
-    __device__ __forceinline__ void issue(int slot, int64_t n) const {
+    // One warp: start the copies of the n-th block, at `c`, into `slot`, and go on to the next.
+    __device__ __forceinline__ void issue(int slot, int64_t n, Cursor& c) const {
         const int lane = threadIdx.x & 31;
         const uint32_t bar = bars + 8 * slot;
 #if RMSNORM_FAULT_INJECT
         if (p.fault == kFaultStagedWithholdCopy && n == 0) {   // armed for bytes that never come
             if (lane == 0) mbar_arrive_expect_tx(bar, 16);
+            advance(c);
             return;
         }
 #endif
-        int64_t gate, row;
-        int rows;
-        where(n, gate, row, rows);
+        const int64_t row = c.row;
+        const int rows = c.rows;
+        advance(c);
         if constexpr (!RAGGED) {
             if (lane != 0) return;
             // one row of a slice, or whole rows, which follow one another
@@ -130,8 +148,8 @@ struct RowBlocks {
         }
     }
 
-    __device__ __forceinline__ void prologue() const {
-        for (int k = 0; k < p.nslots && k < count; ++k) issue(k, k);
+    __device__ __forceinline__ void prologue(Cursor& c) const {
+        for (int k = 0; k < p.nslots && k < count; ++k) issue(k, k, c);
     }
 
     // All threads, after a block has landed: what the arrays' last row, if it is the
