@@ -49,19 +49,17 @@
 extern "C" {
 #endif
 
+/* The heads of q or of k; strides in elements, of batch, token and head. */
 typedef struct {
-    const void* p;
-    int64_t stride[3];          /* elements: batch, token, head */
-} rmsnorm_view_t;
-
-/* The heads of q or of k. */
-typedef struct {
-    rmsnorm_view_t x;           /* forward; backward: read with norm only */
-    rmsnorm_view_t dy;          /* backward */
-    rmsnorm_view_t out;         /* written: the turned heads; backward: dx */
+    const void* x;              /* forward; backward: read with norm only */
+    const void* dy;             /* backward */
+    void* out;                  /* written: the turned heads; backward: dx */
     const void* w;              /* head_dim elements of the same type, NULL: ones */
     float* dw;                  /* backward with norm: head_dim floats, or NULL */
     int64_t heads;
+    int64_t x_stride[3];
+    int64_t dy_stride[3];
+    int64_t out_stride[3];
 } rmsnorm_rope_heads_t;
 
 typedef struct {

@@ -71,13 +71,11 @@ class rmsnorm_block_t(ctypes.Structure):
                 ("post_norm", ctypes.c_int32), ("pre_norm", ctypes.c_int32)]
 
 
-class rmsnorm_view_t(ctypes.Structure):
-    _fields_ = [("p", ctypes.c_void_p), ("stride", ctypes.c_int64 * 3)]
-
-
 class rmsnorm_rope_heads_t(ctypes.Structure):
-    _fields_ = [("x", rmsnorm_view_t), ("dy", rmsnorm_view_t), ("out", rmsnorm_view_t),
-                ("w", ctypes.c_void_p), ("dw", ctypes.c_void_p), ("heads", ctypes.c_int64)]
+    _fields_ = [("x", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("w", ctypes.c_void_p), ("dw", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64 * 3), ("dy_stride", ctypes.c_int64 * 3),
+                ("out_stride", ctypes.c_int64 * 3)]
 
 
 class rmsnorm_rope_t(ctypes.Structure):
@@ -961,7 +959,8 @@ def rowsoftmax_relbias_bucket(relative: int, num_buckets: int, max_distance: int
 # ------------------------------------------------ the boundary of two blocks --
 
 _PACK_BLOCK = struct.Struct("4q4f2i").pack        # rmsnorm_block_t
-_PACK_HEADS = struct.Struct("15q").pack           # rmsnorm_rope_heads_t
+_PACK_POINTERS = struct.Struct("5q").pack         # rmsnorm_rope_heads_t: the pointers,
+_PACK_LAYOUT = struct.Struct("10q").pack          # and heads and strides
 _PACK_ROPE = struct.Struct("4q4i2f").pack         # rmsnorm_rope_t
 
 
@@ -1283,12 +1282,18 @@ def _heads(name, t, dtype, shape, index):
         raise ValueError(f"{name} must be on device cuda:{index}, got {t.device}")
 
 
-def _view(t):
-    """Pointer and strides of batch, token and head; tokens alone: one batch."""
+def _strides(t):
+    """Strides of batch, token and head; tokens alone: one batch."""
     if t is None:
-        return 0, 0, 0, 0
+        return 0, 0, 0
     s = t.stride()
-    return (t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else (t.data_ptr(), 0, s[0], s[1])
+    return s[:3] if len(s) == 4 else (0, s[0], s[1])
+
+
+def _dense(shape):
+    """The strides of a new tensor of this shape."""
+    seq, heads, dim = shape[-3:]
+    return seq * heads * dim, heads * dim, dim
 
 
 def _rope_shapes(first, other):
@@ -1315,10 +1320,18 @@ def _sig(t):
 _ROPE_PLANS = {}
 
 
+def _rope_layout(back, x, y, out):
+    """Heads and strides, packed: forward y is x of the C struct, backward dy."""
+    if back:
+        return _PACK_LAYOUT(y.shape[-2], *_strides(x), *_strides(y), *out)
+    return _PACK_LAYOUT(y.shape[-2], *_strides(y), 0, 0, 0, *out)
+
+
 def _rope_plan(key, want, norm, first, other, freqs, positions, xs, ws):
     """Check a call and keep (dtype code, device, batch, seq, head_dim, rot_dim, number of
-    positions, their bytes, heads, shapes of q and k, whether contiguous).  first and other:
-    q and k, or their gradients; xs: q and k where they are read beside those, else None."""
+    positions, their bytes, heads of both, shapes of q and k, whether contiguous, packed
+    layouts with new outputs).  first and other: q and k, or their gradients; xs: q and k where
+    they are read beside those, else None."""
     torch = _T
     code = _code(first, want)
     shape, index = _rope_shapes(first, other)
@@ -1355,9 +1368,12 @@ def _rope_plan(key, want, norm, first, other, freqs, positions, xs, ws):
         n = max(1, positions.numel())
     batch, seq = lead if len(lead) == 2 else (1, lead[0])
     plan = (code, index, batch, seq, dim, 2 * half, n, size,
-            (shape[-2], 0 if other is None else other.shape[-2]),
+            shape[-2] + (0 if other is None else other.shape[-2]),
             (shape, None if other is None else other.shape),
-            (first.is_contiguous(), other is not None and other.is_contiguous()))
+            (first.is_contiguous(), other is not None and other.is_contiguous()),
+            tuple(None if y is None else _rope_layout(xs is not None, x if norm else None, y,
+                                                      _dense(y.shape))
+                  for x, y in zip(xs or (None, None), (first, other))))
     if len(_ROPE_PLANS) >= 1024:
         _ROPE_PLANS.clear()
     _ROPE_PLANS[key] = plan
@@ -1399,17 +1415,19 @@ def _like(t, shape, contiguous):
 
 
 def _rope_fwd_on(handle, name, plan, q, k, q_w, k_w, q_out, k_out, rule, options):
-    code, _, batch, seq, dim, _, _, _, heads, shapes, dense = plan
+    code, _, batch, seq, dim, _, _, _, _, shapes, dense, layouts = plan
+    hq, hk = layouts
     if q_out is None:
         q_out = _like(q, shapes[0], dense[0])
-    hq = _PACK_HEADS(*_view(q), 0, 0, 0, 0, *_view(q_out), 0 if q_w is None else q_w.data_ptr(), 0,
-                     heads[0])
-    hk = None
+    else:
+        hq = _rope_layout(False, None, q, _strides(q_out))
+    hq = _PACK_POINTERS(q.data_ptr(), 0, q_out.data_ptr(), 0 if q_w is None else q_w.data_ptr(), 0) + hq
     if k is not None:
         if k_out is None:
             k_out = _like(k, shapes[1], dense[1])
-        hk = _PACK_HEADS(*_view(k), 0, 0, 0, 0, *_view(k_out), 0 if k_w is None else k_w.data_ptr(),
-                         0, heads[1])
+        else:
+            hk = _rope_layout(False, None, k, _strides(k_out))
+        hk = _PACK_POINTERS(k.data_ptr(), 0, k_out.data_ptr(), 0 if k_w is None else k_w.data_ptr(), 0) + hk
     if batch and seq:
         st = (_lib or load()).rmsnorm_rope_fwd_ex(
             code, hq, hk, batch, seq, dim, rule, None if options is None else _opt(options), handle)
@@ -1488,22 +1506,27 @@ def _rope_workspace(code, batch, seq, heads, dim, index):
 
 def _rope_bwd_on(handle, name, plan, dq, dk, q, k, q_w, k_w, dq_in, dk_in, dq_w, dk_w, weight_grads,
                  workspace, rule, options):
-    code, index, batch, seq, dim, _, _, _, heads, shapes, dense = plan
+    code, index, batch, seq, dim, _, _, _, heads, shapes, dense, layouts = plan
     f32 = _T.float32
+    hq, hk = layouts
     if dq_in is None:
         dq_in = _like(dq, shapes[0], dense[0])
+    else:
+        hq = _rope_layout(True, q, dq, _strides(dq_in))
     if dq_w is None and weight_grads and q_w is not None:
         dq_w = _T.empty_like(q_w, dtype=f32)
-    hq = _PACK_HEADS(*_view(q), *_view(dq), *_view(dq_in), 0 if q_w is None else q_w.data_ptr(),
-                     0 if dq_w is None else dq_w.data_ptr(), heads[0])
-    hk = None
+    hq = _PACK_POINTERS(0 if q is None else q.data_ptr(), dq.data_ptr(), dq_in.data_ptr(),
+                        0 if q_w is None else q_w.data_ptr(), 0 if dq_w is None else dq_w.data_ptr()) + hq
     if dk is not None:
         if dk_in is None:
             dk_in = _like(dk, shapes[1], dense[1])
+        else:
+            hk = _rope_layout(True, k, dk, _strides(dk_in))
         if dk_w is None and weight_grads and k_w is not None:
             dk_w = _T.empty_like(k_w, dtype=f32)
-        hk = _PACK_HEADS(*_view(k), *_view(dk), *_view(dk_in), 0 if k_w is None else k_w.data_ptr(),
-                         0 if dk_w is None else dk_w.data_ptr(), heads[1])
+        hk = _PACK_POINTERS(0 if k is None else k.data_ptr(), dk.data_ptr(), dk_in.data_ptr(),
+                            0 if k_w is None else k_w.data_ptr(),
+                            0 if dk_w is None else dk_w.data_ptr()) + hk
     if not batch or not seq:
         for dw in (dq_w, dk_w):
             if dw is not None:
@@ -1511,8 +1534,7 @@ def _rope_bwd_on(handle, name, plan, dq, dk, q, k, q_w, k_w, dq_in, dk_in, dq_w,
         return dq_in, dk_in, dq_w, dk_w
     at, size = None, 0
     if dq_w is not None or dk_w is not None:
-        ws, size = _room(workspace, _rope_workspace(code, batch, seq, heads[0] + heads[1], dim, index),
-                         dq)
+        ws, size = _room(workspace, _rope_workspace(code, batch, seq, heads, dim, index), dq)
         at = ws.data_ptr()
     st = (_lib or load()).rmsnorm_rope_bwd_ex(code, hq, hk, batch, seq, dim, rule, at, size,
                                               None if options is None else _opt(options), handle)

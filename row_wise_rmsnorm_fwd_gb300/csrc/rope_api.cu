@@ -93,16 +93,17 @@ struct Box {
 };
 
 // false: strides out of range.
-bool box_of(const rmsnorm_view_t& v, int64_t batch, int64_t seq, int64_t heads, int64_t dim, Box* b) {
-    b->p = reinterpret_cast<uintptr_t>(v.p);
+bool box_of(const void* p, const int64_t (&stride)[3], int64_t batch, int64_t seq, int64_t heads,
+            int64_t dim, Box* b) {
+    b->p = reinterpret_cast<uintptr_t>(p);
     const int64_t n[3] = {batch, seq, heads};
     b->dim = dim;
     b->extent = dim;
     for (int k = 0; k < 3; ++k) {
         b->n[k] = n[k];
-        b->stride[k] = v.stride[k];
+        b->stride[k] = stride[k];
         int64_t far;
-        if (v.stride[k] < 0 || __builtin_mul_overflow(n[k] - 1, v.stride[k], &far) ||
+        if (stride[k] < 0 || __builtin_mul_overflow(n[k] - 1, stride[k], &far) ||
             __builtin_add_overflow(b->extent, far, &b->extent) || b->extent > (INT64_MAX >> 4))
             return false;
     }
@@ -164,8 +165,8 @@ bool apart(const Box& a, const Span& s, int sz) {
     return !overlaps(Span{a.p, static_cast<uint64_t>(a.extent) * sz}, s);
 }
 
-RopeView view_of(const rmsnorm_view_t& v) {
-    return RopeView{const_cast<void*>(v.p), v.stride[0], v.stride[1], v.stride[2]};
+RopeView view_of(const void* p, const int64_t (&stride)[3]) {
+    return RopeView{const_cast<void*>(p), stride[0], stride[1], stride[2]};
 }
 
 rmsnorm_status_t check_options(const rmsnorm_options_t* opt, RopeCall* c) {
@@ -236,21 +237,21 @@ rmsnorm_status_t check_call(int32_t dtype, const rmsnorm_rope_heads_t* q, const 
         const rmsnorm_rope_heads_t* t = both[i];
         if (!t) continue;
         const bool with_x = !back || r->norm;
-        if (!t->out.p || (with_x && !t->x.p) || (back && !t->dy.p)) return RMSNORM_ERR_INVALID_ARG;
+        if (!t->out || (with_x && !t->x) || (back && !t->dy)) return RMSNORM_ERR_INVALID_ARG;
         if (t->dw && !(back && r->norm)) return RMSNORM_ERR_INVALID_ARG;
-        if (!aligned(t->out.p, sz) || (with_x && !aligned(t->x.p, sz)) || (back && !aligned(t->dy.p, sz)) ||
+        if (!aligned(t->out, sz) || (with_x && !aligned(t->x, sz)) || (back && !aligned(t->dy, sz)) ||
             !aligned(t->w, sz) || !aligned(t->dw, 4))
             return RMSNORM_ERR_INVALID_ARG;
-        if ((with_x && !box_of(t->x, b1, s1, t->heads, dim, &in[i])) ||
-            (back && !box_of(t->dy, b1, s1, t->heads, dim, &in[2 + i])) ||
-            !box_of(t->out, b1, s1, t->heads, dim, &out[i]) || !distinct(out[i]))
+        if ((with_x && !box_of(t->x, t->x_stride, b1, s1, t->heads, dim, &in[i])) ||
+            (back && !box_of(t->dy, t->dy_stride, b1, s1, t->heads, dim, &in[2 + i])) ||
+            !box_of(t->out, t->out_stride, b1, s1, t->heads, dim, &out[i]) || !distinct(out[i]))
             return RMSNORM_ERR_INVALID_ARG;
         if (r->norm) small[2 + i] = span(t->w, row);
         small[4 + i] = span(t->dw, static_cast<uint64_t>(dim) * 4);
         RopeHeads& h = p.t[i];
-        if (with_x) h.x = view_of(t->x);
-        if (back) h.dy = view_of(t->dy);
-        h.out = view_of(t->out);
+        if (with_x) h.x = view_of(t->x, t->x_stride);
+        if (back) h.dy = view_of(t->dy, t->dy_stride);
+        h.out = view_of(t->out, t->out_stride);
         h.w = r->norm ? t->w : nullptr;
         h.dw = t->dw;
         h.heads = static_cast<int32_t>(t->heads);

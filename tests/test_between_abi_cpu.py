@@ -107,9 +107,9 @@ def test_block_backward_refuses(lib):
 
 
 def heads(x=X, dy=0, out=Y, w=POST, dw=0, n=4, d=8, strides=None, out_strides=None):
-    view = lambda p, s: binding.rmsnorm_view_t(p, (ctypes.c_int64 * 3)(*s))  # noqa: E731
+    three = lambda s: (ctypes.c_int64 * 3)(*s)  # noqa: E731
     s = strides or (3 * n * d, n * d, d)
-    return binding.rmsnorm_rope_heads_t(view(x, s), view(dy, s), view(out, out_strides or s), w, dw, n)
+    return binding.rmsnorm_rope_heads_t(x, dy, out, w, dw, n, three(s), three(s), three(out_strides or s))
 
 
 def rope(freqs=FREQ, positions=POS, n_positions=6, start=0, position_bytes=8, rot_dim=8,
