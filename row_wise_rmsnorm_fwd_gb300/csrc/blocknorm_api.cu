@@ -95,7 +95,7 @@ int at_most(int64_t want, int64_t most) { return static_cast<int>(want < most ? 
 // --------------------------------------------------------------- staged rows --
 
 constexpr int64_t kBlockThreads = 256;        // threads that narrow rows share a CTA of
-constexpr int64_t kBwdCtasPerSm = 4;          // at most, so that there are few parts
+constexpr int64_t kBwdCtasPerSm = 4;          // CTAs, or clusters, at most: few parts
 
 int64_t pow2_ceil(int64_t v) {
     int64_t p = 1;
@@ -183,8 +183,9 @@ rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t read_bits, uintptr_t other_
                 p.row_slot = static_cast<int32_t>(row_slot);
                 p.status = c->dv.status;
                 if (!p.timeout_ns) p.timeout_ns = kDefaultTimeoutNs;
-                if (back && best > kBwdCtasPerSm && cluster == 1) best = kBwdCtasPerSm;
                 int64_t units = cluster > 1 ? best : static_cast<int64_t>(c->dv.sms) * best;
+                // what the workspace has parts for
+                if (back && units > kBwdCtasPerSm * c->dv.sms) units = kBwdCtasPerSm * c->dv.sms;
                 if (units > p.blocks) units = p.blocks;
                 p.units = units;
                 s->grid = static_cast<int>(units * cluster);

@@ -264,14 +264,6 @@ __device__ __forceinline__ float group_allreduce_sum(float v, int g) {
     return v;
 }
 
-// --------------------------------------------------------------- integers --
-
-// a / b for a >= 0, b > 0; numbers of 32 bits, as most are, in a quarter of the instructions.
-__device__ __forceinline__ int64_t div_nonneg(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
 // ------------------------------------------------------------ status word --
 
 __device__ __forceinline__ void report_timeout(unsigned* status, unsigned site) {

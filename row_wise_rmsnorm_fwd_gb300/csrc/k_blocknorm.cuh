@@ -3,6 +3,7 @@
 #pragma once
 #include "blocknorm_launch.h"
 #include "common.cuh"
+#include "integers.cuh"
 
 namespace rmsnorm {
 

@@ -9,6 +9,7 @@
 // No fp64, and no table in memory.
 #pragma once
 #include "common.cuh"
+#include "integers.cuh"
 #include "rope_launch.h"
 
 namespace rmsnorm {

@@ -15,6 +15,7 @@
 #pragma once
 #include "blocknorm_launch.h"
 #include "common.cuh"
+#include "integers.cuh"
 
 namespace rmsnorm {
 

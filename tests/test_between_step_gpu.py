@@ -259,6 +259,41 @@ def test_back_to_back(n, t):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("n", [192, 1030, 4096])
+def test_weights_written_by_the_call_before(n, t):
+    """Weights and gates that a call writes right behind one that read them, and right before
+    one that reads them again."""
+    x, r = make((400, n), t, 1).cuda(), make((400, n), t, 2).cuda()
+    rows = [make((1, n), t, 10 + i).cuda() for i in range(6)]
+    freqs, _ = binding.rmsnorm_rope_freqs(64, device="cuda")
+    q = make((500, 6, 64), t, 4).cuda()
+    heads = [make((1, 1, 64), t, 20 + i).cuda() for i in range(6)]
+
+    def chain(sync):
+        wait = torch.cuda.synchronize if sync else (lambda: None)
+        w, qw, out = torch.ones_like(rows[0][0]), torch.ones_like(heads[0][0, 0]), []
+        for i in range(6):
+            h, y = binding.rmsnorm_block_fwd_ex(x, r, w, w, w)
+            wait()
+            d = binding.rmsnorm_block_bwd_ex(y, h, x, h, w, w, w)
+            wait()
+            tq, _ = binding.rmsnorm_rope_fwd_ex(q, None, freqs, None, qw)
+            wait()
+            binding.rmsnorm_rope_fwd_ex(heads[i], None, freqs, None, q_out=qw[None, None])
+            wait()
+            e = binding.rmsnorm_rope_bwd_ex(tq, None, freqs, None, q, None, qw)
+            wait()
+            binding.rmsnorm_block_fwd_ex(rows[i], rows[i], h=w[None], pre_norm=False)
+            wait()
+            out += [h, y, *d, tq, e[0], e[2]]
+        torch.cuda.synchronize()
+        return out
+
+    for a, b in zip(chain(False), chain(True)):
+        assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------- failure detection --
 
 @pytest.fixture(scope="module")

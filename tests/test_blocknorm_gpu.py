@@ -159,6 +159,24 @@ def test_rows_over_a_cluster(n, cluster, t):
 
 
 @pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("cluster,n", [(0, 64), (0, 512), (0, 2048), (2, 136), (2, 1024), (4, 1024),
+                                       (0, 66), (0, 1030)])
+def test_nothing_behind_the_workspace(cluster, n, t):
+    """More units of work than there are parts for: the workspace is left as it was behind its
+    size, and the sums are right."""
+    rule = RULES["scaled"]
+    options = {"path": "staged", "cluster": cluster} if cluster else None
+    for gate in ("channel", "sequence"):
+        v = inputs((60, 50), n, t, rule, gate)
+        g = on(v)
+        size = binding.rmsnorm_block_bwd_workspace(g["x"], g["gate"])
+        room = torch.full((size + (1 << 22),), 77, dtype=torch.uint8, device="cuda")
+        got = backward(g, rule, workspace=room[:size], options=options)
+        assert (room[size:] == 77).all()
+        check_backward(v, rule, got)
+
+
+@pytest.mark.parametrize("t", TYPES)
 def test_gate_shapes(t):
     """[hidden], [1, hidden], [batch, hidden], [batch, 1, hidden], [batch, seq, hidden]."""
     rule = RULES["scaled"]

@@ -310,6 +310,27 @@ def test_repeatable_and_any_workspace(tokens, t):
     assert part[2] is None and torch.equal(part[3], backward(g, f, rule)[3])
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("dim", [64, 1023])
+def test_gradients_without_weights_and_the_workspace(dim, t):
+    """dq_w of ones, if it is given, and nothing written behind the workspace."""
+    freqs, _ = freqs_of(32)
+    f = freqs.cuda()
+    rule = Rope(freqs)
+    v = inputs((3, 700), 5, 2, dim, t)
+    v["q_w"] = None
+    g = on(v)
+    size = binding.rmsnorm_rope_bwd_workspace(g["q"], g["k"])
+    room = torch.full((size + (1 << 20),), 77, dtype=torch.uint8, device="cuda")
+    dw = torch.empty(dim, device="cuda")
+    got = backward(g, f, rule, workspace=room[:size], dq_w=dw)
+    assert (room[size:] == 77).all() and got[2] is dw
+    want, tol = ref.rope_bwd(v["dq"], v["q"], None, rule, None)
+    close(dw, want[1], tol[1], "dq_w")
+    close(got[0], want[0], tol[0], "dq")
+    assert backward(g, f, rule)[2] is None
+
+
 def test_offsets_beyond_32_bits():
     """The last tokens of arrays of more than 2^31 elements."""
     freqs, _ = freqs_of(128)
