@@ -37,8 +37,10 @@ static BlockFn pick_reduce(int width, bool gates) {
 }
 
 BlockFn blocknorm_fwd_any_ptr(int dtype, int vb) { return pick_all(dtype, vb, kFwd); }
-BlockFn blocknorm_fwd_regs_ptr(int dtype) {
-    return dtype == 0 ? blocknorm_fwd_regs_kernel<float> : blocknorm_fwd_regs_kernel<__nv_bfloat16>;
+BlockFn blocknorm_fwd_regs_ptr(int dtype, int vb) {
+    if (dtype == 0) return vb == 8 ? blocknorm_fwd_regs_kernel<float, 8> : blocknorm_fwd_regs_kernel<float, 4>;
+    return vb == 8 ? blocknorm_fwd_regs_kernel<__nv_bfloat16, 8>
+           : vb == 4 ? blocknorm_fwd_regs_kernel<__nv_bfloat16, 4> : blocknorm_fwd_regs_kernel<__nv_bfloat16, 2>;
 }
 BlockFn blocknorm_bwd_rows_ptr(int dtype, int vb) { return pick_all(dtype, vb, kRows); }
 BlockFn blocknorm_bwd_cols_ptr(int dtype, int vb) { return pick_all(dtype, vb, kCols); }

@@ -201,15 +201,17 @@ rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t read_bits, uintptr_t other_
 
 // ------------------------------------------------------------------- forward --
 
-constexpr int64_t kRegsRowBytes = 1024;       // narrower rows would leave a CTA few threads
+constexpr int64_t kRegsRowBytes = 512;        // narrower rows share a CTA, staged in pieces
+constexpr int64_t kRegsBf16Threads = 768;     // wider bf16 rows: read for each sum
 
-// Rows of 8-byte vectors held in registers, a CTA to a row.  Leaves s->grid 0, status OK, where
-// rows are of other vectors or a CTA cannot hold one.
+// Rows of vectors of less than 16 bytes held in registers, a CTA to a row.  Leaves s->grid 0,
+// status OK, where they are wider or a CTA cannot hold one.
 rmsnorm_status_t plan_regs(BlockCall* c, int vb, LaunchShape* s, BlockFn* fn) {
     s->grid = 0;
     const int64_t block = div_up(div_up(c->p.nvec, kBlockRegsVecs), 32) * 32;
-    if (vb != 8 || block > kBlockRegsMaxThreads) return RMSNORM_OK;
-    *fn = blocknorm_fwd_regs_ptr(c->dtype);
+    if (vb == 16 || block > kBlockRegsMaxThreads) return RMSNORM_OK;
+    if (c->path == RMSNORM_PATH_AUTO && c->sz == 2 && block > kRegsBf16Threads) return RMSNORM_OK;
+    *fn = blocknorm_fwd_regs_ptr(c->dtype, vb);
     int occ = 0;
     if (cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(*fn),
                          static_cast<int>(block), 0, 1, &occ) != cudaSuccess)
@@ -248,7 +250,7 @@ rmsnorm_status_t fwd_run(int32_t dtype, const void* x, const void* residual, voi
     const uintptr_t other = bits(h) | bits(y) | bits(c.p.post_w) | bits(c.p.pre_w) | bits(c.p.gate);
     const int vb = widest_vector(read | other, hidden * c.sz, c.sz);
     c.p.nvec = static_cast<int32_t>(hidden / (vb / c.sz));
-    if (c.path == RMSNORM_PATH_ROWREG || (c.path == RMSNORM_PATH_AUTO && vb == 8 && hidden * c.sz >= kRegsRowBytes)) {
+    if (c.path == RMSNORM_PATH_ROWREG || (c.path == RMSNORM_PATH_AUTO && vb < 16 && hidden * c.sz >= kRegsRowBytes)) {
         LaunchShape s{0, 0, 1, 0};
         BlockFn fn = nullptr;
         st = plan_regs(&c, vb, &s, &fn);
@@ -256,7 +258,8 @@ rmsnorm_status_t fwd_run(int32_t dtype, const void* x, const void* residual, voi
         if (s.grid) return launch(c, fn, s, stream);
         if (c.path == RMSNORM_PATH_ROWREG) return RMSNORM_ERR_UNSUPPORTED;
     }
-    if (c.path != RMSNORM_PATH_TWOPASS) {
+    if (c.path == RMSNORM_PATH_STAGED ||
+        (c.path == RMSNORM_PATH_AUTO && (vb == 16 || hidden * c.sz < kRegsRowBytes))) {
         LaunchShape s{0, 0, 1, 0};
         BlockFn fn = nullptr;
         st = plan_staged(&c, read, other, 2, false, &s, &fn);

@@ -115,15 +115,17 @@ __global__ void __launch_bounds__(kBlockRowsThreads) blocknorm_fwd_any_kernel(co
     }
 }
 
-// Forward, rows of 8-byte vectors that are wide enough for a CTA of their own: as above, but
-// the row is held in registers, kBlockRegsVecs vectors to a thread, and read once.  Measured
-// (us, this / the kernel above / staged in pieces, k_blocknorm_staged.cuh): fp32 32768 x 2050
-// 218 / 225 / 261, 65536 x 514 110 / 238 / 148, 2555 x 2050 21.4 / 24.5 / 24.4, bf16 32768 x
-// 4100 257 / 296 / 292.  With vectors of 4 and 2 bytes the pieces win: bf16 65536 x 2050 376 /
-// 427 / 338, 65536 x 1027 288 / 334 / 262, fp32 65536 x 1027 315 / 302 / 304.
-template <typename T>
+// Forward, rows of vectors of less than 16 bytes that are wide enough for a CTA of their own: as
+// above, but the row is held in registers, kBlockRegsVecs vectors to a thread, and read once,
+// while the row before it is worked on.  Measured (us, this / the kernel above / staged in
+// pieces, k_blocknorm_staged.cuh): fp32 2555 x 2050 19.1 / 24.4 / 27.4 (21.6 without the next
+// row under way), 32768 x 2050 183 / 225 / 294, 131072 x 258 138 / 355 / 214,
+// 65536 x 1027 258 / 301 / 329, bf16 32768 x 4100 257 / 295 / 332, 65536 x 2050 357 / 424 / 373,
+// 131072 x 515 308 / 494 / 387; in bf16 rows that take more than 768 threads lose: 30000 x 8002
+// 583 / 541 / 593.
+template <typename T, int VB>
 __global__ void __launch_bounds__(kBlockRegsMaxThreads, 1) blocknorm_fwd_regs_kernel(const BlockParams p) {
-    constexpr int VB = 8, EPV = VecTraits<T, VB>::kElems, NV = kBlockRegsVecs;
+    constexpr int EPV = VecTraits<T, VB>::kElems, NV = kBlockRegsVecs;
     __shared__ float red[2][2][32];
     pdl_trigger();
     pdl_wait();
@@ -133,6 +135,14 @@ __global__ void __launch_bounds__(kBlockRegsMaxThreads, 1) blocknorm_fwd_regs_ke
     const int64_t mine = static_cast<int64_t>(threadIdx.x) * VB;
     const int apart = n * VB;
     int it = 0;
+    Vec<VB> nx[NV], nr[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (i < count) {
+            nx[i] = ld_stream<VB>(static_cast<const char*>(p.x) + blockIdx.x * row_bytes + mine + i * apart);
+            nr[i] = ld_stream<VB>(static_cast<const char*>(p.residual) + blockIdx.x * row_bytes + mine + i * apart);
+        }
+    }
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, it ^= 1) {
         const char* xs = static_cast<const char*>(p.x) + row * row_bytes + mine;
         const char* rs = static_cast<const char*>(p.residual) + row * row_bytes + mine;
@@ -142,9 +152,17 @@ __global__ void __launch_bounds__(kBlockRegsMaxThreads, 1) blocknorm_fwd_regs_ke
         Vec<VB> x[NV], r[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (i < count) {
-                x[i] = ld_stream<VB>(xs + i * apart);
-                r[i] = ld_stream<VB>(rs + i * apart);
+            x[i] = nx[i];
+            r[i] = nr[i];
+        }
+        if (row + gridDim.x < p.rows) {
+            const int64_t on = static_cast<int64_t>(gridDim.x) * row_bytes;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (i < count) {
+                    nx[i] = ld_stream<VB>(xs + on + i * apart);
+                    nr[i] = ld_stream<VB>(rs + on + i * apart);
+                }
             }
         }
         float scale = p.branch_scale;
@@ -225,7 +243,9 @@ __device__ __forceinline__ BlockFactors block_factors(const float (&s)[6], const
     return f;
 }
 
-// Any width: the factors of each row ...
+// Any width: the factors of each row ...  (Together, us and % of the HBM copy peak: bf16 65536 x
+// 8192 2275 (42), fp32 16384 x 4097 773 (31): every array is read twice, with a block barrier
+// for each row.)
 template <typename T, int VB>
 __global__ void __launch_bounds__(kBlockRowsThreads) blocknorm_bwd_rows_kernel(const BlockParams p) {
     constexpr int EPV = VecTraits<T, VB>::kElems;

@@ -8,6 +8,23 @@
 // Rows that are not whole 16-byte vectors, or weights or outputs off the boundaries: a
 // thread's 16 bytes are pieces of VB bytes each, taken G pieces apart, so that accesses stay
 // side by side; everything between load and store is the same.
+//
+// What bounds it: HBM, where rows fill their threads.  32 bytes a thread and up to 64
+// registers keep 32 warps to an SM forward; backward the column sums take a thread's 128
+// registers and 16 warps are all there are, so the instructions of a pass count, and the
+// blocks under way while it runs: a ring of three slots refilled as early as can be.  One
+// pass ahead with fewer blocks under way (the sums of the next row between the same barriers
+// as the outputs of this one, rows read again from shared memory) was slower: fp32 16384 x 8192
+// 658 us against 478.  Measured (calls back to back, us and % of the HBM copy peak):
+//   forward bf16 65536 x 4096 342 (92), 32768 x 8192 344 (92), 131072 x 1024 181 (87), 65536 x
+//     1280 136 (73), fp32 16384 x 4096 167 (95), 16384 x 8192 349 (91)
+//   backward bf16 65536 x 8192 951 (100), 32768 x 4096 259 (92), 131072 x 1024 249 (95), 32768 x
+//     5120 398 (75), 65536 x 1280 204 (73), fp32 16384 x 4096 273 (87), 16384 x 8192 498 (95)
+//   with a gate row for 512 rows backward bf16 32768 x 8192 494 (96), for 16 rows 642 (74)
+//   split rows: forward fp32 8192 x 16384 461 (69), backward 484 (98), bf16 16384 x 16384 680 (70)
+//   in pieces: forward bf16 262144 x 110 88 (39), fp32 262144 x 66 110 (37), backward 131072 x 130
+//     163 (37), 65536 x 1027 367 (65), bf16 65536 x 2050 884 (27), 65536 x 1027 587 (20)
+// The kernels for any width instead: forward bf16 65536 x 4096 524, backward 65536 x 8192 2275.
 #pragma once
 #include "k_blocknorm.cuh"
 #include "k_blockring.cuh"
@@ -121,8 +138,8 @@ __device__ __forceinline__ Vec<VB> take_piece(const Vec<16>& v, int j) {
 }
 
 // FAST: a branch for threads that have all pieces (all of a row but its last ones).  Measured
-// (us, with / without): forward bf16 65536 x 1027 261 / 464, 65536 x 2050 337 / 378, but fp32
-// 32768 x 2050 284 / 261, backward 500 / 464, bf16 65536 x 2050 709 / 608.
+// (us, with / without): forward bf16 65536 x 1027 261 / 464, 65536 x 2050 337 / 378, but with
+// 8-byte pieces fp32 32768 x 2050 284 / 261, and backward 500 / 464.
 //
 // A vector of a slot; zeros where (bit j of `on`: piece j) it is missing.  apart: bytes from
 // piece to piece.

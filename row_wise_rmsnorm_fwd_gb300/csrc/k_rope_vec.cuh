@@ -9,6 +9,18 @@
 // pairs for all of them: an angle is formed once for a warp's share of a token's heads, by
 // one of the lanes that need it.  A CTA works on q alone or on k alone, so a lane's
 // weights, and backward its column sums, stay in registers for all its tokens.
+//
+// What bounds it: HBM, where a token has eight rounds of heads or so; with fewer the token's
+// position, angles and addresses (about 200 instructions a warp) weigh more, and lanes are
+// idle where a head is not a power of two units.  Measured (calls back to back, us and % of
+// the HBM copy peak; heads of q + k):
+//   forward with norms bf16 65536 tokens, 32 + 8 of 128: 219 (91), interleaved 218 (91), without
+//     norms 204 (97); 16 + 16 of 64: 115 (69); 32768, 16 + 4 of 256, 64 turned: 117 (84);
+//     fp32 32768, 32 + 8 of 128: 203 (98)
+//   backward the same: 316 (94), 320 (93), 204 (97), 162 (73), 166 (89), 310 (96)
+//   7 + 1 of 96: 84 (36) and 122 (37); 28 + 4 of 80, 20 turned (vectors of 4 bytes): 373 (27)
+//     and 554 (27)
+// A warp per head with every angle formed for itself (k_rope.cuh): 1328 and 3876.
 #pragma once
 #include <type_traits>
 

@@ -233,6 +233,28 @@ def test_weights_and_outputs_off_the_boundaries(lead, n, t):
 
 
 @pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("lead,n", [((7,), 1), ((40, 50), 3), ((9, 5), 259), ((1000,), 514),
+                                    ((500,), 2050), ((300,), 4095), ((5,), 8194)])
+def test_rows_in_registers(lead, n, t):
+    """Rows of short vectors held in registers, several to a CTA one after the other."""
+    for rule, gate in (("scaled", "sequence"), ("post", "channel"), ("pre", "none"), ("none", "element")):
+        v = inputs(lead, n, t, RULES[rule], gate)
+        g = on(v)
+        options = {"path": "rowreg"}
+        if n == 8194:                       # 4097 vectors, one more than a CTA holds
+            with pytest.raises(binding.RmsnormError) as e:
+                forward(g, RULES[rule], options=options)
+            assert e.value.status == binding.RMSNORM_ERR_UNSUPPORTED
+            continue
+        check_forward(v, RULES[rule], forward(g, RULES[rule], options=options))
+        where = dict(h=g["residual"], y=g["x"]) if RULES[rule].pre else dict(h=g["residual"])
+        check_forward(v, RULES[rule], forward(g, RULES[rule], options=options, **where))
+    with pytest.raises(binding.RmsnormError):
+        g = on(inputs((3,), 64, t, RULES["both"]))
+        forward(g, RULES["both"], options={"path": "rowreg"})
+
+
+@pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("n", [5, 33, 1027, 2050, 4097, 6004])
 def test_nothing_behind_the_arrays(n, t):
     """Arrays that end where their memory does hold NaN from there on: nothing of it is
