@@ -92,7 +92,7 @@ rmsnorm_status_t rmsnorm_block_fwd_bf16(const uint16_t* x, const uint16_t* resid
  * 256 KB, split over a thread-block cluster above 32 KB, backward 16 KB, which
  * opt->cluster = 2, 4, 8 or 16 forces; else rows of 16 bytes to 24 KB, backward 16 KB;
  * RMSNORM_ERR_UNSUPPORTED otherwise), RMSNORM_PATH_ROWREG (forward; rows held in registers, at
- * most 4096 vectors of 2, 4 or 8 bytes: what one of those is the widest for; else
+ * most 8192 vectors of 2, 4 or 8 bytes: what one of those is the widest for; else
  * RMSNORM_ERR_UNSUPPORTED) or RMSNORM_PATH_TWOPASS (a CTA per row that reads it again for each
  * sum: any width and alignment); opt->wait_timeout_ns; and in the test build of the library
  * opt->fault_inject with RMSNORM_PATH_STAGED: 1 = each CTA's first copy is withheld, 2 =

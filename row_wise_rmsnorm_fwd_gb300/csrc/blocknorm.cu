@@ -37,10 +37,15 @@ static BlockFn pick_reduce(int width, bool gates) {
 }
 
 BlockFn blocknorm_fwd_any_ptr(int dtype, int vb) { return pick_all(dtype, vb, kFwd); }
-BlockFn blocknorm_fwd_regs_ptr(int dtype, int vb) {
-    if (dtype == 0) return vb == 8 ? blocknorm_fwd_regs_kernel<float, 8> : blocknorm_fwd_regs_kernel<float, 4>;
-    return vb == 8 ? blocknorm_fwd_regs_kernel<__nv_bfloat16, 8>
-           : vb == 4 ? blocknorm_fwd_regs_kernel<__nv_bfloat16, 4> : blocknorm_fwd_regs_kernel<__nv_bfloat16, 2>;
+template <typename T, int VB>
+static BlockFn pick_regs(int nv) {
+    return nv == kBlockRegsVecs ? blocknorm_fwd_regs_kernel<T, VB, kBlockRegsVecs, true>
+                                : blocknorm_fwd_regs_kernel<T, VB, 2 * kBlockRegsVecs, false>;
+}
+BlockFn blocknorm_fwd_regs_ptr(int dtype, int vb, int nv) {
+    if (dtype == 0) return vb == 8 ? pick_regs<float, 8>(nv) : pick_regs<float, 4>(nv);
+    return vb == 8 ? pick_regs<__nv_bfloat16, 8>(nv)
+           : vb == 4 ? pick_regs<__nv_bfloat16, 4>(nv) : pick_regs<__nv_bfloat16, 2>(nv);
 }
 BlockFn blocknorm_bwd_rows_ptr(int dtype, int vb) { return pick_all(dtype, vb, kRows); }
 BlockFn blocknorm_bwd_cols_ptr(int dtype, int vb) { return pick_all(dtype, vb, kCols); }

@@ -138,6 +138,11 @@ rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t read_bits, uintptr_t other_
     // CTAs share it: 16384 x 4096 247 us instead of 276 (3584: 225 / 227, bf16 8192: 716 / 579).
     int64_t least = 1;
     if (back && c->sz == 4 && vb == 16 && group_of(nvec) == kBlockBwdMaxThreads) least = 2;
+    // Forward rows that have to be split, which costs two exchanges a row, are split into slices of
+    // at most 256 threads, so that an SM has several CTAs: fp32 8192 x 16384 with clusters of 2 /
+    // 4 / 8 461 / 443 / 414 us, 8192 x 12288 379 / 357 / 350, bf16 8192 x 32768 508 / 501 / 475.
+    if (!back && vb == 16 && group_of(nvec) > max_threads)
+        while (least < kMaxCluster && group_of(div_up(nvec, least)) > kBlockThreads) least *= 2;
     for (int64_t cluster = c->cluster ? c->cluster : least; cluster <= (vb < 16 ? 1 : kMaxCluster); cluster *= 2) {
         const int64_t slice = div_up(nvec, cluster);
         // a split row's CTA is one group of whole warps, with a thread for each rank to send to
@@ -202,16 +207,22 @@ rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t read_bits, uintptr_t other_
 // ------------------------------------------------------------------- forward --
 
 constexpr int64_t kRegsRowBytes = 512;        // narrower rows share a CTA, staged in pieces
-constexpr int64_t kRegsBf16Threads = 768;     // wider bf16 rows: read for each sum
+constexpr int64_t kRegsBf16Threads = 768;     // wider bf16 rows: twice as much to a thread
 
 // Rows of vectors of less than 16 bytes held in registers, a CTA to a row.  Leaves s->grid 0,
 // status OK, where they are wider or a CTA cannot hold one.
 rmsnorm_status_t plan_regs(BlockCall* c, int vb, LaunchShape* s, BlockFn* fn) {
     s->grid = 0;
-    const int64_t block = div_up(div_up(c->p.nvec, kBlockRegsVecs), 32) * 32;
+    int nv = kBlockRegsVecs;
+    int64_t block = div_up(div_up(c->p.nvec, nv), 32) * 32;
+    if (block > (c->sz == 2 ? kRegsBf16Threads : kBlockRegsMaxThreads)) {
+        nv *= 2;
+        block = div_up(div_up(c->p.nvec, nv), 32) * 32;
+    }
     if (vb == 16 || block > kBlockRegsMaxThreads) return RMSNORM_OK;
-    if (c->path == RMSNORM_PATH_AUTO && c->sz == 2 && block > kRegsBf16Threads) return RMSNORM_OK;
-    *fn = blocknorm_fwd_regs_ptr(c->dtype, vb);
+    // odd bf16 rows of most of an SM's threads: 32768 x 8191 1008 us, read for each sum 846
+    if (c->path == RMSNORM_PATH_AUTO && vb == 2 && block > kRegsBf16Threads) return RMSNORM_OK;
+    *fn = blocknorm_fwd_regs_ptr(c->dtype, vb, nv);
     int occ = 0;
     if (cached_occupancy(c->dv.dev, c->dv.smem_optin, reinterpret_cast<KernelFn>(*fn),
                          static_cast<int>(block), 0, 1, &occ) != cudaSuccess)

@@ -63,8 +63,8 @@ using BlockFn = void (*)(BlockParams);
 
 // dtype: 0 = fp32, 1 = bf16; vb = bytes per vector.  Any width.
 BlockFn blocknorm_fwd_any_ptr(int dtype, int vb);
-// Rows of vectors of less than 16 bytes, kBlockRegsVecs to a thread.
-BlockFn blocknorm_fwd_regs_ptr(int dtype, int vb);
+// Rows of vectors of less than 16 bytes, nv = kBlockRegsVecs or twice as many to a thread.
+BlockFn blocknorm_fwd_regs_ptr(int dtype, int vb, int nv);
 constexpr int kBlockRegsVecs = 4;
 constexpr int kBlockRegsMaxThreads = 1024;
 BlockFn blocknorm_bwd_rows_ptr(int dtype, int vb);

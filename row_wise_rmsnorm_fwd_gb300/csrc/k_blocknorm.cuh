@@ -121,11 +121,13 @@ __global__ void __launch_bounds__(kBlockRowsThreads) blocknorm_fwd_any_kernel(co
 // pieces, k_blocknorm_staged.cuh): fp32 2555 x 2050 19.1 / 24.4 / 27.4 (21.6 without the next
 // row under way), 32768 x 2050 183 / 225 / 294, 131072 x 258 138 / 355 / 214,
 // 65536 x 1027 258 / 301 / 329, bf16 32768 x 4100 257 / 295 / 332, 65536 x 2050 357 / 424 / 373,
-// 131072 x 515 308 / 494 / 387; in bf16 rows that take more than 768 threads lose: 30000 x 8002
-// 583 / 541 / 593.
-template <typename T, int VB>
+// 131072 x 515 308 / 494 / 387.  Twice as many vectors to a thread: bf16 30000 x 8002 487 / 541 /
+// 592 (half as many 583), fp32 16384 x 8190 367 / 536, 16384 x 12002 954 / 898.
+// AHEAD: the next row is loaded while one is worked on (with twice as many vectors to a thread
+// there are no registers for it).
+template <typename T, int VB, int NV, bool AHEAD>
 __global__ void __launch_bounds__(kBlockRegsMaxThreads, 1) blocknorm_fwd_regs_kernel(const BlockParams p) {
-    constexpr int EPV = VecTraits<T, VB>::kElems, NV = kBlockRegsVecs;
+    constexpr int EPV = VecTraits<T, VB>::kElems;
     __shared__ float red[2][2][32];
     pdl_trigger();
     pdl_wait();
@@ -136,34 +138,32 @@ __global__ void __launch_bounds__(kBlockRegsMaxThreads, 1) blocknorm_fwd_regs_ke
     const int apart = n * VB;
     int it = 0;
     Vec<VB> nx[NV], nr[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (i < count) {
-            nx[i] = ld_stream<VB>(static_cast<const char*>(p.x) + blockIdx.x * row_bytes + mine + i * apart);
-            nr[i] = ld_stream<VB>(static_cast<const char*>(p.residual) + blockIdx.x * row_bytes + mine + i * apart);
-        }
-    }
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, it ^= 1) {
+    auto load_row = [&](int64_t row, Vec<VB> (&x)[NV], Vec<VB> (&r)[NV]) {
         const char* xs = static_cast<const char*>(p.x) + row * row_bytes + mine;
         const char* rs = static_cast<const char*>(p.residual) + row * row_bytes + mine;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (i < count) {
+                x[i] = ld_stream<VB>(xs + i * apart);
+                r[i] = ld_stream<VB>(rs + i * apart);
+            }
+        }
+    };
+    if constexpr (AHEAD) load_row(blockIdx.x, nx, nr);
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, it ^= 1) {
         const char* gate = at_or_null(p.gate, row / p.gate_rows * row_bytes + mine);
         const char* post_w = at_or_null(p.post ? p.post_w : nullptr, mine);
         const char* pre_w = at_or_null(p.pre_w, mine);
         Vec<VB> x[NV], r[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            x[i] = nx[i];
-            r[i] = nr[i];
-        }
-        if (row + gridDim.x < p.rows) {
-            const int64_t on = static_cast<int64_t>(gridDim.x) * row_bytes;
+        if constexpr (AHEAD) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (i < count) {
-                    nx[i] = ld_stream<VB>(xs + on + i * apart);
-                    nr[i] = ld_stream<VB>(rs + on + i * apart);
-                }
+                x[i] = nx[i];
+                r[i] = nr[i];
             }
+            if (row + gridDim.x < p.rows) load_row(row + gridDim.x, nx, nr);
+        } else {
+            load_row(row, x, r);
         }
         float scale = p.branch_scale;
         if (p.post) {

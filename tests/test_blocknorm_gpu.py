@@ -234,14 +234,15 @@ def test_weights_and_outputs_off_the_boundaries(lead, n, t):
 
 @pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("lead,n", [((7,), 1), ((40, 50), 3), ((9, 5), 259), ((1000,), 514),
-                                    ((500,), 2050), ((300,), 4095), ((5,), 8194)])
+                                    ((500,), 2050), ((300,), 4095), ((200,), 8191), ((3, 70), 12002),
+                                    ((5,), 16391)])
 def test_rows_in_registers(lead, n, t):
     """Rows of short vectors held in registers, several to a CTA one after the other."""
     for rule, gate in (("scaled", "sequence"), ("post", "channel"), ("pre", "none"), ("none", "element")):
         v = inputs(lead, n, t, RULES[rule], gate)
         g = on(v)
         options = {"path": "rowreg"}
-        if n == 8194:                       # 4097 vectors, one more than a CTA holds
+        if n == 16391:                      # more vectors than a CTA holds
             with pytest.raises(binding.RmsnormError) as e:
                 forward(g, RULES[rule], options=options)
             assert e.value.status == binding.RMSNORM_ERR_UNSUPPORTED
