@@ -21,7 +21,7 @@
 //   backward bf16 65536 x 8192 951 (100), 32768 x 4096 259 (92), 131072 x 1024 249 (95), 32768 x
 //     5120 398 (75), 65536 x 1280 204 (73), fp32 16384 x 4096 273 (87), 16384 x 8192 498 (95)
 //   with a gate row for 512 rows backward bf16 32768 x 8192 494 (96), for 16 rows 642 (74)
-//   split rows: forward fp32 8192 x 16384 461 (69), backward 484 (98), bf16 16384 x 16384 680 (70)
+//   split rows: forward fp32 8192 x 16384 409 (77), backward 484 (98), bf16 16384 x 16384 680 (70)
 //   in pieces: forward bf16 262144 x 110 88 (39), fp32 262144 x 66 110 (37), backward 131072 x 130
 //     163 (37), 65536 x 1027 367 (65), bf16 65536 x 2050 884 (27), 65536 x 1027 587 (20)
 // The kernels for any width instead: forward bf16 65536 x 4096 524, backward 65536 x 8192 2275.

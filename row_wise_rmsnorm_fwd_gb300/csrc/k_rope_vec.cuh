@@ -3,12 +3,13 @@
 // A head is taken as units of two vectors of EPV elements, half of the turned part apart, so
 // that the unit holds EPV whole pairs (interleaved: each vector half of them; vectors of
 // one element: neighbours), and behind that half of the rest apart: neighbouring lanes have
-// neighbouring vectors, so that no sector of memory is asked for twice.  `lanes` lanes (a power of two) share a head, a unit each, so a
-// warp has 32 / lanes heads at a time: of one token, or, where a token has fewer, of
-// several.  It walks over its tokens' heads, and its lanes keep the cosines and sines of their
-// pairs for all of them: an angle is formed once for a warp's share of a token's heads, by
-// one of the lanes that need it.  A CTA works on q alone or on k alone, so a lane's
-// weights, and backward its column sums, stay in registers for all its tokens.
+// neighbouring vectors, so that no sector of memory is asked for twice.  `lanes` lanes (a
+// power of two) share a head, a unit each, so a warp has 32 / lanes heads at a time: of one
+// token, or, where a token has fewer, of several.  It walks over its tokens' heads, and its
+// lanes keep the cosines and sines of their pairs for all of them: an angle is formed once
+// for a warp's share of a token's heads, by one of the lanes that need it.  A CTA works on q
+// alone or on k alone, so a lane's weights, and backward its column sums, stay in registers
+// for all its tokens.
 //
 // What bounds it: HBM, where a token has eight rounds of heads or so; with fewer the token's
 // position, angles and addresses (about 200 instructions a warp) weigh more, and lanes are
