@@ -17,8 +17,8 @@
  * Token (b, s) stands at start + positions[(b * seq + s) mod n_positions], or, without
  * positions, at start + s.  Frequencies are 64-bit fixed-point numbers of turns per
  * position, frequency / (2 pi) * 2^64 modulo 2^64 (rmsnorm_rope_freqs): the product
- * with a 64-bit position modulo 2^64 is the angle modulo a turn, exactly, so far
- * positions are as good as near ones.
+ * with a 64-bit position modulo 2^64 is the angle modulo a turn, exactly.  The frequency
+ * itself is rounded to 2^-65 turns, which position p makes p * 2^-65 turns (2^-25 at 2^40).
  *
  * fp32 arithmetic for both types: bf16 inputs are widened exactly, outputs are
  * rounded once; dw is fp32.

@@ -176,6 +176,32 @@ def test_nothing_behind_the_workspace(cluster, n, t):
         check_backward(v, rule, got)
 
 
+def test_refused_in_python():
+    """Arguments that the binding refuses before the library is called."""
+    x, r, w = (make(s, "f32", 1).cuda() for s in ((4, 6, 64), (4, 6, 64), (64,)))
+    fwd, bwd = binding.rmsnorm_block_fwd_f32, binding.rmsnorm_block_bwd_f32
+    for a, kw in (((x.transpose(0, 1), r), {}), ((x, r[:3]), {}), ((x, r.double()), {}), ((x, r.cpu()), {}),
+                  ((x, r, w[:32]), {}), ((x, r, w, w.cpu()), {}), ((x, r, w), dict(post_norm=False)),
+                  ((x, r, None, w), dict(pre_norm=False)), ((x, r), dict(y=x, pre_norm=False)),
+                  ((x, r), dict(h=x[:2])), ((x, r, w, w, w[:32]), {}), ((x, r, w, w, x[:, :3]), {}),
+                  ((x, r, w, w, x[:3, :1].contiguous()), {}), ((x, r, w, w, x[:1].contiguous()), {}),
+                  ((x, r, w, w, x[:, 0].expand(1, 4, 64).contiguous()), {}),
+                  ((x.bfloat16(), r), {})):
+        with pytest.raises((ValueError, TypeError)):
+            fwd(*a, **kw)
+    for a, kw in (((None, r, x, x), {}), ((x, r, x, None), {}), ((x, r, x, x), dict(pre_norm=False)),
+                  ((x, r[:2], x, x), {}), ((x, r, x, x), dict(dgate=w)), ((x, r, x, x), dict(dpost_w=w.double())),
+                  ((None, r, x, None), dict(pre_norm=False, dpre_w=w)),
+                  ((x, r, x, x), dict(post_norm=False, dpost_w=w)), ((x, r, x, x), dict(dx=x[0])),
+                  ((x, r, x, x, w), dict(workspace=torch.empty(8, dtype=torch.uint8)))):
+        with pytest.raises((ValueError, TypeError)):
+            bwd(*a, **kw)
+    for kw in (dict(residual_scale=float("nan")), dict(post_eps=-1.0), dict(h=x, y=x),
+               dict(branch_scale=1e300)):
+        with pytest.raises((ValueError, binding.RmsnormError)):
+            fwd(x, r, w, w, **kw)
+
+
 @pytest.mark.parametrize("t", TYPES)
 def test_gate_shapes(t):
     """[hidden], [1, hidden], [batch, hidden], [batch, 1, hidden], [batch, seq, hidden]."""

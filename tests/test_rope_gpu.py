@@ -176,6 +176,81 @@ def test_views(inter, t, path):
 
 
 @pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("by", [1, 2, 3, 4])
+@pytest.mark.parametrize("dim,rot", [(16, 8), (32, 32), (64, 64), (128, 32)])
+def test_pointers_off_the_boundaries(dim, rot, by, t):
+    """q, k, the gradients, the outputs and the weights off the 16-byte boundaries, heads and
+    tokens some elements apart; what lies between them stays."""
+    freqs, _ = freqs_of(rot)
+    f = freqs.cuda()
+    for inter in (False, True):
+        for norm in (True, False):
+            rule = Rope(freqs, inter, norm, start=9)
+            v = inputs((2, 11), 3, 2, dim, t, norm)
+
+            def off(a):
+                if a is None:
+                    return None
+                if a.dim() == 1:
+                    return torch.empty(dim + 8, dtype=a.dtype, device="cuda")[by:by + dim].copy_(a)
+                room = torch.full((*a.shape[:-1], dim + by), 7.0, dtype=a.dtype, device="cuda")
+                return room[..., by:].copy_(a)
+
+            g = {n: off(a) for n, a in v.items()}
+            outs = [off(torch.zeros_like(v[n])) for n in "qk"]
+            got = forward(g, f, rule, q_out=outs[0], k_out=outs[1])
+            check_forward(v, rule, None, got)
+            check_backward(v, rule, None, backward(g, f, rule, dq_in=outs[0], dk_in=outs[1]))
+            for o in outs:
+                whole = o.as_strided((*o.shape[:-1], dim + by), o.stride(), o.storage_offset() - by)
+                assert (whole[..., :by] == 7.0).all()
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("lead,hq,hk,dim", [((1,), 300, 3, 64), ((3,), 1, 70, 128), ((5000,), 1, 1, 64),
+                                            ((2, 3), 129, 129, 32), ((800,), 3, 1, 256)])
+def test_many_heads_and_few(lead, hq, hk, dim, t):
+    freqs, _ = freqs_of(dim)
+    rule = Rope(freqs)
+    v = inputs(lead, hq, hk, dim, t)
+    g = on(v)
+    check_forward(v, rule, None, forward(g, freqs.cuda(), rule))
+    check_backward(v, rule, None, backward(g, freqs.cuda(), rule))
+
+
+def test_refused_in_python():
+    """Arguments that the binding refuses before the library is called."""
+    freqs, _ = freqs_of(32)
+    f = freqs.cuda()
+    q, k, w = (make(s, "f32", 1).cuda() for s in ((2, 6, 4, 64), (2, 6, 2, 64), (64,)))
+    fwd = lambda *a, **kw: binding.rmsnorm_rope_fwd_f32(*a, **kw)  # noqa: E731
+    for a, kw in (((q[..., ::2], None, f), {}), ((q, k[:, :5], f), {}), ((q, k.double(), f), {}),
+                  ((q, k.cpu(), f), {}), ((q, k, f.int()), {}), ((q, k, f.cpu()), {}), ((q, k, f[:0]), {}),
+                  ((q[0, 0], None, f), {}), ((q[..., :16], None, f), {}), ((q, k, f[::2]), {}),
+                  ((q, k, f, torch.arange(5, device="cuda")), {}), ((q, k, f, torch.arange(6)), {}),
+                  ((q, k, f, torch.arange(6.0, device="cuda")), {}),
+                  ((q, k, f, torch.arange(12, device="cuda")[::2]), {}), ((q, k, f, None, w[:32]), {}),
+                  ((q, None, f, None, None, w), {}), ((q, k, f, None, w), dict(norm=False)),
+                  ((q, None, f), dict(k_out=k)), ((q, k, f), dict(q_out=k)), ((q, k, f), dict(start=2 ** 63))):
+        with pytest.raises((ValueError, TypeError)):
+            fwd(*a, **kw)
+    for kw in (dict(mscale=1e300), dict(eps=-1.0)):      # not a finite fp32 number, for one
+        with pytest.raises((ValueError, binding.RmsnormError)):
+            fwd(q, k, f, **kw)
+    with pytest.raises(binding.RmsnormError):            # an output over half of its input
+        a = torch.zeros(2, 6, 6, 64, device="cuda")
+        fwd(a[:, :, :4], None, f, q_out=a[:, :, 2:])
+    with pytest.raises(binding.RmsnormError):            # an output that lies over itself
+        fwd(q, k, f, q_out=torch.zeros(2, 6, 1, 64, device="cuda").expand(2, 6, 4, 64))
+    bwd = lambda *a, **kw: binding.rmsnorm_rope_bwd_f32(*a, **kw)  # noqa: E731
+    for a, kw in (((q, k, f, None, q), {}), ((q, k, f, None, q, k[:1]), {}), ((q, None, f, None, q, k), {}),
+                  ((q, k, f), dict(q_w=w)), ((q, k, f), dict(dq_w=w)), ((q, None, f), dict(dk_in=k)),
+                  ((q, k, f, None, q, k), dict(dq_w=w[:32])), ((q, k, f, None, q, k, w, w), dict(dk_in=q))):
+        with pytest.raises((ValueError, TypeError)):
+            bwd(*a, **kw)
+
+
+@pytest.mark.parametrize("t", TYPES)
 def test_expanded_inputs_and_q_alone(t):
     """Inputs whose strides are zero (one gradient for every head), and no k."""
     freqs, _ = freqs_of(32)
