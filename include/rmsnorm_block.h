@@ -96,8 +96,10 @@ rmsnorm_status_t rmsnorm_block_fwd_bf16(const uint16_t* x, const uint16_t* resid
  * RMSNORM_ERR_UNSUPPORTED) or RMSNORM_PATH_TWOPASS (a CTA per row that reads it again for each
  * sum: any width and alignment); opt->wait_timeout_ns; and in the test build of the library
  * opt->fault_inject with RMSNORM_PATH_STAGED: 1 = each CTA's first copy is withheld, 2 =
- * with opt->cluster, rank 0's first sums are (elsewhere RMSNORM_ERR_UNSUPPORTED).  Every other
- * field but epilogue_alpha, which is not read, must be zero, else RMSNORM_ERR_INVALID_ARG. */
+ * with opt->cluster, rank 0's first sums are, 3 = with opt->cluster, the wait of rank 0's last
+ * thread for the first sums counts as run out (elsewhere RMSNORM_ERR_UNSUPPORTED; 3 without the
+ * test build RMSNORM_ERR_INVALID_ARG).  Every other field but epilogue_alpha, which is not read,
+ * must be zero, else RMSNORM_ERR_INVALID_ARG. */
 rmsnorm_status_t rmsnorm_block_fwd_ex(int32_t dtype, const void* x, const void* residual, void* h,
                                       void* y, int64_t rows, int64_t hidden,
                                       const rmsnorm_block_t* block, const rmsnorm_options_t* opt,

@@ -15,6 +15,7 @@ namespace {
 
 constexpr int64_t kMaxHidden = 1 << 20;
 constexpr int kMaxCluster = 16;
+constexpr int kLastFault = RMSNORM_FAULT_INJECT ? 3 : 2;
 
 struct BlockCall {
     int dtype = 0;
@@ -68,14 +69,14 @@ rmsnorm_status_t check_rule(const rmsnorm_block_t& b, const rmsnorm_options_t* o
     const rmsnorm_options_t& o = *opt;
     if (o.cluster < 0 || o.cluster > kMaxCluster || (o.cluster & (o.cluster - 1)) || o.threads || o.grid ||
         o.vec_bytes || o.chunk_bytes || o.stages || o.weights || o.reserved || o.epilogue ||
-        o.fault_inject < 0 || o.fault_inject > 2)
+        o.fault_inject < 0 || o.fault_inject > kLastFault)
         return RMSNORM_ERR_INVALID_ARG;
     if (o.path != RMSNORM_PATH_AUTO && o.path != RMSNORM_PATH_STAGED && o.path != RMSNORM_PATH_TWOPASS &&
         !(o.path == RMSNORM_PATH_ROWREG && !back))
         return RMSNORM_ERR_INVALID_ARG;
     if (o.cluster && o.path != RMSNORM_PATH_STAGED) return RMSNORM_ERR_INVALID_ARG;
     if (o.fault_inject && (!RMSNORM_FAULT_INJECT || o.path != RMSNORM_PATH_STAGED ||
-                           (o.fault_inject == 2 && o.cluster < 2)))
+                           (o.fault_inject >= 2 && o.cluster < 2)))
         return RMSNORM_ERR_UNSUPPORTED;
     c->path = o.path;
     c->cluster = o.cluster;

@@ -42,7 +42,9 @@ struct BlockExchange {
     alignas(8) uint64_t bar[2];
 };
 
-// Sums of all ranks in rank order; false once the bounded wait has run out.
+// Sums of all ranks in rank order; false once the bounded wait has run out, which the thread that
+// it ran out for reports.  Every thread has a clock of its own, so where the sums arrive close to
+// the limit some may get them and some not: what the result decides for the CTA is first agreed on.
 template <int N>
 __device__ __forceinline__ bool exchange_sums(BlockExchange* ex, float (&v)[8], int ncta, uint32_t rank,
                                               uint32_t it, const BlockParams& p) {
@@ -64,7 +66,11 @@ __device__ __forceinline__ bool exchange_sums(BlockExchange* ex, float (&v)[8], 
             for (int k = 0; k < N; k += 2) st_async_v2_f32(to + 4 * k, v[k], v[k + 1], peer_bar);
         }
     }
-    const bool ok = mbar_wait_bounded<true>(bar, (it >> 1) & 1u, p.timeout_ns);
+    bool ok = mbar_wait_bounded<true>(bar, (it >> 1) & 1u, p.timeout_ns);
+#if RMSNORM_FAULT_INJECT
+    if (p.fault == kFaultClusterLateThread && rank == 0 && it == 0 && tid == static_cast<int>(blockDim.x) - 1)
+        ok = false;
+#endif
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = 0.f;
     if (ok) {
@@ -72,7 +78,7 @@ __device__ __forceinline__ bool exchange_sums(BlockExchange* ex, float (&v)[8], 
 #pragma unroll
             for (int k = 0; k < N; ++k) v[k] += ex->slot[b][c][k];
         }
-    } else if (tid == 0) {
+    } else {
         report_timeout(p.status, kSiteClusterExchange);
     }
     return ok;
@@ -409,6 +415,7 @@ blocknorm_fwd_staged_kernel(const BlockParams p) {
             ++use;
         }
     }
+    if constexpr (CL) bad = __syncthreads_or(bad);      // after the last row nothing else says so
     if (n < ring.count && threadIdx.x == 0) {
         if (!bad) report_timeout(p.status, kSiteStagedFull);
         ring.drain(n, slot, use);
@@ -699,6 +706,7 @@ __global__ void __launch_bounds__(kBlockBwdMaxThreads, 1) blocknorm_bwd_staged_k
             ++use;
         }
     }
+    if constexpr (CL) bad = __syncthreads_or(bad);      // after the last row nothing else says so
     if (n < ring.count || bad) {
         if (threadIdx.x == 0) {
             if (!bad) report_timeout(p.status, kSiteStagedFull);
