@@ -15,7 +15,7 @@ namespace {
 
 constexpr int64_t kMaxHidden = 1 << 20;
 constexpr int kMaxCluster = 16;
-constexpr int kLastFault = RMSNORM_FAULT_INJECT ? 3 : 2;
+constexpr int kLastFault = RMSNORM_FAULT_INJECT ? kFaultClusterLateThread : 2;
 
 struct BlockCall {
     int dtype = 0;

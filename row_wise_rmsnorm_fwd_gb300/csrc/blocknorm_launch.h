@@ -5,6 +5,10 @@
 
 namespace rmsnorm {
 
+// Failure injection of this family beside common.cuh's, in the test build only: one thread takes
+// its wait for a cluster's sums as run out.
+constexpr int kFaultClusterLateThread = 3;
+
 // Everything a kernel of this family needs; passed by value.
 struct BlockParams {
     const void* x;

@@ -20,7 +20,6 @@ enum : int {
     kFaultNone = 0,
     kFaultStagedWithholdCopy = 1,      // producer arms a barrier, issues no copy
     kFaultClusterWithholdPartial = 2,  // one cluster CTA never sends its partial
-    kFaultClusterLateThread = 3,       // one thread takes its wait for the partials as run out
 };
 
 // Fused epilogues, applied to each fp32 output value before the store
