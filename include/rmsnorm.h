@@ -141,7 +141,8 @@ typedef struct {
                                 (any path but PAGE): 0 none, 1 y*epilogue_alpha,
                                 2 ReLU (y if y > 0 or y is NaN, else +0) */
     float epilogue_alpha;    /* scale for epilogue 1 (finite) */
-    uint64_t wait_timeout_ns;/* limit of every device-side wait; 0 = 2 seconds */
+    uint64_t wait_timeout_ns;/* limit of every device-side wait; 0 = 2 seconds, less than
+                                a millisecond counts as one */
 } rmsnorm_options_t;
 
 /* What a call with these arguments would launch. */

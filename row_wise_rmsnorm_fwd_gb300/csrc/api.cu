@@ -770,7 +770,7 @@ rmsnorm_status_t run(int32_t dtype, const void* x, const void* w, void* y, int64
     p.fault = c.opt.fault_inject;
     p.alpha = c.opt.epilogue == 1 ? c.opt.epilogue_alpha : 1.0f;
     p.status = c.info->status;
-    p.timeout_ns = c.opt.wait_timeout_ns ? c.opt.wait_timeout_ns : kDefaultTimeoutNs;
+    p.timeout_ns = wait_limit(c.opt.wait_timeout_ns);
 
     LaunchShape s{P.grid, P.block, P.cluster, P.smem};
     if (ensure_prepared(c.dev, P.fn, c.info->smem_optin) != cudaSuccess) return RMSNORM_ERR_CUDA;

@@ -65,6 +65,7 @@ rmsnorm_status_t check_rule(const rmsnorm_block_t& b, const rmsnorm_options_t* o
     p.branch_scale = b.branch_scale;
     p.post_eps = b.post_eps;
     p.pre_eps = b.pre_eps;
+    p.timeout_ns = wait_limit(0);
     if (!opt) return RMSNORM_OK;
     const rmsnorm_options_t& o = *opt;
     if (o.cluster < 0 || o.cluster > kMaxCluster || (o.cluster & (o.cluster - 1)) || o.threads || o.grid ||
@@ -81,7 +82,7 @@ rmsnorm_status_t check_rule(const rmsnorm_block_t& b, const rmsnorm_options_t* o
     c->path = o.path;
     c->cluster = o.cluster;
     p.fault = o.fault_inject;
-    p.timeout_ns = o.wait_timeout_ns;
+    p.timeout_ns = wait_limit(o.wait_timeout_ns);
     return RMSNORM_OK;
 }
 
@@ -188,7 +189,6 @@ rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t read_bits, uintptr_t other_
                 p.slice_vecs = static_cast<int32_t>(slice);
                 p.row_slot = static_cast<int32_t>(row_slot);
                 p.status = c->dv.status;
-                if (!p.timeout_ns) p.timeout_ns = kDefaultTimeoutNs;
                 int64_t units = cluster > 1 ? best : static_cast<int64_t>(c->dv.sms) * best;
                 // what the workspace has parts for
                 if (back && units > kBwdCtasPerSm * c->dv.sms) units = kBwdCtasPerSm * c->dv.sms;

@@ -10,6 +10,16 @@ namespace rmsnorm {
 
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;   // 2 s per bounded wait
 
+// The limit of a call's waits.  A kernel whose wait has run out waits once more, to the same
+// limit, for the copies and partials that are still under way to its shared memory: it must not
+// leave before they have landed, and with a limit of less than they take it would.  A
+// millisecond is some hundred times that.
+constexpr uint64_t kLeastTimeoutNs = 1000000ull;
+inline uint64_t wait_limit(uint64_t asked) {
+    if (asked == 0) return kDefaultTimeoutNs;
+    return asked < kLeastTimeoutNs ? kLeastTimeoutNs : asked;
+}
+
 struct DeviceInfo;
 
 // Keep `e` as the calling thread's last CUDA error if it is one; returns e.

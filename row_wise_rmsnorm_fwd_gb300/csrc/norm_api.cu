@@ -60,7 +60,7 @@ rmsnorm_status_t check_options(const rmsnorm_options_t* opt, NormCall* c) {
 void set_waits(NormCall* c) {
     c->p.status = c->dv.status;
     c->p.fault = c->opt.fault_inject;
-    c->p.timeout_ns = c->opt.wait_timeout_ns ? c->opt.wait_timeout_ns : kDefaultTimeoutNs;
+    c->p.timeout_ns = wait_limit(c->opt.wait_timeout_ns);
 }
 
 void count_vectors(NormCall* c, uintptr_t bits) {

@@ -724,7 +724,7 @@ rmsnorm_status_t sm_run(int32_t dtype, const void* x, void* y, int64_t rows, int
     p.resident = P.res_chunks;
     p.status = c.dv.status;
     p.fault = c.opt.fault_inject;
-    p.timeout_ns = c.opt.wait_timeout_ns ? c.opt.wait_timeout_ns : kDefaultTimeoutNs;
+    p.timeout_ns = wait_limit(c.opt.wait_timeout_ns);
     LaunchShape s{P.grid, P.block, P.cluster, P.smem};
     if (ensure_prepared(c.dv.dev, P.fn, c.dv.smem_optin) != cudaSuccess) return RMSNORM_ERR_CUDA;
     if (P.scratch > 0) {
