@@ -18,7 +18,8 @@
  * positions, at start + s.  Frequencies are 64-bit fixed-point numbers of turns per
  * position, frequency / (2 pi) * 2^64 modulo 2^64 (rmsnorm_rope_freqs): the product
  * with a 64-bit position modulo 2^64 is the angle modulo a turn, exactly.  The frequency
- * itself is rounded to 2^-65 turns, which position p makes p * 2^-65 turns (2^-25 at 2^40).
+ * itself is rounded once, to the nearest of them (frequencies of up to 2^40 turns a position, which
+ * small divisors give): it is off by 2^-65 turns, which position p makes p * 2^-65 (2^-25 at 2^40).
  *
  * fp32 arithmetic for both types: bf16 inputs are widened exactly, outputs are
  * rounded once; dw is fp32.
@@ -83,7 +84,8 @@ typedef enum {
                                    factor, the fastest kept; rot_dim >= 4 */
     RMSNORM_ROPE_RAMP = 3,      /* by pair number: pairs that make more than `high` turns over
                                    original_len kept, fewer than `low` divided, a ramp between the
-                                   two pair numbers (rounded outwards); mscale 0.1 ln(factor) + 1
+                                   two pair numbers (rounded outwards, the first at least 0, the
+                                   second at most rot_dim - 1); mscale 0.1 ln(factor) + 1
                                    (Peng et al., "YaRN: Efficient Context Window Extension of Large
                                    Language Models", 2023) */
     RMSNORM_ROPE_BANDS = 4      /* by turns over original_len: `high` and more kept, `low` and fewer

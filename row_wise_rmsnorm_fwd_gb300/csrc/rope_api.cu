@@ -15,8 +15,70 @@ namespace {
 
 // ---------------------------------------------------------------- frequencies --
 
-static_assert(LDBL_MANT_DIG >= 64, "frequencies are formed to 64 bits");
-constexpr long double kTwoPi = 6.283185307179586476925286766559005768L;
+// Numbers as sums of two long doubles, the second at most half a last place of the first: one
+// long double (64 bits here or 113, by machine) rounds a frequency before its last of 64 bits
+// behind the point is known.  Sums and products are off by a few 2^-2p of themselves, p bits.
+static_assert(LDBL_MANT_DIG >= 64, "two of them have 128 bits");
+
+struct Two {
+    long double hi, lo;
+};
+
+Two normal(long double a, long double b) {          // |a| >= |b|
+    const long double s = a + b;
+    return {s, b - (s - a)};
+}
+
+Two operator+(Two a, Two b) {
+    const long double s = a.hi + b.hi, t = s - a.hi;
+    return normal(s, (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo));
+}
+
+Two operator-(Two a) { return {-a.hi, -a.lo}; }
+
+Two operator*(Two a, Two b) {
+    const long double p = a.hi * b.hi;
+    return normal(p, fmal(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+
+Two operator/(Two a, Two b) {                       // three quotients, each of what is left
+    Two q{0.0L, 0.0L};
+    for (int k = 0; k < 3; ++k) {
+        const Two next{a.hi / b.hi, 0.0L};
+        q = q + next;
+        a = a + -(next * b);
+    }
+    return q;
+}
+
+Two two(long double v) { return {v, 0.0L}; }
+
+// 2 pi to 163 bits, 32 or 35 at a time.
+Two two_pi() {
+    return (((two(0x6.487ED511p0L) + two(0x0B4611A6p-64L)) + two(0x2633145Cp-96L)) + two(0x06E0E689p-128L)) +
+           two(0x48127044p-160L);
+}
+
+Two power(Two v, int n) {
+    Two r = two(1.0L);
+    for (; n > 0; n >>= 1, v = v * v)
+        if (n & 1) r = r * v;
+    return r;
+}
+
+// The n-th root of v >= 1: one step of Newton's method, which doubles powl's bits.
+Two root(double v, int n) {
+    const Two y = two(powl(v, 1.0L / n)), below = power(y, n - 1);
+    return y + -((below * y + two(-static_cast<long double>(v))) / (two(n) * below));
+}
+
+// The nearest multiple of 2^-64 to v >= 0, in those units modulo 2^64.
+uint64_t turns_of(Two v) {
+    const long double part = (v.hi - floorl(v.hi)) * 0x1p64L, whole = floorl(part);
+    long double rest = roundl((part - whole) + (v.lo - roundl(v.lo)) * 0x1p64L);
+    if (rest >= 0x1p63L) rest -= 0x1p64L;
+    return static_cast<uint64_t>(whole) + static_cast<uint64_t>(static_cast<int64_t>(rest));
+}
 
 bool positive(double v) { return std::isfinite(v) && v > 0.0; }
 
@@ -36,37 +98,41 @@ rmsnorm_status_t freqs_of(const rmsnorm_rope_rule_t* r, uint64_t* freqs, float* 
         for (int i = 0; i < half; ++i)
             if (!positive(r->divisors[i])) return RMSNORM_ERR_INVALID_ARG;
     }
-    const long double dim = r->rot_dim, factor = r->factor, len = r->original_len;
-    long double base = r->base;
-    if (r->scaling == RMSNORM_ROPE_BASE) base *= powl(factor, dim / (dim - 2.0L));
+    const Two circle = two_pi(), factor = two(r->factor);
     long double first = 0.0L, last = 0.0L;
     if (r->scaling == RMSNORM_ROPE_RAMP) {
         // the pair that makes t turns: len * base^(-2i / dim) / (2 pi) = t
-        auto pair = [&](long double t) { return dim * logl(len / (t * kTwoPi)) / (2.0L * logl(base)); };
+        const long double len = r->original_len, log_base = logl(r->base);
+        auto pair = [&](long double t) { return half * logl(len / (t * circle.hi)) / log_base; };
         first = fmaxl(floorl(pair(r->high)), 0.0L);
-        last = fminl(ceill(pair(r->low)), dim - 1.0L);
+        last = fminl(ceill(pair(r->low)), r->rot_dim - 1.0L);
     }
-    for (int i = 0; i < half; ++i) {
-        long double f = powl(base, -2.0L * i / dim);
-        long double kept = 1.0L;
+    // each frequency from the one before it, down by base^(1 / half); with a raised base, base *
+    // factor^(half / (half - 1)), by factor^(1 / (half - 1)) more
+    Two step = root(r->base, half);
+    if (r->scaling == RMSNORM_ROPE_BASE) step = step * root(r->factor, half - 1);
+    Two down = two(1.0L);                                       // base^(i / half)
+    for (int i = 0; i < half; ++i, down = down * step) {
+        Two f = two(1.0L) / (circle * down);                    // turns per position
+        Two kept = two(1.0L);
         switch (r->scaling) {
-            case RMSNORM_ROPE_LINEAR: kept = 0.0L; break;
-            case RMSNORM_ROPE_RAMP: kept = 1.0L - (i - first) / fmaxl(last - first, 0.001L); break;
+            case RMSNORM_ROPE_LINEAR: kept = two(0.0L); break;
+            case RMSNORM_ROPE_RAMP:
+                kept = two(1.0L) + -(two(i - first) / two(fmaxl(last - first, 0.001L)));
+                break;
             case RMSNORM_ROPE_BANDS:
-                kept = (len * f / kTwoPi - r->low) / (static_cast<long double>(r->high) - r->low);
+                kept = (two(r->original_len) * f + two(-static_cast<long double>(r->low))) /
+                       (two(r->high) + two(-static_cast<long double>(r->low)));
                 break;
             default: break;
         }
-        kept = fminl(fmaxl(kept, 0.0L), 1.0L);
-        if (kept < 1.0L) f = f / factor * (1.0L - kept) + f * kept;
-        if (r->divisors) f /= r->divisors[i];
-        const long double per = f / kTwoPi;                    // turns per position
-        const long double part = roundl((per - floorl(per)) * 0x1p64L);
-        // 2^64 itself is a whole turn
-        freqs[i] = part >= 0x1p64L ? 0u : static_cast<uint64_t>(part);
+        if (kept.hi < 0.0L) kept = two(0.0L);
+        if (kept.hi < 1.0L) f = f / factor * (two(1.0L) + -kept) + f * kept;
+        if (r->divisors) f = f / two(r->divisors[i]);
+        freqs[i] = turns_of(f);
     }
     *mscale = r->scaling == RMSNORM_ROPE_RAMP
-                  ? static_cast<float>(0.1L * logl(factor) + 1.0L) : 1.0f;
+                  ? static_cast<float>(0.1L * logl(r->factor) + 1.0L) : 1.0f;
     return RMSNORM_OK;
 }
 
