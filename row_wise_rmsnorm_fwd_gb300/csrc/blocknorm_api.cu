@@ -136,8 +136,10 @@ rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t read_bits, uintptr_t other_
     const int64_t max_threads = back ? kBlockBwdMaxThreads
                                 : vb < 16 ? kBlockFwdRaggedMaxThreads : kBlockFwdMaxThreads;
     const int64_t budget = c->dv.smem_optin - 6 * 1024;             // static shared memory beside it
-    // fp32 backward rows that would take all the threads of an SM are split in two, so that two
-    // CTAs share it: 16384 x 4096 247 us instead of 276 (3584: 225 / 227, bf16 8192: 716 / 579).
+    // fp32 backward rows that would take all the threads of an SM (3844 to 4096 elements) are split
+    // in two, so that two CTAs share it.  Measured (us, split / not): 16384 rows of 3844 235 / 263, 3968
+    // 257 / 265, 4096 273 / 273, with the post norm alone 164 / 183, with the pre norm alone 274 / 266;
+    // 2048 rows of 3844 37.8 / 36.5, 4096 38.2 / 38.1.
     int64_t least = 1;
     if (back && c->sz == 4 && vb == 16 && group_of(nvec) == kBlockBwdMaxThreads) least = 2;
     // Forward rows that have to be split, which costs two exchanges a row, are split into slices of

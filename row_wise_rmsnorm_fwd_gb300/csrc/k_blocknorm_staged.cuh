@@ -144,8 +144,9 @@ __device__ __forceinline__ Vec<VB> take_piece(const Vec<16>& v, int j) {
 }
 
 // FAST: a branch for threads that have all pieces (all of a row but its last ones).  Measured
-// (us, with / without): forward bf16 65536 x 1027 261 / 464, 65536 x 2050 337 / 378, but with
-// 8-byte pieces fp32 32768 x 2050 284 / 261, and backward 500 / 464.
+// (us, with / without): forward bf16 262144 x 110 88 / 101, 131072 x 251 119 / 192, fp32 262144 x
+// 101 131 / 154, but with 8-byte pieces 262144 x 66 118 / 110, 131072 x 126 65 / 59; backward fp32 32768
+// x 2050 500 / 464.
 //
 // A vector of a slot; zeros where (bit j of `on`: piece j) it is missing.  apart: bytes from
 // piece to piece.
