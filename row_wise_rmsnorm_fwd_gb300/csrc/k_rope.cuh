@@ -5,7 +5,7 @@
 // the integer product with a position, modulo 2^64, is the angle modulo a turn with
 // nothing lost for any position.  Of its upper 32 bits the nearest quarter turn is taken
 // away in integers, which leaves at most an eighth of a turn for fp32 to hold: the angle
-// is off by at most 2^-23 of that (without, of half a turn).
+// is off by three roundings of that (without, of half a turn).
 // No fp64, and no table in memory.
 #pragma once
 #include "common.cuh"
@@ -15,7 +15,10 @@
 namespace rmsnorm {
 
 // (cos, sin) * mscale at a position.  Within an eighth of a turn the Taylor series of sine and
-// cosine end at x^9 / 9! and x^10 / 10!: the next terms are below 2^-29 of either.
+// cosine end at x^9 / 9! and x^10 / 10!: the next terms are below 2^-29 (2^-28 of the sine itself)
+// and 2^-33.  In units of 2^-24 both are off by at most 2.4 from the angle (its conversion, the
+// constant and their product, each of at most an eighth of a turn, and the turns below 2^-32),
+// 1.8 from the series and 1 from mscale.
 __device__ __forceinline__ float2 rope_turn(uint64_t freq, int64_t position, float mscale) {
     const uint32_t turns = static_cast<uint32_t>((freq * static_cast<uint64_t>(position)) >> 32);
     const uint32_t quarter = (turns + 0x20000000u) >> 30;
