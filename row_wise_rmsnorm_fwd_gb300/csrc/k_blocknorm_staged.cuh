@@ -19,9 +19,15 @@
 //   forward bf16 65536 x 4096 342 (92), 32768 x 8192 344 (92), 131072 x 1024 181 (87), 65536 x
 //     1280 136 (73), fp32 16384 x 4096 167 (95), 16384 x 8192 349 (91)
 //   backward bf16 65536 x 8192 951 (100), 32768 x 4096 259 (92), 131072 x 1024 249 (95), 32768 x
-//     5120 398 (75), 65536 x 1280 204 (73), fp32 16384 x 4096 273 (87), 16384 x 8192 498 (95)
-//   with a gate row for 512 rows backward bf16 32768 x 8192 494 (96), for 16 rows 642 (74)
-//   split rows: forward fp32 8192 x 16384 409 (77), backward 484 (98), bf16 16384 x 16384 680 (70)
+//     5120 398 (75), 65536 x 1280 204 (73), fp32 16384 x 4096 273 (87), 16384 x 8192 495 (96)
+//   the sum and the norm before the next block alone: forward bf16 65536 x 4096 359 (88), 32768 x 8192 355
+//     (89), 131072 x 1024 184 (86), 65536 x 1280 118 (84), fp32 16384 x 4096 176 (90), 16384 x 8192 340
+//     (93); backward 545 (87), 543 (87), 269 (88), 164 (91), 274 (87), 528 (90)
+//   with a gate row for 512 rows backward bf16 32768 x 8192 486 (98), for 16 rows 638 (74), for 4 1056
+//     (45), for one 2777 (17): a part in fp32 for each, read twice by the sums' two launches; forward 349
+//     (91), 352 (90), 360 (88), 400 (79)
+//   split rows: forward fp32 8192 x 16384 410 (77), 8192 x 12288 349 (68), backward 479 (99), 429 (83),
+//     bf16 16384 x 16384 697 (68), 16384 x 12288 555 (64)
 //   in pieces: forward bf16 262144 x 110 88 (39), fp32 262144 x 66 110 (37), backward 131072 x 130
 //     163 (37), 65536 x 1027 367 (65), bf16 65536 x 2050 884 (27), 65536 x 1027 587 (20)
 // The kernels for any width instead: forward bf16 65536 x 4096 524, backward 65536 x 8192 2275.

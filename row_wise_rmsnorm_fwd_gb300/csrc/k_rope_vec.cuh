@@ -19,6 +19,8 @@
 //     norms 204 (97); 16 + 16 of 64: 115 (69); 32768, 16 + 4 of 256, 64 turned: 117 (84);
 //     fp32 32768, 32 + 8 of 128: 203 (98)
 //   backward the same: 316 (94), 320 (93), 204 (97), 162 (73), 166 (89), 310 (96)
+//   16 + 16 of 64 without positions (token s stands at s) 103 (77) and 142 (84), without norms too 84 (94)
+//     and 84 (94)
 //   7 + 1 of 96: 84 (36) and 122 (37); 28 + 4 of 80, 20 turned (vectors of 4 bytes): 373 (27)
 //     and 554 (27)
 // A warp per head with every angle formed for itself (k_rope.cuh): 1328 and 3876.
