@@ -41,17 +41,12 @@ Two operator*(Two a, Two b) {
     return normal(p, fmal(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
 }
 
-Two operator/(Two a, Two b) {                       // three quotients, each of what is left
-    Two q{0.0L, 0.0L};
-    for (int k = 0; k < 3; ++k) {
-        const Two next{a.hi / b.hi, 0.0L};
-        q = q + next;
-        a = a + -(next * b);
-    }
-    return q;
-}
-
 Two two(long double v) { return {v, 0.0L}; }
+
+Two operator/(Two a, Two b) {                       // a quotient, and that of what it leaves
+    const long double q = a.hi / b.hi;
+    return normal(q, (a + -(two(q) * b)).hi / b.hi);
+}
 
 // 2 pi to 163 bits, 32 or 35 at a time.
 Two two_pi() {
@@ -98,7 +93,7 @@ rmsnorm_status_t freqs_of(const rmsnorm_rope_rule_t* r, uint64_t* freqs, float* 
         for (int i = 0; i < half; ++i)
             if (!positive(r->divisors[i])) return RMSNORM_ERR_INVALID_ARG;
     }
-    const Two circle = two_pi(), factor = two(r->factor);
+    const Two one = two(1.0L), circle = two_pi();
     long double first = 0.0L, last = 0.0L;
     if (r->scaling == RMSNORM_ROPE_RAMP) {
         // the pair that makes t turns: len * base^(-2i / dim) / (2 pi) = t
@@ -111,23 +106,22 @@ rmsnorm_status_t freqs_of(const rmsnorm_rope_rule_t* r, uint64_t* freqs, float* 
     // factor^(half / (half - 1)), by factor^(1 / (half - 1)) more
     Two step = root(r->base, half);
     if (r->scaling == RMSNORM_ROPE_BASE) step = step * root(r->factor, half - 1);
-    Two down = two(1.0L);                                       // base^(i / half)
-    for (int i = 0; i < half; ++i, down = down * step) {
-        Two f = two(1.0L) / (circle * down);                    // turns per position
-        Two kept = two(1.0L);
-        switch (r->scaling) {
-            case RMSNORM_ROPE_LINEAR: kept = two(0.0L); break;
-            case RMSNORM_ROPE_RAMP:
-                kept = two(1.0L) + -(two(i - first) / two(fmaxl(last - first, 0.001L)));
-                break;
-            case RMSNORM_ROPE_BANDS:
-                kept = (two(r->original_len) * f + two(-static_cast<long double>(r->low))) /
-                       (two(r->high) + two(-static_cast<long double>(r->low)));
-                break;
-            default: break;
+    step = one / step;
+    const bool part = r->scaling != RMSNORM_ROPE_NONE && r->scaling != RMSNORM_ROPE_BASE;
+    const Two divided = part ? one / two(r->factor) : one;
+    const Two low = two(-static_cast<long double>(r->low)), len = two(r->original_len);
+    const Two per_turn = turns ? one / (two(r->high) + low) : one;
+    const Two per_pair = one / two(fmaxl(last - first, 0.001L));
+    Two plain = one / circle;                                   // turns per position, not scaled
+    for (int i = 0; i < half; ++i, plain = plain * step) {
+        Two f = plain;
+        if (part) {
+            Two kept = two(0.0L);
+            if (r->scaling == RMSNORM_ROPE_RAMP) kept = one + -(two(i - first) * per_pair);
+            if (r->scaling == RMSNORM_ROPE_BANDS) kept = (len * f + low) * per_turn;
+            if (kept.hi <= 0.0L) f = f * divided;
+            else if (kept.hi < 1.0L) f = f * (kept + (one + -kept) * divided);
         }
-        if (kept.hi < 0.0L) kept = two(0.0L);
-        if (kept.hi < 1.0L) f = f / factor * (two(1.0L) + -kept) + f * kept;
         if (r->divisors) f = f / two(r->divisors[i]);
         freqs[i] = turns_of(f);
     }
