@@ -165,13 +165,8 @@ rmsnorm_status_t plan_staged(BlockCall* c, uintptr_t read_bits, uintptr_t other_
             const int64_t row_slot = vb < 16 ? div_up(row_bytes + 16 - vb, 16) * 16 : slice * 16;
             const int64_t slot = narr * rows * row_slot;
             const int64_t scratch = back && rows > 1 ? rows * row_bytes * 4 / c->sz : 0;
-            // Kernels without predicates or filled-in weights, measured (us, with / without, no gate):
-            // both norms fp32 16384 x 8192 328 / 339, backward 497 / 505, bf16 65536 x 4096 352 / 340,
-            // backward 503 / 512; pre norm alone bf16 131072 x 1024 183 / 190, fp32 16384 x 4096 175 /
-            // 181, backward 16384 x 8192 527 / 539.  With the post norm alone there are none: bf16
-            // 32768 x 8192 275 / 263, backward 335 / 321, fp32 16384 x 4096 135 / 138.
-            const bool whole = vb == 16 && nvec == cluster * group * (kBlockStagedBytes / 16) && p.pre && p.pre_w &&
-                               (!p.post || p.post_w);
+            const bool whole = vb == 16 && nvec == cluster * group * (kBlockStagedBytes / 16) && (!p.post || p.post_w) &&
+                               (!p.pre || p.pre_w) && (p.post || p.pre);
             *fn = staged_ptr({c->dtype, vb, back, p.post != 0, p.pre != 0, cluster > 1, whole, p.gate != nullptr});
             int best = 0;
             for (int64_t slots = 3; slots >= 2; --slots) {

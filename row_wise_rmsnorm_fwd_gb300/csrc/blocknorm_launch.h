@@ -79,8 +79,8 @@ int blocknorm_cols_block();
 // dpre_w and one for each gate row; else dpost_w from the sums of several gate rows.
 BlockFn blocknorm_reduce_ptr(int dtype, int width, bool gates);
 // Rows staged in shared memory, read once.  post, pre: the norms; cluster: rows split over
-// a thread-block cluster; whole (with pre): every thread has all its vectors, there are weights
-// for the norms, and a gate as `gate` says.
+// a thread-block cluster; whole: every thread has all its vectors, there are weights for
+// the norms (one at least), and a gate as `gate` says.
 struct BlockVariant {
     int dtype;
     int vb;               // bytes of a vector; less than 16: ragged rows

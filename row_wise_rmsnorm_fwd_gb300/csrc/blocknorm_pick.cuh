@@ -12,7 +12,7 @@ static BlockFn blocknorm_kernel() {
 
 template <typename T, bool BACK, bool POST, bool PRE>
 static BlockFn blocknorm_pick(const BlockVariant& v) {
-    if constexpr (PRE) {
+    if constexpr (POST || PRE) {
         if (v.whole && v.gate)
             return v.cluster ? blocknorm_kernel<T, BACK, POST, PRE, true, kBlockGated>()
                              : blocknorm_kernel<T, BACK, POST, PRE, false, kBlockGated>();
